@@ -27,7 +27,9 @@ QTYPES = {"q8_0": Q8_0, "q4_0": Q4_0, "q4_k": Q4_K}
 __all__ = ["Q8_0", "Q4_0", "Q4_K", "BLOCK_BYTES", "BQError", "packed_bytes", "quantize_pack",
            "gemv", "gemv_q8_0", "gemv_q4_0", "gemv_q4_k", "gemv_gate_up_silu", "gemv_verify",
            "gemv_qkv_bias", "gemv_f16", "concat_packed",
-           "device_status", "tree_lanes", "version", "StreamOp", "StreamPlan"]
+           "device_status", "tree_lanes", "version", "StreamOp", "StreamPlan",
+           "PagedKVCache", "Rope", "BlockTables", "kv_block_tables", "kv_append", "paged_attention",
+           "paged_attention_workspace", "sandwich_norm"]
 
 
 def _qt(qtype):
@@ -318,3 +320,7 @@ class StreamPlan:
         if h is not None and h.value:
             lib.bq_stream_plan_destroy(h)
             self._handle = None
+
+
+from .cache import (BlockTables, PagedKVCache, Rope, kv_append, kv_block_tables,  # noqa: E402
+                    paged_attention, paged_attention_workspace, sandwich_norm)

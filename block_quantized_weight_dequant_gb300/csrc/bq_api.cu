@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "../../include/bqgemv.h"
+#include "bq_cache.cuh"
 #include "bq_dot.cuh"
 #include "bq_exec.cuh"
 #include "bq_multi.cuh"
@@ -1446,7 +1447,11 @@ bq_status bq_device_status(unsigned int *flags, int clear) {
     if (bq_internal_status_q8_0(&a, clear) != 0) return BQ_ERR_CUDA;
     if (bq_internal_status_q4_0(&b, clear) != 0) return BQ_ERR_CUDA;
     if (bq_internal_status_q4_k(&c, clear) != 0) return BQ_ERR_CUDA;
-    *flags = a | b | c;
+    unsigned int d = 0, e = 0, f = 0;  // the calls around the paged cache
+    if (bq_internal_status_tables(&d, clear) != 0) return BQ_ERR_CUDA;
+    if (bq_internal_status_append(&e, clear) != 0) return BQ_ERR_CUDA;
+    if (bq_internal_status_attn(&f, clear) != 0) return BQ_ERR_CUDA;
+    *flags = a | b | c | d | e | f;
     return *flags ? BQ_ERR_DEVICE : BQ_OK;
 }
 

@@ -1,0 +1,210 @@
+// bq_attn.cu -- planning of the paged attention and the join of its chunks
+// (bq_paged_attention in include/bqgemv.h; the kernel is bq_attn.cuh).
+#include <atomic>
+#include <cmath>
+
+#include "bq_attn.h"
+
+namespace {
+
+constexpr int JOIN_THREADS = 128;
+
+// Joins a request's chunks: one CTA per query row and head.  Chunk i's weight
+// is 2^(m_i - max m); the chunks are taken by thread groups of D / 4 lanes in a
+// fixed order.  A request of one chunk was written by the attention kernel.
+template <int DT>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constant__ bq::AttnArgs a, int tile_rows) {
+    extern __shared__ float w_s[];  // [max_chunks] weights, then [groups][D] partial sums
+    __shared__ float red[2][JOIN_THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int D = a.c.head_dim, R = a.x.rows;
+    const int head = blockIdx.x % a.x.heads;
+    const int token = blockIdx.x / a.x.heads;  // request * rows + row
+    const int b = token / R, row = token - b * R;
+    const int h = (int)a.group.div((uint32_t)head);
+    const int g = row * (int)a.group.d + head - h * (int)a.group.d;
+    const int rt = g / tile_rows, i = g - rt * tile_rows;
+    bq::pdl_wait();
+    const int len = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
+    const int chunks = bq::attn_chunks(len, a.chunk);
+    if (chunks == 1) return;
+    const long long unit0 = (((long long)b * a.max_chunks) * a.c.kv_heads + h) * a.row_tiles + rt;
+    const long long step = (long long)a.c.kv_heads * a.row_tiles;
+    float top = -INFINITY;
+    for (int k = tid; k < chunks; k += JOIN_THREADS)
+        top = fmaxf(top, a.part_ml[(unit0 + k * step) * tile_rows + i].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+    for (int w = 0; w < JOIN_THREADS / 32; ++w) top = fmaxf(top, red[0][w]);
+    float sum = 0.0f;
+    for (int k = tid; k < chunks; k += JOIN_THREADS) {
+        const float2 ml = a.part_ml[(unit0 + k * step) * tile_rows + i];
+        const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+        w_s[k] = f;
+        sum = fmaf(f, ml.y, sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int w = 0; w < JOIN_THREADS / 32; ++w) sum += red[1][w];
+
+    const int vecs = D / 4, groups = JOIN_THREADS / vecs;  // D <= 256: at least two groups
+    const int gr = tid / vecs, v = tid - gr * vecs;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (gr < groups) {
+        const float *src = a.part_o + (unit0 * tile_rows + i) * D + 4 * v;
+        const long long hop = step * tile_rows * D;
+#pragma unroll 4
+        for (int k = gr; k < chunks; k += groups) {
+            const float4 o = *reinterpret_cast<const float4 *>(src + k * hop);
+            const float f = w_s[k];
+            acc.x = fmaf(f, o.x, acc.x);
+            acc.y = fmaf(f, o.y, acc.y);
+            acc.z = fmaf(f, o.z, acc.z);
+            acc.w = fmaf(f, o.w, acc.w);
+        }
+    }
+    float *sums = w_s + (a.max_chunks + 3) / 4 * 4;
+    if (gr < groups) *reinterpret_cast<float4 *>(sums + gr * D + 4 * v) = acc;
+    __syncthreads();
+    const long long at = (long long)token * a.x.out_row_stride + (long long)head * a.x.out_head_stride;
+    const bool empty = len - R + row + 1 <= 0;
+    for (int d = tid; d < D; d += JOIN_THREADS) {
+        float o = 0.0f;
+        for (int k = 0; k < groups; ++k) o += sums[k * D + d];
+        o = empty ? 0.0f : o / sum;
+        if constexpr (DT == BQ_F32) ((float *)a.x.out)[at + d] = o;
+        else if constexpr (DT == BQ_F16) ((__half *)a.x.out)[at + d] = __float2half_rn(o);
+        else ((__nv_bfloat16 *)a.x.out)[at + d] = __float2bfloat16_rn(o);
+    }
+}
+
+struct Plan {
+    const bq::AttnInstance *inst;
+    bq::AttnArgs a;
+    size_t smem;
+    int64_t units;  // most units that the table can hold
+    int64_t o_bytes, ml_bytes;
+};
+
+// Positions per work unit, from the geometry alone (not the query rows, so that
+// every number of rows shares one order of sums): the table's capacity cut into
+// about TARGET units, 128 positions at least (two tiles per warp) and 1024 at most
+// (so that the longest table, 2^23 positions, has 8192 units, whose weights the
+// join keeps in shared memory).
+constexpr int64_t TARGET = 1824, CHUNK_MIN = 128, CHUNK_MAX = 1024;
+int chunk_of(int64_t requests, int64_t kv_heads, int64_t capacity) {
+    int64_t n = (requests * kv_heads * capacity + TARGET - 1) / TARGET;
+    n = (n + 63) / 64 * 64;
+    return (int)(n < CHUNK_MIN ? CHUNK_MIN : n > CHUNK_MAX ? CHUNK_MAX : n);
+}
+
+// validation of shapes and choice of the instance
+bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
+    if (!c || !x) return BQ_ERR_NULL;
+    const bq_status s = bq::check_cache_shape(c);
+    if (s != BQ_OK) return s;
+    if (!bq::dtype_bytes(x->dtype)) return BQ_ERR_QTYPE;
+    if (x->requests < 0 || x->requests > bq::ATTN_MAX_REQUESTS || x->rows < 1 || x->rows > BQ_VERIFY_MAX_ROWS ||
+        x->heads < 1 || x->heads > 4096 || x->heads % c->kv_heads || x->table_width < 1 ||
+        (int64_t)x->table_width * c->page_size > (1LL << 23) || x->table_stride < x->table_width ||
+        x->table_stride > (1LL << 40) || !std::isfinite(x->scale))
+        return BQ_ERR_SHAPE;
+    const int64_t strides[] = {x->q_row_stride, x->q_head_stride, x->out_row_stride, x->out_head_stride};
+    for (int64_t v : strides)
+        if (v < 0 || v > (1LL << 40)) return BQ_ERR_SHAPE;
+    bq::AttnArgs &a = p->a;
+    a.c = *c;
+    a.x = *x;
+    a.page.set((uint32_t)c->page_size);
+    a.group.set((uint32_t)(x->heads / c->kv_heads));
+    a.group_rows = x->heads / c->kv_heads * x->rows;
+    const int64_t capacity = (int64_t)x->table_width * c->page_size;
+    a.chunk = chunk_of(x->requests, c->kv_heads, capacity);
+    a.max_chunks = bq::attn_chunks((int)capacity, a.chunk);
+    a.scale_log2 = x->scale * 1.44269504088896340736f;
+    const int dim = c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256;
+    const int nt = a.group_rows <= 8 || dim == 256 ? 1 : 2;
+    a.row_tiles = (a.group_rows + 8 * nt - 1) / (8 * nt);
+    const int own = c->type == BQ_Q8_0 ? BQ_BF16 : c->type;  // the type that the tensor cores multiply
+    const int parts = x->dtype == own ? 1 : 2;
+    int n = 0;
+    const bq::AttnInstance *inst = c->type == BQ_F16    ? bq_internal_attn_f16(&n)
+                                   : c->type == BQ_BF16 ? bq_internal_attn_bf16(&n)
+                                                        : bq_internal_attn_q8_0(&n);
+    p->inst = nullptr;
+    for (int i = 0; i < n; ++i)
+        if (inst[i].parts == parts && inst[i].dim == dim && inst[i].nt == nt) p->inst = &inst[i];
+    if (!p->inst) return BQ_ERR_SHAPE;
+    p->smem = p->inst->smem + (size_t)(x->requests + 1) * sizeof(int);
+    p->units = (int64_t)x->requests * a.max_chunks * c->kv_heads * a.row_tiles;
+    if ((int64_t)x->requests * a.max_chunks > 0x7fffffffLL || p->units > (1LL << 40) ||
+        (int64_t)x->requests * x->rows * x->heads > 0x7fffffffLL)
+        return BQ_ERR_SHAPE;
+    const int64_t rows = a.max_chunks > 1 ? p->units * 8 * nt : 0;
+    p->ml_bytes = (rows * (int64_t)sizeof(float2) + 15) / 16 * 16;
+    p->o_bytes = rows * c->head_dim * (int64_t)sizeof(float);
+    return BQ_OK;
+}
+
+}  // namespace
+
+int bq_internal_status_attn(unsigned int *flags, int clear) {
+    unsigned int w[3] = {0, 0, 0};
+    int e = bq_internal_attn_status_f16(&w[0], clear);
+    if (!e) e = bq_internal_attn_status_bf16(&w[1], clear);
+    if (!e) e = bq_internal_attn_status_q8_0(&w[2], clear);
+    *flags = w[0] | w[1] | w[2];
+    return e;
+}
+
+extern "C" int64_t bq_paged_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args) {
+    Plan p;
+    if (plan_of(cache, args, &p) != BQ_OK) return -1;
+    return p.ml_bytes + p.o_bytes;
+}
+
+extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, void *workspace,
+                                        int64_t workspace_bytes, void *stream) {
+    Plan p;
+    bq_status s = plan_of(cache, x, &p);
+    if (s != BQ_OK) return s;
+    if (x->requests == 0) return BQ_OK;
+    s = bq::check_cache_pointers(cache);
+    if (s != BQ_OK) return s;
+    if (!x->q || !x->out || !x->table || !x->lens) return BQ_ERR_NULL;
+    const uintptr_t es = (uintptr_t)bq::dtype_bytes(x->dtype);
+    if (!bq::aligned_to(x->q, es) || !bq::aligned_to(x->out, es) || !bq::aligned_to(x->table, 4) ||
+        !bq::aligned_to(x->lens, 4))
+        return BQ_ERR_ALIGN;
+    bq::AttnArgs &a = p.a;
+    const int64_t need = p.ml_bytes + p.o_bytes;
+    if (need) {
+        if (!workspace) return BQ_ERR_NULL;
+        if (!bq::aligned_to(workspace, 16)) return BQ_ERR_ALIGN;
+        if (workspace_bytes < need) return BQ_ERR_SHAPE;
+    }
+    a.part_ml = static_cast<float2 *>(workspace);
+    a.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + p.ml_bytes);
+    const int sms = bq::device_sms();
+    if (!sms) return BQ_ERR_CUDA;
+    int occ = 0;
+    if (p.inst->occupancy(p.smem, &occ) != 0 || occ < 1) return BQ_ERR_CUDA;
+    const int64_t grid = p.units < (int64_t)sms * occ ? p.units : (int64_t)sms * occ;
+    cudaError_t e = p.inst->launch(a, (int)grid, p.smem, stream);
+    if (e != cudaSuccess || a.max_chunks == 1) return bq::from_cuda_error(e);
+    const int groups = JOIN_THREADS / (cache->head_dim / 4);
+    const size_t smem = ((size_t)(a.max_chunks + 3) / 4 * 4 + (size_t)groups * cache->head_dim) * sizeof(float);
+    const dim3 blocks((unsigned)(x->requests * x->rows * x->heads));
+    const int tile_rows = 8 * p.inst->nt;
+    e = x->dtype == BQ_F32
+            ? bq::launch_pdl(join_kernel<BQ_F32>, blocks, JOIN_THREADS, smem, stream, 1, a, tile_rows)
+        : x->dtype == BQ_F16
+            ? bq::launch_pdl(join_kernel<BQ_F16>, blocks, JOIN_THREADS, smem, stream, 1, a, tile_rows)
+            : bq::launch_pdl(join_kernel<BQ_BF16>, blocks, JOIN_THREADS, smem, stream, 1, a, tile_rows);
+    return bq::from_cuda_error(e);
+}

@@ -352,6 +352,190 @@ bq_status bq_stream_plan_destroy(bq_stream_plan *plan);
 #define BQ_NOALLOC_MAX_OPS 512
 bq_status bq_stream_run_noalloc(int qtype, const bq_op *ops, int n_ops, void *stream);
 
+/* ------------------------------------------------------------------------
+ * What stands between the weight products of a decode step: a paged
+ * key-value cache (its block tables, the append with rotary positions, and
+ * the attention of the new tokens over it) and the norms around a block.
+ * (RunIT README, data-flow diagram: RMSNorm -> Q/K/V projections ->
+ * attention -> FFN; its kernel table's attention and rope kernels.)
+ *
+ * Conventions beyond those at the top of this file:
+ *  - Activations may be fp32, fp16 or bf16 (bq_dtype).  The last dimension of
+ *    every tensor is contiguous; the other strides are given in elements and
+ *    are not negative.
+ *  - Every call waits for the work before it on the stream before it reads or
+ *    writes anything.
+ *  - The structs are read by the call and need not outlive it.
+ * ------------------------------------------------------------------------ */
+typedef enum { BQ_F32 = 0, BQ_F16 = 1, BQ_BF16 = 30 } bq_dtype; /* (Q8_0 = 8: bq_qtype) */
+
+/* bits of bq_device_status set by the calls below: the entry concerned is
+ * skipped (treated as masked, or not written), nothing is read or written
+ * out of range */
+#define BQ_DEVERR_PAGE 0x100u /* attention: a table entry of a live position outside the pool */
+#define BQ_DEVERR_LENGTH 0x200u /* attention: a length below 0 or beyond the table */
+#define BQ_DEVERR_SLOT 0x400u /* append: a slot beyond the pool */
+#define BQ_DEVERR_POOL 0x800u /* tables: the free stack would pass the pool */
+
+/* One layer's paged cache: `pages` pages of `page_size` positions each, of
+ * kv_heads heads of head_dim values.  Value d of head h in slot s of page p
+ * is element p * page_stride + h * head_stride + s * slot_stride + d of k (and
+ * of v), so pages may hold heads before slots or slots before heads, and k and
+ * v may be slices of one tensor.
+ *  - type BQ_F16 or BQ_BF16: 16-bit values; head_dim % 8 == 0, 8..256;
+ *    strides multiples of 8 elements; k and v 16-byte aligned.
+ *  - type BQ_Q8_0: k and v hold int8 codes, k_scale and v_scale the fp16
+ *    scale of each 32 codes of a head (the value is d * q: the block of the
+ *    weights' Q8_0 with codes and scales in planes of their own, so that
+ *    rows of codes stay aligned); head_dim % 32 == 0, 32..256; strides
+ *    multiples of head_dim; the scale of element e is element e / 32 of its
+ *    plane; all four pointers 16-byte aligned.
+ *  1 <= kv_heads <= 1024, 1 <= page_size <= 65536, 1 <= pages < 2^31. */
+typedef struct {
+    int32_t type, kv_heads, head_dim, page_size;
+    int64_t pages, page_stride, head_stride, slot_stride;
+    void *k, *v, *k_scale, *v_scale;
+} bq_kv_cache;
+
+/* Block tables, slot map and free pages of a step, from the requests' lengths.
+ *   pages(n) = ceil(n / page_size).
+ *   Request b goes from lens[b] to new_lens[b] positions.
+ *   Shrinking releases its pages behind pages(new): they are pushed on the
+ *   stack of free pages in (request, position) order.  Growing asks for
+ *   pages(new) - pages(old) pages: they are popped, after all pushes, in
+ *   (request, position) order, and written to its row of the table.
+ *   Token rows: request b has new - lens rows (none if it does not grow),
+ *   the requests' rows back to back: starts[b] .. starts[b + 1] - 1.
+ *   positions[t] = the token's position in its request, slots[t] =
+ *   page * page_size + position % page_size.
+ * A request is refused (keeps its length, its rows' slots are -1, its rows'
+ * positions 0) if it asks for pages and the pages asked up to and including it
+ * exceed the free ones, if it has rows and they end behind max_tokens, or if
+ * a length of it is below 0 or beyond the table (it then has no rows).
+ * Slots behind the last row are -1, positions there 0.  Table entries and
+ * stack entries that are no longer in use are left as they were, and so are
+ * the table's rows of requests that do not grow.
+ *  - lens_out may be lens, free_count_out may be free_count; apart from that
+ *    nothing overlaps.  refused receives the number of refused requests.
+ *  - 0 <= requests <= 4096, 1 <= page_size <= 65536, table_width >= 1,
+ *    table_stride >= table_width, 0 <= max_tokens < 2^31 - 1, 1 <= pool < 2^31 - 1.
+ *  - free_count outside 0 .. pool sets BQ_DEVERR_POOL and counts as the
+ *    nearest; so does a push beyond `pool` entries, which is dropped. */
+typedef struct {
+    int32_t requests, page_size, table_width, pool; /* pool: entries of free_pages */
+    int64_t table_stride, max_tokens;
+    const int32_t *lens, *new_lens;
+    int32_t *table;      /* [requests, table_width] */
+    int32_t *free_pages; /* [pool], the first *free_count of them free */
+    const int32_t *free_count;
+    int64_t *slots;     /* [max_tokens] */
+    int32_t *positions; /* [max_tokens] */
+    int32_t *starts;    /* [requests + 1] */
+    int32_t *lens_out;  /* [requests] */
+    int32_t *free_count_out, *refused;
+} bq_kv_tables;
+bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream);
+
+/* Append keys and values of `tokens` tokens to the cache, with rotary
+ * positions if freq is given: pair p < rot/2 of a head turns by the angle
+ * positions[axis(p)][t] * freq[p] radians, axis 0 for the first sections[0]
+ * pairs, 1 for the next sections[1], 2 for the rest (time, height and width
+ * of images and video; one axis for text).  A pair is (p, p + rot/2), or
+ * (2p, 2p + 1) with interleaved != 0; values from rot on pass unchanged.
+ * Keys are rotated, and queries if q is given (into q_out, which may be q);
+ * values are not.
+ * The angle is reduced to a turn at 48 bits, so far positions keep their
+ * accuracy; sine, cosine and the turn are fp32.  The cache receives the value
+ * rounded to nearest even (BQ_F16, BQ_BF16), or the Q8_0 block of
+ * bq_quantize_pack: d = fp16_rne(max|x| / 127), q = clamp(round(x / d)).
+ *  - slots[t] < 0: the token is not stored (its q is still rotated).  A slot
+ *    beyond the pool is not stored and sets BQ_DEVERR_SLOT.  The slots of one
+ *    call that are >= 0 must differ from one another.
+ *  - dtype: of k, v, q and q_out.  Their strides (token, head) are in
+ *    elements.  q NULL: keys and values alone (q_out ignored).
+ *  - freq: fp64 [rot / 2] or NULL (no rotation; rot, axes, sections ignored).
+ *    rot % 8 == 0, 8 <= rot <= head_dim; 1 <= axes <= 3; the sections (not
+ *    negative) sum to rot / 2; positions: int32 [axes, tokens], rows
+ *    position_stride apart.
+ *  - 0 <= tokens < 2^31, 1 <= heads <= 4096; heads ignored without q.
+ *  - k, v, q and q_out aligned to their elements. */
+typedef struct {
+    int32_t dtype, heads, rot, axes, interleaved;
+    int32_t sections[3];
+    int64_t tokens;
+    const void *k, *v, *q;
+    void *q_out;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    const int64_t *slots;
+    const int32_t *positions;
+    int64_t position_stride;
+    const double *freq;
+} bq_kv_append_args;
+bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, void *stream);
+
+/* Attention of the last `rows` tokens of each request over its cache:
+ *   out[b, r, h] = sum_t softmax_t(scale * q[b, r, h] . k[t, h / group]) v[t, h / group]
+ * over positions t < lens[b] - rows + r + 1 (lens counts the new tokens, which
+ * have been appended), group = heads / kv_heads.  A row that sees no position
+ * gives zeros.  What lies behind a row's positions (stale slots, later draft
+ * tokens, NaN) does not reach it; a NaN or infinity within them makes the
+ * head's row NaN.  A position whose table entry is outside the pool is
+ * treated as masked and sets BQ_DEVERR_PAGE; a length below 0 or beyond
+ * table_width * page_size counts as the nearest and sets BQ_DEVERR_LENGTH.
+ * Statistics and sums are fp32; with fp32 q the products are exact to fp32
+ * rounding (queries and probabilities are carried as several 16-bit parts),
+ * otherwise probabilities are.  For one geometry (requests, table_width,
+ * page_size, kv_heads, head_dim, types) each row's bits depend on its own
+ * inputs alone: row r of a call with several rows is bit-identical to the
+ * one-row call at the length that the row sees.
+ *  - q, out: [requests * rows, heads, head_dim] of dtype, row and head strides
+ *    in elements.  heads is a multiple of kv_heads, heads <= 4096; 1 <= rows
+ *    <= BQ_VERIFY_MAX_ROWS; 0 <= requests <= 4096; scale finite.
+ *  - table: int32 [requests, table_width], rows table_stride apart,
+ *    table_width * page_size <= 2^23.
+ *  - workspace: bq_paged_attention_workspace_bytes bytes, 16-byte aligned;
+ *    need not be initialised; not shared by calls that may overlap on the GPU
+ *    (two streams, two captured graphs). */
+typedef struct {
+    int32_t dtype, requests, rows, heads, table_width;
+    float scale;
+    int64_t table_stride, q_row_stride, q_head_stride, out_row_stride, out_head_stride;
+    const void *q;
+    void *out;
+    const int32_t *table, *lens;
+} bq_attention_args;
+/* -1 for arguments that bq_paged_attention refuses by shape (pointers are not read) */
+int64_t bq_paged_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args);
+bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *args, void *workspace,
+                             int64_t workspace_bytes, void *stream);
+
+/* The norms after one block and before the next, with the block's gate and
+ * the residual scales, per row of `width` values:
+ *   b = y                                                  (post NULL), or
+ *   b = y / sqrt(mean(y^2) + eps) * post
+ *   h' = alpha * h + beta * gate * b                       (gate NULL: 1)
+ *   x' = h' / sqrt(mean(h'^2) + eps) * pre                 (x NULL: not computed)
+ * h' is rounded to its type when it is stored; the norm of x' uses the
+ * unrounded one.  All in fp32 in an order that depends on width alone.
+ *  - dtype: of y, gate and x; h_dtype: of h and h_out; fp32 for h with any
+ *    dtype, otherwise the same as dtype.  post, pre: fp32 [width].
+ *  - gate: row stride 0 for one gate per channel.  Strides in elements.
+ *  - h_out may be h, x may be y; otherwise outputs overlap nothing.
+ *  - 0 <= rows < 2^31, 1 <= width <= 16384; pointers aligned to their
+ *    elements (16-byte aligned rows take the wide loads); eps finite, >= 0;
+ *    alpha and beta finite. */
+typedef struct {
+    int32_t dtype, h_dtype;
+    int64_t rows, width;
+    const void *y, *h, *gate;
+    const float *post, *pre;
+    void *h_out, *x;
+    int64_t y_stride, h_stride, gate_stride, h_out_stride, x_stride;
+    float alpha, beta, eps;
+} bq_sandwich_args;
+bq_status bq_sandwich_norm(const bq_sandwich_args *args, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
