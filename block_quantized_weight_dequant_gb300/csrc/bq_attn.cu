@@ -7,6 +7,25 @@
 
 namespace {
 
+BQ_STATUS_WORD(attn)
+
+// the status word's device address, looked up once per device
+cudaError_t status_address(unsigned int **out) {
+    static std::atomic<unsigned int *> addr[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    unsigned int *p = addr[dev].load();
+    if (!p) {
+        e = cudaGetSymbolAddress(reinterpret_cast<void **>(&p), g_status_attn);
+        if (e != cudaSuccess) return e;
+        addr[dev].store(p);
+    }
+    *out = p;
+    return cudaSuccess;
+}
+
 constexpr int JOIN_THREADS = 128;
 
 // Joins a request's chunks: one CTA per query row and head.  Chunk i's weight
@@ -93,10 +112,10 @@ struct Plan {
 
 // Positions per work unit, from the geometry alone (not the query rows, so that
 // every number of rows shares one order of sums): the table's capacity cut into
-// about TARGET units, 128 positions at least (two tiles per warp) and 1024 at most
-// (so that the longest table, 2^23 positions, has 8192 units, whose weights the
+// about TARGET units, 128 positions at least (two tiles per warp) and 2048 at most
+// (so that the longest table, 2^23 positions, has 4096 units, whose weights the
 // join keeps in shared memory).
-constexpr int64_t TARGET = 1824, CHUNK_MIN = 128, CHUNK_MAX = 1024;
+constexpr int64_t TARGET = 304, CHUNK_MIN = 128, CHUNK_MAX = 2048;
 int chunk_of(int64_t requests, int64_t kv_heads, int64_t capacity) {
     int64_t n = (requests * kv_heads * capacity + TARGET - 1) / TARGET;
     n = (n + 63) / 64 * 64;
@@ -128,14 +147,17 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     a.max_chunks = bq::attn_chunks((int)capacity, a.chunk);
     a.scale_log2 = x->scale * 1.44269504088896340736f;
     const int dim = c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256;
-    const int nt = a.group_rows <= 8 || dim == 256 ? 1 : 2;
+    // 8 query rows per n-tile, as few row tiles as the registers allow: each
+    // reads the cache again
+    const int nt = a.group_rows <= 8 ? 1 : a.group_rows <= 16 || dim == 256 ? 2 : 4;
     a.row_tiles = (a.group_rows + 8 * nt - 1) / (8 * nt);
     const int own = c->type == BQ_Q8_0 ? BQ_BF16 : c->type;  // the type that the tensor cores multiply
     const int parts = x->dtype == own ? 1 : 2;
     int n = 0;
-    const bq::AttnInstance *inst = c->type == BQ_F16    ? bq_internal_attn_f16(&n)
-                                   : c->type == BQ_BF16 ? bq_internal_attn_bf16(&n)
-                                                        : bq_internal_attn_q8_0(&n);
+    const bq::AttnInstance *inst =
+        c->type == BQ_F16    ? (parts == 1 ? bq_internal_attn_f16_own(&n) : bq_internal_attn_f16_split(&n))
+        : c->type == BQ_BF16 ? (parts == 1 ? bq_internal_attn_bf16_own(&n) : bq_internal_attn_bf16_split(&n))
+                             : (parts == 1 ? bq_internal_attn_q8_0_own(&n) : bq_internal_attn_q8_0_split(&n));
     p->inst = nullptr;
     for (int i = 0; i < n; ++i)
         if (inst[i].parts == parts && inst[i].dim == dim && inst[i].nt == nt) p->inst = &inst[i];
@@ -153,14 +175,7 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
 
 }  // namespace
 
-int bq_internal_status_attn(unsigned int *flags, int clear) {
-    unsigned int w[3] = {0, 0, 0};
-    int e = bq_internal_attn_status_f16(&w[0], clear);
-    if (!e) e = bq_internal_attn_status_bf16(&w[1], clear);
-    if (!e) e = bq_internal_attn_status_q8_0(&w[2], clear);
-    *flags = w[0] | w[1] | w[2];
-    return e;
-}
+int bq_internal_status_attn(unsigned int *flags, int clear) { return read_status_attn(flags, clear); }
 
 extern "C" int64_t bq_paged_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args) {
     Plan p;
@@ -195,7 +210,9 @@ extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_atten
     int occ = 0;
     if (p.inst->occupancy(p.smem, &occ) != 0 || occ < 1) return BQ_ERR_CUDA;
     const int64_t grid = p.units < (int64_t)sms * occ ? p.units : (int64_t)sms * occ;
-    cudaError_t e = p.inst->launch(a, (int)grid, p.smem, stream);
+    unsigned int *status = nullptr;
+    cudaError_t e = status_address(&status);
+    if (e == cudaSuccess) e = p.inst->launch(a, (int)grid, p.smem, stream, status);
     if (e != cudaSuccess || a.max_chunks == 1) return bq::from_cuda_error(e);
     const int groups = JOIN_THREADS / (cache->head_dim / 4);
     const size_t smem = ((size_t)(a.max_chunks + 3) / 4 * 4 + (size_t)groups * cache->head_dim) * sizeof(float);

@@ -11,26 +11,23 @@
 // the length alone, and an empty chunk joins with weight zero, so a row's bits
 // depend on its own inputs and the geometry only.
 //
-// Bound by HBM: every live byte of the cache is read once (twice or more for
-// the row tiles of more than 8 NT query rows per kv head, through L2), about
-// 4 flop per byte and query row.  So the kernel is built around the loads:
-//  - A warp loads 16-byte pieces of K and V rows from global memory straight
-//    into the registers from which mma.sync reads them; no shared memory, no
-//    barrier and no transposing copy stand between.  mma.sync sums over its
-//    k index, so any order of the summed index will do as long as both
-//    operands share it, and any order of the output rows:
-//      S^T = K Q^T: rows are positions, summed over d.  Lane (r, c) = (lane /
-//        4, lane % 4) takes d = 8 (c + 4 j) .. + 7 of positions r and r + 8:
-//        one 16-byte load feeds two instructions.
-//      O^T = V^T P^T: rows are d, summed over positions.  Lane (r, c) takes
-//        d = 8 (r + 8 m) .. + 7 of positions 2c, 2c + 1, 2c + 8, 2c + 9; a
-//        byte permute pairs two positions' values into an A register.
-//    The scores come out with positions along r, the weights go in with
-//    positions along c: movmatrix transposes the 8 x 8 tile in registers.
-//  - The K registers of the next tile are loaded while the weights of this one
-//    are computed, the V registers while its scores are.
+// Bound by HBM: every live byte of the cache is read once (again per 8 NT query
+// rows of a kv head, through L2), about 4 flop per byte and query row.  So the
+// kernel is built around the loads:
+//  - Every warp has a ring of STAGES tiles of K and V rows in shared memory
+//    that it fills itself by 16-byte asynchronous copies (any page size and
+//    stride; what is not there is filled with zeros), two tiles ahead of the
+//    one it works on: 16 KB in flight per warp, 128 KB per SM, with no barrier
+//    between warps.  Rows are swizzled by 16-byte pieces, so that every read of
+//    a matrix operand is free of bank conflicts.
+//  - S^T = K Q^T has positions as rows and is summed over d; O^T = V^T P^T has d
+//    as rows and is summed over positions, V read with ldmatrix's transpose.
+//    So K and V are the 16-row operand and the query rows of a kv head (all
+//    heads of its group, all new tokens) the 8-column one: 8 rows per n-tile.
+//    The scores come out with positions along the lanes' r, the weights go in
+//    with positions along c: movmatrix transposes the 8 x 8 tile in registers.
 //  - tcgen05 would hold 128 rows of accumulator for 1 to 48 query rows; with 8
-//    query rows per n-tile the tensor pipe is about a fifth busy at HBM speed.
+//    query rows per n-tile mma.sync's pipe is about a fifth busy at HBM speed.
 // Precision.  The tensor cores multiply 16-bit values exactly.  A query of
 // the cache's own type is used as it is; any other is split into QP 16-bit
 // parts (fp16: 2 parts, 22 bits, after scaling the row by a power of two; bf16:
@@ -55,37 +52,54 @@ struct Words {
     uint32_t w[N];
 };
 
-__device__ __forceinline__ uint4 ldg16(const void *p) {
+// asynchronous copy of 16 (4, 8) bytes to shared memory, zeros where !ok
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(ok ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t smem_address(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint4 ldmatrix4(uint32_t at) {
     uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+                 : "r"(at)
+                 : "memory");
     return v;
 }
-__device__ __forceinline__ uint2 ldg8(const void *p) {
-    uint2 v;
-    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-    return v;
-}
-__device__ __forceinline__ uint32_t ldg4(const void *p) {
-    uint32_t v;
-    asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(v) : "l"(p));
+__device__ __forceinline__ uint4 ldmatrix4_trans(uint32_t at) {
+    uint4 v;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 
 template <bool HALF>
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
     if constexpr (HALF)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
             "{%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
             "{%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -138,17 +152,23 @@ template <int KV, int QP, int PP, int DP, int NT>
 struct AttnShape {
     static constexpr bool Q8 = KV == KV_Q8, HALF = KV == KV_F16;
     static constexpr int ROWS = 8 * NT;
-    // positions per tile and warp, in steps of 16: enough loads in flight for
-    // the registers at hand
-    static constexpr int TT = Q8 ? (DP <= 128 ? 2 : 1) : (DP <= 64 ? 2 : 1);
-    static constexpr int QROW = 2 * DP + 64;  // bytes: rows 64 apart modulo 128, so 8 lanes' 16-byte
-                                              // reads of 2 rows and 4 pieces hit 8 bank groups
+    // positions per tile: 8 KB of K and V per stage (16 KB with heads of 256)
+    static constexpr int TT = NT > 2 ? 1 : Q8 ? (DP <= 128 ? 2 : 1) : (DP <= 64 ? 2 : 1);
+    static constexpr int TILE = 16 * TT;
+    static constexpr int ROWB = Q8 ? DP : 2 * DP;  // bytes of a row in the ring
+    static constexpr int SCALEB = Q8 ? (DP / 32 + 1) / 2 * 4 + (DP <= 32 ? 4 : 0) : 0;  // words of a row's scales
+    static constexpr int STAGE = 2 * TILE * (ROWB + SCALEB) + 4 * TILE;
+    static constexpr int FIT = (24 * 1024 + 1024) / STAGE;
+    static constexpr int STAGES = FIT < 3 ? 3 : FIT > 6 ? 6 : FIT;
+    // query rows: 16 bytes apart modulo 128 for ldmatrix; 64 for the Q8_0 order,
+    // where 8 lanes read 16-byte pieces of 2 rows
+    static constexpr int QROW = 2 * DP + (Q8 ? 64 : 16);
+    static constexpr int OROW = DP + 4;  // floats: 8 lanes r and 4 row pairs c in 32 banks
     static constexpr int Q_BYTES = QP * ROWS * QROW;
-    static constexpr int O_BYTES = ATTN_WARPS * ROWS * DP * 4;
-    // q parts, the join of the warps, row statistics
-    static constexpr int SMEM = Q_BYTES + O_BYTES + (2 * ATTN_WARPS + 1) * ROWS * 4;
-    // resident CTAs that the registers are sized for
-    static constexpr int OCC = DP * NT <= 64 ? 4 : DP * NT <= 128 ? 3 : 2;
+    static constexpr int RING = STAGES * STAGE;  // per warp; holds its O for the join afterwards
+    static_assert(RING >= ROWS * OROW * 4 && RING % 16 == 0 && STAGE % 16 == 0);
+    static constexpr int SMEM = ATTN_WARPS * RING + Q_BYTES + (2 * ATTN_WARPS + 1) * ROWS * 4;
+    static constexpr int OCC = SMEM <= 112 * 1024 ? 2 : 1;
 };
 
 template <int KV, int QP, int PP, int DP, int NT>
@@ -156,22 +176,18 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
     attn_kernel(const __grid_constant__ AttnArgs a, unsigned int *status) {
     using S = AttnShape<KV, QP, PP, DP, NT>;
     constexpr bool Q8 = S::Q8, HALF = S::HALF;
-    constexpr int TT = S::TT, ROWS = S::ROWS, TILE = 16 * TT;
-    constexpr int KJ = DP / 32;             // groups of 32 d per row in S^T
-    constexpr int KW = Q8 ? 2 : 4;          // words of a K piece (8 values)
-    constexpr int VM = Q8 ? DP / 32 : DP / 64;  // pieces per position in O^T
-    constexpr int VW = Q8 ? 1 : 4;          // words of a V piece
-    constexpr int OJ = Q8 ? 2 : 4;          // 16-row output tiles per piece
+    constexpr int TT = S::TT, ROWS = S::ROWS, TILE = S::TILE, STAGES = S::STAGES, ROWB = S::ROWB;
+    constexpr int MT = DP / 16;  // 16-row tiles of O^T
     constexpr float SHIFT = HALF ? (float)ATTN_SHIFT_F16 : 0.0f;
-    extern __shared__ __align__(16) uint8_t smem[];
-    uint8_t *q_s = smem;
-    float *o_s = reinterpret_cast<float *>(smem + S::Q_BYTES);
-    float *m_s = o_s + ATTN_WARPS * ROWS * DP, *l_s = m_s + ATTN_WARPS * ROWS;
-    float *f_s = l_s + ATTN_WARPS * ROWS;          // per row: factor of its scores
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint8_t *q_s = smem + ATTN_WARPS * S::RING;
+    float *m_s = reinterpret_cast<float *>(q_s + S::Q_BYTES), *l_s = m_s + ATTN_WARPS * ROWS;
+    float *f_s = l_s + ATTN_WARPS * ROWS;            // per row: factor of its scores
     int *pre = reinterpret_cast<int *>(f_s + ROWS);  // [requests + 1]
     __shared__ int scan_s[ATTN_WARPS];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
+    uint8_t *ring = smem + warp * S::RING;
     const int B = a.x.requests, R = a.x.rows, D = a.c.head_dim, KVH = a.c.kv_heads;
     const int most = a.x.table_width * a.c.page_size;
     pdl_wait();
@@ -220,6 +236,84 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
         const int ck = cu - pre[b], len = length(b);
         const int begin = ck * a.chunk, end = min(len, begin + a.chunk);
         const int first_row = rt * ROWS;
+
+        // ---- the ring: tile `t0` of this warp into stage `st` ----
+        const int *row_table = a.x.table + b * a.x.table_stride;
+        const long long head_off = (long long)h * a.c.head_stride;
+        const int mine = lane & (TILE - 1);  // the position of a tile that this lane looks up
+        auto entry_of = [&](int t) { return t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
+        auto fill = [&](int t0, int entry, int st) {
+            const int t = t0 + mine;
+            long long off = -1;  // element offset, -1 where there is nothing to read
+            if (t < end) {
+                if (entry >= 0 && entry < a.c.pages) {
+                    const uint32_t in_page = (uint32_t)t - a.page.div((uint32_t)t) * a.page.d;
+                    off = entry * a.c.page_stride + in_page * a.c.slot_stride + head_off;
+                } else {
+                    atomicOr(status, BQ_DEVERR_PAGE);
+                }
+            }
+            const uint32_t base = smem_address(ring) + st * S::STAGE;
+            int *meta = reinterpret_cast<int *>(ring + st * S::STAGE + 2 * TILE * (ROWB + S::SCALEB));
+            // -1: nothing there; else the first scale's place in its word
+            if (lane < TILE) meta[lane] = off < 0 ? -1 : (int)((off >> 5) & 1);
+            constexpr int PIECES = ROWB / 16;       // of a row
+            constexpr int ROWS_AT_ONCE = 32 / PIECES > 0 ? 32 / PIECES : 1;
+            static_assert(PIECES <= 32);
+            const int piece = lane % PIECES;
+            const bool inside = piece * (Q8 ? 16 : 8) < D;
+#pragma unroll
+            for (int i = 0; i < TILE / ROWS_AT_ONCE; ++i) {
+                const int row = i * ROWS_AT_ONCE + lane / PIECES;
+                const long long o = __shfl_sync(~0u, off, row);
+                const bool ok = o >= 0 && inside;
+                const long long at = ok ? (Q8 ? o : 2 * o) + 16 * piece : 0;
+                const int kk = Q8 ? ((row & 3) << 1 | (row >> 2 & 1)) : row & 7;
+                copy16(base + row * ROWB + ((piece ^ (kk & (PIECES - 1))) << 4), (const uint8_t *)a.c.k + at, ok);
+                copy16(base + (TILE + row) * ROWB + ((piece ^ (row & 7 & (PIECES - 1))) << 4),
+                       (const uint8_t *)a.c.v + at, ok);
+            }
+            if constexpr (Q8) {
+                const int nb = D >> 5;  // scales of a row; an odd number of them may start mid-word
+                const uint32_t sk = base + 2 * TILE * ROWB + mine * S::SCALEB, sv = sk + TILE * S::SCALEB;
+                const long long so = off < 0 ? 0 : off >> 5;
+                const uint8_t *ks = (const uint8_t *)a.c.k_scale + (so & ~1ll) * 2;
+                const uint8_t *vs = (const uint8_t *)a.c.v_scale + (so & ~1ll) * 2;
+                if (lane < TILE) {
+                    if (nb % 4 == 0) {
+#pragma unroll
+                        for (int i = 0; i < (DP + 127) / 128; ++i)
+                            if (4 * i < nb) {
+                                copy8(sk + 8 * i, ks + 8 * i, off >= 0);
+                                copy8(sv + 8 * i, vs + 8 * i, off >= 0);
+                            }
+                    } else {
+                        const int bytes = 2 * nb + 2 * (int)(so & 1);
+#pragma unroll
+                        for (int i = 0; i < S::SCALEB / 4; ++i) {
+                            const int n = off < 0 ? 0 : min(4, max(0, bytes - 4 * i));
+                            copy4(sk + 4 * i, n ? ks + 4 * i : ks, n);
+                            copy4(sv + 4 * i, n ? vs + 4 * i : vs, n);
+                        }
+                    }
+                }
+            }
+        };
+
+        const int stride = ATTN_WARPS * TILE;
+        int tile = begin + warp * TILE;
+        int ahead = tile;  // the next tile to fetch
+        int entry = entry_of(ahead + mine);
+#pragma unroll
+        for (int st = 0; st < STAGES - 1; ++st) {
+            if (ahead < end) {
+                const int now = entry;
+                entry = entry_of(ahead + stride + mine);
+                fill(ahead, now, st);
+            }
+            copies_commit();
+            ahead += stride;
+        }
 
         // ---- queries: fp32 -> 16-bit parts in shared memory ----
         for (int i = warp; i < ROWS; i += ATTN_WARPS) {
@@ -281,175 +375,147 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                 fac[nt][x] = f_s[i];
             }
 
-        float O[VM][OJ][NT][4], m[NT][2], l[NT][2];
+        float O[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.0f;
 #pragma unroll
-            for (int v = 0; v < VM; ++v)
+            for (int v = 0; v < MT; ++v)
 #pragma unroll
-                for (int j = 0; j < OJ; ++j)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) O[v][j][nt][x] = 0.0f;
+                for (int x = 0; x < 4; ++x) O[v][nt][x] = 0.0f;
         }
 
-        const int *row_table = a.x.table + b * a.x.table_stride;
-        const long long head_off = (long long)h * a.c.head_stride;
-        // element offset of this lane's position of a tile, -1 where there is none
-        auto entry_of = [&](int t) { return t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
-        auto offset_of = [&](int t, int page) -> long long {
-            if (t >= end) return -1;
-            if (page < 0 || page >= a.c.pages) {
-                atomicOr(status, BQ_DEVERR_PAGE);
-                return -1;
+        for (int st = 0; tile < end; tile += stride, st = st + 1 == STAGES ? 0 : st + 1) {
+            copies_wait<STAGES - 2>();  // this tile's copies have landed,
+            __syncwarp();               // every lane's, and every lane is done with the tile before
+            {
+                const int into = st == 0 ? STAGES - 1 : st - 1;
+                if (ahead < end) {
+                    const int now = entry;
+                    entry = entry_of(ahead + stride + mine);
+                    fill(ahead, now, into);
+                }
+                copies_commit();
+                ahead += stride;
             }
-            const uint32_t in_page = (uint32_t)t - a.page.div((uint32_t)t) * a.page.d;
-            return page * a.c.page_stride + in_page * a.c.slot_stride + head_off;
-        };
-        uint32_t kreg[TT][2][KJ][KW];
-        [[maybe_unused]] __half kscale[TT][2][KJ];
-        auto load_k = [&](long long off) {
+            const uint8_t *k_s = ring + st * S::STAGE, *v_s = k_s + TILE * ROWB;
+            const uint8_t *ks_s = v_s + TILE * ROWB, *vs_s = ks_s + TILE * S::SCALEB;
+            const int *meta = reinterpret_cast<const int *>(vs_s + TILE * S::SCALEB);
+            int there[TT][2];
 #pragma unroll
             for (int s = 0; s < TT; ++s)
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    const long long o = __shfl_sync(~0u, off, 16 * s + 8 * x + r);
-#pragma unroll
-                    for (int j = 0; j < KJ; ++j) {
-                        const bool ok = o >= 0 && 8 * (c + 4 * j) < D;
-                        if constexpr (Q8) {
-                            const uint2 v = ok ? ldg8((const uint8_t *)a.c.k + o + 8 * (c + 4 * j)) : make_uint2(0, 0);
-                            kreg[s][x][j][0] = v.x, kreg[s][x][j][1] = v.y;
-                            kscale[s][x][j] = ok ? ((const __half *)a.c.k_scale)[(o >> 5) + j] : __half(0.0f);
-                        } else {
-                            const uint4 v = ok ? ldg16((const uint8_t *)a.c.k + 2 * o + 16 * (c + 4 * j))
-                                               : make_uint4(0, 0, 0, 0);
-                            kreg[s][x][j][0] = v.x, kreg[s][x][j][1] = v.y;
-                            kreg[s][x][j][KW - 2] = v.z, kreg[s][x][j][KW - 1] = v.w;
-                        }
-                    }
-                }
-        };
-
-        int tile = begin + warp * TILE;
-        const int stride = ATTN_WARPS * TILE;
-        const int mine = lane & (TILE - 1);
-        int entry = entry_of(tile + mine);
-        long long off = offset_of(tile + mine, entry);
-        if (tile < end) load_k(off);
-        entry = entry_of(tile + stride + mine);
-
-        for (; tile < end; tile += stride) {
-            // ---- V of this tile on its way while the scores are computed ----
-            uint32_t vreg[TT][4][VM][VW];
-            [[maybe_unused]] __half vscale[TT][2][VM];
-#pragma unroll
-            for (int s = 0; s < TT; ++s) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const long long o = __shfl_sync(~0u, off, 16 * s + 2 * c + (x & 1) + 8 * (x >> 1));
-#pragma unroll
-                    for (int v = 0; v < VM; ++v) {
-                        if constexpr (Q8) {
-                            const bool ok = o >= 0 && 32 * v < D;
-                            vreg[s][x][v][0] = ok ? ldg4((const uint8_t *)a.c.v + o + 32 * v + 4 * r) : 0;
-                        } else {
-                            const bool ok = o >= 0 && 8 * (r + 8 * v) < D;
-                            const uint4 w = ok ? ldg16((const uint8_t *)a.c.v + 2 * o + 16 * (r + 8 * v))
-                                               : make_uint4(0, 0, 0, 0);
-                            vreg[s][x][v][0] = w.x, vreg[s][x][v][VW > 1 ? 1 : 0] = w.y;
-                            vreg[s][x][v][VW > 2 ? 2 : 0] = w.z, vreg[s][x][v][VW > 3 ? 3 : 0] = w.w;
-                        }
-                    }
-                }
-                if constexpr (Q8) {
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const long long o = __shfl_sync(~0u, off, 16 * s + 8 * x + r);
-#pragma unroll
-                        for (int v = 0; v < VM; ++v)
-                            vscale[s][x][v] =
-                                o >= 0 && 32 * v < D ? ((const __half *)a.c.v_scale)[(o >> 5) + v] : __half(0.0f);
-                    }
-                }
-            }
-            // masked as bad pages are: positions whose offset is -1
-            bool live[TT][2];
-#pragma unroll
-            for (int s = 0; s < TT; ++s)
-#pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    live[s][x] = __shfl_sync(~0u, (int)(off >= 0), 16 * s + 8 * x + r) != 0;
+                for (int y = 0; y < 2; ++y) there[s][y] = meta[16 * s + 8 * y + r];
+            // the scale of 32 values of a position of this thread
+            [[maybe_unused]] auto scale_of = [&](const uint8_t *base, int s, int y, int j) {
+                const int odd = (D >> 5) % 2 ? max(there[s][y], 0) : 0;
+                return __half2float(
+                    *reinterpret_cast<const __half *>(base + (16 * s + 8 * y + r) * S::SCALEB + 2 * (j + odd)));
+            };
 
             // ---- scores ----
             float sc[TT][NT][4];
-#pragma unroll
-            for (int s = 0; s < TT; ++s)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) sc[s][nt][x] = 0.0f;
             if constexpr (Q8) {
 #pragma unroll
-                for (int j = 0; j < KJ; ++j) {
-                    uint2 k0[TT][2], k1[TT][2];  // [pieces' first and second 4 codes]
+                for (int s = 0; s < TT; ++s)
 #pragma unroll
-                    for (int s = 0; s < TT; ++s)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            k0[s][x] = codes_to_bf16(kreg[s][x][j][0]);
-                            k1[s][x] = codes_to_bf16(kreg[s][x][j][1]);
+                        for (int x = 0; x < 4; ++x) sc[s][nt][x] = 0.0f;
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    uint4 lo[TT], hi[TT];  // the operand over the pieces' first and second 4 codes
+                    float d[TT][2];
+#pragma unroll
+                    for (int s = 0; s < TT; ++s) {
+                        uint2 f[2], g[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int row = 16 * s + 8 * y + r;
+                            const int key = ((r & 3) << 1 | (r >> 2 & 1)) & (ROWB / 16 - 1);
+                            const uint2 w = *reinterpret_cast<const uint2 *>(
+                                k_s + row * ROWB + (((2 * j + (c >> 1)) ^ key) << 4) + 8 * (c & 1));
+                            f[y] = codes_to_bf16(w.x);
+                            g[y] = codes_to_bf16(w.y);
+                            d[s][y] = 32 * j < D ? scale_of(ks_s, s, y, j) : 0.0f;
                         }
+                        lo[s] = make_uint4(f[0].x, f[1].x, f[0].y, f[1].y);
+                        hi[s] = make_uint4(g[0].x, g[1].x, g[0].y, g[1].y);
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float t[TT][4];
-#pragma unroll
-                        for (int s = 0; s < TT; ++s) t[s][0] = t[s][1] = t[s][2] = t[s][3] = 0.0f;
+                        float t[TT][QP][4];
 #pragma unroll
                         for (int p = QP - 1; p >= 0; --p) {
                             const uint4 q = *reinterpret_cast<const uint4 *>(
                                 q_s + (p * ROWS + 8 * nt + r) * S::QROW + 16 * (c + 4 * j));
 #pragma unroll
                             for (int s = 0; s < TT; ++s) {
-                                mma16816<HALF>(t[s], k0[s][0].x, k0[s][1].x, k0[s][0].y, k0[s][1].y, q.x, q.y);
-                                mma16816<HALF>(t[s], k1[s][0].x, k1[s][1].x, k1[s][0].y, k1[s][1].y, q.z, q.w);
+                                t[s][p][0] = t[s][p][1] = t[s][p][2] = t[s][p][3] = 0.0f;
+                                mma16816<HALF>(t[s][p], lo[s], q.x, q.y);
+                                mma16816<HALF>(t[s][p], hi[s], q.z, q.w);
                             }
                         }
 #pragma unroll
-                        for (int s = 0; s < TT; ++s) {
-                            const float d0 = __half2float(kscale[s][0][j]), d1 = __half2float(kscale[s][1][j]);
-                            sc[s][nt][0] = fmaf(d0, t[s][0], sc[s][nt][0]);
-                            sc[s][nt][1] = fmaf(d0, t[s][1], sc[s][nt][1]);
-                            sc[s][nt][2] = fmaf(d1, t[s][2], sc[s][nt][2]);
-                            sc[s][nt][3] = fmaf(d1, t[s][3], sc[s][nt][3]);
-                        }
+                        for (int s = 0; s < TT; ++s)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                float sum = t[s][QP - 1][x];
+#pragma unroll
+                                for (int p = QP - 2; p >= 0; --p) sum += t[s][p][x];
+                                sc[s][nt][x] = fmaf(d[s][x >> 1], sum, sc[s][nt][x]);
+                            }
                     }
                 }
             } else {
+                // a sum per part and parity of the step: short chains, added smallest first
+                float t[2][QP][TT][NT][4];
 #pragma unroll
-                for (int p = QP - 1; p >= 0; --p)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int j = 0; j < KJ; ++j)
+                    for (int p = 0; p < QP; ++p)
+#pragma unroll
+                        for (int s = 0; s < TT; ++s)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) t[e][p][s][nt][x] = 0.0f;
+                const int krow = (lane & 7) + (lane >> 3 & 1) * 8;
+                const uint32_t k_at = smem_address(k_s) + krow * ROWB;
+                const uint32_t q_at = smem_address(q_s) + (lane & 7) * S::QROW + (lane >> 3) * 16;
+#pragma unroll
+                for (int j = 0; j < DP / 32; ++j) {
+                    uint4 k0[TT], k1[TT];
+#pragma unroll
+                    for (int s = 0; s < TT; ++s) {
+                        k0[s] = ldmatrix4(k_at + 16 * s * ROWB + (((4 * j + (lane >> 4)) ^ (krow & 7)) << 4));
+                        k1[s] = ldmatrix4(k_at + 16 * s * ROWB + (((4 * j + 2 + (lane >> 4)) ^ (krow & 7)) << 4));
+                    }
+#pragma unroll
+                    for (int p = 0; p < QP; ++p)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const uint4 q = *reinterpret_cast<const uint4 *>(
-                                q_s + (p * ROWS + 8 * nt + r) * S::QROW + 16 * (c + 4 * j));
+                            const uint4 q = ldmatrix4(q_at + (p * ROWS + 8 * nt) * S::QROW + 64 * j);
 #pragma unroll
                             for (int s = 0; s < TT; ++s) {
-                                mma16816<HALF>(sc[s][nt], kreg[s][0][j][0], kreg[s][1][j][0], kreg[s][0][j][1],
-                                               kreg[s][1][j][1], q.x, q.y);
-                                mma16816<HALF>(sc[s][nt], kreg[s][0][j][KW - 2], kreg[s][1][j][KW - 2],
-                                               kreg[s][0][j][KW - 1], kreg[s][1][j][KW - 1], q.z, q.w);
+                                mma16816<HALF>(t[0][p][s][nt], k0[s], q.x, q.y);
+                                mma16816<HALF>(t[1][p][s][nt], k1[s], q.z, q.w);
                             }
                         }
+                }
+#pragma unroll
+                for (int s = 0; s < TT; ++s)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float sum = t[0][QP - 1][s][nt][x] + t[1][QP - 1][s][nt][x];
+#pragma unroll
+                            for (int p = QP - 2; p >= 0; --p) sum += t[0][p][s][nt][x] + t[1][p][s][nt][x];
+                            sc[s][nt][x] = sum;
+                        }
             }
-
-            // ---- K of the next tile, table entry of the one after it ----
-            const int next = tile + stride;
-            off = offset_of(next + mine, entry);
-            if (next < end) load_k(off);
-            entry = entry_of(next + stride + mine);
 
             // ---- softmax weights ----
             float alpha[NT][2];
@@ -464,7 +530,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                         for (int y = 0; y < 2; ++y) {
                             const int t = tile + 16 * s + 8 * y + r;
                             float &v = sc[s][nt][2 * y + x];
-                            v = t < lim[nt][x] && live[s][y] ? v * fac[nt][x] : -INFINITY;
+                            v = t < lim[nt][x] && there[s][y] >= 0 ? v * fac[nt][x] : -INFINITY;
                             top = fmaxf(top, v);
                         }
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
@@ -487,105 +553,109 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                     l[nt][x] = fmaf(l[nt][x], alpha[nt][x], sum);
                 }
 
-            // ---- O = O alpha + V^T P^T.  A query row's own later positions carry
-            // weight 0, but 0 times a draft token's NaN is NaN: a tile that holds
-            // positions some rows do not see is done row by row, last row first, the
-            // values behind the row's positions set to zero ----
-            const bool mixed = R > 1 && tile + TILE > len - R + 1;
-            const int passes = mixed ? R : 1;
-            for (int pass = 0; pass < passes; ++pass) {
-                const int row = R - 1 - pass;
-                bool take[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) take[nt][x] = !mixed || lim[nt][x] == len - R + row + 1;
-                if (mixed) {
-                    const int n = len - R + row + 1;
+            // ---- O = O alpha + V^T P^T ----
+            // with `mixed`, for the query rows of the new token `row` alone, the values
+            // behind its positions set to zero
+            auto values = [&](auto mixed, int row) {
+                constexpr bool MIXED = decltype(mixed)::value;
+                const int n = len - R + row + 1;
+                [[maybe_unused]] uint32_t keep[TT][2];  // of this thread's pairs of positions
+                if constexpr (MIXED) {
 #pragma unroll
                     for (int s = 0; s < TT; ++s)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (tile + 16 * s + 2 * c + (x & 1) + 8 * (x >> 1) >= n)
-#pragma unroll
-                                for (int v = 0; v < VM; ++v)
-#pragma unroll
-                                    for (int w = 0; w < VW; ++w) vreg[s][x][v][w] = 0;
+                        for (int y = 0; y < 2; ++y) {
+                            const int t = tile + 16 * s + 8 * y + 2 * c;
+                            keep[s][y] = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
+                        }
                 }
                 uint32_t pf[TT][NT][PP][2];
-                if constexpr (!Q8) {
+                auto weights = [&](auto scale) {
 #pragma unroll
                     for (int s = 0; s < TT; ++s)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int y = 0; y < 2; ++y) {
+                            const float d = scale(s, y);
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const Words<PP> w = split_pair<HALF, PP>(sc[s][nt][2 * y], sc[s][nt][2 * y + 1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float x0 = sc[s][nt][2 * y], x1 = sc[s][nt][2 * y + 1];
+                                if constexpr (Q8) x0 *= d, x1 *= d;
+                                const Words<PP> w = split_pair<HALF, PP>(x0, x1);
 #pragma unroll
                                 for (int p = 0; p < PP; ++p) pf[s][nt][p][y] = transpose8x8(w.w[p]);
                             }
-                }
+                        }
+                };
+                if constexpr (!Q8) weights([](int, int) { return 1.0f; });
+                [[maybe_unused]] uint2 vb[TT][4];
 #pragma unroll
-                for (int v = 0; v < VM; ++v) {
+                for (int mt = 0; mt < MT; ++mt) {
+                    uint4 A[TT];
                     if constexpr (Q8) {
+                        if (mt % 2 == 0) {
+                            const int v = mt / 2;
+                            weights([&](int s, int y) { return 32 * v < D ? scale_of(vs_s, s, y, v) : 0.0f; });
 #pragma unroll
-                        for (int s = 0; s < TT; ++s)
+                            for (int s = 0; s < TT; ++s)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int y = 0; y < 2; ++y) {
-                                    const float d = __half2float(vscale[s][y][v]);
-                                    const Words<PP> w =
-                                        split_pair<HALF, PP>(sc[s][nt][2 * y] * d, sc[s][nt][2 * y + 1] * d);
-#pragma unroll
-                                    for (int p = 0; p < PP; ++p) pf[s][nt][p][y] = transpose8x8(w.w[p]);
+                                for (int x = 0; x < 4; ++x) {
+                                    const int in = 2 * c + (x & 1) + 8 * (x >> 1);
+                                    const int key = (in & 7) & (ROWB / 16 - 1);
+                                    const uint32_t w = *reinterpret_cast<const uint32_t *>(
+                                        v_s + (16 * s + in) * ROWB + (((2 * v + (r >> 2)) ^ key) << 4) + 4 * (r & 3));
+                                    vb[s][x] = codes_to_bf16(w);
                                 }
-                    }
-                    [[maybe_unused]] uint2 vb[TT][4];
-                    if constexpr (Q8) {
-#pragma unroll
-                        for (int s = 0; s < TT; ++s)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) vb[s][x] = codes_to_bf16(vreg[s][x][v][0]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < OJ; ++j) {
-                        float t[NT][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.0f;
-                        uint32_t A[TT][4];
+                        }
 #pragma unroll
                         for (int s = 0; s < TT; ++s) {
                             uint32_t w[4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                if constexpr (Q8) w[x] = j ? vb[s][x].y : vb[s][x].x;
-                                else w[x] = vreg[s][x][v][j];
-                            }
-                            A[s][0] = __byte_perm(w[0], w[1], 0x5410);
-                            A[s][1] = __byte_perm(w[0], w[1], 0x7632);
-                            A[s][2] = __byte_perm(w[2], w[3], 0x5410);
-                            A[s][3] = __byte_perm(w[2], w[3], 0x7632);
+                            for (int x = 0; x < 4; ++x) w[x] = mt % 2 ? vb[s][x].y : vb[s][x].x;
+                            A[s] = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                                              __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632));
                         }
+                    } else {
+                        const int vrow = (lane & 7) + (lane >> 4) * 8;
 #pragma unroll
-                        for (int p = PP - 1; p >= 0; --p)
-#pragma unroll
-                            for (int s = 0; s < TT; ++s)
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma16816<HALF>(t[nt], A[s][0], A[s][1], A[s][2], A[s][3], pf[s][nt][p][0],
-                                                   pf[s][nt][p][1]);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                float &o = O[v][j][nt][x];
-                                if (take[nt][x & 1]) o = fmaf(o, alpha[nt][x & 1], t[nt][x]);
-                            }
+                        for (int s = 0; s < TT; ++s)
+                            A[s] = ldmatrix4_trans(smem_address(v_s) + (16 * s + vrow) * ROWB +
+                                                   (((2 * mt + (lane >> 3 & 1)) ^ (vrow & 7)) << 4));
                     }
+                    if constexpr (MIXED) {
+#pragma unroll
+                        for (int s = 0; s < TT; ++s) {
+                            A[s].x &= keep[s][0], A[s].y &= keep[s][0];
+                            A[s].z &= keep[s][1], A[s].w &= keep[s][1];
+                        }
+                    }
+                    float t[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.0f;
+#pragma unroll
+                    for (int p = PP - 1; p >= 0; --p)
+#pragma unroll
+                        for (int s = 0; s < TT; ++s)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma16816<HALF>(t[nt], A[s], pf[s][nt][p][0], pf[s][nt][p][1]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (!MIXED || lim[nt][x & 1] == n)
+                                O[mt][nt][x] = fmaf(O[mt][nt][x], alpha[nt][x & 1], t[nt][x]);
                 }
+            };
+            // A query row's own later positions carry weight 0, but 0 times a draft
+            // token's NaN is NaN: a tile with positions that some rows do not see is
+            // done token by token.
+            if (R > 1 && tile + TILE > len - R + 1) {
+                for (int row = R - 1; row >= 0; --row) values(std::true_type{}, row);
+            } else {
+                values(std::false_type{}, 0);
             }
         }
+        copies_wait<0>();
+        __syncwarp();  // the ring is free: it takes this warp's O
 
         // ---- join of the four warps ----
 #pragma unroll
@@ -600,27 +670,12 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                     m_s[warp * ROWS + 8 * nt + 2 * c + x] = m[nt][x];
                     l_s[warp * ROWS + 8 * nt + 2 * c + x] = v;
                 }
-            }
-        __syncthreads();
+                float *dst = reinterpret_cast<float *>(ring) + (8 * nt + 2 * c + x) * S::OROW;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                const int i = 8 * nt + 2 * c + x;
-                float top = m_s[i];
-#pragma unroll
-                for (int w = 1; w < ATTN_WARPS; ++w) top = fmaxf(top, m_s[w * ROWS + i]);
-                const float f = m[nt][x] == -INFINITY ? 0.0f : exp2f(m[nt][x] - top);
-                float *dst = o_s + (warp * ROWS + i) * DP;
-#pragma unroll
-                for (int v = 0; v < VM; ++v) {
-                    // this thread's values of d: 2 OJ consecutive ones
-                    float *at = dst + (Q8 ? 32 * v + 4 * r : 8 * (r + 8 * v));
-#pragma unroll
-                    for (int j = 0; j < OJ; ++j) {
-                        at[2 * j] = O[v][j][nt][x] * f;
-                        at[2 * j + 1] = O[v][j][nt][x + 2] * f;
-                    }
+                for (int mt = 0; mt < MT; ++mt) {
+                    const int d0 = Q8 ? 32 * (mt / 2) + 4 * r + 2 * (mt % 2) : 16 * mt + r;
+                    dst[d0] = O[mt][nt][x];
+                    dst[d0 + (Q8 ? 1 : 8)] = O[mt][nt][x + 2];
                 }
             }
         __syncthreads();
@@ -632,22 +687,27 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
             float top = m_s[i];
 #pragma unroll
             for (int w = 1; w < ATTN_WARPS; ++w) top = fmaxf(top, m_s[w * ROWS + i]);
-            float sum = 0.0f;
+            float sum = 0.0f, f[ATTN_WARPS];
 #pragma unroll
             for (int w = 0; w < ATTN_WARPS; ++w) {
                 const float mw = m_s[w * ROWS + i];
-                sum += mw == -INFINITY ? 0.0f : l_s[w * ROWS + i] * exp2f(mw - top);
+                f[w] = mw == -INFINITY ? 0.0f : exp2f(mw - top);
+                sum = fmaf(f[w], l_s[w * ROWS + i], sum);
             }
+            auto joined = [&](int d) {
+                float v = 0.0f;
+#pragma unroll
+                for (int w = 0; w < ATTN_WARPS; ++w)
+                    v = fmaf(f[w], reinterpret_cast<const float *>(smem + w * S::RING)[i * S::OROW + d], v);
+                return v;
+            };
             const int row = (int)a.group.div((uint32_t)g);
             if (whole) {
                 const int head = h * (int)a.group.d + g - row * (int)a.group.d;
                 const long long at = ((long long)b * R + row) * a.x.out_row_stride + head * a.x.out_head_stride;
                 const bool empty = len - R + row + 1 <= 0;
                 for (int d = lane; d < D; d += 32) {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < ATTN_WARPS; ++w) v += o_s[(w * ROWS + i) * DP + d];
-                    v = empty ? 0.0f : v / sum;
+                    const float v = empty ? 0.0f : joined(d) / sum;
                     if (a.x.dtype == BQ_F32) ((float *)a.x.out)[at + d] = v;
                     else if (a.x.dtype == BQ_F16) ((__half *)a.x.out)[at + d] = __float2half_rn(v);
                     else ((__nv_bfloat16 *)a.x.out)[at + d] = __float2bfloat16_rn(v);
@@ -655,15 +715,10 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
             } else {
                 if (lane == 0) a.part_ml[unit * ROWS + i] = make_float2(top, sum);
                 float *dst = a.part_o + (unit * ROWS + i) * D;
-                for (int d = lane; d < D; d += 32) {
-                    float v = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < ATTN_WARPS; ++w) v += o_s[(w * ROWS + i) * DP + d];
-                    dst[d] = v;
-                }
+                for (int d = lane; d < D; d += 32) dst[d] = joined(d);
             }
         }
-        __syncthreads();  // the next unit rewrites q_s, m_s and o_s
+        __syncthreads();  // the next unit fills the rings and rewrites q_s and m_s
     }
 }
 
@@ -686,47 +741,25 @@ int attn_occupancy(size_t smem, int *out) {
 
 }  // namespace bq
 
-// the instances of one cache type: parts 1 (q in the cache's 16-bit type) and
-// the split one, for head_dim up to 64, 128 and 256
+// the instances of one cache type and split (parts 1: q in the cache's 16-bit
+// type), for head_dim up to 64, 128 and 256
 #define BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, DP, NT)                                              \
     {                                                                                              \
-        KV, PARTS, DP, NT, bq::ATTN_WARPS * 32, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,   \
+        PARTS, DP, NT, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,                            \
             bq::attn_occupancy<KV, QP, PP, DP, NT>,                                                \
-            [](const bq::AttnArgs &a, int grid, size_t smem, void *stream) -> cudaError_t {        \
-                unsigned int *status = nullptr;                                                    \
-                cudaError_t e = status_addr_##NAME(&status);                                       \
-                if (e != cudaSuccess) return e;                                                    \
+            [](const bq::AttnArgs &a, int grid, size_t smem, void *stream,                         \
+               unsigned int *status) -> cudaError_t {                                              \
                 return bq::launch_pdl(bq::attn_kernel<KV, QP, PP, DP, NT>, dim3((unsigned)grid),   \
                                       bq::ATTN_WARPS * 32, smem, stream, 1, a, status);            \
             }                                                                                      \
     }
-#define BQ_ATTN_UNIT(NAME, KV, QP1, PP1, QPS, PPS)                                                 \
-    BQ_STATUS_WORD(attn_##NAME)                                                                    \
-    static cudaError_t status_addr_##NAME(unsigned int **out) {                                    \
-        static std::atomic<unsigned int *> addr[64];                                               \
-        int dev = 0;                                                                               \
-        cudaError_t e = cudaGetDevice(&dev);                                                       \
-        if (e != cudaSuccess) return e;                                                            \
-        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;                                   \
-        unsigned int *p = addr[dev].load();                                                        \
-        if (!p) {                                                                                  \
-            e = cudaGetSymbolAddress(reinterpret_cast<void **>(&p), g_status_attn_##NAME);         \
-            if (e != cudaSuccess) return e;                                                        \
-            addr[dev].store(p);                                                                    \
-        }                                                                                          \
-        *out = p;                                                                                  \
-        return cudaSuccess;                                                                        \
-    }                                                                                              \
+#define BQ_ATTN_UNIT(NAME, KV, PARTS, QP, PP)                                                      \
     const bq::AttnInstance *bq_internal_attn_##NAME(int *n) {                                      \
         static const bq::AttnInstance inst[] = {                                                   \
-            BQ_ATTN_INST(NAME, KV, 1, QP1, PP1, 64, 1),  BQ_ATTN_INST(NAME, KV, 1, QP1, PP1, 64, 2),   \
-            BQ_ATTN_INST(NAME, KV, 1, QP1, PP1, 128, 1), BQ_ATTN_INST(NAME, KV, 1, QP1, PP1, 128, 2),  \
-            BQ_ATTN_INST(NAME, KV, 1, QP1, PP1, 256, 1), BQ_ATTN_INST(NAME, KV, 2, QPS, PPS, 64, 1),   \
-            BQ_ATTN_INST(NAME, KV, 2, QPS, PPS, 64, 2),  BQ_ATTN_INST(NAME, KV, 2, QPS, PPS, 128, 1),  \
-            BQ_ATTN_INST(NAME, KV, 2, QPS, PPS, 128, 2), BQ_ATTN_INST(NAME, KV, 2, QPS, PPS, 256, 1)}; \
+            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 64, 1),  BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 64, 2),  \
+            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 64, 4),  BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 128, 1), \
+            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 128, 2), BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 128, 4), \
+            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 256, 1), BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 256, 2)}; \
         *n = (int)(sizeof inst / sizeof inst[0]);                                                  \
         return inst;                                                                               \
-    }                                                                                              \
-    int bq_internal_attn_status_##NAME(unsigned int *flags, int clear) {                           \
-        return read_status_attn_##NAME(flags, clear);                                              \
     }

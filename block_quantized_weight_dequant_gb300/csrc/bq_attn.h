@@ -34,20 +34,19 @@ struct AttnArgs {
 __host__ __device__ inline int attn_chunks(int n, int chunk) { return n <= chunk ? 1 : (n + chunk - 1) / chunk; }
 
 struct AttnInstance {
-    int cache, parts;  // parts: 1 if q is read in the cache's 16-bit type, else the split one
-    int dim, nt;       // head_dim up to dim, 8 nt query rows per CTA
-    int threads;
-    size_t smem;       // without the scan of the requests
+    int parts;    // 1: q in the type that the tensor cores multiply; 2: split
+    int dim, nt;  // head_dim up to dim, 8 nt query rows per CTA
+    size_t smem;  // without the scan of the requests
     int (*occupancy)(size_t smem, int *out);
-    cudaError_t (*launch)(const AttnArgs &, int grid, size_t smem, void *stream);
+    cudaError_t (*launch)(const AttnArgs &, int grid, size_t smem, void *stream, unsigned int *status);
 };
 
 }  // namespace bq
 
-// instance tables, one per cache type; n receives the number
-const bq::AttnInstance *bq_internal_attn_f16(int *n);
-const bq::AttnInstance *bq_internal_attn_bf16(int *n);
-const bq::AttnInstance *bq_internal_attn_q8_0(int *n);
-int bq_internal_attn_status_f16(unsigned int *flags, int clear);
-int bq_internal_attn_status_bf16(unsigned int *flags, int clear);
-int bq_internal_attn_status_q8_0(unsigned int *flags, int clear);
+// instance tables by cache type and split; n receives the number
+const bq::AttnInstance *bq_internal_attn_f16_own(int *n);
+const bq::AttnInstance *bq_internal_attn_f16_split(int *n);
+const bq::AttnInstance *bq_internal_attn_bf16_own(int *n);
+const bq::AttnInstance *bq_internal_attn_bf16_split(int *n);
+const bq::AttnInstance *bq_internal_attn_q8_0_own(int *n);
+const bq::AttnInstance *bq_internal_attn_q8_0_split(int *n);

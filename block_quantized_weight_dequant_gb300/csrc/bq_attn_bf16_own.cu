@@ -1,0 +1,7 @@
+// bq_attn_bf16_own.cu -- paged attention over a bf16 cache, bf16 queries (bq_attn.cuh).
+#include <atomic>
+#include <type_traits>
+
+#include "bq_attn.cuh"
+
+BQ_ATTN_UNIT(bf16_own, bq::KV_BF16, 1, 1, 2)

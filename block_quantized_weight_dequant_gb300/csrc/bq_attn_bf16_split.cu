@@ -1,0 +1,7 @@
+// bq_attn_bf16_split.cu -- paged attention over a bf16 cache, queries of other types (bq_attn.cuh).
+#include <atomic>
+#include <type_traits>
+
+#include "bq_attn.cuh"
+
+BQ_ATTN_UNIT(bf16_split, bq::KV_BF16, 2, 3, 3)
