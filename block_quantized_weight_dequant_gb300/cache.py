@@ -24,9 +24,17 @@ _DTYPES = {torch.float32: _lib.BQ_F32, torch.float16: _lib.BQ_F16, torch.bfloat1
 _KINDS = {"f16": torch.float16, "bf16": torch.bfloat16, "q8_0": torch.int8}
 
 
+# (one attribute lookup each: a call's checks cost as much as its launch)
+_Tensor = torch.Tensor
+_byref = ctypes.byref
+# the current stream's handle and the current device, without a Stream object
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _need(t, name, dtype=None, like=None):
     """A CUDA tensor of the given dtype on the device of `like`."""
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -37,32 +45,54 @@ def _need(t, name, dtype=None, like=None):
 
 
 def _activation(t, name, shape, dtype, device):
-    """An activation [..., n] of a known shape whose last dimension is contiguous."""
+    """An activation of a known shape whose last dimension is contiguous."""
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
+            and t.stride(-1) == 1):
+        return
     _need(t, name, dtype, device)
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
+def _first(t, name, device=None):
+    """An activation that says dtype, and device if that is None."""
+    _need(t, name, None, device)
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
+
+
 def _dense(t, name, dtype, device, numel=None):
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
+            and (numel is None or t.numel() == numel)):
+        return
     _need(t, name, dtype, device)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+
+
+def _table(t, n, device):
+    """The block table: rows of contiguous page numbers; returns width and row stride."""
+    _need(t, "table", torch.int32, device)
+    if t.dim() != 2 or t.shape[0] != n or (n and t.shape[1] < 1):
+        raise ValueError(f"table must be [{n}, width]")
+    if t.stride(1) != 1 and t.shape[1] > 1 and n:
+        raise ValueError("rows of table must be contiguous")
+    width = t.shape[1] or 1
+    return width, (t.stride(0) if n > 1 else width)
 
 
 def _call(fn, what, device, *args):
     """fn(*args, stream) on `device`'s current stream."""
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, torch.cuda.current_stream().cuda_stream)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch.cuda.current_stream().cuda_stream)
-    if status != _lib.BQ_OK:
+            status = fn(*args, _raw_stream(index))
+    if status:
         raise _lib.BQError(status, what)
 
 
@@ -134,20 +164,21 @@ class PagedKVCache:
 class Rope:
     """Rotary positions: pair p of a head turns by position * freq[p] radians.
     ``freq``: fp64 CUDA [rot / 2] (rot values of a head are rotated, a multiple
-    of 8; the rest pass).  ``sections``: pairs of each position axis, one to
+    of 16; the rest pass).  ``sections``: pairs of each position axis, one to
     three of them, in order (time, height, width); one axis by default.
     ``interleaved``: pairs are (2p, 2p + 1) instead of (p, p + rot / 2)."""
 
     def __init__(self, freq, sections=None, interleaved=False):
         _need(freq, "freq", torch.float64)
         _dense(freq, "freq", torch.float64, freq.device)
-        if freq.dim() != 1 or freq.numel() == 0 or freq.numel() % 4:
-            raise ValueError("freq must be [rot / 2] with rot a multiple of 8")
+        if freq.dim() != 1 or freq.numel() == 0 or freq.numel() % 8:
+            raise ValueError("freq must be [rot / 2] with rot a multiple of 16")
         sections = [freq.numel()] if sections is None else [int(s) for s in sections]
         if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != freq.numel():
             raise ValueError("sections must be one to three counts that sum to rot / 2")
         self.freq, self.sections, self.interleaved = freq, sections, bool(interleaved)
         self.rot, self.axes = 2 * freq.numel(), len(sections)
+        self.device, self._ptr = freq.device, freq.data_ptr()
         self._sections = (ctypes.c_int32 * 3)(*(sections + [0] * (3 - len(sections))))
 
     @classmethod
@@ -177,11 +208,7 @@ def kv_block_tables(lens, new_lens, table, free_pages, free_count, page_size, sl
     _dense(lens, "lens", i32, dev)
     n = lens.numel()
     _dense(new_lens, "new_lens", i32, dev, n)
-    _need(table, "table", i32, dev)
-    if table.dim() != 2 or table.shape[0] != n or (n and table.shape[1] < 1):
-        raise ValueError(f"table must be [{n}, width]")
-    if table.numel() and table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError("rows of table must be contiguous")
+    width, stride = _table(table, n, dev)
     _dense(free_pages, "free_pages", i32, dev)
     _dense(free_count, "free_count", i32, dev, 1)
     _dense(slots, "slots", torch.int64, dev)
@@ -193,13 +220,11 @@ def kv_block_tables(lens, new_lens, table, free_pages, free_count, page_size, sl
     _dense(lens_out, "lens_out", i32, dev, n)
     _dense(free_count_out, "free_count_out", i32, dev, 1)
     _dense(refused, "refused", i32, dev, 1)
-    width = max(1, table.shape[1])
-    stride = table.stride(0) if n > 1 else width
     args = _lib.BqKvTables(n, int(page_size), width, free_pages.numel(), stride, slots.numel(),
                            lens.data_ptr(), new_lens.data_ptr(), table.data_ptr(), free_pages.data_ptr(),
                            free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(), starts.data_ptr(),
                            lens_out.data_ptr(), free_count_out.data_ptr(), refused.data_ptr())
-    _call(lib.bq_kv_block_tables, "kv_block_tables", dev, ctypes.byref(args))
+    _call(lib.bq_kv_block_tables, "kv_block_tables", dev, _byref(args))
     return refused
 
 
@@ -230,9 +255,10 @@ class BlockTables:
                                self.page_size, self.slots, self.positions, self.starts, refused=self.refused)
 
 
-def _strides(t):
+def _strides(t, tokens, heads):
     """Token and head strides of [tokens, heads, head_dim]; 0 over one entry."""
-    return (t.stride(0) if t.shape[0] > 1 else 0), (t.stride(1) if t.shape[1] > 1 else 0)
+    a, b, _ = t.stride()
+    return (a if tokens > 1 else 0), (b if heads > 1 else 0)
 
 
 def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None):
@@ -245,20 +271,22 @@ def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None)
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")
     dev, kv, D = cache.device, cache.kv_heads, cache.head_dim
-    _need(k, "k", None, dev)
+    _first(k, "k", dev)
+    dtype = k.dtype
     T = k.shape[0] if k.dim() == 3 else -1
-    _activation(k, "k", (T, kv, D), None, dev)
-    _activation(v, "v", (T, kv, D), k.dtype, dev)
+    _activation(k, "k", (T, kv, D), dtype, dev)
+    _activation(v, "v", (T, kv, D), dtype, dev)
     _dense(slots, "slots", torch.int64, dev, T)
     heads, qp, op, qs, os = 0, None, None, (0, 0), (0, 0)
     if q is not None:
-        _need(q, "q", k.dtype, dev)
+        _need(q, "q", dtype, dev)
         heads = q.shape[1] if q.dim() == 3 else -1
-        _activation(q, "q", (T, heads, D), k.dtype, dev)
+        _activation(q, "q", (T, heads, D), dtype, dev)
         if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=q.dtype, device=dev)
-        _activation(q_out, "q_out", (T, heads, D), q.dtype, dev)
-        qp, op, qs, os = q.data_ptr(), q_out.data_ptr(), _strides(q), _strides(q_out)
+            q_out = torch.empty((T, heads, D), dtype=dtype, device=dev)
+        else:
+            _activation(q_out, "q_out", (T, heads, D), dtype, dev)
+        qp, op, qs, os = q.data_ptr(), q_out.data_ptr(), _strides(q, T, heads), _strides(q_out, T, heads)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rot, axes, inter, sections, freq, pos, ps = 0, 0, 0, _NO_SECTIONS, None, None, 0
@@ -266,22 +294,22 @@ def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None)
         if not isinstance(rope, Rope):
             raise TypeError("rope must be a Rope")
         _need(positions, "positions", torch.int32, dev)
-        if rope.freq.device != dev:
-            raise ValueError(f"rope is on {rope.freq.device}, expected {dev}")
-        want = (rope.axes, T)
-        if tuple(positions.shape) != want and not (rope.axes == 1 and tuple(positions.shape) == (T,)):
-            raise ValueError(f"positions must be {list(want)}, got {list(positions.shape)}")
+        if rope.device != dev:
+            raise ValueError(f"rope is on {rope.device}, expected {dev}")
+        axes = rope.axes
+        if tuple(positions.shape) != (axes, T) and not (axes == 1 and tuple(positions.shape) == (T,)):
+            raise ValueError(f"positions must be {[axes, T]}, got {list(positions.shape)}")
         if T > 1 and positions.stride(-1) != 1:
             raise ValueError("positions must be contiguous over the tokens")
-        ps = positions.stride(0) if rope.axes > 1 else 0
-        rot, axes, inter, sections = rope.rot, rope.axes, rope.interleaved, rope._sections
-        freq, pos = rope.freq.data_ptr(), positions.data_ptr()
+        ps = positions.stride(0) if axes > 1 else 0
+        rot, inter, sections = rope.rot, rope.interleaved, rope._sections
+        freq, pos = rope._ptr, positions.data_ptr()
     elif positions is not None:
         raise ValueError("positions without rope")
-    args = _lib.BqKvAppendArgs(_DTYPES[k.dtype], heads, rot, axes, inter, sections, T, k.data_ptr(),
-                               v.data_ptr(), qp, op, *_strides(k), *_strides(v), *qs, *os,
+    args = _lib.BqKvAppendArgs(_DTYPES[dtype], heads, rot, axes, inter, sections, T, k.data_ptr(),
+                               v.data_ptr(), qp, op, *_strides(k, T, kv), *_strides(v, T, kv), *qs, *os,
                                slots.data_ptr(), pos, ps, freq)
-    _call(lib.bq_kv_append, "kv_append", dev, cache._ref, ctypes.byref(args))
+    _call(lib.bq_kv_append, "kv_append", dev, cache._ref, _byref(args))
     return q_out
 
 
@@ -305,31 +333,29 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
         raise ValueError(f"rows must be 1 to {BQ_VERIFY_MAX_ROWS}, got {rows}")
     _dense(lens, "lens", torch.int32, dev)
     n = lens.numel()
-    _need(q, "q", None, dev)
-    heads = q.shape[1] if q.dim() == 3 else -1
-    _activation(q, "q", (n * rows, heads, D), None, dev)
-    _need(table, "table", torch.int32, dev)
-    if table.dim() != 2 or table.shape[0] != n or (n and table.shape[1] < 1):
-        raise ValueError(f"table must be [{n}, width]")
-    if table.numel() and table.stride(1) != 1 and table.shape[1] > 1:
-        raise ValueError("rows of table must be contiguous")
+    _first(q, "q", dev)
+    dtype = q.dtype
+    T, heads = n * rows, (q.shape[1] if q.dim() == 3 else -1)
+    shape = (T, heads, D)
+    _activation(q, "q", shape, dtype, dev)
+    width, stride = _table(table, n, dev)
     if out is None:
-        out = torch.empty((n * rows, heads, D), dtype=q.dtype, device=dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        os = (heads * D, D)
     else:
-        _activation(out, "out", (n * rows, heads, D), q.dtype, dev)
-    width = max(1, table.shape[1])
-    args = _lib.BqAttentionArgs(_DTYPES[q.dtype], n, rows, heads, width,
-                                1.0 / math.sqrt(D) if scale is None else scale,
-                                table.stride(0) if n > 1 else width, *_strides(q), *_strides(out),
-                                q.data_ptr(), out.data_ptr(), table.data_ptr(), lens.data_ptr())
-    ref = ctypes.byref(args)
-    key = (n, rows, heads, width)
-    nbytes = cache._workspace.get(key)
-    if nbytes is None:
-        nbytes = lib.bq_paged_attention_workspace_bytes(cache._ref, ref)
-        if nbytes >= 0:
-            cache._workspace[key] = nbytes
+        _activation(out, "out", shape, dtype, dev)
+        os = _strides(out, T, heads)
+    args = _lib.BqAttentionArgs(_DTYPES[dtype], n, rows, heads, width, 1.0 / math.sqrt(D) if scale is None else scale,
+                                stride, *_strides(q, T, heads), *os, q.data_ptr(), out.data_ptr(),
+                                table.data_ptr(), lens.data_ptr())
+    ref = _byref(args)
     if workspace is None:
+        key = (n, rows, heads, width)
+        nbytes = cache._workspace.get(key)
+        if nbytes is None:
+            nbytes = lib.bq_paged_attention_workspace_bytes(cache._ref, ref)
+            if nbytes >= 0:
+                cache._workspace[key] = nbytes
         if nbytes > 0:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
@@ -362,44 +388,44 @@ def sandwich_norm(y, h, pre_gain=None, post_gain=None, gate=None, alpha=1.0, bet
     fp32 [width]; gate of y's dtype, [width] or [rows, width].  Returns (h',
     x'), x' of y's dtype (None without pre_gain).  h_out may be h, x_out may be
     y."""
-    _need(y, "y")
-    dev = y.device
-    if y.dim() != 2:
+    _first(y, "y")
+    dev, dtype, shape = y.device, y.dtype, y.shape
+    if len(shape) != 2:
         raise ValueError("y must be [rows, width]")
-    shape = tuple(y.shape)
-    _activation(y, "y", shape, None, dev)
-    _need(h, "h", None, dev)
-    _activation(h, "h", shape, None, dev)
-    if h.dtype != y.dtype and h.dtype != torch.float32:
-        raise TypeError(f"h must be {y.dtype} or fp32, got {h.dtype}")
-    width = shape[1]
-    gp, gs = None, 0
+    _activation(y, "y", shape, dtype, dev)
+    _first(h, "h", dev)
+    h_dtype = h.dtype
+    _activation(h, "h", shape, h_dtype, dev)
+    if h_dtype != dtype and h_dtype != torch.float32:
+        raise TypeError(f"h must be {dtype} or fp32, got {h_dtype}")
+    T, width = shape
+    gp = post = pre = xp = None
+    gs = xs = 0
     if gate is not None:
-        _need(gate, "gate", y.dtype, dev)
-        _activation(gate, "gate", (width,) if gate.dim() == 1 else shape, y.dtype, dev)
-        gp, gs = gate.data_ptr(), (gate.stride(0) if gate.dim() == 2 and shape[0] > 1 else 0)
-    for name, g in (("pre_gain", pre_gain), ("post_gain", post_gain)):
-        if g is not None:
-            _dense(g, name, torch.float32, dev, width)
+        one = gate.dim() == 1 if isinstance(gate, _Tensor) else False
+        _activation(gate, "gate", (width,) if one else shape, dtype, dev)
+        gp, gs = gate.data_ptr(), (0 if one or T < 2 else gate.stride(0))
+    if post_gain is not None:
+        _dense(post_gain, "post_gain", torch.float32, dev, width)
+        post = post_gain.data_ptr()
     if h_out is None:
-        h_out = torch.empty(shape, dtype=h.dtype, device=dev)
+        h_out = torch.empty(shape, dtype=h_dtype, device=dev)
     else:
-        _activation(h_out, "h_out", shape, h.dtype, dev)
-    if pre_gain is None:
-        if x_out is not None:
-            raise ValueError("x_out without pre_gain")
-    elif x_out is None:
-        x_out = torch.empty(shape, dtype=y.dtype, device=dev)
-    else:
-        _activation(x_out, "x_out", shape, y.dtype, dev)
-
-    def row(t):
-        return t.stride(0) if shape[0] > 1 else 0
-
-    args = _lib.BqSandwichArgs(_DTYPES[y.dtype], _DTYPES[h.dtype], shape[0], width, y.data_ptr(), h.data_ptr(),
-                               gp, None if post_gain is None else post_gain.data_ptr(),
-                               None if pre_gain is None else pre_gain.data_ptr(), h_out.data_ptr(),
-                               None if x_out is None else x_out.data_ptr(), row(y), row(h), gs, row(h_out),
-                               0 if x_out is None else row(x_out), alpha, beta, eps)
-    _call(lib.bq_sandwich_norm, "sandwich_norm", dev, ctypes.byref(args))
+        _activation(h_out, "h_out", shape, h_dtype, dev)
+    if pre_gain is not None:
+        _dense(pre_gain, "pre_gain", torch.float32, dev, width)
+        pre = pre_gain.data_ptr()
+        if x_out is None:
+            x_out = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _activation(x_out, "x_out", shape, dtype, dev)
+        xp, xs = x_out.data_ptr(), x_out.stride(0)
+    elif x_out is not None:
+        raise ValueError("x_out without pre_gain")
+    ys, hs, hos = y.stride(0), h.stride(0), h_out.stride(0)
+    if T < 2:
+        ys = hs = hos = xs = 0
+    args = _lib.BqSandwichArgs(_DTYPES[dtype], _DTYPES[h_dtype], T, width, y.data_ptr(), h.data_ptr(), gp, post, pre,
+                               h_out.data_ptr(), xp, ys, hs, gs, hos, xs, alpha, beta, eps)
+    _call(lib.bq_sandwich_norm, "sandwich_norm", dev, _byref(args))
     return h_out, x_out

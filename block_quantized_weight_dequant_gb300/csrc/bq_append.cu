@@ -2,18 +2,23 @@
 // rotary positions of one to three axes (bq_kv_append in include/bqgemv.h).
 //
 // Angles: the turn of pair p at position n is n * freq / (2 pi).  freq/(2 pi)
-// is split once per warp into hi + lo (two fp32 words, 48 bits); per token
+// is split once per thread into hi + lo (two fp32 words, 48 bits); per token
 // n * hi is formed exactly as product and remainder (one FMUL, one FFMA), each
 // reduced by its nearest whole number, so the fraction of a turn is right to
 // about 2^-24 of a turn plus n * freq * 2^-48, at positions up to 2^31.  fp64
-// runs once per warp and pair only (its rate is far below fp32's).
+// runs once per thread and pair only (its rate is far below fp32's).
 //
-// One warp takes a head of a token: lane l holds elements 4l .. 4l+3 (and
-// 128 + 4l .. for heads over 128), one 16-byte load of fp32; the partner of a
-// (p, p + rot/2) pair comes by shuffle, a Q8_0 block is 8 lanes.  A warp stays
-// with one residue of the heads over the tokens that it takes, so its angles
-// serve all its heads of a token; with few tokens there is a warp for every
-// head.  Bound by HBM for a prompt, by latency for one token.
+// A CTA takes a few tokens at a time (or, with few tokens, a share of one
+// token's heads): its threads put the tokens' cosines and sines into shared
+// memory, one pair each, then its warps take the tokens' heads, the loads of
+// the next heads on their way while the present ones are turned and stored.
+// A lane holds 8 values of a head, so that a warp takes 1, 2 or 4 heads: the
+// two quarters 4i .. 4i+3 and rot/2 + 4i .. of four (p, p + rot/2) pairs, or 8
+// values in a row (four interleaved pairs, or values behind rot).  So no value
+// moves between lanes for the rotation; a Q8_0 block is the first (or second)
+// quarter of 8 lanes, or both of 4, or, where rot / 2 is not whole blocks, is
+// put in order through shared memory.  Bound by HBM for a prompt, by latency for
+// one token.
 #include <atomic>
 #include <type_traits>
 
@@ -23,208 +28,213 @@ namespace {
 
 BQ_STATUS_WORD(append)
 
-constexpr int THREADS = 128;
-constexpr int UNROLL = 4;  // heads in flight per warp
+constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int MAX_BATCH = 4;  // tokens at a time
 
 struct Args {
     bq_kv_cache c;
     bq_kv_append_args x;
     bq::FastDiv page;
     int items;  // heads of a token: q, k and v
-    int parts;  // warps that share a token's heads
-    int wide_k, wide_v, wide_q, wide_o;  // 4-element accesses allowed
+    int parts;  // CTAs that share a token's heads
+    int batch;  // tokens at a time
+    int wide, wide_out;  // 4-element accesses of the inputs, of q_out
+    // strides (below 2^31) as 32-bit numbers: a product with an index is one instruction
+    uint32_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h, page_s, head_s, slot_s;
 };
 
-// pair and partner of element e < rot
-struct Place {
-    int pair, partner;
-    bool second;  // the pair's second element
-};
-__device__ __forceinline__ Place place_of(int e, int rot, int interleaved) {
-    const int half = rot >> 1;
-    Place p;
-    if (interleaved) {
-        p.pair = e >> 1;
-        p.partner = e ^ 1;
-        p.second = e & 1;
-    } else {
-        p.second = e >= half;
-        p.pair = p.second ? e - half : e;
-        p.partner = p.second ? e - half : e + half;
-    }
-    return p;
-}
-
-template <class E, int CT, int ITS>
-__global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__ Args a) {
+// GL lanes per head: 8 for head_dim up to 64, 16 up to 128, 32 up to 256
+template <class E, int CT, int GL>
+__global__ void __launch_bounds__(THREADS, 3) append_kernel(const __grid_constant__ Args a) {
     using T = typename E::T;
-    const int lane = threadIdx.x & 31;
-    const int warps = gridDim.x * (THREADS / 32);
-    const int wid = blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
-    const int part = wid % a.parts;
-    const int step = warps / a.parts;
-    const long long first = wid / a.parts;
-    bq::pdl_wait();
-    if (first >= step) return;
-
+    constexpr int HPW = 32 / GL;       // heads of a warp at a time
+    constexpr int UNROLL = 2;          // times that in flight, and again the next
+    constexpr int HALF_MAX = 4 * GL;   // pairs of a head
+    constexpr int DMAX = 8 * GL;
+    __shared__ __align__(16) float2 cs_s[2][MAX_BATCH][HALF_MAX];
+    __shared__ long long row_s[2][MAX_BATCH];
+    __shared__ __align__(16) float order_s[CT == BQ_Q8_0 ? WARPS * HPW * DMAX : 4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int sub = lane / GL, i = lane % GL;
+    const int part = blockIdx.x % a.parts;
+    const long long groups = gridDim.x / a.parts;
     const int D = a.c.head_dim, rot = a.x.freq ? a.x.rot : 0, half = rot >> 1;
-    float hi[ITS][4], lo[ITS][4];
-    int axis[ITS][4];
-#pragma unroll
-    for (int it = 0; it < ITS; ++it)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int e = 128 * it + 4 * lane + i;
-            hi[it][i] = lo[it][i] = 0.0f;
-            axis[it][i] = 0;
-            if (e < rot) {
-                const int p = place_of(e, rot, a.x.interleaved).pair;
-                const double t = a.x.freq[p] * 0.15915494309189533576888;  // 1 / (2 pi)
-                hi[it][i] = (float)t;
-                lo[it][i] = (float)(t - (double)hi[it][i]);
-                axis[it][i] = (p >= a.x.sections[0] && a.x.axes > 1) +
-                              (p >= a.x.sections[0] + a.x.sections[1] && a.x.axes > 2);
-            }
-        }
+    bq::pdl_wait();
+
+    // the turn of this thread's pair
+    const int pair = tid % HALF_MAX;
+    float hi = 0.0f, lo = 0.0f;
+    int axis = 0;
+    if (pair < half) {
+        const double t = a.x.freq[pair] * 0.15915494309189533576888;  // 1 / (2 pi)
+        hi = (float)t;
+        lo = (float)(t - (double)hi);
+        axis = (pair >= a.x.sections[0] && a.x.axes > 1) +
+               (pair >= a.x.sections[0] + a.x.sections[1] && a.x.axes > 2);
+    }
 
     const int heads = a.x.q ? a.x.heads : 0, kv = a.c.kv_heads;
     const long long slots_all = a.c.pages * a.c.page_size;
-    for (long long t = first; t < a.x.tokens; t += step) {
-        const long long slot = a.x.slots[t];
-        long long row = -1;  // element offset of the token's slot, head 0
-        if (slot >= 0 && slot < slots_all) {
-            const long long page = slot <= 0x7fffffffLL ? (long long)a.page.div((uint32_t)slot)
-                                                        : slot / a.c.page_size;
-            row = page * a.c.page_stride + (slot - page * a.c.page_size) * a.c.slot_stride;
-        } else if (slot >= slots_all && lane == 0) {
-            atomicOr(&g_status_append, BQ_DEVERR_SLOT);
+    const bool in_rot = 8 * i < rot, apart = in_rot && !a.x.interleaved;
+    const int e0 = apart ? 4 * i : 8 * i, e1 = apart ? half + 4 * i : 8 * i + 4;
+    const bool there = 8 * i < D;
+    // heads of a token that this lane takes: first, first + stride, ...
+    const int first = (part * WARPS + warp) * HPW + sub, stride = a.parts * WARPS * HPW;
+    const int warp_first = first - sub;
+    const int rounds = a.items > warp_first ? (a.items - warp_first + stride * UNROLL - 1) / (stride * UNROLL) : 0;
+
+    auto load = [&](long long t, int round, float (&x)[UNROLL][2][4]) {
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            const int item = first + (round * UNROLL + u) * stride;
+            if (item >= a.items || !there) continue;
+            const int type = item < heads ? 0 : item < heads + kv ? 1 : 2;
+            const T *base = (const T *)(type == 0 ? a.x.q : type == 1 ? a.x.k : a.x.v);
+            const uint32_t ts = type == 0 ? a.q_t : type == 1 ? a.k_t : a.v_t;
+            const uint32_t hs = type == 0 ? a.q_h : type == 1 ? a.k_h : a.v_h;
+            const uint32_t head = item - (type == 0 ? 0 : type == 1 ? heads : heads + kv);
+            const T *src = base + (uint64_t)(uint32_t)t * ts + (uint64_t)head * hs;
+            bq::load_n<E, 4>(src + e0, a.wide, x[u][0]);
+            bq::load_n<E, 4>(src + e1, a.wide, x[u][1]);
         }
-        float cs[ITS][4], sn[ITS][4];
-        if (rot) {
-            float pf[3], pr[3];
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                const int n = x < a.x.axes ? a.x.positions[x * a.x.position_stride + t] : 0;
-                pf[x] = (float)n;  // beyond 2^24 rounded: the rest is pr, exact
-                pr[x] = (float)((long long)n - (long long)pf[x]);
+    };
+
+    int buf = 0;
+    for (long long t0 = blockIdx.x / a.parts * (long long)a.batch; t0 < a.x.tokens;
+         t0 += groups * a.batch, buf ^= 1) {
+        const int batch = (int)(a.x.tokens - t0 < a.batch ? a.x.tokens - t0 : a.batch);
+        float x[UNROLL][2][4];
+        if (rounds) load(t0, 0, x);
+        // ---- slots and angles of the batch ----
+        if (tid < batch) {
+            const long long slot = a.x.slots[t0 + tid];
+            long long row = -1;  // element offset of the token's slot, head 0
+            if (slot >= 0 && slot < slots_all) {
+                const long long page = slot <= 0x7fffffffLL ? (long long)a.page.div((uint32_t)slot)
+                                                            : slot / a.c.page_size;
+                row = page * (long long)a.page_s + (slot - page * a.c.page_size) * (long long)a.slot_s;
+            } else if (slot >= slots_all && part == 0) {
+                atomicOr(&g_status_append, BQ_DEVERR_SLOT);
             }
-#pragma unroll
-            for (int it = 0; it < ITS; ++it)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int ax = axis[it][i];
-                    const float n = ax == 0 ? pf[0] : ax == 1 ? pf[1] : pf[2];
-                    const float r = ax == 0 ? pr[0] : ax == 1 ? pr[1] : pr[2];
-                    const float p = __fmul_rn(n, hi[it][i]);
-                    const float e = __fmaf_rn(n, hi[it][i], -p);
-                    float f = (p - rintf(p)) + (e - rintf(e));
-                    const float rest = __fmaf_rn(n, lo[it][i], r * hi[it][i]);
-                    f += rest - rintf(rest);
-                    sincospif(2.0f * (f - rintf(f)), &sn[it][i], &cs[it][i]);
-                }
+            row_s[buf][tid] = row;
         }
-        for (int i0 = part; i0 < a.items; i0 += UNROLL * a.parts) {
-            float x[UNROLL][ITS][4];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int item = i0 + u * a.parts;
-                if (item >= a.items || (item >= heads && row < 0)) continue;
-                const T *src;
-                int wide;
-                if (item < heads) {
-                    src = (const T *)a.x.q + t * a.x.q_token_stride + item * a.x.q_head_stride;
-                    wide = a.wide_q;
-                } else if (item < heads + kv) {
-                    src = (const T *)a.x.k + t * a.x.k_token_stride + (item - heads) * a.x.k_head_stride;
-                    wide = a.wide_k;
-                } else {
-                    src = (const T *)a.x.v + t * a.x.v_token_stride + (item - heads - kv) * a.x.v_head_stride;
-                    wide = a.wide_v;
-                }
-#pragma unroll
-                for (int it = 0; it < ITS; ++it) {
-                    const int e = 128 * it + 4 * lane;
-                    if (e < D) bq::load_n<E, 4>(src + e, wide, x[u][it]);
-                }
+        if (pair < half)
+            for (int b = tid / HALF_MAX; b < batch; b += THREADS / HALF_MAX) {
+                const int n = a.x.positions[axis * a.x.position_stride + t0 + b];
+                const float nf = (float)n;  // beyond 2^24 rounded: the rest is nr, exact
+                const float nr = (float)((long long)n - (long long)nf);
+                const float p = __fmul_rn(nf, hi);
+                const float e = __fmaf_rn(nf, hi, -p);
+                float f = (p - rintf(p)) + (e - rintf(e));
+                const float rest = __fmaf_rn(nf, lo, nr * hi);
+                f += rest - rintf(rest);
+                float s, c;
+                sincospif(2.0f * (f - rintf(f)), &s, &c);
+                cs_s[buf][b][pair] = make_float2(c, s);
             }
+        __syncthreads();  // (the batch after the next rewrites this buffer, two barriers on)
+
+        for (int b = 0; b < batch; ++b) {
+            const long long t = t0 + b, row = row_s[buf][b];
+            float2 w[4];  // cosine and sine of this lane's four pairs
 #pragma unroll
-            for (int u = 0; u < UNROLL; ++u) {
-                const int item = i0 + u * a.parts;
-                if (item >= a.items || (item >= heads && row < 0)) continue;
-                float y[ITS][4];
-                if (rot && item < heads + kv) {
+            for (int k = 0; k < 4; ++k) w[k] = in_rot ? cs_s[buf][b][4 * i + k] : make_float2(1.0f, 0.0f);
+            for (int round = 0; round < rounds; ++round) {
+                float y[UNROLL][2][4];
 #pragma unroll
-                    for (int it = 0; it < ITS; ++it) {
-                        const int e = 128 * it + 4 * lane;
-                        float z[4];
-                        if (a.x.interleaved) {
-                            z[0] = x[u][it][1], z[1] = x[u][it][0], z[2] = x[u][it][3], z[3] = x[u][it][2];
+                for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) y[u][0][k] = x[u][0][k], y[u][1][k] = x[u][1][k];
+                // the next heads, of this token or the next of the batch
+                if (round + 1 < rounds) load(t, round + 1, x);
+                else if (b + 1 < batch) load(t + 1, 0, x);
+#pragma unroll
+                for (int u = 0; u < UNROLL; ++u) {
+                    const int item = first + (round * UNROLL + u) * stride;
+                    if (item - sub >= a.items) break;  // whole warps
+                    const int type = item >= a.items ? 3 : item < heads ? 0 : item < heads + kv ? 1 : 2;
+                    float(&p)[4] = y[u][0], (&q)[4] = y[u][1];
+                    if (in_rot && type < 2) {
+                        if (apart) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float e = p[k], o = q[k];
+                                p[k] = fmaf(o, -w[k].y, e * w[k].x);
+                                q[k] = fmaf(e, w[k].y, o * w[k].x);
+                            }
                         } else {
-                            // rot / 2 is a multiple of 4: the four partners are one lane's
-                            const int pe = e >= half ? e - half : e + half;
-                            const int from = (pe >> 2) & 31;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                z[i] = __shfl_sync(~0u, x[u][0][i], from);
-                                if constexpr (ITS == 2) {
-                                    const float z1 = __shfl_sync(~0u, x[u][1][i], from);
-                                    if (pe >= 128) z[i] = z1;
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                float(&z)[4] = y[u][k >> 1];
+                                const float e = z[2 * (k & 1)], o = z[2 * (k & 1) + 1];
+                                z[2 * (k & 1)] = fmaf(o, -w[k].y, e * w[k].x);
+                                z[2 * (k & 1) + 1] = fmaf(e, w[k].y, o * w[k].x);
                             }
                         }
-                        const bool turn = e < rot;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bool second = a.x.interleaved ? (i & 1) : e >= half;
-                            const float s = second ? sn[it][i] : -sn[it][i];
-                            y[it][i] = turn ? fmaf(z[i], s, x[u][it][i] * cs[it][i]) : x[u][it][i];
-                        }
                     }
-                } else {
-#pragma unroll
-                    for (int it = 0; it < ITS; ++it)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) y[it][i] = x[u][it][i];
-                }
-                if (item < heads) {
-                    T *dst = (T *)a.x.q_out + t * a.x.q_out_token_stride + item * a.x.q_out_head_stride;
-#pragma unroll
-                    for (int it = 0; it < ITS; ++it) {
-                        const int e = 128 * it + 4 * lane;
-                        if (e < D) bq::store_n<E, 4>(dst + e, a.wide_o, y[it]);
+                    if (type == 0 && there) {
+                        T *dst = (T *)a.x.q_out + (uint64_t)(uint32_t)t * a.o_t + (uint64_t)(uint32_t)item * a.o_h;
+                        bq::store_n<E, 4>(dst + e0, a.wide_out, p);
+                        bq::store_n<E, 4>(dst + e1, a.wide_out, q);
                     }
-                    continue;
-                }
-                const bool is_k = item < heads + kv;
-                const long long at = row + (item - heads - (is_k ? 0 : kv)) * a.c.head_stride;
-                void *plane = is_k ? a.c.k : a.c.v;
-#pragma unroll
-                for (int it = 0; it < ITS; ++it) {
-                    const int e = 128 * it + 4 * lane;
+                    const bool keep = there && row >= 0 && (type == 1 || type == 2);
+                    const long long at = row + (long long)((uint64_t)(uint32_t)(item - heads - (type == 2 ? kv : 0)) * a.head_s);
+                    void *plane = type == 1 ? a.c.k : a.c.v;
                     if constexpr (CT == BQ_Q8_0) {
-                        float m = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) m = e < D ? fmaxf(m, fabsf(y[it][i])) : 0.0f;
-#pragma unroll
-                        for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-                        const __half d = __float2half_rn(__fdiv_rn(m, 127.0f));
-                        const float df = __half2float(d);
-                        uint32_t word = 0;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            int q = 0;
-                            if (df != 0.0f)
-                                q = (int)fminf(fmaxf(roundf(__fdiv_rn(y[it][i], df)), -127.0f), 127.0f);
-                            word |= (uint32_t)(q & 0xff) << (8 * i);
+                        if (item - sub + HPW <= heads) continue;  // only queries in this warp
+                        int f0 = e0, f1 = e1;  // where the quarters lie
+                        bool rows_of_8 = !apart;
+                        if (half % 32 && !a.x.interleaved) {  // rotated halves cut blocks: put in order
+                            float *mine = order_s + (warp * HPW + sub) * DMAX;
+                            __syncwarp();
+                            if (there) {
+                                *reinterpret_cast<float4 *>(mine + e0) = make_float4(p[0], p[1], p[2], p[3]);
+                                *reinterpret_cast<float4 *>(mine + e1) = make_float4(q[0], q[1], q[2], q[3]);
+                            }
+                            __syncwarp();
+                            f0 = 8 * i, f1 = 8 * i + 4, rows_of_8 = true;
+                            const float4 g0 = *reinterpret_cast<const float4 *>(mine + f0);
+                            const float4 g1 = *reinterpret_cast<const float4 *>(mine + f1);
+                            p[0] = g0.x, p[1] = g0.y, p[2] = g0.z, p[3] = g0.w;
+                            q[0] = g1.x, q[1] = g1.y, q[2] = g1.z, q[3] = g1.w;
                         }
-                        if (e < D) {
-                            *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + e) = word;
-                            if ((lane & 7) == 0)
-                                ((__half *)(is_k ? a.c.k_scale : a.c.v_scale))[(at + e) >> 5] = d;
+                        float m0 = 0.0f, m1 = 0.0f;
+                        if (there) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) m0 = fmaxf(m0, fabsf(p[k])), m1 = fmaxf(m1, fabsf(q[k]));
                         }
-                    } else {
+                        if (rows_of_8) m0 = m1 = fmaxf(m0, m1);
+#pragma unroll
+                        for (int o = 1; o < 4; o <<= 1) {
+                            m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, o));
+                            m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, o));
+                        }
+                        const float n0 = __shfl_xor_sync(~0u, m0, 4), n1 = __shfl_xor_sync(~0u, m1, 4);
+                        if (!rows_of_8) m0 = fmaxf(m0, n0), m1 = fmaxf(m1, n1);
+                        if (keep) {
+                            __half *scales = (__half *)(type == 1 ? a.c.k_scale : a.c.v_scale);
+                            auto quantize = [&](const float(&z)[4], float m, int f, bool writes_scale) {
+                                const __half d = __float2half_rn(__fdiv_rn(m, 127.0f));
+                                const float df = __half2float(d);
+                                uint32_t word = 0;
+                                if (df != 0.0f) {
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const int c =
+                                            (int)fminf(fmaxf(roundf(__fdiv_rn(z[k], df)), -127.0f), 127.0f);
+                                        word |= (uint32_t)(c & 0xff) << (8 * k);
+                                    }
+                                }
+                                *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + f) = word;
+                                if (writes_scale) scales[(at + f) >> 5] = d;
+                            };
+                            quantize(p, m0, f0, (f0 & 31) == 0);
+                            quantize(q, m1, f1, (f1 & 31) == 0);
+                        }
+                    } else if (keep) {
                         using C = typename std::conditional<CT == BQ_F16, bq::F16, bq::BF16>::type;
-                        if (e < D) bq::store_n<C, 4>((typename C::T *)plane + at + e, true, y[it]);
+                        bq::store_wide<C, 4>((typename C::T *)plane + at + e0, p);
+                        bq::store_wide<C, 4>((typename C::T *)plane + at + e1, q);
                     }
                 }
             }
@@ -234,9 +244,10 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const __grid_constant__
 
 template <class E, int CT>
 cudaError_t launch(const Args &a, int grid, void *stream) {
-    return a.c.head_dim <= 128
-               ? bq::launch_pdl(append_kernel<E, CT, 1>, dim3((unsigned)grid), THREADS, 0, stream, 1, a)
-               : bq::launch_pdl(append_kernel<E, CT, 2>, dim3((unsigned)grid), THREADS, 0, stream, 1, a);
+    auto *kern = a.c.head_dim <= 64    ? append_kernel<E, CT, 8>
+                 : a.c.head_dim <= 128 ? append_kernel<E, CT, 16>
+                                       : append_kernel<E, CT, 32>;
+    return bq::launch_pdl(kern, dim3((unsigned)grid), THREADS, 0, stream, 1, a);
 }
 template <class E>
 cudaError_t launch(const Args &a, int grid, void *stream) {
@@ -245,7 +256,7 @@ cudaError_t launch(const Args &a, int grid, void *stream) {
                                  : launch<E, BQ_Q8_0>(a, grid, stream);
 }
 
-bool stride_ok(int64_t s) { return s >= 0 && s <= (1LL << 40); }
+bool stride_ok(int64_t s) { return s >= 0 && s <= 0x7fffffffLL; }
 
 }  // namespace
 
@@ -282,7 +293,7 @@ extern "C" bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_a
             if (!stride_ok(v)) return BQ_ERR_SHAPE;
     }
     if (x->freq) {
-        if (x->rot < 8 || x->rot % 8 || x->rot > cache->head_dim || x->axes < 1 || x->axes > 3 ||
+        if (x->rot < 16 || x->rot % 16 || x->rot > cache->head_dim || x->axes < 1 || x->axes > 3 ||
             !stride_ok(x->position_stride))
             return BQ_ERR_SHAPE;
         int64_t sum = 0;
@@ -311,18 +322,26 @@ extern "C" bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_a
     auto wide = [&](const void *p, int64_t t, int64_t h) {
         return bq::aligned_to(p, (uintptr_t)(4 * es)) && t % 4 == 0 && h % 4 == 0;
     };
-    a.wide_k = wide(x->k, x->k_token_stride, x->k_head_stride);
-    a.wide_v = wide(x->v, x->v_token_stride, x->v_head_stride);
-    a.wide_q = x->q && wide(x->q, x->q_token_stride, x->q_head_stride);
-    a.wide_o = x->q && wide(x->q_out, x->q_out_token_stride, x->q_out_head_stride);
-    // a warp for every head while that many warps fit the GPU, then fewer per token
-    const long long fit = (long long)sms * 32;
-    long long parts = (fit + x->tokens - 1) / x->tokens;
-    a.parts = (int)(parts < a.items ? parts : a.items);
-    long long warps = x->tokens * a.parts;
-    const long long most = fit > a.parts ? fit : a.parts;
-    if (warps > most) warps = most / a.parts * a.parts;
-    const int grid = (int)((warps + THREADS / 32 - 1) / (THREADS / 32));
+    a.wide = wide(x->k, x->k_token_stride, x->k_head_stride) && wide(x->v, x->v_token_stride, x->v_head_stride) &&
+             (!x->q || wide(x->q, x->q_token_stride, x->q_head_stride));
+    a.wide_out = x->q && wide(x->q_out, x->q_out_token_stride, x->q_out_head_stride);
+    a.q_t = (uint32_t)x->q_token_stride, a.q_h = (uint32_t)x->q_head_stride;
+    a.k_t = (uint32_t)x->k_token_stride, a.k_h = (uint32_t)x->k_head_stride;
+    a.v_t = (uint32_t)x->v_token_stride, a.v_h = (uint32_t)x->v_head_stride;
+    a.o_t = (uint32_t)x->q_out_token_stride, a.o_h = (uint32_t)x->q_out_head_stride;
+    a.page_s = (uint32_t)cache->page_stride, a.head_s = (uint32_t)cache->head_stride;
+    a.slot_s = (uint32_t)cache->slot_stride;
+    // Few tokens: a warp for every head, the heads of a token over several CTAs.
+    // Many: one CTA for a token's heads, then several tokens per CTA.
+    const long long fit = (long long)sms * 3;
+    const int heads_at_once = WARPS * (cache->head_dim <= 64 ? 4 : cache->head_dim <= 128 ? 2 : 1);
+    const int most_parts = (a.items + heads_at_once - 1) / heads_at_once;
+    const long long parts = fit / x->tokens;
+    a.parts = parts < 1 ? 1 : parts > most_parts ? most_parts : (int)parts;
+    const long long each = (x->tokens + 4 * fit - 1) / (4 * fit);
+    a.batch = each < 1 ? 1 : each > MAX_BATCH ? MAX_BATCH : (int)each;
+    const long long groups = (x->tokens + a.batch - 1) / a.batch;
+    const int grid = (int)(groups < 4 * fit ? groups : 4 * fit) * a.parts;
     return bq::from_cuda_error(x->dtype == BQ_F32   ? launch<bq::F32>(a, grid, stream)
                                : x->dtype == BQ_F16 ? launch<bq::F16>(a, grid, stream)
                                                     : launch<bq::BF16>(a, grid, stream));

@@ -26,7 +26,7 @@ cudaError_t status_address(unsigned int **out) {
     return cudaSuccess;
 }
 
-constexpr int JOIN_THREADS = 128;
+constexpr int JOIN_THREADS = 256;
 
 // Joins a request's chunks: one CTA per query row and head.  Chunk i's weight
 // is 2^(m_i - max m); the chunks are taken by thread groups of D / 4 lanes in a
@@ -71,13 +71,13 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     sum = 0.0f;
     for (int w = 0; w < JOIN_THREADS / 32; ++w) sum += red[1][w];
 
-    const int vecs = D / 4, groups = JOIN_THREADS / vecs;  // D <= 256: at least two groups
+    const int vecs = D / 4, groups = JOIN_THREADS / vecs;  // D <= 256: at least four groups
     const int gr = tid / vecs, v = tid - gr * vecs;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (gr < groups) {
         const float *src = a.part_o + (unit0 * tile_rows + i) * D + 4 * v;
         const long long hop = step * tile_rows * D;
-#pragma unroll 4
+#pragma unroll 8
         for (int k = gr; k < chunks; k += groups) {
             const float4 o = *reinterpret_cast<const float4 *>(src + k * hop);
             const float f = w_s[k];
@@ -151,7 +151,7 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     // reads the cache again
     const int nt = a.group_rows <= 8 ? 1 : a.group_rows <= 16 || dim == 256 ? 2 : 4;
     a.row_tiles = (a.group_rows + 8 * nt - 1) / (8 * nt);
-    const int own = c->type == BQ_Q8_0 ? BQ_BF16 : c->type;  // the type that the tensor cores multiply
+    const int own = c->type == BQ_Q8_0 ? BQ_F16 : c->type;  // the type that the tensor cores multiply
     const int parts = x->dtype == own ? 1 : 2;
     int n = 0;
     const bq::AttnInstance *inst =

@@ -16,9 +16,9 @@
 // kernel is built around the loads:
 //  - Every warp has a ring of STAGES tiles of K and V rows in shared memory
 //    that it fills itself by 16-byte asynchronous copies (any page size and
-//    stride; what is not there is filled with zeros), two tiles ahead of the
-//    one it works on: 16 KB in flight per warp, 128 KB per SM, with no barrier
-//    between warps.  Rows are swizzled by 16-byte pieces, so that every read of
+//    stride; what is not there is filled with zeros), STAGES - 1 tiles ahead of
+//    the one it works on: about 16 KB in flight per warp, 128 KB per SM, with no
+//    barrier between warps.  Rows are swizzled by 16-byte pieces, so that every read of
 //    a matrix operand is free of bank conflicts.
 //  - S^T = K Q^T has positions as rows and is summed over d; O^T = V^T P^T has d
 //    as rows and is summed over positions, V read with ldmatrix's transpose.
@@ -35,8 +35,8 @@
 // the output's own rounding stays the largest error).  Each tile's products
 // are summed by the tensor core from zero, smallest parts first, and added to
 // the fp32 accumulator by an fp32 FMA, since the tensor core truncates its sums.
-// Q8_0 codes are exact in bf16; a key's scale multiplies its block's partial
-// score, a value's scale its weight, both in fp32.
+// Q8_0 codes are exact in fp16; a key's scale multiplies its block's partial
+// score, a value's scale its weight, both in fp32 before any rounding to parts.
 #pragma once
 
 #include <cmath>
@@ -88,18 +88,28 @@ __device__ __forceinline__ uint4 ldmatrix4_trans(uint32_t at) {
     return v;
 }
 
-template <bool HALF>
+// d = a b + d on the tensor cores; FROM_ZERO: d = a b
+template <bool HALF, bool FROM_ZERO = false>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    const float c0 = FROM_ZERO ? 0.0f : d[0], c1 = FROM_ZERO ? 0.0f : d[1], c2 = FROM_ZERO ? 0.0f : d[2],
+                c3 = FROM_ZERO ? 0.0f : d[3];
     if constexpr (HALF)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
     else
         asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-            "{%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+            "{%10,%11,%12,%13};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// 2^x by the hardware's approximation (2 ulp; below 2^-126: 0)
+__device__ __forceinline__ float pow2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
@@ -134,57 +144,69 @@ __device__ __forceinline__ Words<PARTS> split_pair(float x, float y) {
     return o;
 }
 
-// four int8 codes as two pairs of bf16.  With b = code mod 256 and the
-// exponent byte 0x43, 0x4300 | (b & 127) is 128 + (b & 127) and 0x4300 | (b &
-// 128) is 128 or 256, both whole numbers that bf16 holds; their difference is
-// the code, exact.
-__device__ __forceinline__ uint2 codes_to_bf16(uint32_t w) {
+// Four int8 codes as two pairs of fp16.  With b = code + 128 (the sign bit
+// turned) 0x6400 | b is 1024 + b, a whole number that fp16 holds; less 1152 it
+// is the code, exact.
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
     uint2 o;
-    const uint32_t lo = __byte_perm(w, 0x43434343u, 0x4140), hi = __byte_perm(w, 0x43434343u, 0x4342);
-    const uint32_t la = lo & 0xff7fff7fu, lb = lo & 0xff80ff80u;
-    const uint32_t ha = hi & 0xff7fff7fu, hb = hi & 0xff80ff80u;
-    asm("sub.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(la), "r"(lb));
-    asm("sub.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(ha), "r"(hb));
+    w ^= 0x80808080u;
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(o.x) : "r"(lo), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(o.y) : "r"(hi), "r"(0x64806480u));
     return o;
 }
 
 template <int KV, int QP, int PP, int DP, int NT>
 struct AttnShape {
-    static constexpr bool Q8 = KV == KV_Q8, HALF = KV == KV_F16;
+    static constexpr bool Q8 = KV == KV_Q8, HALF = KV != KV_BF16;
     static constexpr int ROWS = 8 * NT;
-    // positions per tile: 8 KB of K and V per stage (16 KB with heads of 256)
-    static constexpr int TT = NT > 2 ? 1 : Q8 ? (DP <= 128 ? 2 : 1) : (DP <= 64 ? 2 : 1);
-    static constexpr int TILE = 16 * TT;
+    static constexpr int WARPS = ATTN_WARPS;
+    // 16 positions per tile (32 of the short rows) whatever NT: the order of the sums, and so a row's
+    // bits, must not depend on how many rows are computed beside it
+    static constexpr int TT = DP <= 64 ? 2 : 1, TILE = 16 * TT;
     static constexpr int ROWB = Q8 ? DP : 2 * DP;  // bytes of a row in the ring
-    static constexpr int SCALEB = Q8 ? (DP / 32 + 1) / 2 * 4 + (DP <= 32 ? 4 : 0) : 0;  // words of a row's scales
+    static constexpr int SCALEB = Q8 ? (DP / 32 + 1) / 2 * 4 : 0;  // words of a row's scales
     static constexpr int STAGE = 2 * TILE * (ROWB + SCALEB) + 4 * TILE;
-    static constexpr int FIT = (24 * 1024 + 1024) / STAGE;
-    static constexpr int STAGES = FIT < 3 ? 3 : FIT > 6 ? 6 : FIT;
+    static constexpr int OROW = DP + 4;  // floats: 8 lanes r and 4 row pairs c in 32 banks
     // query rows: 16 bytes apart modulo 128 for ldmatrix; 64 for the Q8_0 order,
     // where 8 lanes read 16-byte pieces of 2 rows
     static constexpr int QROW = 2 * DP + (Q8 ? 64 : 16);
-    static constexpr int OROW = DP + 4;  // floats: 8 lanes r and 4 row pairs c in 32 banks
     static constexpr int Q_BYTES = QP * ROWS * QROW;
-    static constexpr int RING = STAGES * STAGE;  // per warp; holds its O for the join afterwards
-    static_assert(RING >= ROWS * OROW * 4 && RING % 16 == 0 && STAGE % 16 == 0);
-    static constexpr int SMEM = ATTN_WARPS * RING + Q_BYTES + (2 * ATTN_WARPS + 1) * ROWS * 4;
-    static constexpr int OCC = SMEM <= 112 * 1024 ? 2 : 1;
+    // a warp's ring holds its O for the join once its tiles are done
+    static constexpr int ring_of(int stages) {
+        return stages * STAGE > ROWS * OROW * 4 ? stages * STAGE : ROWS * OROW * 4;
+    }
+    static constexpr int smem_of(int stages) {
+        return WARPS * ring_of(stages) + Q_BYTES + (2 * WARPS + 1) * ROWS * 4;
+    }
+    static constexpr int most_stages(int limit) {
+        int n = 6;
+        while (n > 1 && smem_of(n) > limit) --n;
+        return n;
+    }
+    // two CTAs per SM where two stages fit (the scan of 1024 requests besides),
+    // else one, with the scan of the most requests
+    static constexpr int OCC = most_stages(108 * 1024) >= 2 ? 2 : 1;
+    static constexpr int STAGES = most_stages(OCC == 2 ? 108 * 1024 : 209 * 1024);
+    static constexpr int RING = ring_of(STAGES), SMEM = smem_of(STAGES);
+    static_assert(STAGES >= 2 && RING % 16 == 0 && STAGE % 16 == 0 && TILE > BQ_VERIFY_MAX_ROWS);
 };
 
 template <int KV, int QP, int PP, int DP, int NT>
-__global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>::OCC)
+__global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, AttnShape<KV, QP, PP, DP, NT>::OCC)
     attn_kernel(const __grid_constant__ AttnArgs a, unsigned int *status) {
     using S = AttnShape<KV, QP, PP, DP, NT>;
     constexpr bool Q8 = S::Q8, HALF = S::HALF;
     constexpr int TT = S::TT, ROWS = S::ROWS, TILE = S::TILE, STAGES = S::STAGES, ROWB = S::ROWB;
+    constexpr int WARPS = S::WARPS;
     constexpr int MT = DP / 16;  // 16-row tiles of O^T
     constexpr float SHIFT = HALF ? (float)ATTN_SHIFT_F16 : 0.0f;
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t *q_s = smem + ATTN_WARPS * S::RING;
-    float *m_s = reinterpret_cast<float *>(q_s + S::Q_BYTES), *l_s = m_s + ATTN_WARPS * ROWS;
-    float *f_s = l_s + ATTN_WARPS * ROWS;            // per row: factor of its scores
+    uint8_t *q_s = smem + WARPS * S::RING;
+    float *m_s = reinterpret_cast<float *>(q_s + S::Q_BYTES), *l_s = m_s + WARPS * ROWS;
+    float *f_s = l_s + WARPS * ROWS;            // per row: factor of its scores
     int *pre = reinterpret_cast<int *>(f_s + ROWS);  // [requests + 1]
-    __shared__ int scan_s[ATTN_WARPS];
+    __shared__ int scan_s[WARPS];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, r = lane >> 2, c = lane & 3;
     uint8_t *ring = smem + warp * S::RING;
@@ -196,7 +218,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
     auto length = [&](int b) { return min(max(a.x.lens[b], 0), most); };
     // exclusive prefix sums of the requests' units
     {
-        const int per = (B + ATTN_WARPS * 32 - 1) / (ATTN_WARPS * 32);
+        const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
         const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
         int n = 0;
         for (int b = b0; b < b1; ++b) {
@@ -300,7 +322,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
             }
         };
 
-        const int stride = ATTN_WARPS * TILE;
+        const int stride = WARPS * TILE;
         int tile = begin + warp * TILE;
         int ahead = tile;  // the next tile to fetch
         int entry = entry_of(ahead + mine);
@@ -316,7 +338,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
         }
 
         // ---- queries: fp32 -> 16-bit parts in shared memory ----
-        for (int i = warp; i < ROWS; i += ATTN_WARPS) {
+        for (int i = warp; i < ROWS; i += WARPS) {
             const int g = first_row + i;
             float x[DP / 32];
             float top = 0.0f;
@@ -386,6 +408,12 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                 for (int x = 0; x < 4; ++x) O[v][nt][x] = 0.0f;
         }
 
+        // Q8_0: a weight times its value's scale goes into fp16.  It is divided by
+        // 2^vexp, which bounds the scales seen so far from above, and so is O; a
+        // larger scale than before rescales O along with alpha.  -14: fp16's least
+        // normal exponent.  vend: the same per query row after the last tile.
+        [[maybe_unused]] int vexp = -14, vend[NT][2];
+        [[maybe_unused]] bool ended = false;
         for (int st = 0; tile < end; tile += stride, st = st + 1 == STAGES ? 0 : st + 1) {
             copies_wait<STAGES - 2>();  // this tile's copies have landed,
             __syncwarp();               // every lane's, and every lane is done with the tile before
@@ -436,8 +464,8 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                             const int key = ((r & 3) << 1 | (r >> 2 & 1)) & (ROWB / 16 - 1);
                             const uint2 w = *reinterpret_cast<const uint2 *>(
                                 k_s + row * ROWB + (((2 * j + (c >> 1)) ^ key) << 4) + 8 * (c & 1));
-                            f[y] = codes_to_bf16(w.x);
-                            g[y] = codes_to_bf16(w.y);
+                            f[y] = codes_to_f16(w.x);
+                            g[y] = codes_to_f16(w.y);
                             d[s][y] = 32 * j < D ? scale_of(ks_s, s, y, j) : 0.0f;
                         }
                         lo[s] = make_uint4(f[0].x, f[1].x, f[0].y, f[1].y);
@@ -452,8 +480,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                                 q_s + (p * ROWS + 8 * nt + r) * S::QROW + 16 * (c + 4 * j));
 #pragma unroll
                             for (int s = 0; s < TT; ++s) {
-                                t[s][p][0] = t[s][p][1] = t[s][p][2] = t[s][p][3] = 0.0f;
-                                mma16816<HALF>(t[s][p], lo[s], q.x, q.y);
+                                mma16816<HALF, true>(t[s][p], lo[s], q.x, q.y);
                                 mma16816<HALF>(t[s][p], hi[s], q.z, q.w);
                             }
                         }
@@ -471,16 +498,6 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
             } else {
                 // a sum per part and parity of the step: short chains, added smallest first
                 float t[2][QP][TT][NT][4];
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int p = 0; p < QP; ++p)
-#pragma unroll
-                        for (int s = 0; s < TT; ++s)
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int x = 0; x < 4; ++x) t[e][p][s][nt][x] = 0.0f;
                 const int krow = (lane & 7) + (lane >> 3 & 1) * 8;
                 const uint32_t k_at = smem_address(k_s) + krow * ROWB;
                 const uint32_t q_at = smem_address(q_s) + (lane & 7) * S::QROW + (lane >> 3) * 16;
@@ -499,8 +516,13 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                             const uint4 q = ldmatrix4(q_at + (p * ROWS + 8 * nt) * S::QROW + 64 * j);
 #pragma unroll
                             for (int s = 0; s < TT; ++s) {
-                                mma16816<HALF>(t[0][p][s][nt], k0[s], q.x, q.y);
-                                mma16816<HALF>(t[1][p][s][nt], k1[s], q.z, q.w);
+                                if (j == 0) {
+                                    mma16816<HALF, true>(t[0][p][s][nt], k0[s], q.x, q.y);
+                                    mma16816<HALF, true>(t[1][p][s][nt], k1[s], q.z, q.w);
+                                } else {
+                                    mma16816<HALF>(t[0][p][s][nt], k0[s], q.x, q.y);
+                                    mma16816<HALF>(t[1][p][s][nt], k1[s], q.z, q.w);
+                                }
                             }
                         }
                 }
@@ -539,7 +561,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                     const float now = fmaxf(m[nt][x], top);
                     // nothing seen yet: any finite reference will do, the weights are 0
                     const float ref = now == -INFINITY ? 0.0f : now;
-                    alpha[nt][x] = exp2f(m[nt][x] - ref);
+                    alpha[nt][x] = pow2(m[nt][x] - ref);
                     m[nt][x] = now;
                     float sum = 0.0f;
 #pragma unroll
@@ -547,7 +569,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
                             float &v = sc[s][nt][2 * y + x];
-                            v = exp2f(v - ref + SHIFT);
+                            v = pow2(v - ref + SHIFT);
                             sum += v;
                         }
                     l[nt][x] = fmaf(l[nt][x], alpha[nt][x], sum);
@@ -568,6 +590,37 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                             const int t = tile + 16 * s + 8 * y + 2 * c;
                             keep[s][y] = (t < n ? 0xffffu : 0u) | (t + 1 < n ? 0xffff0000u : 0u);
                         }
+                }
+                [[maybe_unused]] float unscale = 1.0f, vshrink = 1.0f;
+                if constexpr (Q8) {
+                    float top = 0.0f;
+#pragma unroll
+                    for (int s = 0; s < TT; ++s)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+#pragma unroll
+                            for (int i = 0; i < (DP + 127) / 128; ++i) {
+                                const int j = 4 * i + c;  // lanes c of a position: every fourth scale
+                                if (32 * j < D && (!MIXED || tile + 16 * s + 8 * y + r < n)) {
+                                    const float d = fabsf(scale_of(vs_s, s, y, j));
+                                    if (d <= 65504.0f) top = fmaxf(top, d);
+                                }
+                            }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                    const int now = max(vexp, (int)(__float_as_uint(top) >> 23) - 126);  // 2^now > top
+                    vshrink = pow2((float)(vexp - now));
+                    unscale = pow2((float)-now);
+                    if constexpr (!MIXED) {
+                        vexp = now;
+                    } else {  // this warp's last tile
+                        ended = true;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                if (lim[nt][x] == n) vend[nt][x] = now;
+                    }
                 }
                 uint32_t pf[TT][NT][PP][2];
                 auto weights = [&](auto scale) {
@@ -594,7 +647,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                     if constexpr (Q8) {
                         if (mt % 2 == 0) {
                             const int v = mt / 2;
-                            weights([&](int s, int y) { return 32 * v < D ? scale_of(vs_s, s, y, v) : 0.0f; });
+                            weights([&](int s, int y) { return 32 * v < D ? scale_of(vs_s, s, y, v) * unscale : 0.0f; });
 #pragma unroll
                             for (int s = 0; s < TT; ++s)
 #pragma unroll
@@ -603,7 +656,7 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                                     const int key = (in & 7) & (ROWB / 16 - 1);
                                     const uint32_t w = *reinterpret_cast<const uint32_t *>(
                                         v_s + (16 * s + in) * ROWB + (((2 * v + (r >> 2)) ^ key) << 4) + 4 * (r & 3));
-                                    vb[s][x] = codes_to_bf16(w);
+                                    vb[s][x] = codes_to_f16(w);
                                 }
                         }
 #pragma unroll
@@ -630,24 +683,29 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                     }
                     float t[NT][4];
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) t[nt][0] = t[nt][1] = t[nt][2] = t[nt][3] = 0.0f;
-#pragma unroll
                     for (int p = PP - 1; p >= 0; --p)
 #pragma unroll
                         for (int s = 0; s < TT; ++s)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma16816<HALF>(t[nt], A[s], pf[s][nt][p][0], pf[s][nt][p][1]);
+                            for (int nt = 0; nt < NT; ++nt) {
+                                if (p == PP - 1 && s == 0)
+                                    mma16816<HALF, true>(t[nt], A[s], pf[s][nt][p][0], pf[s][nt][p][1]);
+                                else
+                                    mma16816<HALF>(t[nt], A[s], pf[s][nt][p][0], pf[s][nt][p][1]);
+                            }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             if (!MIXED || lim[nt][x & 1] == n)
-                                O[mt][nt][x] = fmaf(O[mt][nt][x], alpha[nt][x & 1], t[nt][x]);
+                                O[mt][nt][x] =
+                                    fmaf(O[mt][nt][x], Q8 ? alpha[nt][x & 1] * vshrink : alpha[nt][x & 1], t[nt][x]);
                 }
             };
             // A query row's own later positions carry weight 0, but 0 times a draft
             // token's NaN is NaN: a tile with positions that some rows do not see is
-            // done token by token.
+            // done token by token.  It is the last one of its warp: the new tokens lie
+            // within two tiles, which belong to two warps.
             if (R > 1 && tile + TILE > len - R + 1) {
                 for (int row = R - 1; row >= 0; --row) values(std::true_type{}, row);
             } else {
@@ -670,34 +728,35 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
                     m_s[warp * ROWS + 8 * nt + 2 * c + x] = m[nt][x];
                     l_s[warp * ROWS + 8 * nt + 2 * c + x] = v;
                 }
+                const float back = Q8 ? pow2((float)(ended ? vend[nt][x] : vexp)) : 1.0f;
                 float *dst = reinterpret_cast<float *>(ring) + (8 * nt + 2 * c + x) * S::OROW;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     const int d0 = Q8 ? 32 * (mt / 2) + 4 * r + 2 * (mt % 2) : 16 * mt + r;
-                    dst[d0] = O[mt][nt][x];
-                    dst[d0 + (Q8 ? 1 : 8)] = O[mt][nt][x + 2];
+                    dst[d0] = Q8 ? O[mt][nt][x] * back : O[mt][nt][x];
+                    dst[d0 + (Q8 ? 1 : 8)] = Q8 ? O[mt][nt][x + 2] * back : O[mt][nt][x + 2];
                 }
             }
         __syncthreads();
         const bool whole = pre[b + 1] - pre[b] == 1;  // one unit: the result itself
         const long long unit = (((long long)b * a.max_chunks + ck) * KVH + h) * a.row_tiles + rt;
-        for (int i = warp; i < ROWS; i += ATTN_WARPS) {
+        for (int i = warp; i < ROWS; i += WARPS) {
             const int g = first_row + i;
             if (g >= a.group_rows) break;
             float top = m_s[i];
 #pragma unroll
-            for (int w = 1; w < ATTN_WARPS; ++w) top = fmaxf(top, m_s[w * ROWS + i]);
-            float sum = 0.0f, f[ATTN_WARPS];
+            for (int w = 1; w < WARPS; ++w) top = fmaxf(top, m_s[w * ROWS + i]);
+            float sum = 0.0f, f[WARPS];
 #pragma unroll
-            for (int w = 0; w < ATTN_WARPS; ++w) {
+            for (int w = 0; w < WARPS; ++w) {
                 const float mw = m_s[w * ROWS + i];
-                f[w] = mw == -INFINITY ? 0.0f : exp2f(mw - top);
+                f[w] = mw == -INFINITY ? 0.0f : pow2(mw - top);
                 sum = fmaf(f[w], l_s[w * ROWS + i], sum);
             }
             auto joined = [&](int d) {
                 float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < ATTN_WARPS; ++w)
+                for (int w = 0; w < WARPS; ++w)
                     v = fmaf(f[w], reinterpret_cast<const float *>(smem + w * S::RING)[i * S::OROW + d], v);
                 return v;
             };
@@ -725,18 +784,24 @@ __global__ void __launch_bounds__(ATTN_WARPS * 32, AttnShape<KV, QP, PP, DP, NT>
 template <int KV, int QP, int PP, int DP, int NT>
 int attn_occupancy(size_t smem, int *out) {
     auto *kern = attn_kernel<KV, QP, PP, DP, NT>;
-    static std::atomic<int> set[64];
+    static std::atomic<unsigned long long> known[64];  // per device: smem << 8 | CTAs per SM
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return (int)e;
     if (dev < 0 || dev >= 64) return (int)cudaErrorInvalidDevice;
-    const int need = (int)(AttnShape<KV, QP, PP, DP, NT>::SMEM + (ATTN_MAX_REQUESTS + 1) * sizeof(int));
-    if (!set[dev].load()) {
+    const unsigned long long was = known[dev].load();
+    if (was >> 8 == smem) {
+        *out = (int)(was & 255);
+        return 0;
+    }
+    if (!was) {
+        const int need = (int)(AttnShape<KV, QP, PP, DP, NT>::SMEM + (ATTN_MAX_REQUESTS + 1) * sizeof(int));
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, need);
         if (e != cudaSuccess) return (int)e;
-        set[dev].store(1);
     }
-    return (int)cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kern, ATTN_WARPS * 32, smem);
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(out, kern, ATTN_WARPS * 32, smem);
+    if (e == cudaSuccess) known[dev].store((unsigned long long)smem << 8 | (unsigned)*out);
+    return (int)e;
 }
 
 }  // namespace bq
@@ -750,7 +815,7 @@ int attn_occupancy(size_t smem, int *out) {
             [](const bq::AttnArgs &a, int grid, size_t smem, void *stream,                         \
                unsigned int *status) -> cudaError_t {                                              \
                 return bq::launch_pdl(bq::attn_kernel<KV, QP, PP, DP, NT>, dim3((unsigned)grid),   \
-                                      bq::ATTN_WARPS * 32, smem, stream, 1, a, status);            \
+                                      bq::AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, smem, stream, 1, a, status);            \
             }                                                                                      \
     }
 #define BQ_ATTN_UNIT(NAME, KV, PARTS, QP, PP)                                                      \

@@ -58,7 +58,7 @@ inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-// element types of activations as template tags
+// element types of activations as template tags; two of a 16-bit type at a time
 struct F32 {
     using T = float;
     static __device__ __forceinline__ float up(float v) { return v; }
@@ -68,57 +68,90 @@ struct F16 {
     using T = __half;
     static __device__ __forceinline__ float up(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half down(float v) { return __float2half_rn(v); }
+    static __device__ __forceinline__ float2 up2(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    static __device__ __forceinline__ uint32_t down2(float x, float y) {
+        uint32_t w;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+        return w;
+    }
 };
 struct BF16 {
     using T = __nv_bfloat16;
     static __device__ __forceinline__ float up(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 down(float v) { return __float2bfloat16_rn(v); }
+    static __device__ __forceinline__ float2 up2(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t down2(float x, float y) {
+        uint32_t w;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(y), "f"(x));
+        return w;
+    }
 };
 
-// N consecutive elements; `wide`: the address is aligned to the N elements
+// N (4 or 8) consecutive elements by 16-byte (8-byte) accesses; the address is
+// aligned to 4 elements of a 16-bit type for N = 4, else to 16 bytes
 template <class E, int N>
-__device__ __forceinline__ void load_n(const typename E::T *p, bool wide, float (&out)[N]) {
-    typename E::T v[N];
-    constexpr int bytes = N * (int)sizeof(typename E::T);
-    if (wide) {
-        if constexpr (bytes == 4) {
-            *reinterpret_cast<uint32_t *>(v) = *reinterpret_cast<const uint32_t *>(p);
-        } else if constexpr (bytes == 8) {
-            *reinterpret_cast<uint2 *>(v) = *reinterpret_cast<const uint2 *>(p);
-        } else {
-            static_assert(bytes % 16 == 0);
+__device__ __forceinline__ void load_wide(const typename E::T *p, float (&out)[N]) {
+    if constexpr (sizeof(typename E::T) == 4) {
 #pragma unroll
-            for (int i = 0; i < bytes / 16; ++i)
-                reinterpret_cast<uint4 *>(v)[i] = reinterpret_cast<const uint4 *>(p)[i];
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 v = reinterpret_cast<const float4 *>(p)[i];
+            out[4 * i] = v.x, out[4 * i + 1] = v.y, out[4 * i + 2] = v.z, out[4 * i + 3] = v.w;
         }
     } else {
+        uint32_t w[N / 2];
+        if constexpr (N == 4) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p);
+            w[0] = v.x, w[1] = v.y;
+        } else {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p);
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+        }
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = p[i];
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 f = E::up2(w[i]);
+            out[2 * i] = f.x, out[2 * i + 1] = f.y;
+        }
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = E::up(v[i]);
 }
 
 template <class E, int N>
-__device__ __forceinline__ void store_n(typename E::T *p, bool wide, const float (&in)[N]) {
-    __align__(16) typename E::T v[N];
-    constexpr int bytes = N * (int)sizeof(typename E::T);
+__device__ __forceinline__ void store_wide(typename E::T *p, const float (&in)[N]) {
+    if constexpr (sizeof(typename E::T) == 4) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = E::down(in[i]);
+        for (int i = 0; i < N / 4; ++i)
+            reinterpret_cast<float4 *>(p)[i] = make_float4(in[4 * i], in[4 * i + 1], in[4 * i + 2], in[4 * i + 3]);
+    } else {
+        uint32_t w[N / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) w[i] = E::down2(in[2 * i], in[2 * i + 1]);
+        if constexpr (N == 4)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// the same, element by element unless `wide`
+template <class E, int N>
+__device__ __forceinline__ void load_n(const typename E::T *p, bool wide, float (&out)[N]) {
     if (wide) {
-        if constexpr (bytes == 4) {
-            *reinterpret_cast<uint32_t *>(p) = *reinterpret_cast<uint32_t *>(v);
-        } else if constexpr (bytes == 8) {
-            *reinterpret_cast<uint2 *>(p) = *reinterpret_cast<uint2 *>(v);
-        } else {
-            static_assert(bytes % 16 == 0);
-#pragma unroll
-            for (int i = 0; i < bytes / 16; ++i)
-                reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<uint4 *>(v)[i];
-        }
+        load_wide<E, N>(p, out);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) p[i] = v[i];
+        for (int i = 0; i < N; ++i) out[i] = E::up(p[i]);
+    }
+}
+template <class E, int N>
+__device__ __forceinline__ void store_n(typename E::T *p, bool wide, const float (&in)[N]) {
+    if (wide) {
+        store_wide<E, N>(p, in);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = E::down(in[i]);
     }
 }
 
@@ -140,7 +173,7 @@ inline bq_status check_cache_shape(const bq_kv_cache *c) {
     const int64_t mul = q8 ? c->head_dim : 8;
     const int64_t strides[3] = {c->page_stride, c->head_stride, c->slot_stride};
     for (int64_t s : strides)
-        if (s < 0 || s > (1LL << 40) || s % mul) return BQ_ERR_SHAPE;
+        if (s < 0 || s > 0x7fffffffLL || s % mul) return BQ_ERR_SHAPE;
     return BQ_OK;
 }
 inline bq_status check_cache_pointers(const bq_kv_cache *c) {

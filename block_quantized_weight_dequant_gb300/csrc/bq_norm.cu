@@ -3,11 +3,20 @@
 // include/bqgemv.h).
 //
 // A row is read once and kept in registers over both sums of squares: thread t
-// of N holds the 4-element vectors t, t + N, ...; N and the vectors per thread
+// of N holds the 8-element vectors t, t + N, ...; N and the vectors per thread
 // follow from the width alone, and so does the order of every sum (each
 // thread's vectors, a butterfly over the warp, the warps in order).  A row's
 // bits are the same whichever rows are computed beside it.  Bound by HBM for
 // many rows, by two block-wide sums and the launch for one.
+//
+// Three instances of the one kernel differ in how a row reaches the registers:
+//  ONCE   rows of whole aligned vectors, a CTA per row: direct loads.
+//  AHEAD  the same with more rows than CTAs: a thread copies its own vectors of
+//         the CTA's next row into shared memory (cp.async) before it works on
+//         the present one, so loads are in flight across the two sums; a thread
+//         reads only what it copied, so no barrier goes with it.
+//  RAGGED any width and alignment: rows pass through shared memory in both
+//         directions, so that global accesses stay coalesced.
 #include "bq_cache.cuh"
 
 #include <cmath>
@@ -18,8 +27,7 @@ constexpr int MAX_WIDTH = 16384;
 
 struct Args {
     bq_sandwich_args x;
-    int wide;  // 4-element accesses of the rows allowed
-    int wide_gain;
+    int wide;  // whole 16-byte vectors throughout
 };
 
 __device__ __forceinline__ float block_sum(float v, float *sm) {
@@ -33,109 +41,205 @@ __device__ __forceinline__ float block_sum(float v, float *sm) {
     return s;
 }
 
-template <class E, int N>
-__device__ __forceinline__ void load_part(const typename E::T *p, int at, int width, bool wide, float (&out)[N]) {
-    if (at + N <= width) {
-        bq::load_n<E, N>(p + at, wide, out);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) out[i] = at + i < width ? E::up(p[at + i]) : 0.0f;
-    }
-}
-template <class E, int N>
-__device__ __forceinline__ void store_part(typename E::T *p, int at, int width, bool wide, const float (&in)[N]) {
-    if (at + N <= width) {
-        bq::store_n<E, N>(p + at, wide, in);
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (at + i < width) p[at + i] = E::down(in[i]);
-    }
+// 8 elements to shared memory, asynchronously
+template <class E>
+__device__ __forceinline__ void copy8(typename E::T *dst, const typename E::T *src) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+    if constexpr (sizeof(typename E::T) == 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16), "l"(src + 4) : "memory");
 }
 
-template <class EY, class EH, int VPT>
-__global__ void sandwich_kernel(const __grid_constant__ Args a) {
+constexpr int MAX_THREADS = 512;
+enum { ONCE, AHEAD, RAGGED };
+
+template <class EY, class EH, int VPT, int MODE>
+__global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel(const __grid_constant__ Args a) {
     using TY = typename EY::T;
     using TH = typename EH::T;
+    extern __shared__ __align__(16) uint8_t rows_s[];
     __shared__ float sm[2][32];
-    const int width = (int)a.x.width, n = blockDim.x;
-    const bool wide = a.wide, wg = a.wide_gain;
+    const int width = (int)a.x.width, n = blockDim.x, tid = threadIdx.x;
+    const float inv_width = 1.0f / (float)width;
+    // AHEAD: two rows, h then y; RAGGED: one row of each in fp32, whole vectors
+    const int row_elems = n * VPT * 8;
+    TH *h_s = reinterpret_cast<TH *>(rows_s);
+    TY *y_s = reinterpret_cast<TY *>(rows_s + 2 * row_elems * sizeof(TH));
+    float *hf_s = reinterpret_cast<float *>(rows_s), *yf_s = hf_s + row_elems;
+    // this thread's vectors of a row
+    auto fetch = [&](long long row, int k) {
+        if (row < a.x.rows) {
+            const TY *y = (const TY *)a.x.y + row * a.x.y_stride;
+            const TH *h = (const TH *)a.x.h + row * a.x.h_stride;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int at = 8 * (tid + v * n);
+                if (at < width) {
+                    copy8<EY>(y_s + k * row_elems + at, y + at);
+                    copy8<EH>(h_s + k * row_elems + at, h + at);
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    // factors of this thread's elements, read by 16 bytes where the row is whole vectors
+    auto factor = [&](auto tag, const auto *p, int at, float(&g)[8]) {
+        using E = decltype(tag);
+        if constexpr (MODE != RAGGED) {
+            bq::load_wide<E, 8>(p + at, g);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = at + i < width ? E::up(p[at + i]) : 0.0f;
+        }
+    };
     bq::pdl_wait();
-    for (long long row = blockIdx.x; row < a.x.rows; row += gridDim.x) {
+    if constexpr (MODE == AHEAD) fetch(blockIdx.x, 0);
+    int k = 0;
+    for (long long row = blockIdx.x; row < a.x.rows; row += gridDim.x, k ^= 1) {
         const TY *y = (const TY *)a.x.y + row * a.x.y_stride;
         const TH *h = (const TH *)a.x.h + row * a.x.h_stride;
-        float b[VPT][4], r[VPT][4];
+        float b[VPT][8], r[VPT][8];
+        if constexpr (MODE == AHEAD) {
+            fetch(row + gridDim.x, k ^ 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        }
+        if constexpr (MODE == RAGGED) {
+            for (int i = tid; i < row_elems; i += n) {
+                yf_s[i] = i < width ? EY::up(y[i]) : 0.0f;
+                hf_s[i] = i < width ? EH::up(h[i]) : 0.0f;
+            }
+            __syncthreads();
+        }
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) load_part<EY, 4>(y, 4 * (threadIdx.x + v * n), width, wide, b[v]);
+        for (int v = 0; v < VPT; ++v) {
+            const int at = 8 * (tid + v * n);
+            if (MODE == RAGGED) {
+                bq::load_wide<bq::F32, 8>(yf_s + at, b[v]);
+                bq::load_wide<bq::F32, 8>(hf_s + at, r[v]);
+            } else if (at < width) {
+                bq::load_wide<EY, 8>(MODE == AHEAD ? y_s + k * row_elems + at : y + at, b[v]);
+                bq::load_wide<EH, 8>(MODE == AHEAD ? h_s + k * row_elems + at : h + at, r[v]);
+            } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) load_part<EH, 4>(h, 4 * (threadIdx.x + v * n), width, wide, r[v]);
+                for (int i = 0; i < 8; ++i) b[v][i] = r[v][i] = 0.0f;
+            }
+        }
         if (a.x.post) {
             float s = 0.0f;
 #pragma unroll
             for (int v = 0; v < VPT; ++v)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s = fmaf(b[v][i], b[v][i], s);
-            const float scale = rsqrtf(block_sum(s, sm[0]) / (float)width + a.x.eps);
+                for (int i = 0; i < 8; ++i) s = fmaf(b[v][i], b[v][i], s);
+            const float scale = rsqrtf(fmaf(block_sum(s, sm[0]), inv_width, a.x.eps));
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                float g[4];
-                load_part<bq::F32, 4>(a.x.post, 4 * (threadIdx.x + v * n), width, wg, g);
+                const int at = 8 * (tid + v * n);
+                if (at < width) {
+                    float g[8];
+                    factor(bq::F32{}, a.x.post, at, g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) b[v][i] = b[v][i] * scale * g[i];
+                    for (int i = 0; i < 8; ++i) b[v][i] *= scale * g[i];
+                }
             }
         }
         if (a.x.gate) {
             const TY *gate = (const TY *)a.x.gate + row * a.x.gate_stride;
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                float g[4];
-                load_part<EY, 4>(gate, 4 * (threadIdx.x + v * n), width, wide, g);
+                const int at = 8 * (tid + v * n);
+                if (at < width) {
+                    float g[8];
+                    factor(EY{}, gate, at, g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) b[v][i] *= g[i];
+                    for (int i = 0; i < 8; ++i) b[v][i] *= g[i];
+                }
             }
         }
         TH *ho = (TH *)a.x.h_out + row * a.x.h_out_stride;
         float s = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
+            const int at = 8 * (tid + v * n);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 r[v][i] = fmaf(a.x.alpha, r[v][i], a.x.beta * b[v][i]);
                 s = fmaf(r[v][i], r[v][i], s);
             }
-            store_part<EH, 4>(ho, 4 * (threadIdx.x + v * n), width, wide, r[v]);
+            if constexpr (MODE == RAGGED) bq::store_wide<bq::F32, 8>(hf_s + at, r[v]);
+            else if (at < width) bq::store_wide<EH, 8>(ho + at, r[v]);
         }
+        TY *x = (TY *)a.x.x + (a.x.x ? row * a.x.x_stride : 0);
         if (a.x.x) {
-            const float scale = rsqrtf(block_sum(s, sm[1]) / (float)width + a.x.eps);
-            TY *x = (TY *)a.x.x + row * a.x.x_stride;
+            const float scale = rsqrtf(fmaf(block_sum(s, sm[1]), inv_width, a.x.eps));
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
-                float g[4];
-                load_part<bq::F32, 4>(a.x.pre, 4 * (threadIdx.x + v * n), width, wg, g);
+                const int at = 8 * (tid + v * n);
+                if (at < width) {
+                    float g[8];
+                    factor(bq::F32{}, a.x.pre, at, g);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) g[i] = r[v][i] * scale * g[i];
-                store_part<EY, 4>(x, 4 * (threadIdx.x + v * n), width, wide, g);
+                    for (int i = 0; i < 8; ++i) g[i] *= r[v][i] * scale;
+                    if constexpr (MODE == RAGGED) bq::store_wide<bq::F32, 8>(yf_s + at, g);
+                    else bq::store_wide<EY, 8>(x + at, g);
+                }
             }
         }
-        // the next row's sums reuse sm: sm[0] is rewritten only after every warp
-        // has passed the barrier inside block_sum on sm[1], and the other way round
-        if (!(a.x.post && a.x.x)) __syncthreads();
+        if constexpr (MODE == RAGGED) {
+            __syncthreads();
+            for (int i = tid; i < width; i += n) {
+                ho[i] = EH::down(hf_s[i]);
+                if (a.x.x) x[i] = EY::down(yf_s[i]);
+            }
+            __syncthreads();
+        } else if (!(a.x.post && a.x.x)) {
+            // the next row's sums reuse sm: with both, sm[0] is rewritten only after every
+            // warp has passed the barrier inside block_sum on sm[1], and the other way round
+            __syncthreads();
+        }
     }
+}
+
+template <class EY, class EH, int VPT>
+cudaError_t launch_vpt(const Args &a, int threads, int sms, void *stream) {
+    const int elems = threads * VPT * 8;
+    const size_t ahead = (size_t)2 * elems * (sizeof(typename EY::T) + sizeof(typename EH::T));
+    const size_t ragged = (size_t)elems * 8;
+    if (!a.wide) {
+        const long long most = (long long)sms * (1024 / threads < 1 ? 1 : 1024 / threads);
+        auto *kern = sandwich_kernel<EY, EH, VPT, RAGGED>;
+        if (ragged > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       MAX_THREADS * VPT * 64);
+            if (e != cudaSuccess) return e;
+        }
+        return bq::launch_pdl(kern, dim3((unsigned)(a.x.rows < most ? a.x.rows : most)), threads, ragged, stream, 1,
+                              a);
+    }
+    // CTAs per SM: two rows of shared memory each, about 48 KB left to L1 for the gains
+    int fit = (int)(176 * 1024 / ahead);
+    if (fit > (VPT <= 2 ? 1024 : 512) / threads) fit = (VPT <= 2 ? 1024 : 512) / threads;
+    if (fit < 1) fit = 1;
+    const long long most = (long long)sms * fit;
+    if (a.x.rows <= most)
+        return bq::launch_pdl(sandwich_kernel<EY, EH, VPT, ONCE>, dim3((unsigned)a.x.rows), threads, 0, stream, 1, a);
+    auto *kern = sandwich_kernel<EY, EH, VPT, AHEAD>;
+    if (ahead > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   MAX_THREADS * VPT * 128);
+        if (e != cudaSuccess) return e;
+    }
+    return bq::launch_pdl(kern, dim3((unsigned)most), threads, ahead, stream, 1, a);
 }
 
 template <class EY, class EH>
 cudaError_t launch(const Args &a, int sms, void *stream) {
-    const int vecs = (int)((a.x.width + 3) / 4);
-    // vectors per thread: one up to 2048 values, two up to 4096, four beyond
-    const int vpt = vecs <= 512 ? 1 : vecs <= 1024 ? 2 : 4;
+    const int vecs = (int)((a.x.width + 7) / 8);
+    // vectors per thread: one up to 2048 values, two up to 8192, four beyond
+    const int vpt = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
     const int threads = ((vecs + vpt - 1) / vpt + 31) / 32 * 32;
-    long long grid = a.x.rows;
-    const long long most = (long long)sms * (2048 / threads);
-    if (grid > most) grid = most;
-    auto kern = vpt == 1   ? sandwich_kernel<EY, EH, 1>
-                : vpt == 2 ? sandwich_kernel<EY, EH, 2>
-                           : sandwich_kernel<EY, EH, 4>;
-    return bq::launch_pdl(kern, dim3((unsigned)grid), threads, 0, stream, 1, a);
+    return vpt == 1   ? launch_vpt<EY, EH, 1>(a, threads, sms, stream)
+           : vpt == 2 ? launch_vpt<EY, EH, 2>(a, threads, sms, stream)
+                      : launch_vpt<EY, EH, 4>(a, threads, sms, stream);
 }
 
 }  // namespace
@@ -147,7 +251,7 @@ extern "C" bq_status bq_sandwich_norm(const bq_sandwich_args *x, void *stream) {
     if (x->rows < 0 || x->rows > 0x7fffffffLL || x->width < 1 || x->width > MAX_WIDTH) return BQ_ERR_SHAPE;
     const int64_t strides[] = {x->y_stride, x->h_stride, x->gate_stride, x->h_out_stride, x->x_stride};
     for (int64_t s : strides)
-        if (s < 0 || s > (1LL << 40)) return BQ_ERR_SHAPE;
+        if (s < 0 || s > 0x7fffffffLL) return BQ_ERR_SHAPE;
     if (!(std::isfinite(x->eps) && x->eps >= 0.0f) || !std::isfinite(x->alpha) || !std::isfinite(x->beta))
         return BQ_ERR_SHAPE;
     if (x->rows == 0) return BQ_OK;
@@ -162,15 +266,13 @@ extern "C" bq_status bq_sandwich_norm(const bq_sandwich_args *x, void *stream) {
     if (!sms) return BQ_ERR_CUDA;
     Args a;
     a.x = *x;
-    a.wide = 1;
-    // rows of 4-element vectors: the base pointers and, with several rows, the strides
-    auto row_ok = [&](const void *p, int64_t stride, int es) {
-        return !p || (bq::aligned_to(p, (uintptr_t)(4 * es)) && (x->rows == 1 || stride % 4 == 0));
+    // rows of 8-element vectors: the base pointers and, with several rows, the strides
+    auto row_ok = [&](const void *p, int64_t stride) {
+        return bq::aligned_to(p, 16) && (x->rows == 1 || stride % 8 == 0);
     };
-    a.wide = row_ok(x->y, x->y_stride, ey) && row_ok(x->gate, x->gate_stride, ey) &&
-             row_ok(x->x, x->x_stride, ey) && row_ok(x->h, x->h_stride, eh) &&
-             row_ok(x->h_out, x->h_out_stride, eh);
-    a.wide_gain = bq::aligned_to(x->post, 16) && bq::aligned_to(x->pre, 16);
+    a.wide = x->width % 8 == 0 && row_ok(x->y, x->y_stride) && row_ok(x->gate, x->gate_stride) &&
+             row_ok(x->x, x->x_stride) && row_ok(x->h, x->h_stride) && row_ok(x->h_out, x->h_out_stride) &&
+             bq::aligned_to(x->post, 16) && bq::aligned_to(x->pre, 16);
     cudaError_t e;
     if (x->dtype == BQ_F32)
         e = launch<bq::F32, bq::F32>(a, sms, stream);

@@ -361,8 +361,8 @@ bq_status bq_stream_run_noalloc(int qtype, const bq_op *ops, int n_ops, void *st
  *
  * Conventions beyond those at the top of this file:
  *  - Activations may be fp32, fp16 or bf16 (bq_dtype).  The last dimension of
- *    every tensor is contiguous; the other strides are given in elements and
- *    are not negative.
+ *    every tensor is contiguous; the other strides are given in elements, not
+ *    negative and below 2^31.
  *  - Every call waits for the work before it on the stream before it reads or
  *    writes anything.
  *  - The structs are read by the call and need not outlive it.
@@ -454,7 +454,7 @@ bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream);
  *  - dtype: of k, v, q and q_out.  Their strides (token, head) are in
  *    elements.  q NULL: keys and values alone (q_out ignored).
  *  - freq: fp64 [rot / 2] or NULL (no rotation; rot, axes, sections ignored).
- *    rot % 8 == 0, 8 <= rot <= head_dim; 1 <= axes <= 3; the sections (not
+ *    rot % 16 == 0, 16 <= rot <= head_dim; 1 <= axes <= 3; the sections (not
  *    negative) sum to rot / 2; positions: int32 [axes, tokens], rows
  *    position_stride apart.
  *  - 0 <= tokens < 2^31, 1 <= heads <= 4096; heads ignored without q.
