@@ -6,8 +6,9 @@
 // maximum m' rescales what was summed by 2^(m - m') (all exponents in base 2,
 // the factor log2 e folded into scale).  The positions are cut into chunks of
 // a fixed length, each chunk's tiles are shared by four warps, and the partial
-// (m, l, O) are joined in a fixed order, by warps in shared memory and by
-// chunks in a second kernel.  Which chunks exist depends on the geometry and
+// (m, l, O) are joined in a fixed order: the warps' in shared memory, the
+// chunks' over a thread-block cluster where the table holds few of them (the
+// call is one launch), else in a second kernel.  Which chunks exist depends on the geometry and
 // the length alone, and an empty chunk joins with weight zero, so a row's bits
 // depend on its own inputs and the geometry only.
 //
@@ -30,9 +31,10 @@
 //    query rows per n-tile mma.sync's pipe is about a fifth busy at HBM speed.
 // Precision.  The tensor cores multiply 16-bit values exactly.  A query of
 // the cache's own type is used as it is; any other is split into QP 16-bit
-// parts (fp16: 2 parts, 22 bits, after scaling the row by a power of two; bf16:
-// 3 parts, 24 bits), the weights into PP parts (2 for 16-bit queries, so that
-// the output's own rounding stays the largest error).  Each tile's products
+// parts (fp16: 2 parts, 22 bits, after scaling the row by a power of two, which
+// lets a bf16 query through in one; bf16: 3 parts, 24 bits), the weights into PP
+// parts: 2 for 16-bit queries, so that the output's own rounding stays the
+// largest error, 1 where fp16 weights make a bf16 output (2^-12 beside 2^-9).  Each tile's products
 // are summed by the tensor core from zero, smallest parts first, and added to
 // the fp32 accumulator by an fp32 FMA, since the tensor core truncates its sums.
 // Q8_0 codes are exact in fp16; a key's scale multiplies its block's partial
@@ -156,14 +158,39 @@ __device__ __forceinline__ uint2 codes_to_f16(uint32_t w) {
     return o;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// a word of shared memory of another CTA of the cluster
+__device__ __forceinline__ float peer_float(uint32_t at, int rank) {
+    float v;
+    asm volatile(
+        "{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %1, %2;\n\tld.shared::cluster.f32 %0, [p];\n\t}"
+        : "=f"(v)
+        : "r"(at), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// element d of query row g (of the rows of kv head h) of request b
+__device__ __forceinline__ void attn_store(const AttnArgs &a, int b, int h, int g, int d, float v) {
+    const int row = (int)a.group.div((uint32_t)g);
+    const int head = h * (int)a.group.d + g - row * (int)a.group.d;
+    const long long at = ((long long)b * a.x.rows + row) * a.x.out_row_stride + head * a.x.out_head_stride + d;
+    if (a.x.dtype == BQ_F32) ((float *)a.x.out)[at] = v;
+    else if (a.x.dtype == BQ_F16) ((__half *)a.x.out)[at] = __float2half_rn(v);
+    else ((__nv_bfloat16 *)a.x.out)[at] = __float2bfloat16_rn(v);
+}
+
 template <int KV, int QP, int PP, int DP, int NT>
 struct AttnShape {
     static constexpr bool Q8 = KV == KV_Q8, HALF = KV != KV_BF16;
     static constexpr int ROWS = 8 * NT;
     static constexpr int WARPS = ATTN_WARPS;
-    // 16 positions per tile (32 of the short rows) whatever NT: the order of the sums, and so a row's
+    // 16 positions per tile (32 of short rows) whatever NT: the order of the sums, and so a row's
     // bits, must not depend on how many rows are computed beside it
-    static constexpr int TT = DP <= 64 ? 2 : 1, TILE = 16 * TT;
+    static constexpr int TT = DP <= 64 || (Q8 && DP <= 128) ? 2 : 1, TILE = 16 * TT;
     static constexpr int ROWB = Q8 ? DP : 2 * DP;  // bytes of a row in the ring
     static constexpr int SCALEB = Q8 ? (DP / 32 + 1) / 2 * 4 : 0;  // words of a row's scales
     static constexpr int STAGE = 2 * TILE * (ROWB + SCALEB) + 4 * TILE;
@@ -184,10 +211,14 @@ struct AttnShape {
         while (n > 1 && smem_of(n) > limit) --n;
         return n;
     }
-    // two CTAs per SM where two stages fit (the scan of 1024 requests besides),
-    // else one, with the scan of the most requests
-    static constexpr int OCC = most_stages(108 * 1024) >= 2 ? 2 : 1;
-    static constexpr int STAGES = most_stages(OCC == 2 ? 108 * 1024 : 209 * 1024);
+    // Two CTAs per SM where two stages fit (the scan of 1024 requests besides),
+    // else one, with the scan of the most requests.  Three with heads of up to 64
+    // and one n-tile (160 requests to 2500 positions: 34 us against 43; with heads
+    // of 128 and two stages left, 217 against 209 for 48 requests to 12001).
+    static constexpr int OCC = DP <= 64 && NT == 1 && most_stages(74 * 1024) >= 2 ? 3
+                               : most_stages(108 * 1024) >= 2                     ? 2
+                                                                                  : 1;
+    static constexpr int STAGES = most_stages(OCC == 3 ? 74 * 1024 : OCC == 2 ? 108 * 1024 : 209 * 1024);
     static constexpr int RING = ring_of(STAGES), SMEM = smem_of(STAGES);
     static_assert(STAGES >= 2 && RING % 16 == 0 && STAGE % 16 == 0 && TILE > BQ_VERIFY_MAX_ROWS);
 };
@@ -213,17 +244,24 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     const int B = a.x.requests, R = a.x.rows, D = a.c.head_dim, KVH = a.c.kv_heads;
     const int most = a.x.table_width * a.c.page_size;
     pdl_wait();
-    if (a.max_chunks > 1) pdl_launch_dependents();
+    if (a.max_chunks > 1 && !a.cluster) pdl_launch_dependents();
 
     auto length = [&](int b) { return min(max(a.x.lens[b], 0), most); };
-    // exclusive prefix sums of the requests' units
-    {
+    const long long per_chunk = (long long)KVH * a.row_tiles;
+    // DIRECT: a CTA per unit that the table can hold, units beyond a request's
+    // length are empty.  Else a CTA takes every gridDim.x-th live unit, which
+    // exclusive prefix sums of the requests' units tell.
+    const bool direct = a.direct;
+    auto checked = [&](int b) {
+        const int len = a.x.lens[b];
+        if (len < 0 || len > most) atomicOr(status, BQ_DEVERR_LENGTH);
+    };
+    if (!direct) {
         const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
         const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
         int n = 0;
         for (int b = b0; b < b1; ++b) {
-            const int len = a.x.lens[b];
-            if ((len < 0 || len > most) && blockIdx.x == 0) atomicOr(status, BQ_DEVERR_LENGTH);
+            if (blockIdx.x == 0) checked(b);
             n += attn_chunks(length(b), a.chunk);
         }
         int v = n;
@@ -243,27 +281,59 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         if (b0 < B && b1 == B) pre[B] = excl;
         __syncthreads();
     }
-    const long long per_chunk = (long long)KVH * a.row_tiles;
-    const long long units = pre[B] * per_chunk;
+    const long long units = direct ? gridDim.x : pre[B] * per_chunk;
 
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
-        const int cu = (int)(u / per_chunk), hr = (int)(u - cu * per_chunk);
-        const int h = hr / a.row_tiles, rt = hr - h * a.row_tiles;
-        int b = 0;
-        for (int hi = B; hi - b > 1;) {
-            const int mid = (b + hi) >> 1;
-            if (pre[mid] <= cu) b = mid;
-            else hi = mid;
+        int b = 0, hr, ck;
+        if (direct) {
+            const uint32_t rest = (uint32_t)u / (uint32_t)a.max_chunks;
+            ck = (int)((uint32_t)u - rest * (uint32_t)a.max_chunks);
+            b = (int)(rest / (uint32_t)per_chunk);
+            hr = (int)(rest - (uint32_t)b * (uint32_t)per_chunk);
+        } else {
+            const int cu = (int)(u / per_chunk);
+            hr = (int)(u - cu * per_chunk);
+            for (int hi = B; hi - b > 1;) {
+                const int mid = (b + hi) >> 1;
+                if (pre[mid] <= cu) b = mid;
+                else hi = mid;
+            }
+            ck = cu - pre[b];
         }
-        const int ck = cu - pre[b], len = length(b);
-        const int begin = ck * a.chunk, end = min(len, begin + a.chunk);
-        const int first_row = rt * ROWS;
+        const int h = hr / a.row_tiles, rt = hr - h * a.row_tiles;
+        const int begin = ck * a.chunk, first_row = rt * ROWS;
+
+        // ---- loads whose addresses do not wait for the length: table entries
+        // (there is one for every position of the table), queries ----
+        const int *row_table = a.x.table + b * a.x.table_stride;
+        const int mine = lane & (TILE - 1);  // the position of a tile that this lane looks up
+        const int chunk_end = min(begin + a.chunk, most);
+        auto entry_of = [&](int t) { return t < chunk_end ? row_table[a.page.div((uint32_t)t)] : -1; };
+        int entry = entry_of(begin + warp * TILE + mine);
+        float qx[ROWS / WARPS][DP / 32];
+#pragma unroll
+        for (int k = 0; k < ROWS / WARPS; ++k) {
+            const int g = first_row + warp + WARPS * k;
+            const int row = (int)a.group.div((uint32_t)g);
+            const int head = h * (int)a.group.d + g - row * (int)a.group.d;
+            const long long at = ((long long)b * R + row) * a.x.q_row_stride + head * a.x.q_head_stride;
+#pragma unroll
+            for (int e = 0; e < DP / 32; ++e) {
+                const int d = lane + 32 * e;
+                qx[k][e] = d >= D || g >= a.group_rows ? 0.0f
+                           : a.x.dtype == BQ_F32       ? ((const float *)a.x.q)[at + d]
+                           : a.x.dtype == BQ_F16       ? __half2float(((const __half *)a.x.q)[at + d])
+                                                       : __bfloat162float(((const __nv_bfloat16 *)a.x.q)[at + d]);
+            }
+        }
+        const int len = length(b), end = min(len, begin + a.chunk);
+        if (direct) {
+            if (ck == 0 && hr == 0 && tid == 0) checked(b);
+            if (!a.cluster && ck >= attn_chunks(len, a.chunk)) continue;
+        }
 
         // ---- the ring: tile `t0` of this warp into stage `st` ----
-        const int *row_table = a.x.table + b * a.x.table_stride;
         const long long head_off = (long long)h * a.c.head_stride;
-        const int mine = lane & (TILE - 1);  // the position of a tile that this lane looks up
-        auto entry_of = [&](int t) { return t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
         auto fill = [&](int t0, int entry, int st) {
             const int t = t0 + mine;
             long long off = -1;  // element offset, -1 where there is nothing to read
@@ -325,7 +395,6 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         const int stride = WARPS * TILE;
         int tile = begin + warp * TILE;
         int ahead = tile;  // the next tile to fetch
-        int entry = entry_of(ahead + mine);
 #pragma unroll
         for (int st = 0; st < STAGES - 1; ++st) {
             if (ahead < end) {
@@ -338,29 +407,15 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         }
 
         // ---- queries: fp32 -> 16-bit parts in shared memory ----
-        for (int i = warp; i < ROWS; i += WARPS) {
-            const int g = first_row + i;
-            float x[DP / 32];
+#pragma unroll
+        for (int k = 0; k < ROWS / WARPS; ++k) {
+            const int i = warp + WARPS * k;
+            float(&x)[DP / 32] = qx[k];
             float top = 0.0f;
-            if (g < a.group_rows) {
-                const int row = (int)a.group.div((uint32_t)g);
-                const int head = h * (int)a.group.d + g - row * (int)a.group.d;
-                const long long at = ((long long)b * R + row) * a.x.q_row_stride + head * a.x.q_head_stride;
 #pragma unroll
-                for (int e = 0; e < DP / 32; ++e) {
-                    const int d = lane + 32 * e;
-                    x[e] = d >= D ? 0.0f
-                           : a.x.dtype == BQ_F32 ? ((const float *)a.x.q)[at + d]
-                           : a.x.dtype == BQ_F16 ? __half2float(((const __half *)a.x.q)[at + d])
-                                                 : __bfloat162float(((const __nv_bfloat16 *)a.x.q)[at + d]);
-                    top = fmaxf(top, fabsf(x[e]));
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < DP / 32; ++e) x[e] = 0.0f;
-            }
+            for (int e = 0; e < DP / 32; ++e) top = fmaxf(top, fabsf(x[e]));
             float factor = a.scale_log2;
-            if constexpr (HALF && QP > 1) {
+            if constexpr (HALF && (QP > 1 || Q8)) {
                 // the largest of the row to [2^14, 2^15): the second part of anything
                 // down to 2^-29 of it is still a normal fp16 number
 #pragma unroll
@@ -435,11 +490,30 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
             for (int s = 0; s < TT; ++s)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) there[s][y] = meta[16 * s + 8 * y + r];
-            // the scale of 32 values of a position of this thread
-            [[maybe_unused]] auto scale_of = [&](const uint8_t *base, int s, int y, int j) {
-                const int odd = (D >> 5) % 2 ? max(there[s][y], 0) : 0;
-                return __half2float(
-                    *reinterpret_cast<const __half *>(base + (16 * s + 8 * y + r) * S::SCALEB + 2 * (j + odd)));
+            // Q8_0: the scales of this thread's positions, a word holds two; a row of an
+            // odd number of scales may start in the middle of a word
+            constexpr int SW = S::SCALEB / 4 > 0 ? S::SCALEB / 4 : 1;
+            [[maybe_unused]] auto scales_of = [&](const uint8_t *base, int s, int y, uint32_t(&w)[SW]) {
+                const uint8_t *at = base + (16 * s + 8 * y + r) * S::SCALEB;
+                if constexpr (SW % 2 == 0) {
+#pragma unroll
+                    for (int i = 0; i < SW / 2; ++i) {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(at + 8 * i);
+                        w[2 * i] = v.x, w[2 * i + 1] = v.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < SW; ++i) w[i] = *reinterpret_cast<const uint32_t *>(at + 4 * i);
+                }
+                if ((D >> 5) & 1) {
+                    const int shift = 16 * max(there[s][y], 0);
+#pragma unroll
+                    for (int i = 0; i < SW; ++i) w[i] = __funnelshift_r(w[i], i + 1 < SW ? w[i + 1] : 0u, shift);
+                    // (a word's last half is no scale of this row, and its values are 0)
+                }
+            };
+            [[maybe_unused]] auto scale = [](const uint32_t(&w)[SW], int j) {
+                return __half2float(__ushort_as_half((unsigned short)(w[j >> 1] >> (16 * (j & 1)))));
             };
 
             // ---- scores ----
@@ -451,6 +525,11 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) sc[s][nt][x] = 0.0f;
+                uint32_t kw[TT][2][SW];
+#pragma unroll
+                for (int s = 0; s < TT; ++s)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) scales_of(ks_s, s, y, kw[s][y]);
 #pragma unroll
                 for (int j = 0; j < DP / 32; ++j) {
                     uint4 lo[TT], hi[TT];  // the operand over the pieces' first and second 4 codes
@@ -466,7 +545,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                                 k_s + row * ROWB + (((2 * j + (c >> 1)) ^ key) << 4) + 8 * (c & 1));
                             f[y] = codes_to_f16(w.x);
                             g[y] = codes_to_f16(w.y);
-                            d[s][y] = 32 * j < D ? scale_of(ks_s, s, y, j) : 0.0f;
+                            d[s][y] = scale(kw[s][y], j);
                         }
                         lo[s] = make_uint4(f[0].x, f[1].x, f[0].y, f[1].y);
                         hi[s] = make_uint4(g[0].x, g[1].x, g[0].y, g[1].y);
@@ -592,23 +671,27 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                         }
                 }
                 [[maybe_unused]] float unscale = 1.0f, vshrink = 1.0f;
+                [[maybe_unused]] uint32_t vw[TT][2][SW];
                 if constexpr (Q8) {
-                    float top = 0.0f;
+                    uint32_t top = 0;  // of the finite scales' bits: ordered as the numbers
 #pragma unroll
                     for (int s = 0; s < TT; ++s)
 #pragma unroll
-                        for (int y = 0; y < 2; ++y)
+                        for (int y = 0; y < 2; ++y) {
+                            scales_of(vs_s, s, y, vw[s][y]);
+                            if (MIXED && tile + 16 * s + 8 * y + r >= n) {
 #pragma unroll
-                            for (int i = 0; i < (DP + 127) / 128; ++i) {
-                                const int j = 4 * i + c;  // lanes c of a position: every fourth scale
-                                if (32 * j < D && (!MIXED || tile + 16 * s + 8 * y + r < n)) {
-                                    const float d = fabsf(scale_of(vs_s, s, y, j));
-                                    if (d <= 65504.0f) top = fmaxf(top, d);
-                                }
+                                for (int i = 0; i < SW; ++i) vw[s][y][i] = 0;
                             }
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                    const int now = max(vexp, (int)(__float_as_uint(top) >> 23) - 126);  // 2^now > top
+                            for (int i = 0; i < SW; ++i) {
+                                const uint32_t lo = vw[s][y][i] & 0x7fffu, hi = vw[s][y][i] >> 16 & 0x7fffu;
+                                if (lo < 0x7c00u) top = max(top, lo);
+                                if (hi < 0x7c00u) top = max(top, hi);
+                            }
+                        }
+                    top = __reduce_max_sync(~0u, top);
+                    const int now = max(vexp, (int)(top >> 10) - 14);  // 2^now > top
                     vshrink = pow2((float)(vexp - now));
                     unscale = pow2((float)-now);
                     if constexpr (!MIXED) {
@@ -623,12 +706,12 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                     }
                 }
                 uint32_t pf[TT][NT][PP][2];
-                auto weights = [&](auto scale) {
+                auto weights = [&](auto factor) {
 #pragma unroll
                     for (int s = 0; s < TT; ++s)
 #pragma unroll
                         for (int y = 0; y < 2; ++y) {
-                            const float d = scale(s, y);
+                            const float d = factor(s, y);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 float x0 = sc[s][nt][2 * y], x1 = sc[s][nt][2 * y + 1];
@@ -647,7 +730,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                     if constexpr (Q8) {
                         if (mt % 2 == 0) {
                             const int v = mt / 2;
-                            weights([&](int s, int y) { return 32 * v < D ? scale_of(vs_s, s, y, v) * unscale : 0.0f; });
+                            weights([&](int s, int y) { return scale(vw[s][y], v) * unscale; });
 #pragma unroll
                             for (int s = 0; s < TT; ++s)
 #pragma unroll
@@ -738,7 +821,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                 }
             }
         __syncthreads();
-        const bool whole = pre[b + 1] - pre[b] == 1;  // one unit: the result itself
+        const int chunks = attn_chunks(len, a.chunk);
         const long long unit = (((long long)b * a.max_chunks + ck) * KVH + h) * a.row_tiles + rt;
         for (int i = warp; i < ROWS; i += WARPS) {
             const int g = first_row + i;
@@ -760,22 +843,46 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                     v = fmaf(f[w], reinterpret_cast<const float *>(smem + w * S::RING)[i * S::OROW + d], v);
                 return v;
             };
-            const int row = (int)a.group.div((uint32_t)g);
-            if (whole) {
-                const int head = h * (int)a.group.d + g - row * (int)a.group.d;
-                const long long at = ((long long)b * R + row) * a.x.out_row_stride + head * a.x.out_head_stride;
+            if (a.cluster) {  // this CTA's part of the join below, in warp 0's place
+                for (int d = lane; d < D; d += 32) reinterpret_cast<float *>(smem)[i * S::OROW + d] = joined(d);
+                __syncwarp();
+                if (lane == 0) m_s[i] = top, l_s[i] = sum;
+            } else if (chunks == 1) {  // the result itself
+                const int row = (int)a.group.div((uint32_t)g);
                 const bool empty = len - R + row + 1 <= 0;
-                for (int d = lane; d < D; d += 32) {
-                    const float v = empty ? 0.0f : joined(d) / sum;
-                    if (a.x.dtype == BQ_F32) ((float *)a.x.out)[at + d] = v;
-                    else if (a.x.dtype == BQ_F16) ((__half *)a.x.out)[at + d] = __float2half_rn(v);
-                    else ((__nv_bfloat16 *)a.x.out)[at + d] = __float2bfloat16_rn(v);
-                }
+                for (int d = lane; d < D; d += 32) attn_store(a, b, h, g, d, empty ? 0.0f : joined(d) / sum);
             } else {
                 if (lane == 0) a.part_ml[unit * ROWS + i] = make_float2(top, sum);
                 float *dst = a.part_o + (unit * ROWS + i) * D;
                 for (int d = lane; d < D; d += 32) dst[d] = joined(d);
             }
+        }
+        if (a.cluster) {
+            // ---- join of a request's chunks over the cluster's shared memory: each
+            // CTA takes a share of the elements, chunk by chunk ----
+            cluster_sync();
+            const int n = a.max_chunks, all = min(ROWS, a.group_rows - first_row) * D;
+            const uint32_t m_at = smem_address(m_s), l_at = smem_address(l_s), o_at = smem_address(smem);
+            for (int e = ck * WARPS * 32 + tid; e < all; e += n * WARPS * 32) {
+                const int i = e / D, d = e - i * D, g = first_row + i;
+                float mk[ATTN_CLUSTER], top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < ATTN_CLUSTER; ++k) {
+                    mk[k] = k < n ? peer_float(m_at + 4 * i, k) : -INFINITY;
+                    top = fmaxf(top, mk[k]);
+                }
+                float sum = 0.0f, v = 0.0f;
+#pragma unroll
+                for (int k = 0; k < ATTN_CLUSTER; ++k)
+                    if (k < n) {
+                        const float f = mk[k] == -INFINITY ? 0.0f : pow2(mk[k] - top);
+                        sum = fmaf(f, peer_float(l_at + 4 * i, k), sum);
+                        v = fmaf(f, peer_float(o_at + 4 * (i * S::OROW + d), k), v);
+                    }
+                const bool empty = len - R + (int)a.group.div((uint32_t)g) + 1 <= 0;
+                attn_store(a, b, h, g, d, empty ? 0.0f : v / sum);
+            }
+            cluster_sync();  // shared memory stays until the others have read it
         }
         __syncthreads();  // the next unit fills the rings and rewrites q_s and m_s
     }
@@ -806,25 +913,25 @@ int attn_occupancy(size_t smem, int *out) {
 
 }  // namespace bq
 
-// the instances of one cache type and split (parts 1: q in the cache's 16-bit
-// type), for head_dim up to 64, 128 and 256
-#define BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, DP, NT)                                              \
+// the instances of one cache type and way of carrying queries, for head_dim up to
+// 64, 128 and 256
+#define BQ_ATTN_INST(NAME, KV, QP, PP, DP, NT)                                              \
     {                                                                                              \
-        PARTS, DP, NT, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,                            \
+        DP, NT, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,                            \
             bq::attn_occupancy<KV, QP, PP, DP, NT>,                                                \
             [](const bq::AttnArgs &a, int grid, size_t smem, void *stream,                         \
                unsigned int *status) -> cudaError_t {                                              \
                 return bq::launch_pdl(bq::attn_kernel<KV, QP, PP, DP, NT>, dim3((unsigned)grid),   \
-                                      bq::AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, smem, stream, 1, a, status);            \
+                                      bq::AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, smem, stream, a.cluster ? a.max_chunks : 1, a, status);            \
             }                                                                                      \
     }
-#define BQ_ATTN_UNIT(NAME, KV, PARTS, QP, PP)                                                      \
+#define BQ_ATTN_UNIT(NAME, KV, QP, PP)                                                             \
     const bq::AttnInstance *bq_internal_attn_##NAME(int *n) {                                      \
         static const bq::AttnInstance inst[] = {                                                   \
-            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 64, 1),  BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 64, 2),  \
-            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 64, 4),  BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 128, 1), \
-            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 128, 2), BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 128, 4), \
-            BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 256, 1), BQ_ATTN_INST(NAME, KV, PARTS, QP, PP, 256, 2)}; \
+            BQ_ATTN_INST(NAME, KV, QP, PP, 64, 1),  BQ_ATTN_INST(NAME, KV, QP, PP, 64, 2),  \
+            BQ_ATTN_INST(NAME, KV, QP, PP, 64, 4),  BQ_ATTN_INST(NAME, KV, QP, PP, 128, 1), \
+            BQ_ATTN_INST(NAME, KV, QP, PP, 128, 2), BQ_ATTN_INST(NAME, KV, QP, PP, 128, 4), \
+            BQ_ATTN_INST(NAME, KV, QP, PP, 256, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 256, 2)}; \
         *n = (int)(sizeof inst / sizeof inst[0]);                                                  \
         return inst;                                                                               \
     }

@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(bf16_own, bq::KV_BF16, 1, 1, 2)
+BQ_ATTN_UNIT(bf16_own, bq::KV_BF16, 1, 2)

@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(bf16_split, bq::KV_BF16, 2, 3, 3)
+BQ_ATTN_UNIT(bf16_split, bq::KV_BF16, 3, 3)

@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(f16_own, bq::KV_F16, 1, 1, 2)
+BQ_ATTN_UNIT(f16_own, bq::KV_F16, 1, 2)

@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(f16_split, bq::KV_F16, 2, 2, 2)
+BQ_ATTN_UNIT(f16_split, bq::KV_F16, 2, 2)

@@ -158,7 +158,13 @@ __device__ __forceinline__ void store_n(typename E::T *p, bool wide, const float
 // host-side argument checks
 inline bool aligned_to(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline int dtype_bytes(int t) { return t == BQ_F32 ? 4 : t == BQ_F16 || t == BQ_BF16 ? 2 : 0; }
-inline bq_status from_cuda_error(cudaError_t e) { return e == cudaSuccess ? BQ_OK : BQ_ERR_CUDA; }
+// (a failed call's error is taken off the thread, so that it is not found by a
+// later, unrelated cudaGetLastError)
+inline bq_status from_cuda_error(cudaError_t e) {
+    if (e == cudaSuccess) return BQ_OK;
+    cudaGetLastError();
+    return BQ_ERR_CUDA;
+}
 
 // what bqgemv.h says of bq_kv_cache: shapes and strides, then pointers
 inline bq_status check_cache_shape(const bq_kv_cache *c) {
@@ -181,7 +187,7 @@ inline bq_status check_cache_pointers(const bq_kv_cache *c) {
     if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16)) return BQ_ERR_ALIGN;
     if (c->type == BQ_Q8_0) {
         if (!c->k_scale || !c->v_scale) return BQ_ERR_NULL;
-        if (!aligned_to(c->k_scale, 16) || !aligned_to(c->v_scale, 16)) return BQ_ERR_ALIGN;
+        if (!aligned_to(c->k_scale, 8) || !aligned_to(c->v_scale, 8)) return BQ_ERR_ALIGN;
     }
     return BQ_OK;
 }

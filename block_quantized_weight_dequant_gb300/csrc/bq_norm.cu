@@ -220,12 +220,13 @@ cudaError_t launch_vpt(const Args &a, int threads, int sms, void *stream) {
     if (fit > (VPT <= 2 ? 1024 : 512) / threads) fit = (VPT <= 2 ? 1024 : 512) / threads;
     if (fit < 1) fit = 1;
     const long long most = (long long)sms * fit;
-    if (a.x.rows <= most)
+    constexpr size_t MOST_AHEAD = 200 * 1024;  // beyond it (fp32 rows over 12800) a CTA per row
+    if (a.x.rows <= most || ahead > MOST_AHEAD)
         return bq::launch_pdl(sandwich_kernel<EY, EH, VPT, ONCE>, dim3((unsigned)a.x.rows), threads, 0, stream, 1, a);
     auto *kern = sandwich_kernel<EY, EH, VPT, AHEAD>;
     if (ahead > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   MAX_THREADS * VPT * 128);
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MOST_AHEAD);
         if (e != cudaSuccess) return e;
     }
     return bq::launch_pdl(kern, dim3((unsigned)most), threads, ahead, stream, 1, a);

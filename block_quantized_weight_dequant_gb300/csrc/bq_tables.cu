@@ -292,7 +292,7 @@ extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)(5 * (MAX_REQUESTS + 1) * sizeof(int)));
-        if (e != cudaSuccess) return BQ_ERR_CUDA;
+        if (e != cudaSuccess) return bq::from_cuda_error(e);
     }
     cudaError_t e = bq::launch_pdl(tables_kernel, dim3((unsigned)cluster), THREADS, smem, stream, cluster, a,
                                    (int)with_rows);

@@ -389,7 +389,7 @@ typedef enum { BQ_F32 = 0, BQ_F16 = 1, BQ_BF16 = 30 } bq_dtype; /* (Q8_0 = 8: bq
  *    weights' Q8_0 with codes and scales in planes of their own, so that
  *    rows of codes stay aligned); head_dim % 32 == 0, 32..256; strides
  *    multiples of head_dim; the scale of element e is element e / 32 of its
- *    plane; all four pointers 16-byte aligned.
+ *    plane; codes 16-byte, scales 8-byte aligned.
  *  1 <= kv_heads <= 1024, 1 <= page_size <= 65536, 1 <= pages < 2^31. */
 typedef struct {
     int32_t type, kv_heads, head_dim, page_size;
