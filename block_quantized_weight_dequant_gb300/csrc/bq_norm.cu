@@ -14,7 +14,10 @@
 //  AHEAD  the same with more rows than CTAs: a thread copies its own vectors of
 //         the CTA's next row into shared memory (cp.async) before it works on
 //         the present one, so loads are in flight across the two sums; a thread
-//         reads only what it copied, so no barrier goes with it.
+//         reads only what it copied, so no barrier goes with it.  The gains (and
+//         a gate per channel) are copied the same way once, where two CTAs per SM
+//         still fit: read again for every row they cost an L2 latency after
+//         each sum.
 //  RAGGED any width and alignment: rows pass through shared memory in both
 //         directions, so that global accesses stay coalesced.
 #include "bq_cache.cuh"
@@ -27,7 +30,8 @@ constexpr int MAX_WIDTH = 16384;
 
 struct Args {
     bq_sandwich_args x;
-    int wide;  // whole 16-byte vectors throughout
+    int wide;     // whole 16-byte vectors throughout
+    int gains_s;  // AHEAD: gains and gate kept in shared memory
 };
 
 __device__ __forceinline__ float block_sum(float v, float *sm) {
@@ -82,6 +86,10 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    const bool gate_s = a.gains_s && a.x.gate && a.x.gate_stride == 0;
+    float *post_s = reinterpret_cast<float *>(rows_s + 2 * row_elems * (sizeof(TH) + sizeof(TY)));
+    float *pre_s = post_s + row_elems;
+    TY *gates_s = reinterpret_cast<TY *>(pre_s + row_elems);
     // factors of this thread's elements, read by 16 bytes where the row is whole vectors
     auto factor = [&](auto tag, const auto *p, int at, float(&g)[8]) {
         using E = decltype(tag);
@@ -93,7 +101,20 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
         }
     };
     bq::pdl_wait();
-    if constexpr (MODE == AHEAD) fetch(blockIdx.x, 0);
+    if constexpr (MODE == AHEAD) {
+        if (a.gains_s) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int at = 8 * (tid + v * n);
+                if (at < width) {
+                    if (a.x.post) copy8<bq::F32>(post_s + at, a.x.post + at);
+                    if (a.x.pre) copy8<bq::F32>(pre_s + at, a.x.pre + at);
+                    if (gate_s) copy8<EY>(gates_s + at, (const TY *)a.x.gate + at);
+                }
+            }
+        }
+        fetch(blockIdx.x, 0);
+    }
     int k = 0;
     for (long long row = blockIdx.x; row < a.x.rows; row += gridDim.x, k ^= 1) {
         const TY *y = (const TY *)a.x.y + row * a.x.y_stride;
@@ -136,7 +157,7 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
                 const int at = 8 * (tid + v * n);
                 if (at < width) {
                     float g[8];
-                    factor(bq::F32{}, a.x.post, at, g);
+                    factor(bq::F32{}, MODE == AHEAD && a.gains_s ? post_s : a.x.post, at, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) b[v][i] *= scale * g[i];
                 }
@@ -149,7 +170,7 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
                 const int at = 8 * (tid + v * n);
                 if (at < width) {
                     float g[8];
-                    factor(EY{}, gate, at, g);
+                    factor(EY{}, MODE == AHEAD && gate_s ? gates_s : gate, at, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) b[v][i] *= g[i];
                 }
@@ -176,7 +197,7 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
                 const int at = 8 * (tid + v * n);
                 if (at < width) {
                     float g[8];
-                    factor(bq::F32{}, a.x.pre, at, g);
+                    factor(bq::F32{}, MODE == AHEAD && a.gains_s ? pre_s : a.x.pre, at, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] *= r[v][i] * scale;
                     if constexpr (MODE == RAGGED) bq::store_wide<bq::F32, 8>(yf_s + at, g);
@@ -215,21 +236,28 @@ cudaError_t launch_vpt(const Args &a, int threads, int sms, void *stream) {
         return bq::launch_pdl(kern, dim3((unsigned)(a.x.rows < most ? a.x.rows : most)), threads, ragged, stream, 1,
                               a);
     }
-    // CTAs per SM: two rows of shared memory each, about 48 KB left to L1 for the gains
-    int fit = (int)(176 * 1024 / ahead);
-    if (fit > (VPT <= 2 ? 1024 : 512) / threads) fit = (VPT <= 2 ? 1024 : 512) / threads;
+    // CTAs per SM: two rows of shared memory each and, where two CTAs fit with
+    // them, the gains; else about 48 KB are left to L1 for those
+    constexpr int MOST_THREADS = VPT <= 2 ? 1024 : 512;
+    const size_t gains = (size_t)elems * (8 + sizeof(typename EY::T));
+    const bool gains_s = 2 * (ahead + gains + 1280) <= 228 * 1024;
+    const size_t smem = ahead + (gains_s ? gains : 0);
+    int fit = (int)((gains_s ? 228 * 1024 : 176 * 1024) / (smem + 1280));
+    if (fit > MOST_THREADS / threads) fit = MOST_THREADS / threads;
     if (fit < 1) fit = 1;
     const long long most = (long long)sms * fit;
     constexpr size_t MOST_AHEAD = 200 * 1024;  // beyond it (fp32 rows over 12800) a CTA per row
-    if (a.x.rows <= most || ahead > MOST_AHEAD)
+    if (a.x.rows <= most || smem > MOST_AHEAD)
         return bq::launch_pdl(sandwich_kernel<EY, EH, VPT, ONCE>, dim3((unsigned)a.x.rows), threads, 0, stream, 1, a);
     auto *kern = sandwich_kernel<EY, EH, VPT, AHEAD>;
-    if (ahead > 48 * 1024) {
+    if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MOST_AHEAD);
         if (e != cudaSuccess) return e;
     }
-    return bq::launch_pdl(kern, dim3((unsigned)most), threads, ahead, stream, 1, a);
+    Args with = a;
+    with.gains_s = gains_s;
+    return bq::launch_pdl(kern, dim3((unsigned)most), threads, smem, stream, 1, with);
 }
 
 template <class EY, class EH>
@@ -271,6 +299,7 @@ extern "C" bq_status bq_sandwich_norm(const bq_sandwich_args *x, void *stream) {
     auto row_ok = [&](const void *p, int64_t stride) {
         return bq::aligned_to(p, 16) && (x->rows == 1 || stride % 8 == 0);
     };
+    a.gains_s = 0;
     a.wide = x->width % 8 == 0 && row_ok(x->y, x->y_stride) && row_ok(x->gate, x->gate_stride) &&
              row_ok(x->x, x->x_stride) && row_ok(x->h, x->h_stride) && row_ok(x->h_out, x->h_out_stride) &&
              bq::aligned_to(x->post, 16) && bq::aligned_to(x->pre, 16);
