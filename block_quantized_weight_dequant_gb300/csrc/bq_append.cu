@@ -8,10 +8,11 @@
 // about 2^-24 of a turn plus n * freq * 2^-48, at positions up to 2^31.  fp64
 // runs once per thread and pair only (its rate is far below fp32's).
 //
-// A CTA takes a few tokens at a time (or, with few tokens, a share of one
-// token's heads): its threads put the tokens' cosines and sines into shared
-// memory, one pair each, then its warps take the tokens' heads, the loads of
-// the next heads on their way while the present ones are turned and stored.
+// A CTA takes a few tokens at a time: its threads put the tokens' cosines and
+// sines into shared memory, one pair each, then its warps take the tokens' heads,
+// the next token's on their way while the present ones are turned and stored.  A
+// lane keeps to the same heads for all tokens, so their addresses are one
+// multiply-add a token.
 // A lane holds 8 values of a head, so that a warp takes 1, 2 or 4 heads: the
 // two quarters 4i .. 4i+3 and rot/2 + 4i .. of four (p, p + rot/2) pairs, or 8
 // values in a row (four interleaved pairs, or values behind rot).  So no value
@@ -28,8 +29,9 @@ namespace {
 
 BQ_STATUS_WORD(append)
 
-constexpr int THREADS = 256, WARPS = THREADS / 32;
+constexpr int MAX_WARPS = 12;  // of a CTA: as many as a token's heads need
 constexpr int MAX_BATCH = 4;  // tokens at a time
+constexpr int UNROLL = 2;     // times the heads of a warp that it takes of a token
 
 struct Args {
     bq_kv_cache c;
@@ -37,6 +39,7 @@ struct Args {
     bq::FastDiv page;
     int items;  // heads of a token: q, k and v
     int parts;  // CTAs that share a token's heads
+    int warps;  // of a CTA
     int batch;  // tokens at a time
     int wide, wide_out;  // 4-element accesses of the inputs, of q_out
     // strides (below 2^31) as 32-bit numbers: a product with an index is one instruction
@@ -45,69 +48,96 @@ struct Args {
 
 // GL lanes per head: 8 for head_dim up to 64, 16 up to 128, 32 up to 256
 template <class E, int CT, int GL>
-__global__ void __launch_bounds__(THREADS, 3) append_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_constant__ Args a) {
     using T = typename E::T;
     constexpr int HPW = 32 / GL;       // heads of a warp at a time
-    constexpr int UNROLL = 2;          // times that in flight, and again the next
     constexpr int HALF_MAX = 4 * GL;   // pairs of a head
     constexpr int DMAX = 8 * GL;
     __shared__ __align__(16) float2 cs_s[2][MAX_BATCH][HALF_MAX];
     __shared__ long long row_s[2][MAX_BATCH];
-    __shared__ __align__(16) float order_s[CT == BQ_Q8_0 ? WARPS * HPW * DMAX : 4];
+    __shared__ __align__(16) float order_s[CT == BQ_Q8_0 ? MAX_WARPS * HPW * DMAX : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane / GL, i = lane % GL;
     const int part = blockIdx.x % a.parts;
     const long long groups = gridDim.x / a.parts;
     const int D = a.c.head_dim, rot = a.x.freq ? a.x.rot : 0, half = rot >> 1;
+    const int WARPS = blockDim.x >> 5;
     bq::pdl_wait();
-
-    // the turn of this thread's pair
-    const int pair = tid % HALF_MAX;
-    float hi = 0.0f, lo = 0.0f;
-    int axis = 0;
-    if (pair < half) {
-        const double t = a.x.freq[pair] * 0.15915494309189533576888;  // 1 / (2 pi)
-        hi = (float)t;
-        lo = (float)(t - (double)hi);
-        axis = (pair >= a.x.sections[0] && a.x.axes > 1) +
-               (pair >= a.x.sections[0] + a.x.sections[1] && a.x.axes > 2);
-    }
 
     const int heads = a.x.q ? a.x.heads : 0, kv = a.c.kv_heads;
     const long long slots_all = a.c.pages * a.c.page_size;
     const bool in_rot = 8 * i < rot, apart = in_rot && !a.x.interleaved;
     const int e0 = apart ? 4 * i : 8 * i, e1 = apart ? half + 4 * i : 8 * i + 4;
     const bool there = 8 * i < D;
-    // heads of a token that this lane takes: first, first + stride, ...
-    const int first = (part * WARPS + warp) * HPW + sub, stride = a.parts * WARPS * HPW;
-    const int warp_first = first - sub;
-    const int rounds = a.items > warp_first ? (a.items - warp_first + stride * UNROLL - 1) / (stride * UNROLL) : 0;
+    // The heads of every token that this lane takes, and where they come from and
+    // go to: the same for all tokens, so that an address is one multiply-add.
+    int type[UNROLL];          // 0 query, 1 key, 2 value, 3 none
+    const T *src[UNROLL];      // of token 0
+    uint32_t src_step[UNROLL];
+    T *out[UNROLL];            // of a query of token 0
+    uint32_t head_at[UNROLL];  // of a key's or value's head in its page
+    bool any_kept = false;     // a key or value in this warp
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const int item = ((part * UNROLL + u) * WARPS + warp) * HPW + sub;
+        type[u] = item >= a.items ? 3 : item < heads ? 0 : item < heads + kv ? 1 : 2;
+        const uint32_t head = item - (type[u] == 1 ? heads : type[u] == 2 ? heads + kv : 0);
+        src[u] = type[u] == 0   ? (const T *)a.x.q + (uint64_t)head * a.q_h
+                 : type[u] == 1 ? (const T *)a.x.k + (uint64_t)head * a.k_h
+                                : (const T *)a.x.v + (uint64_t)head * a.v_h;
+        src_step[u] = type[u] == 0 ? a.q_t : type[u] == 1 ? a.k_t : a.v_t;
+        out[u] = type[u] == 0 ? (T *)a.x.q_out + (uint64_t)head * a.o_h : nullptr;
+        head_at[u] = head;
+        if (!there && CT != BQ_Q8_0) type[u] = 3;
+        any_kept |= type[u] == 1 || type[u] == 2;
+    }
+    any_kept = __any_sync(~0u, any_kept);
 
-    auto load = [&](long long t, int round, float (&x)[UNROLL][2][4]) {
+    auto load = [&](uint32_t t, float (&x)[UNROLL][2][4]) {
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
-            const int item = first + (round * UNROLL + u) * stride;
-            if (item >= a.items || !there) continue;
-            const int type = item < heads ? 0 : item < heads + kv ? 1 : 2;
-            const T *base = (const T *)(type == 0 ? a.x.q : type == 1 ? a.x.k : a.x.v);
-            const uint32_t ts = type == 0 ? a.q_t : type == 1 ? a.k_t : a.v_t;
-            const uint32_t hs = type == 0 ? a.q_h : type == 1 ? a.k_h : a.v_h;
-            const uint32_t head = item - (type == 0 ? 0 : type == 1 ? heads : heads + kv);
-            const T *src = base + (uint64_t)(uint32_t)t * ts + (uint64_t)head * hs;
-            bq::load_n<E, 4>(src + e0, a.wide, x[u][0]);
-            bq::load_n<E, 4>(src + e1, a.wide, x[u][1]);
+            if (type[u] == 3 || !there) continue;
+            const T *at = src[u] + (uint64_t)t * src_step[u];
+            bq::load_n<E, 4>(at + e0, a.wide, x[u][0]);
+            bq::load_n<E, 4>(at + e1, a.wide, x[u][1]);
         }
     };
+
+    // this thread's pair, of every `at_once`-th token of a batch
+    const int pair = tid % HALF_MAX, at_once = blockDim.x / HALF_MAX, mine = tid / HALF_MAX;
+    const bool turns = pair < half && mine < at_once;
+    int axis = 0;
+    if (turns)
+        axis = (pair >= a.x.sections[0] && a.x.axes > 1) +
+               (pair >= a.x.sections[0] + a.x.sections[1] && a.x.axes > 2);
+    float hi = 0.0f, lo = 0.0f;
+    bool split = false;
 
     int buf = 0;
     for (long long t0 = blockIdx.x / a.parts * (long long)a.batch; t0 < a.x.tokens;
          t0 += groups * a.batch, buf ^= 1) {
         const int batch = (int)(a.x.tokens - t0 < a.batch ? a.x.tokens - t0 : a.batch);
+        // everything that this batch reads is on its way before anything is computed
         float x[UNROLL][2][4];
-        if (rounds) load(t0, 0, x);
+        load((uint32_t)t0, x);
+        int n[MAX_BATCH];
+#pragma unroll
+        for (int k = 0; k < MAX_BATCH; ++k) {
+            const int b = mine + k * at_once;
+            n[k] = turns && b < batch ? a.x.positions[axis * a.x.position_stride + t0 + b] : 0;
+        }
+        long long slot = -1;
+        if (tid < batch) slot = a.x.slots[t0 + tid];
+        if (!split) {
+            split = true;
+            if (turns) {
+                const double t = a.x.freq[pair] * 0.15915494309189533576888;  // 1 / (2 pi)
+                hi = (float)t;
+                lo = (float)(t - (double)hi);
+            }
+        }
         // ---- slots and angles of the batch ----
         if (tid < batch) {
-            const long long slot = a.x.slots[t0 + tid];
             long long row = -1;  // element offset of the token's slot, head 0
             if (slot >= 0 && slot < slots_all) {
                 const long long page = slot <= 0x7fffffffLL ? (long long)a.page.div((uint32_t)slot)
@@ -118,11 +148,13 @@ __global__ void __launch_bounds__(THREADS, 3) append_kernel(const __grid_constan
             }
             row_s[buf][tid] = row;
         }
-        if (pair < half)
-            for (int b = tid / HALF_MAX; b < batch; b += THREADS / HALF_MAX) {
-                const int n = a.x.positions[axis * a.x.position_stride + t0 + b];
-                const float nf = (float)n;  // beyond 2^24 rounded: the rest is nr, exact
-                const float nr = (float)((long long)n - (long long)nf);
+        if (turns) {
+#pragma unroll
+            for (int k = 0; k < MAX_BATCH; ++k) {
+                const int b = mine + k * at_once;
+                if (b >= batch) break;
+                const float nf = (float)n[k];  // beyond 2^24 rounded: the rest is nr, exact
+                const float nr = (float)((long long)n[k] - (long long)nf);
                 const float p = __fmul_rn(nf, hi);
                 const float e = __fmaf_rn(nf, hi, -p);
                 float f = (p - rintf(p)) + (e - rintf(e));
@@ -132,110 +164,110 @@ __global__ void __launch_bounds__(THREADS, 3) append_kernel(const __grid_constan
                 sincospif(2.0f * (f - rintf(f)), &s, &c);
                 cs_s[buf][b][pair] = make_float2(c, s);
             }
+        }
         __syncthreads();  // (the batch after the next rewrites this buffer, two barriers on)
 
+#pragma unroll 2
         for (int b = 0; b < batch; ++b) {
-            const long long t = t0 + b, row = row_s[buf][b];
+            const uint32_t t = (uint32_t)t0 + b;
+            const long long row = row_s[buf][b];
             float2 w[4];  // cosine and sine of this lane's four pairs
+            if (in_rot) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = in_rot ? cs_s[buf][b][4 * i + k] : make_float2(1.0f, 0.0f);
-            for (int round = 0; round < rounds; ++round) {
-                float y[UNROLL][2][4];
+                for (int k = 0; k < 2; ++k) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&cs_s[buf][b][4 * i + 2 * k]);
+                    w[2 * k] = make_float2(v.x, v.y), w[2 * k + 1] = make_float2(v.z, v.w);
+                }
+            }
+            float y[UNROLL][2][4];
 #pragma unroll
-                for (int u = 0; u < UNROLL; ++u)
+            for (int u = 0; u < UNROLL; ++u)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) y[u][0][k] = x[u][0][k], y[u][1][k] = x[u][1][k];
-                // the next heads, of this token or the next of the batch
-                if (round + 1 < rounds) load(t, round + 1, x);
-                else if (b + 1 < batch) load(t + 1, 0, x);
+                for (int k = 0; k < 4; ++k) y[u][0][k] = x[u][0][k], y[u][1][k] = x[u][1][k];
+            if (b + 1 < batch) load(t + 1, x);  // the next token's heads
 #pragma unroll
-                for (int u = 0; u < UNROLL; ++u) {
-                    const int item = first + (round * UNROLL + u) * stride;
-                    if (item - sub >= a.items) break;  // whole warps
-                    const int type = item >= a.items ? 3 : item < heads ? 0 : item < heads + kv ? 1 : 2;
-                    float(&p)[4] = y[u][0], (&q)[4] = y[u][1];
-                    if (in_rot && type < 2) {
-                        if (apart) {
+            for (int u = 0; u < UNROLL; ++u) {
+                float(&p)[4] = y[u][0], (&q)[4] = y[u][1];
+                if (in_rot && type[u] < 2) {
+                    if (apart) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float e = p[k], o = q[k];
-                                p[k] = fmaf(o, -w[k].y, e * w[k].x);
-                                q[k] = fmaf(e, w[k].y, o * w[k].x);
-                            }
-                        } else {
+                        for (int k = 0; k < 4; ++k) {
+                            const float e = p[k], o = q[k];
+                            p[k] = fmaf(o, -w[k].y, e * w[k].x);
+                            q[k] = fmaf(e, w[k].y, o * w[k].x);
+                        }
+                    } else {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                float(&z)[4] = y[u][k >> 1];
-                                const float e = z[2 * (k & 1)], o = z[2 * (k & 1) + 1];
-                                z[2 * (k & 1)] = fmaf(o, -w[k].y, e * w[k].x);
-                                z[2 * (k & 1) + 1] = fmaf(e, w[k].y, o * w[k].x);
-                            }
+                        for (int k = 0; k < 4; ++k) {
+                            float(&z)[4] = y[u][k >> 1];
+                            const float e = z[2 * (k & 1)], o = z[2 * (k & 1) + 1];
+                            z[2 * (k & 1)] = fmaf(o, -w[k].y, e * w[k].x);
+                            z[2 * (k & 1) + 1] = fmaf(e, w[k].y, o * w[k].x);
                         }
                     }
-                    if (type == 0 && there) {
-                        T *dst = (T *)a.x.q_out + (uint64_t)(uint32_t)t * a.o_t + (uint64_t)(uint32_t)item * a.o_h;
-                        bq::store_n<E, 4>(dst + e0, a.wide_out, p);
-                        bq::store_n<E, 4>(dst + e1, a.wide_out, q);
-                    }
-                    const bool keep = there && row >= 0 && (type == 1 || type == 2);
-                    const long long at = row + (long long)((uint64_t)(uint32_t)(item - heads - (type == 2 ? kv : 0)) * a.head_s);
-                    void *plane = type == 1 ? a.c.k : a.c.v;
-                    if constexpr (CT == BQ_Q8_0) {
-                        if (item - sub + HPW <= heads) continue;  // only queries in this warp
-                        int f0 = e0, f1 = e1;  // where the quarters lie
-                        bool rows_of_8 = !apart;
-                        if (half % 32 && !a.x.interleaved) {  // rotated halves cut blocks: put in order
-                            float *mine = order_s + (warp * HPW + sub) * DMAX;
-                            __syncwarp();
-                            if (there) {
-                                *reinterpret_cast<float4 *>(mine + e0) = make_float4(p[0], p[1], p[2], p[3]);
-                                *reinterpret_cast<float4 *>(mine + e1) = make_float4(q[0], q[1], q[2], q[3]);
-                            }
-                            __syncwarp();
-                            f0 = 8 * i, f1 = 8 * i + 4, rows_of_8 = true;
-                            const float4 g0 = *reinterpret_cast<const float4 *>(mine + f0);
-                            const float4 g1 = *reinterpret_cast<const float4 *>(mine + f1);
-                            p[0] = g0.x, p[1] = g0.y, p[2] = g0.z, p[3] = g0.w;
-                            q[0] = g1.x, q[1] = g1.y, q[2] = g1.z, q[3] = g1.w;
-                        }
-                        float m0 = 0.0f, m1 = 0.0f;
+                }
+                if (type[u] == 0 && there) {
+                    T *dst = out[u] + (uint64_t)t * a.o_t;
+                    bq::store_n<E, 4>(dst + e0, a.wide_out, p);
+                    bq::store_n<E, 4>(dst + e1, a.wide_out, q);
+                }
+                const bool keep = there && row >= 0 && (type[u] == 1 || type[u] == 2);
+                const long long at = row + (long long)((uint64_t)head_at[u] * a.head_s);
+                void *plane = type[u] == 1 ? a.c.k : a.c.v;
+                if constexpr (CT == BQ_Q8_0) {
+                    if (!any_kept) continue;  // only queries in this warp
+                    int f0 = e0, f1 = e1;     // where the quarters lie
+                    bool rows_of_8 = !apart;
+                    if (half % 32 && !a.x.interleaved) {  // rotated halves cut blocks: put in order
+                        float *mine = order_s + (warp * HPW + sub) * DMAX;
+                        __syncwarp();
                         if (there) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) m0 = fmaxf(m0, fabsf(p[k])), m1 = fmaxf(m1, fabsf(q[k]));
+                            *reinterpret_cast<float4 *>(mine + e0) = make_float4(p[0], p[1], p[2], p[3]);
+                            *reinterpret_cast<float4 *>(mine + e1) = make_float4(q[0], q[1], q[2], q[3]);
                         }
-                        if (rows_of_8) m0 = m1 = fmaxf(m0, m1);
-#pragma unroll
-                        for (int o = 1; o < 4; o <<= 1) {
-                            m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, o));
-                            m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, o));
-                        }
-                        const float n0 = __shfl_xor_sync(~0u, m0, 4), n1 = __shfl_xor_sync(~0u, m1, 4);
-                        if (!rows_of_8) m0 = fmaxf(m0, n0), m1 = fmaxf(m1, n1);
-                        if (keep) {
-                            __half *scales = (__half *)(type == 1 ? a.c.k_scale : a.c.v_scale);
-                            auto quantize = [&](const float(&z)[4], float m, int f, bool writes_scale) {
-                                const __half d = __float2half_rn(__fdiv_rn(m, 127.0f));
-                                const float df = __half2float(d);
-                                uint32_t word = 0;
-                                if (df != 0.0f) {
-#pragma unroll
-                                    for (int k = 0; k < 4; ++k) {
-                                        const int c =
-                                            (int)fminf(fmaxf(roundf(__fdiv_rn(z[k], df)), -127.0f), 127.0f);
-                                        word |= (uint32_t)(c & 0xff) << (8 * k);
-                                    }
-                                }
-                                *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + f) = word;
-                                if (writes_scale) scales[(at + f) >> 5] = d;
-                            };
-                            quantize(p, m0, f0, (f0 & 31) == 0);
-                            quantize(q, m1, f1, (f1 & 31) == 0);
-                        }
-                    } else if (keep) {
-                        using C = typename std::conditional<CT == BQ_F16, bq::F16, bq::BF16>::type;
-                        bq::store_wide<C, 4>((typename C::T *)plane + at + e0, p);
-                        bq::store_wide<C, 4>((typename C::T *)plane + at + e1, q);
+                        __syncwarp();
+                        f0 = 8 * i, f1 = 8 * i + 4, rows_of_8 = true;
+                        const float4 g0 = *reinterpret_cast<const float4 *>(mine + f0);
+                        const float4 g1 = *reinterpret_cast<const float4 *>(mine + f1);
+                        p[0] = g0.x, p[1] = g0.y, p[2] = g0.z, p[3] = g0.w;
+                        q[0] = g1.x, q[1] = g1.y, q[2] = g1.z, q[3] = g1.w;
                     }
+                    float m0 = 0.0f, m1 = 0.0f;
+                    if (there) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) m0 = fmaxf(m0, fabsf(p[k])), m1 = fmaxf(m1, fabsf(q[k]));
+                    }
+                    if (rows_of_8) m0 = m1 = fmaxf(m0, m1);
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        m0 = fmaxf(m0, __shfl_xor_sync(~0u, m0, o));
+                        m1 = fmaxf(m1, __shfl_xor_sync(~0u, m1, o));
+                    }
+                    const float n0 = __shfl_xor_sync(~0u, m0, 4), n1 = __shfl_xor_sync(~0u, m1, 4);
+                    if (!rows_of_8) m0 = fmaxf(m0, n0), m1 = fmaxf(m1, n1);
+                    if (keep) {
+                        __half *scales = (__half *)(type[u] == 1 ? a.c.k_scale : a.c.v_scale);
+                        auto quantize = [&](const float(&z)[4], float m, int f, bool writes_scale) {
+                            const __half d = __float2half_rn(__fdiv_rn(m, 127.0f));
+                            const float df = __half2float(d);
+                            uint32_t word = 0;
+                            if (df != 0.0f) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int c = (int)fminf(fmaxf(roundf(__fdiv_rn(z[k], df)), -127.0f), 127.0f);
+                                    word |= (uint32_t)(c & 0xff) << (8 * k);
+                                }
+                            }
+                            *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + f) = word;
+                            if (writes_scale) scales[(at + f) >> 5] = d;
+                        };
+                        quantize(p, m0, f0, (f0 & 31) == 0);
+                        quantize(q, m1, f1, (f1 & 31) == 0);
+                    }
+                } else if (keep) {
+                    using C = typename std::conditional<CT == BQ_F16, bq::F16, bq::BF16>::type;
+                    bq::store_wide<C, 4>((typename C::T *)plane + at + e0, p);
+                    bq::store_wide<C, 4>((typename C::T *)plane + at + e1, q);
                 }
             }
         }
@@ -247,7 +279,7 @@ cudaError_t launch(const Args &a, int grid, void *stream) {
     auto *kern = a.c.head_dim <= 64    ? append_kernel<E, CT, 8>
                  : a.c.head_dim <= 128 ? append_kernel<E, CT, 16>
                                        : append_kernel<E, CT, 32>;
-    return bq::launch_pdl(kern, dim3((unsigned)grid), THREADS, 0, stream, 1, a);
+    return bq::launch_pdl(kern, dim3((unsigned)grid), a.warps * 32, 0, stream, 1, a);
 }
 template <class E>
 cudaError_t launch(const Args &a, int grid, void *stream) {
@@ -331,17 +363,23 @@ extern "C" bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_a
     a.o_t = (uint32_t)x->q_out_token_stride, a.o_h = (uint32_t)x->q_out_head_stride;
     a.page_s = (uint32_t)cache->page_stride, a.head_s = (uint32_t)cache->head_stride;
     a.slot_s = (uint32_t)cache->slot_stride;
-    // Few tokens: a warp for every head, the heads of a token over several CTAs.
-    // Many: one CTA for a token's heads, then several tokens per CTA.
-    const long long fit = (long long)sms * 3;
-    const int heads_at_once = WARPS * (cache->head_dim <= 64 ? 4 : cache->head_dim <= 128 ? 2 : 1);
-    const int most_parts = (a.items + heads_at_once - 1) / heads_at_once;
-    const long long parts = fit / x->tokens;
-    a.parts = parts < 1 ? 1 : parts > most_parts ? most_parts : (int)parts;
-    const long long each = (x->tokens + 4 * fit - 1) / (4 * fit);
+    // A CTA has a warp for every 2 HPW heads of a token, and enough to turn a
+    // token's pairs; more heads go to more CTAs, each with the angles once more.
+    const int gl = cache->head_dim <= 64 ? 8 : cache->head_dim <= 128 ? 16 : 32;
+    const int of_warp = UNROLL * (32 / gl);
+    const int warps = (a.items + of_warp - 1) / of_warp;
+    a.parts = (warps + MAX_WARPS - 1) / MAX_WARPS;
+    a.warps = (warps + a.parts - 1) / a.parts;
+    const int least = 4 * gl / 32 > 4 ? 4 * gl / 32 : 4;
+    if (a.warps < least) a.warps = least;
+    // as many CTAs as are resident together (24 warps of 80 registers per SM), at
+    // MAX_BATCH tokens at a time if there are that many
+    const long long fit = (long long)sms * (24 / a.warps);
+    const long long each = (x->tokens * a.parts + fit - 1) / fit;
     a.batch = each < 1 ? 1 : each > MAX_BATCH ? MAX_BATCH : (int)each;
     const long long groups = (x->tokens + a.batch - 1) / a.batch;
-    const int grid = (int)(groups < 4 * fit ? groups : 4 * fit) * a.parts;
+    const long long most = (fit + a.parts - 1) / a.parts;
+    const int grid = (int)(groups < most ? groups : most) * a.parts;
     return bq::from_cuda_error(x->dtype == BQ_F32   ? launch<bq::F32>(a, grid, stream)
                                : x->dtype == BQ_F16 ? launch<bq::F16>(a, grid, stream)
                                                     : launch<bq::BF16>(a, grid, stream));
