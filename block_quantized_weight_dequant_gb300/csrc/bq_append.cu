@@ -9,10 +9,10 @@
 // runs once per thread and pair only (its rate is far below fp32's).
 //
 // A CTA takes a few tokens at a time: its threads put the tokens' cosines and
-// sines into shared memory, one pair each, then its warps take the tokens' heads,
-// the next token's on their way while the present ones are turned and stored.  A
-// lane keeps to the same heads for all tokens, so their addresses are one
-// multiply-add a token.
+// sines into shared memory, one pair each, then its warps turn and store the
+// tokens' heads.  A lane keeps to the same heads for all tokens, so that their
+// addresses are one multiply-add a token, and copies its own values of the next
+// MAX_BATCH tokens into its own place in shared memory (cp.async, no barrier).
 // A lane holds 8 values of a head, so that a warp takes 1, 2 or 4 heads: the
 // two quarters 4i .. 4i+3 and rot/2 + 4i .. of four (p, p + rot/2) pairs, or 8
 // values in a row (four interleaved pairs, or values behind rot).  So no value
@@ -46,6 +46,32 @@ struct Args {
     uint32_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h, page_s, head_s, slot_s;
 };
 
+// The Q8_0 code of x in its low byte: clamp(round(x / d), -127, 127), the fp32
+// quotient rounded to nearest and then half away from zero, without the division.
+// Any half h = c - 1/2 has at most 8 bits and d, an fp16 number, 11, so h d is an
+// fp32 number; the fp32 numbers below it are below it by 2^-24 of it or more, and
+// so are their quotients below h, which therefore round to less than h.  So the
+// quotient's rounding does not matter: the code is the largest c with |x| >= (c -
+// 1/2) d, a comparison that one FMA decides.  The guess |x| / d + 1/2, rounded
+// down and taken a little small, is that c or one less.
+__device__ __forceinline__ uint32_t q8_code(float x, float d, float inv) {
+    const float v = fabsf(x);
+    float c = __fadd_rd(__fmaf_rd(v, inv, 0.5f), 8388608.0f) - 8388608.0f;
+    if (__fmaf_rn(-(c + 0.5f), d, v) >= 0.0f) c += 1.0f;
+    c = d != 0.0f ? fminf(c, 127.0f) : 0.0f;
+    return __float_as_uint(copysignf(c, x) + 12582912.0f);  // 1.5 2^23: the low bits are the whole number
+}
+
+// 4 elements to shared memory, asynchronously
+template <class T>
+__device__ __forceinline__ void copy4(void *dst, const T *src) {
+    const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (sizeof(T) == 4)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(src) : "memory");
+}
+
 // GL lanes per head: 8 for head_dim up to 64, 16 up to 128, 32 up to 256
 template <class E, int CT, int GL>
 __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_constant__ Args a) {
@@ -55,6 +81,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
     constexpr int DMAX = 8 * GL;
     __shared__ __align__(16) float2 cs_s[2][MAX_BATCH][HALF_MAX];
     __shared__ long long row_s[2][MAX_BATCH];
+    extern __shared__ __align__(16) uint8_t ahead_s[];  // [MAX_BATCH][UNROLL][2][threads] vectors
     __shared__ __align__(16) float order_s[CT == BQ_Q8_0 ? MAX_WARPS * HPW * DMAX : 4];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane / GL, i = lane % GL;
@@ -93,13 +120,35 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
     }
     any_kept = __any_sync(~0u, any_kept);
 
-    auto load = [&](uint32_t t, float (&x)[UNROLL][2][4]) {
+    // This lane's values of a token on their way into its own place in shared
+    // memory, MAX_BATCH tokens ahead (rows that allow no wide access are read when
+    // they are used).
+    constexpr int VEC = 4 * (int)sizeof(T);
+    auto place = [&](int b, int u, int v) { return ahead_s + ((b * UNROLL + u) * 2 + v) * (int)blockDim.x * VEC + tid * VEC; };
+    auto fetch = [&](long long t, int b) {
+        if (a.wide && t < a.x.tokens) {
+#pragma unroll
+            for (int u = 0; u < UNROLL; ++u) {
+                if (type[u] == 3 || !there) continue;
+                const T *at = src[u] + (uint64_t)(uint32_t)t * src_step[u];
+                copy4(place(b, u, 0), at + e0);
+                copy4(place(b, u, 1), at + e1);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto load = [&](uint32_t t, int b, float (&x)[UNROLL][2][4]) {
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             if (type[u] == 3 || !there) continue;
-            const T *at = src[u] + (uint64_t)t * src_step[u];
-            bq::load_n<E, 4>(at + e0, a.wide, x[u][0]);
-            bq::load_n<E, 4>(at + e1, a.wide, x[u][1]);
+            if (a.wide) {
+                bq::load_wide<E, 4>(reinterpret_cast<const T *>(place(b, u, 0)), x[u][0]);
+                bq::load_wide<E, 4>(reinterpret_cast<const T *>(place(b, u, 1)), x[u][1]);
+            } else {
+                const T *at = src[u] + (uint64_t)t * src_step[u];
+                bq::load_n<E, 4>(at + e0, false, x[u][0]);
+                bq::load_n<E, 4>(at + e1, false, x[u][1]);
+            }
         }
     };
 
@@ -111,31 +160,32 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
         axis = (pair >= a.x.sections[0] && a.x.axes > 1) +
                (pair >= a.x.sections[0] + a.x.sections[1] && a.x.axes > 2);
     float hi = 0.0f, lo = 0.0f;
-    bool split = false;
 
-    int buf = 0;
-    for (long long t0 = blockIdx.x / a.parts * (long long)a.batch; t0 < a.x.tokens;
-         t0 += groups * a.batch, buf ^= 1) {
-        const int batch = (int)(a.x.tokens - t0 < a.batch ? a.x.tokens - t0 : a.batch);
-        // everything that this batch reads is on its way before anything is computed
-        float x[UNROLL][2][4];
-        load((uint32_t)t0, x);
-        int n[MAX_BATCH];
+    const long long stride = groups * a.batch;
+    int n[MAX_BATCH];  // positions and a slot of the next batch
+    long long slot = -1;
+    auto look_up = [&](long long t0) {
+        const long long left = a.x.tokens - t0;
 #pragma unroll
         for (int k = 0; k < MAX_BATCH; ++k) {
             const int b = mine + k * at_once;
-            n[k] = turns && b < batch ? a.x.positions[axis * a.x.position_stride + t0 + b] : 0;
+            n[k] = turns && b < a.batch && b < left ? a.x.positions[axis * a.x.position_stride + t0 + b] : 0;
         }
-        long long slot = -1;
-        if (tid < batch) slot = a.x.slots[t0 + tid];
-        if (!split) {
-            split = true;
-            if (turns) {
-                const double t = a.x.freq[pair] * 0.15915494309189533576888;  // 1 / (2 pi)
-                hi = (float)t;
-                lo = (float)(t - (double)hi);
-            }
-        }
+        slot = tid < a.batch && tid < left ? a.x.slots[t0 + tid] : -1;
+    };
+    const long long start = blockIdx.x / a.parts * (long long)a.batch;
+#pragma unroll
+    for (int b = 0; b < MAX_BATCH; ++b) fetch(b < a.batch ? start + b : a.x.tokens, b);
+    look_up(start);
+    if (turns) {
+        const double t = a.x.freq[pair] * 0.15915494309189533576888;  // 1 / (2 pi)
+        hi = (float)t;
+        lo = (float)(t - (double)hi);
+    }
+
+    int buf = 0;
+    for (long long t0 = start; t0 < a.x.tokens; t0 += stride, buf ^= 1) {
+        const int batch = (int)(a.x.tokens - t0 < a.batch ? a.x.tokens - t0 : a.batch);
         // ---- slots and angles of the batch ----
         if (tid < batch) {
             long long row = -1;  // element offset of the token's slot, head 0
@@ -167,8 +217,14 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
         }
         __syncthreads();  // (the batch after the next rewrites this buffer, two barriers on)
 
-#pragma unroll 2
-        for (int b = 0; b < batch; ++b) {
+        look_up(t0 + stride);
+#pragma unroll
+        for (int b = 0; b < MAX_BATCH; ++b) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(MAX_BATCH - 1) : "memory");
+            float y[UNROLL][2][4];
+            if (b < batch) load((uint32_t)t0 + b, b, y);
+            fetch(b < a.batch ? t0 + stride + b : a.x.tokens, b);
+            if (b >= batch) continue;
             const uint32_t t = (uint32_t)t0 + b;
             const long long row = row_s[buf][b];
             float2 w[4];  // cosine and sine of this lane's four pairs
@@ -179,12 +235,6 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                     w[2 * k] = make_float2(v.x, v.y), w[2 * k + 1] = make_float2(v.z, v.w);
                 }
             }
-            float y[UNROLL][2][4];
-#pragma unroll
-            for (int u = 0; u < UNROLL; ++u)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) y[u][0][k] = x[u][0][k], y[u][1][k] = x[u][1][k];
-            if (b + 1 < batch) load(t + 1, x);  // the next token's heads
 #pragma unroll
             for (int u = 0; u < UNROLL; ++u) {
                 float(&p)[4] = y[u][0], (&q)[4] = y[u][1];
@@ -250,14 +300,13 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                         auto quantize = [&](const float(&z)[4], float m, int f, bool writes_scale) {
                             const __half d = __float2half_rn(__fdiv_rn(m, 127.0f));
                             const float df = __half2float(d);
-                            uint32_t word = 0;
-                            if (df != 0.0f) {
+                            // a little below 1 / d, so that the first guess is never too large
+                            const float inv = df != 0.0f ? __fdiv_rn(1.0f - 0x1p-20f, df) : 0.0f;
+                            uint32_t c[4];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int c = (int)fminf(fmaxf(roundf(__fdiv_rn(z[k], df)), -127.0f), 127.0f);
-                                    word |= (uint32_t)(c & 0xff) << (8 * k);
-                                }
-                            }
+                            for (int k = 0; k < 4; ++k) c[k] = q8_code(z[k], df, inv);
+                            const uint32_t word = __byte_perm(__byte_perm(c[0], c[1], 0x0040),
+                                                              __byte_perm(c[2], c[3], 0x0040), 0x5410);
                             *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + f) = word;
                             if (writes_scale) scales[(at + f) >> 5] = d;
                         };
@@ -279,7 +328,13 @@ cudaError_t launch(const Args &a, int grid, void *stream) {
     auto *kern = a.c.head_dim <= 64    ? append_kernel<E, CT, 8>
                  : a.c.head_dim <= 128 ? append_kernel<E, CT, 16>
                                        : append_kernel<E, CT, 32>;
-    return bq::launch_pdl(kern, dim3((unsigned)grid), a.warps * 32, 0, stream, 1, a);
+    const size_t smem = (size_t)MAX_BATCH * UNROLL * 2 * a.warps * 32 * 4 * sizeof(typename E::T);
+    if (smem > 24 * 1024) {  // (up to 24 KB of static shared memory beside it)
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   MAX_BATCH * UNROLL * 2 * MAX_WARPS * 32 * 16);
+        if (e != cudaSuccess) return e;
+    }
+    return bq::launch_pdl(kern, dim3((unsigned)grid), a.warps * 32, smem, stream, 1, a);
 }
 template <class E>
 cudaError_t launch(const Args &a, int grid, void *stream) {
