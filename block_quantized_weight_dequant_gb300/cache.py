@@ -46,8 +46,8 @@ def _need(t, name, dtype=None, like=None):
 
 def _activation(t, name, shape, dtype, device):
     """An activation of a known shape whose last dimension is contiguous."""
-    if (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.shape == shape
-            and t.stride(-1) == 1):
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device.index and t.shape == shape
+            and t.is_contiguous()):
         return
     _need(t, name, dtype, device)
     if tuple(t.shape) != tuple(shape):
@@ -58,13 +58,13 @@ def _activation(t, name, shape, dtype, device):
 
 def _first(t, name, device=None):
     """An activation that says dtype, and device if that is None."""
-    _need(t, name, None, device)
-    if t.dtype not in _DTYPES:
+    if not (isinstance(t, _Tensor) and t.dtype in _DTYPES and t.is_cuda and (device is None or t.device == device)):
+        _need(t, name, None, device)
         raise TypeError(f"{name} must be fp32, fp16 or bf16, got {t.dtype}")
 
 
 def _dense(t, name, dtype, device, numel=None):
-    if (isinstance(t, _Tensor) and t.dtype is dtype and t.device == device and t.is_contiguous()
+    if (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == device.index and t.is_contiguous()
             and (numel is None or t.numel() == numel)):
         return
     _need(t, name, dtype, device)
@@ -337,7 +337,8 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     dtype = q.dtype
     T, heads = n * rows, (q.shape[1] if q.dim() == 3 else -1)
     shape = (T, heads, D)
-    _activation(q, "q", shape, dtype, dev)
+    if q.shape != shape or not q.is_contiguous():
+        _activation(q, "q", shape, dtype, dev)
     width, stride = _table(table, n, dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=dev)
@@ -392,12 +393,13 @@ def sandwich_norm(y, h, pre_gain=None, post_gain=None, gate=None, alpha=1.0, bet
     dev, dtype, shape = y.device, y.dtype, y.shape
     if len(shape) != 2:
         raise ValueError("y must be [rows, width]")
-    _activation(y, "y", shape, dtype, dev)
-    _first(h, "h", dev)
-    h_dtype = h.dtype
-    _activation(h, "h", shape, h_dtype, dev)
-    if h_dtype != dtype and h_dtype != torch.float32:
+    if not y.is_contiguous():
+        _activation(y, "y", shape, dtype, dev)
+    h_dtype = h.dtype if isinstance(h, _Tensor) else None
+    if h_dtype is not dtype and h_dtype is not torch.float32:
+        _need(h, "h")
         raise TypeError(f"h must be {dtype} or fp32, got {h_dtype}")
+    _activation(h, "h", shape, h_dtype, dev)
     T, width = shape
     gp = post = pre = xp = None
     gs = xs = 0
