@@ -164,8 +164,12 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     a.scale_log2 = x->scale * 1.44269504088896340736f;
     const int dim = c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256;
     // 8 query rows per n-tile, as few row tiles as the registers allow: each
-    // reads the cache again
-    const int nt = a.group_rows <= 8 ? 1 : a.group_rows <= 16 || dim == 256 ? 2 : 4;
+    // reads the cache again.  A Q8_0 cache takes two n-tiles at most: with four its
+    // code outgrows the instruction cache (5 rows of 40 heads over 8, 24577
+    // positions: 57 us against 63).
+    const int nt = a.group_rows <= 8                                                  ? 1
+                   : a.group_rows <= 16 || dim == 256 || c->type == BQ_Q8_0 ? 2
+                                                                                      : 4;
     a.row_tiles = (a.group_rows + 8 * nt - 1) / (8 * nt);
     int n = 0;
     const bool same = x->dtype == c->type;

@@ -552,26 +552,22 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float t[TT][QP][4];
+                        float t[TT][4];  // smallest parts first
 #pragma unroll
                         for (int p = QP - 1; p >= 0; --p) {
                             const uint4 q = *reinterpret_cast<const uint4 *>(
                                 q_s + (p * ROWS + 8 * nt + r) * S::QROW + 16 * (c + 4 * j));
 #pragma unroll
                             for (int s = 0; s < TT; ++s) {
-                                mma16816<HALF, true>(t[s][p], lo[s], q.x, q.y);
-                                mma16816<HALF>(t[s][p], hi[s], q.z, q.w);
+                                if (p == QP - 1) mma16816<HALF, true>(t[s], lo[s], q.x, q.y);
+                                else mma16816<HALF>(t[s], lo[s], q.x, q.y);
+                                mma16816<HALF>(t[s], hi[s], q.z, q.w);
                             }
                         }
 #pragma unroll
                         for (int s = 0; s < TT; ++s)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) {
-                                float sum = t[s][QP - 1][x];
-#pragma unroll
-                                for (int p = QP - 2; p >= 0; --p) sum += t[s][p][x];
-                                sc[s][nt][x] = fmaf(d[s][x >> 1], sum, sc[s][nt][x]);
-                            }
+                            for (int x = 0; x < 4; ++x) sc[s][nt][x] = fmaf(d[s][x >> 1], t[s][x], sc[s][nt][x]);
                     }
                 }
             } else {
@@ -925,13 +921,13 @@ int attn_occupancy(size_t smem, int *out) {
                                       bq::AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, smem, stream, a.cluster ? a.max_chunks : 1, a, status);            \
             }                                                                                      \
     }
-#define BQ_ATTN_UNIT(NAME, KV, QP, PP)                                                             \
+#define BQ_ATTN_INSTS(NAME, KV, QP, PP)                                                            \
+    BQ_ATTN_INST(NAME, KV, QP, PP, 64, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 64, 2),                  \
+        BQ_ATTN_INST(NAME, KV, QP, PP, 128, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 128, 2),            \
+        BQ_ATTN_INST(NAME, KV, QP, PP, 256, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 256, 2)
+#define BQ_ATTN_UNIT(NAME, ...)                                                                    \
     const bq::AttnInstance *bq_internal_attn_##NAME(int *n) {                                      \
-        static const bq::AttnInstance inst[] = {                                                   \
-            BQ_ATTN_INST(NAME, KV, QP, PP, 64, 1),  BQ_ATTN_INST(NAME, KV, QP, PP, 64, 2),  \
-            BQ_ATTN_INST(NAME, KV, QP, PP, 64, 4),  BQ_ATTN_INST(NAME, KV, QP, PP, 128, 1), \
-            BQ_ATTN_INST(NAME, KV, QP, PP, 128, 2), BQ_ATTN_INST(NAME, KV, QP, PP, 128, 4), \
-            BQ_ATTN_INST(NAME, KV, QP, PP, 256, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 256, 2)}; \
+        static const bq::AttnInstance inst[] = {__VA_ARGS__};                                      \
         *n = (int)(sizeof inst / sizeof inst[0]);                                                  \
         return inst;                                                                               \
     }

@@ -4,4 +4,5 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(bf16_split, bq::KV_BF16, 3, 3)
+BQ_ATTN_UNIT(bf16_split, BQ_ATTN_INSTS(bf16_split, bq::KV_BF16, 3, 3),
+             BQ_ATTN_INST(bf16_split, bq::KV_BF16, 3, 3, 64, 4), BQ_ATTN_INST(bf16_split, bq::KV_BF16, 3, 3, 128, 4))

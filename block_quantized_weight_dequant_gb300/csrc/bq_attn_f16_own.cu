@@ -4,4 +4,5 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(f16_own, bq::KV_F16, 1, 2)
+BQ_ATTN_UNIT(f16_own, BQ_ATTN_INSTS(f16_own, bq::KV_F16, 1, 2),
+             BQ_ATTN_INST(f16_own, bq::KV_F16, 1, 2, 64, 4), BQ_ATTN_INST(f16_own, bq::KV_F16, 1, 2, 128, 4))

@@ -4,4 +4,5 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(f16_split, bq::KV_F16, 2, 2)
+BQ_ATTN_UNIT(f16_split, BQ_ATTN_INSTS(f16_split, bq::KV_F16, 2, 2),
+             BQ_ATTN_INST(f16_split, bq::KV_F16, 2, 2, 64, 4), BQ_ATTN_INST(f16_split, bq::KV_F16, 2, 2, 128, 4))

@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(q8_0_bf16, bq::KV_Q8, 1, 1)
+BQ_ATTN_UNIT(q8_0_bf16, BQ_ATTN_INSTS(q8_0_bf16, bq::KV_Q8, 1, 1))

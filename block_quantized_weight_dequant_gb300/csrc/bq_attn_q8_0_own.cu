@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(q8_0_own, bq::KV_Q8, 1, 2)
+BQ_ATTN_UNIT(q8_0_own, BQ_ATTN_INSTS(q8_0_own, bq::KV_Q8, 1, 2))

@@ -4,4 +4,4 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(q8_0_split, bq::KV_Q8, 2, 2)
+BQ_ATTN_UNIT(q8_0_split, BQ_ATTN_INSTS(q8_0_split, bq::KV_Q8, 2, 2))
