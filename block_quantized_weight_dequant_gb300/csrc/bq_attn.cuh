@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
 
     auto length = [&](int b) { return min(max(a.x.lens[b], 0), most); };
     const long long per_chunk = (long long)KVH * a.row_tiles;
-    // DIRECT: a CTA per unit that the table can hold, units beyond a request's
+    // direct: a CTA per unit that the table can hold, units beyond a request's
     // length are empty.  Else a CTA takes every gridDim.x-th live unit, which
     // exclusive prefix sums of the requests' units tell.
     const bool direct = a.direct;
@@ -286,8 +286,13 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         int b = 0, hr, ck;
         if (direct) {
-            const uint32_t rest = (uint32_t)u / (uint32_t)a.max_chunks;
-            ck = (int)((uint32_t)u - rest * (uint32_t)a.max_chunks);
+            // a cluster's units are neighbours; else all requests' first chunks come
+            // first, the ragged last ones fill the gaps
+            const uint32_t pairs = (uint32_t)B * (uint32_t)per_chunk;
+            const uint32_t q = (uint32_t)u / (a.cluster ? (uint32_t)a.max_chunks : pairs);
+            const uint32_t m = (uint32_t)u - q * (a.cluster ? (uint32_t)a.max_chunks : pairs);
+            const uint32_t rest = a.cluster ? q : m;
+            ck = (int)(a.cluster ? m : q);
             b = (int)(rest / (uint32_t)per_chunk);
             hr = (int)(rest - (uint32_t)b * (uint32_t)per_chunk);
         } else {
