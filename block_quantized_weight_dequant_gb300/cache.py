@@ -356,6 +356,8 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
         if nbytes is None:
             nbytes = lib.bq_paged_attention_workspace_bytes(cache._ref, ref)
             if nbytes >= 0:
+                if len(cache._workspace) >= 1024:
+                    cache._workspace.clear()
                 cache._workspace[key] = nbytes
         if nbytes > 0:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)

@@ -268,6 +268,8 @@ extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
         t->table_width < 1 || t->table_stride < t->table_width || t->table_stride > (1LL << 40) ||
         t->max_tokens < 0 || t->max_tokens > 0x7ffffffeLL || t->pool < 1 || t->pool == 0x7fffffff)
         return BQ_ERR_SHAPE;
+    // the slot map is made from the lengths asked and the lengths given
+    if (t->requests && t->lens_out && t->lens_out == t->new_lens) return BQ_ERR_SHAPE;
     const void *need[] = {t->free_pages, t->free_count, t->starts, t->free_count_out, t->refused};
     for (const void *p : need)
         if (!p) return BQ_ERR_NULL;
@@ -281,8 +283,8 @@ extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
     Args a;
     a.t = *t;
     a.page.set((uint32_t)t->page_size);
-    // One launch for few rows (a decode step), two for many: measured on GB300
-    // with 256 requests, see the entry's limit below.
+    // One launch for few rows (a decode step), two for many (1000 requests with
+    // 92000 rows of prompts: 11.6 us, 41 us in one launch of 8 CTAs).
     const bool with_rows = t->max_tokens <= ROWS_ALONE;
     // CTAs for the pages that may be asked, each of its threads a few
     const long long work = (with_rows ? t->max_tokens : t->max_tokens / t->page_size) + t->requests;

@@ -416,7 +416,7 @@ typedef struct {
  * stack entries that are no longer in use are left as they were, and so are
  * the table's rows of requests that do not grow.
  *  - lens_out may be lens, free_count_out may be free_count; apart from that
- *    nothing overlaps.  refused receives the number of refused requests.
+ *    nothing overlaps (lens_out == new_lens returns BQ_ERR_SHAPE).  refused receives the number of refused requests.
  *  - 0 <= requests <= 4096, 1 <= page_size <= 65536, table_width >= 1,
  *    table_stride >= table_width, 0 <= max_tokens < 2^31 - 1, 1 <= pool < 2^31 - 1.
  *  - free_count outside 0 .. pool sets BQ_DEVERR_POOL and counts as the

@@ -33,7 +33,7 @@ def cache(kind=_lib.BQ_F16, **over):
 
 
 def tables(**over):
-    c = dict(requests=0, page_size=16, table_width=8, pool=100, table_stride=8, max_tokens=64, lens=A, new_lens=A,
+    c = dict(requests=0, page_size=16, table_width=8, pool=100, table_stride=8, max_tokens=64, lens=A, new_lens=A + 256,
              table=A, free_pages=A, free_count=A, slots=A, positions=A, starts=A, lens_out=A, free_count_out=A,
              refused=A)
     c.update(over)
@@ -182,7 +182,7 @@ def test_fast_division(lib):
     (dict(starts=None), NULL), (dict(free_count_out=None), NULL), (dict(refused=None), NULL),
     (dict(requests=1, lens=None), NULL), (dict(requests=1, new_lens=None), NULL), (dict(requests=1, table=None), NULL),
     (dict(requests=1, lens_out=None), NULL), (dict(slots=None), NULL), (dict(positions=None), NULL),
-    (dict(table=A + 2), ALIGN), (dict(slots=A + 4), ALIGN)])
+    (dict(table=A + 2), ALIGN), (dict(slots=A + 4), ALIGN), (dict(requests=1, lens_out=A, new_lens=A, lens=A + 64), SHAPE)])
 def test_block_table_arguments(lib, over, status):
     assert lib.bq_kv_block_tables(tables(**over), None) == status
 

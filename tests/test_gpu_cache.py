@@ -1,6 +1,9 @@
 """The paged key-value cache on the GPU: block tables, append with rotary
 positions and attention, each against a plain 64-bit form at the sizes and masks
 where it can go wrong, and a run of them together as a server would use them."""
+import os
+import subprocess
+import sys
 import zlib
 
 import numpy as np
@@ -192,6 +195,65 @@ def test_attention_of_long_caches(lens, width):
     assert torch.equal(a, bq.paged_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV)))
     rows = 3
     check_attention(cache, normal(g, (len(lens) * rows, 6, 64)), table, lens, rows=rows)
+
+
+def test_attention_of_short_requests_in_a_wide_table():
+    """Many more units than the requests fill: live ones are found by a scan."""
+    g = rng(42)
+    lens = [int(n) for n in g.integers(0, 60, 300)]
+    lens[7], lens[200] = 5000, 2049
+    page = 16
+    pages = sum(-(-n // page) for n in lens)
+    cache = filled_cache(g, "bf16", pages, page, 2, 64)
+    table = request_tables(g, lens, page, pages, width=1000)
+    check_attention(cache, normal(g, (300, 4, 64), BF16), table, lens)
+    check_attention(cache, normal(g, (600, 4, 64)), table, lens, rows=2)
+
+
+@pytest.mark.parametrize("D", [8, 24, 40, 72, 104, 200])
+def test_odd_head_sizes(D):
+    g = rng(D, 43)
+    lens, page = [0, 5, 33, 400], 8
+    pages = sum(-(-n // page) for n in lens) + 1
+    cache = filled_cache(g, "f16", pages, page, 3, D)
+    table = request_tables(g, lens, page, pages)
+    poison(cache, table, lens)
+    check_attention(cache, normal(g, (4, 6, D)), table, lens)
+    check_attention(cache, normal(g, (8, 3, D), BF16), table, lens, rows=2)
+    check_append(g, "f16", F32, 9, 4, 3, D, 16 if D >= 16 else 0, None, False, 8, 300)
+    check_append(g, "bf16", F16, 9, 4, 3, D, D // 16 * 16, None, True, 8, 300)
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """A process whose first call of each kernel is captured."""
+    code = """
+import torch, sys
+sys.path.insert(0, {root!r})
+import block_quantized_weight_dequant_gb300 as bq
+dev = "cuda"
+cache = bq.PagedKVCache.zeros(40, 16, 2, 64, "q8_0")
+t = bq.BlockTables(2, 20, 40, 16, 8)
+goal = torch.tensor([3, 4], dtype=torch.int32, device=dev)
+k, q = torch.randn(8, 2, 64, device=dev), torch.randn(8, 4, 64, device=dev)
+rope = bq.Rope.from_theta(64)
+ws = torch.empty(1 << 24, dtype=torch.uint8, device=dev)
+out, turned, x = torch.empty(2, 4, 64, device=dev), torch.empty_like(q), torch.empty(8, 256, device=dev)
+gain = torch.ones(256, device=dev)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    t.resize(goal)
+    bq.kv_append(cache, k, k, t.slots, q=q, q_out=turned, rope=rope, positions=t.positions)
+    bq.paged_attention(cache, turned[:2], t.table, t.lens, out=out, workspace=ws)
+    bq.sandwich_norm(turned.view(8, 256), turned.view(8, 256), gain, h_out=x, x_out=torch.empty_like(x))
+graph.replay()
+torch.cuda.synchronize()
+assert t.lens.tolist() == [3, 4] and torch.isfinite(out).all() and bool(out.abs().sum() > 0)
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
 
 
 @pytest.mark.parametrize("kind", ["f16", "q8_0"])
@@ -390,6 +452,7 @@ def check_append(g, kind, dtype, T, heads, kv, D, rot, sections, interleaved, pa
         rope = bq.Rope(freq.to(DEV), sections, interleaved)
         positions = torch.from_numpy(g.integers(0, far, (rope.axes, T)).astype(np.int32))
         positions[:, 0] = far - 1
+        positions[:, -1] = -positions[:, -1]
     q0, k0, v0 = q.cpu().clone(), k.cpu().clone(), v.cpu().clone()
     out = bq.kv_append(cache, k, v, slots, q=q, q_out=q if in_place else None, rope=rope,
                        positions=None if rope is None else positions.to(DEV))
@@ -619,6 +682,15 @@ def test_block_tables_step_by_step_keep_every_page():
         used += t.free_pages[:int(t.free_count)].tolist()
         assert sorted(used) == list(range(pages))
     assert refused > 0
+
+
+def test_lengths_may_not_be_written_over_the_lengths_asked():
+    i32 = dict(dtype=torch.int32, device=DEV)
+    new = torch.zeros(2, **i32)
+    with pytest.raises(bq.BQError):
+        bq.kv_block_tables(torch.zeros(2, **i32), new, torch.zeros((2, 4), **i32), torch.zeros(8, **i32),
+                           torch.zeros(1, **i32), 16, torch.zeros(4, dtype=torch.int64, device=DEV), torch.zeros(4, **i32),
+                           torch.zeros(3, **i32), lens_out=new)
 
 
 def test_block_table_refusals():
