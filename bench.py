@@ -75,7 +75,8 @@ NCU_TRAFFIC = {
 
 # CUDA sources that no part of the streaming kernel or its planner is built
 # from: changing them leaves the captured traffic valid
-DIGEST_EXCLUDES = ("bq_f16.cu",)
+DIGEST_EXCLUDES = ("bq_f16.cu", "bq_cache.cuh", "bq_tables.cu", "bq_append.cu", "bq_norm.cu")
+DIGEST_EXCLUDED_PREFIX = "bq_attn"
 
 
 def csrc_digest():
@@ -85,7 +86,8 @@ def csrc_digest():
     d = os.path.join(ROOT, "block_quantized_weight_dequant_gb300", "csrc")
     h = hashlib.sha256()
     for n in sorted(os.listdir(d)):
-        if n.endswith((".cu", ".cuh", ".h")) and n not in DIGEST_EXCLUDES:
+        if (n.endswith((".cu", ".cuh", ".h")) and n not in DIGEST_EXCLUDES
+                and not n.startswith(DIGEST_EXCLUDED_PREFIX)):
             h.update(n.encode())
             with open(os.path.join(d, n), "rb") as f:
                 h.update(f.read())

@@ -149,7 +149,9 @@ def get():
 
 class _LazyLib:
     def __getattr__(self, name):
-        return getattr(get(), name)
+        fn = getattr(get(), name)
+        self.__dict__[name] = fn  # found without this call from now on
+        return fn
 
 
 lib = _LazyLib()

@@ -75,6 +75,11 @@ def _dense(t, name, dtype, device, numel=None):
 
 def _table(t, n, device):
     """The block table: rows of contiguous page numbers; returns width and row stride."""
+    if (isinstance(t, _Tensor) and t.dtype is torch.int32 and t.get_device() == device.index and t.dim() == 2
+            and t.is_contiguous()):
+        rows, width = t.shape
+        if rows == n and width:
+            return width, width
     _need(t, "table", torch.int32, device)
     if t.dim() != 2 or t.shape[0] != n or (n and t.shape[1] < 1):
         raise ValueError(f"table must be [{n}, width]")
@@ -82,6 +87,23 @@ def _table(t, n, device):
         raise ValueError("rows of table must be contiguous")
     width = t.shape[1] or 1
     return width, (t.stride(0) if n > 1 else width)
+
+
+_workspaces = {}  # (device, stream) -> the largest workspace that its calls have needed
+
+
+def _workspace(nbytes, device):
+    """Workspace of a call on the current stream.  Calls on one stream follow one
+    another, so they share one that stays with the stream; a captured call gets its
+    own, which its graph keeps, since graphs may be replayed side by side."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    index = device.index
+    key = (index, _raw_stream(index))
+    ws = _workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws
 
 
 def _call(fn, what, device, *args):
@@ -146,6 +168,7 @@ class PagedKVCache:
         self._c = _lib.BqKvCache(kind, kv_heads, head_dim, page_size, pages, *strides, k.data_ptr(),
                                  v.data_ptr(), ptr(k_scale), ptr(v_scale))
         self._ref = ctypes.byref(self._c)
+        self._scale = 1.0 / math.sqrt(head_dim)
         self._workspace = {}  # workspace bytes by call geometry
 
     @classmethod
@@ -325,7 +348,8 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     cache's kv_heads.  A row that sees nothing gives zeros.  scale defaults to
     1 / sqrt(head_dim).  Row r's bits are those of the one-row call at its
     length.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
-    call that may overlap others; allocated when None."""
+    call that may overlap others; None: the stream's own, or in a capture one of
+    the call's own."""
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")
     dev, D = cache.device, cache.head_dim
@@ -346,8 +370,8 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     else:
         _activation(out, "out", shape, dtype, dev)
         os = _strides(out, T, heads)
-    args = _lib.BqAttentionArgs(_DTYPES[dtype], n, rows, heads, width, 1.0 / math.sqrt(D) if scale is None else scale,
-                                stride, *_strides(q, T, heads), *os, q.data_ptr(), out.data_ptr(),
+    args = _lib.BqAttentionArgs(_DTYPES[dtype], n, rows, heads, width, cache._scale if scale is None else scale, stride,
+                                *_strides(q, T, heads), *os, q.data_ptr(), out.data_ptr(),
                                 table.data_ptr(), lens.data_ptr())
     ref = _byref(args)
     if workspace is None:
@@ -360,7 +384,7 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
                     cache._workspace.clear()
                 cache._workspace[key] = nbytes
         if nbytes > 0:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            workspace = _workspace(nbytes, dev)
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
         nbytes = workspace.numel()

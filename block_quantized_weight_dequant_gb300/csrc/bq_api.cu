@@ -14,7 +14,6 @@
 #include <vector>
 
 #include "../../include/bqgemv.h"
-#include "bq_cache.cuh"
 #include "bq_dot.cuh"
 #include "bq_exec.cuh"
 #include "bq_multi.cuh"

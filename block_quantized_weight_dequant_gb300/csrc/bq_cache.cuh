@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "../../include/bqgemv.h"
+#include "bq_internal.h"
 
 namespace bq {
 
@@ -196,11 +197,6 @@ inline bq_status check_cache_pointers(const bq_kv_cache *c) {
 int device_sms();
 
 }  // namespace bq
-
-// device status words of these translation units (bits of bq_device_status)
-int bq_internal_status_tables(unsigned int *flags, int clear);
-int bq_internal_status_append(unsigned int *flags, int clear);
-int bq_internal_status_attn(unsigned int *flags, int clear);
 
 // a translation unit's status word and its reader
 #define BQ_STATUS_WORD(NAME)                                                                       \
