@@ -114,6 +114,79 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     }
 }
 
+// The same for tables of few chunks: a warp per query row and head, its lanes'
+// four elements at a time, the chunks in order.
+template <int DT>
+__global__ void __launch_bounds__(JOIN_THREADS) join_few_kernel(const __grid_constant__ bq::AttnArgs a, int tile_rows) {
+    const int lane = threadIdx.x & 31;
+    const int index = (int)((blockIdx.x * JOIN_THREADS + threadIdx.x) >> 5);
+    const int D = a.c.head_dim, R = a.x.rows;
+    const int token = index / a.x.heads, head = index - token * a.x.heads;
+    const int b = token / R, row = token - b * R;
+    const int h = (int)a.group.div((uint32_t)head);
+    const int g = row * (int)a.group.d + head - h * (int)a.group.d;
+    const int rt = g / tile_rows, i = g - rt * tile_rows;
+    bq::pdl_wait();
+    if (b >= a.x.requests) return;
+    const int len = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
+    const int chunks = bq::attn_chunks(len, a.chunk);
+    if (chunks == 1) return;
+    const long long unit0 = (((long long)b * a.max_chunks) * a.c.kv_heads + h) * a.row_tiles + rt;
+    const long long step = (long long)a.c.kv_heads * a.row_tiles;
+    const float *src = a.part_o + (unit0 * tile_rows + i) * D;
+    const long long hop = step * tile_rows * D;
+    const float2 ml = lane < chunks ? a.part_ml[(unit0 + lane * step) * tile_rows + i] : make_float2(-INFINITY, 0.0f);
+    float top = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+    float sum = f * ml.y;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    const bool empty = len - R + row + 1 <= 0;
+    const long long at = (long long)token * a.x.out_row_stride + (long long)head * a.x.out_head_stride;
+    for (int d0 = 0; d0 < D; d0 += 128) {
+        const int d = d0 + 4 * lane;
+        const bool mine = d < D;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int k = 0; k < chunks; ++k) {
+            const float w = __shfl_sync(~0u, f, k);
+            const float4 o = mine ? *reinterpret_cast<const float4 *>(src + k * hop + d) : acc;
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+        if (mine) {
+            const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float y = empty ? 0.0f : v[x] / sum;
+                if constexpr (DT == BQ_F32) ((float *)a.x.out)[at + d + x] = y;
+                else if constexpr (DT == BQ_F16) ((__half *)a.x.out)[at + d + x] = __float2half_rn(y);
+                else ((__nv_bfloat16 *)a.x.out)[at + d + x] = __float2bfloat16_rn(y);
+            }
+        }
+    }
+}
+
+template <int DT>
+cudaError_t join(const bq::AttnArgs &a, int tile_rows, void *stream) {
+    const int64_t rows = (int64_t)a.x.requests * a.x.rows * a.x.heads;
+    // up to 16 chunks a warp joins a row (160 requests of 14 heads, two chunks at
+    // most: the call 30 us against 33 with a CTA per row), beyond it a CTA
+    constexpr int JOIN_FEW = 16;
+    if (a.max_chunks <= JOIN_FEW) {
+        constexpr int PER = JOIN_THREADS / 32;
+        return bq::launch_pdl(join_few_kernel<DT>, dim3((unsigned)((rows + PER - 1) / PER)), JOIN_THREADS, 0, stream, 1,
+                              a, tile_rows);
+    }
+    const int groups = JOIN_THREADS / (a.c.head_dim / 4);
+    const size_t smem = ((size_t)(a.max_chunks + 3) / 4 * 4 + (size_t)groups * a.c.head_dim) * sizeof(float);
+    return bq::launch_pdl(join_kernel<DT>, dim3((unsigned)rows), JOIN_THREADS, smem, stream, 1, a, tile_rows);
+}
+
 struct Plan {
     const bq::AttnInstance *inst;
     bq::AttnArgs a;
@@ -270,14 +343,9 @@ extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_atten
     cudaError_t e = status_address(&status);
     if (e == cudaSuccess) e = p.inst->launch(a, (int)grid, p.smem, stream, status);
     if (e != cudaSuccess || a.max_chunks == 1 || a.cluster) return bq::from_cuda_error(e);
-    const int groups = JOIN_THREADS / (cache->head_dim / 4);
-    const size_t smem = ((size_t)(a.max_chunks + 3) / 4 * 4 + (size_t)groups * cache->head_dim) * sizeof(float);
-    const dim3 blocks((unsigned)(x->requests * x->rows * x->heads));
     const int tile_rows = 8 * p.inst->nt;
-    e = x->dtype == BQ_F32
-            ? bq::launch_pdl(join_kernel<BQ_F32>, blocks, JOIN_THREADS, smem, stream, 1, a, tile_rows)
-        : x->dtype == BQ_F16
-            ? bq::launch_pdl(join_kernel<BQ_F16>, blocks, JOIN_THREADS, smem, stream, 1, a, tile_rows)
-            : bq::launch_pdl(join_kernel<BQ_BF16>, blocks, JOIN_THREADS, smem, stream, 1, a, tile_rows);
+    e = x->dtype == BQ_F32   ? join<BQ_F32>(a, tile_rows, stream)
+        : x->dtype == BQ_F16 ? join<BQ_F16>(a, tile_rows, stream)
+                             : join<BQ_BF16>(a, tile_rows, stream);
     return bq::from_cuda_error(e);
 }
