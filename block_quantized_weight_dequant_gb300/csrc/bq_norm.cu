@@ -18,8 +18,9 @@
 //         a gate per channel) are copied the same way once, where two CTAs per SM
 //         still fit: read again for every row they cost an L2 latency after
 //         each sum.
-//  RAGGED any width and alignment: rows pass through shared memory in both
-//         directions, so that global accesses stay coalesced.
+//  RAGGED any width and alignment, a CTA per row: element by element with a warp's
+//         lanes side by side, put in the threads' order (and back) through 1 KB
+//         of shared memory per warp.
 #include "bq_cache.cuh"
 
 #include <cmath>
@@ -30,8 +31,9 @@ constexpr int MAX_WIDTH = 16384;
 
 struct Args {
     bq_sandwich_args x;
-    int wide;     // whole 16-byte vectors throughout
-    int gains_s;  // AHEAD: gains and gate kept in shared memory
+    int wide;       // whole 16-byte vectors throughout
+    int wide_gain;  // the gains are aligned to them
+    int gains_s;    // AHEAD: gains and gate kept in shared memory
 };
 
 __device__ __forceinline__ float block_sum(float v, float *sm) {
@@ -54,6 +56,23 @@ __device__ __forceinline__ void copy8(typename E::T *dst, const typename E::T *s
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 16), "l"(src + 4) : "memory");
 }
 
+// A warp's 256 elements from lanes side by side (element 32 i + lane in x[i]) to
+// eight in a row per lane, and back
+__device__ __forceinline__ void to_rows(float *warp_s, int lane, float (&x)[8]) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) warp_s[32 * i + lane] = x[i];
+    __syncwarp();
+    bq::load_wide<bq::F32, 8>(warp_s + 8 * lane, x);
+}
+__device__ __forceinline__ void to_lanes(float *warp_s, int lane, float (&x)[8]) {
+    __syncwarp();
+    bq::store_wide<bq::F32, 8>(warp_s + 8 * lane, x);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = warp_s[32 * i + lane];
+}
+
 constexpr int MAX_THREADS = 512;
 enum { ONCE, AHEAD, RAGGED };
 
@@ -65,11 +84,14 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
     __shared__ float sm[2][32];
     const int width = (int)a.x.width, n = blockDim.x, tid = threadIdx.x;
     const float inv_width = 1.0f / (float)width;
-    // AHEAD: two rows, h then y; RAGGED: one row of each in fp32, whole vectors
+    // AHEAD: two rows, h then y; RAGGED: 256 floats per warp
     const int row_elems = n * VPT * 8;
     TH *h_s = reinterpret_cast<TH *>(rows_s);
     TY *y_s = reinterpret_cast<TY *>(rows_s + 2 * row_elems * sizeof(TH));
-    float *hf_s = reinterpret_cast<float *>(rows_s), *yf_s = hf_s + row_elems;
+    const int lane = tid & 31;
+    float *warp_s = reinterpret_cast<float *>(rows_s) + 256 * (tid >> 5);
+    // first element of this warp's v-th 256, less its lane
+    auto side_by_side = [&](int v) { return 8 * ((tid & ~31) + v * n) + lane; };
     // this thread's vectors of a row
     auto fetch = [&](long long row, int k) {
         if (row < a.x.rows) {
@@ -93,7 +115,7 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
     // factors of this thread's elements, read by 16 bytes where the row is whole vectors
     auto factor = [&](auto tag, const auto *p, int at, float(&g)[8]) {
         using E = decltype(tag);
-        if constexpr (MODE != RAGGED) {
+        if (MODE != RAGGED || (at + 8 <= width && a.wide_gain)) {
             bq::load_wide<E, 8>(p + at, g);
         } else {
 #pragma unroll
@@ -124,25 +146,29 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
             fetch(row + gridDim.x, k ^ 1);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
         }
-        if constexpr (MODE == RAGGED) {
-            for (int i = tid; i < row_elems; i += n) {
-                yf_s[i] = i < width ? EY::up(y[i]) : 0.0f;
-                hf_s[i] = i < width ? EH::up(h[i]) : 0.0f;
-            }
-            __syncthreads();
-        }
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int at = 8 * (tid + v * n);
-            if (MODE == RAGGED) {
-                bq::load_wide<bq::F32, 8>(yf_s + at, b[v]);
-                bq::load_wide<bq::F32, 8>(hf_s + at, r[v]);
+            if constexpr (MODE == RAGGED) {
+                const int e = side_by_side(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    b[v][i] = e + 32 * i < width ? EY::up(y[e + 32 * i]) : 0.0f;
+                    r[v][i] = e + 32 * i < width ? EH::up(h[e + 32 * i]) : 0.0f;
+                }
             } else if (at < width) {
                 bq::load_wide<EY, 8>(MODE == AHEAD ? y_s + k * row_elems + at : y + at, b[v]);
                 bq::load_wide<EH, 8>(MODE == AHEAD ? h_s + k * row_elems + at : h + at, r[v]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) b[v][i] = r[v][i] = 0.0f;
+            }
+        }
+        if constexpr (MODE == RAGGED) {
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                to_rows(warp_s, lane, b[v]);
+                to_rows(warp_s, lane, r[v]);
             }
         }
         if (a.x.post) {
@@ -168,9 +194,16 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int at = 8 * (tid + v * n);
-                if (at < width) {
+                if (MODE == RAGGED || at < width) {
                     float g[8];
-                    factor(EY{}, MODE == AHEAD && gate_s ? gates_s : gate, at, g);
+                    if constexpr (MODE == RAGGED) {
+                        const int e = side_by_side(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) g[i] = e + 32 * i < width ? EY::up(gate[e + 32 * i]) : 0.0f;
+                        to_rows(warp_s, lane, g);
+                    } else {
+                        factor(EY{}, MODE == AHEAD && gate_s ? gates_s : gate, at, g);
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) b[v][i] *= g[i];
                 }
@@ -186,8 +219,18 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
                 r[v][i] = fmaf(a.x.alpha, r[v][i], a.x.beta * b[v][i]);
                 s = fmaf(r[v][i], r[v][i], s);
             }
-            if constexpr (MODE == RAGGED) bq::store_wide<bq::F32, 8>(hf_s + at, r[v]);
-            else if (at < width) bq::store_wide<EH, 8>(ho + at, r[v]);
+            if constexpr (MODE == RAGGED) {
+                float o[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = r[v][i];
+                to_lanes(warp_s, lane, o);
+                const int e = side_by_side(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (e + 32 * i < width) ho[e + 32 * i] = EH::down(o[i]);
+            } else if (at < width) {
+                bq::store_wide<EH, 8>(ho + at, r[v]);
+            }
         }
         TY *x = (TY *)a.x.x + (a.x.x ? row * a.x.x_stride : 0);
         if (a.x.x) {
@@ -195,24 +238,24 @@ __global__ void __launch_bounds__(MAX_THREADS, VPT <= 2 ? 2 : 1) sandwich_kernel
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int at = 8 * (tid + v * n);
-                if (at < width) {
+                if (MODE == RAGGED || at < width) {
                     float g[8];
                     factor(bq::F32{}, MODE == AHEAD && a.gains_s ? pre_s : a.x.pre, at, g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) g[i] *= r[v][i] * scale;
-                    if constexpr (MODE == RAGGED) bq::store_wide<bq::F32, 8>(yf_s + at, g);
-                    else bq::store_wide<EY, 8>(x + at, g);
+                    if constexpr (MODE == RAGGED) {
+                        to_lanes(warp_s, lane, g);
+                        const int e = side_by_side(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (e + 32 * i < width) x[e + 32 * i] = EY::down(g[i]);
+                    } else {
+                        bq::store_wide<EY, 8>(x + at, g);
+                    }
                 }
             }
         }
-        if constexpr (MODE == RAGGED) {
-            __syncthreads();
-            for (int i = tid; i < width; i += n) {
-                ho[i] = EH::down(hf_s[i]);
-                if (a.x.x) x[i] = EY::down(yf_s[i]);
-            }
-            __syncthreads();
-        } else if (!(a.x.post && a.x.x)) {
+        if (!(a.x.post && a.x.x)) {
             // the next row's sums reuse sm: with both, sm[0] is rewritten only after every
             // warp has passed the barrier inside block_sum on sm[1], and the other way round
             __syncthreads();
@@ -224,17 +267,9 @@ template <class EY, class EH, int VPT>
 cudaError_t launch_vpt(const Args &a, int threads, int sms, void *stream) {
     const int elems = threads * VPT * 8;
     const size_t ahead = (size_t)2 * elems * (sizeof(typename EY::T) + sizeof(typename EH::T));
-    const size_t ragged = (size_t)elems * 8;
     if (!a.wide) {
-        const long long most = (long long)sms * (1024 / threads < 1 ? 1 : 1024 / threads);
-        auto *kern = sandwich_kernel<EY, EH, VPT, RAGGED>;
-        if (ragged > 48 * 1024) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       MAX_THREADS * VPT * 64);
-            if (e != cudaSuccess) return e;
-        }
-        return bq::launch_pdl(kern, dim3((unsigned)(a.x.rows < most ? a.x.rows : most)), threads, ragged, stream, 1,
-                              a);
+        return bq::launch_pdl(sandwich_kernel<EY, EH, VPT, RAGGED>, dim3((unsigned)a.x.rows), threads,
+                              (size_t)threads * 32, stream, 1, a);
     }
     // CTAs per SM: two rows of shared memory each and, where two CTAs fit with
     // them, the gains; else about 48 KB are left to L1 for those
@@ -246,8 +281,12 @@ cudaError_t launch_vpt(const Args &a, int threads, int sms, void *stream) {
     if (fit > MOST_THREADS / threads) fit = MOST_THREADS / threads;
     if (fit < 1) fit = 1;
     const long long most = (long long)sms * fit;
-    constexpr size_t MOST_AHEAD = 200 * 1024;  // beyond it (fp32 rows over 12800) a CTA per row
-    if (a.x.rows <= most || smem > MOST_AHEAD)
+    // Rows ahead pay where the gains are kept or two rows leave L1 room for them
+    // (72 KB a CTA), and where 32 elements a thread leave one CTA per SM; else the
+    // hardware's next CTA hides as much (fp32 rows of 8192: 126 us against 158).
+    constexpr size_t MOST_AHEAD = 200 * 1024;
+    const bool pays = gains_s || VPT == 4 || ahead <= 72 * 1024;
+    if (a.x.rows <= most || smem > MOST_AHEAD || !pays)
         return bq::launch_pdl(sandwich_kernel<EY, EH, VPT, ONCE>, dim3((unsigned)a.x.rows), threads, 0, stream, 1, a);
     auto *kern = sandwich_kernel<EY, EH, VPT, AHEAD>;
     if (smem > 48 * 1024) {
@@ -300,9 +339,9 @@ extern "C" bq_status bq_sandwich_norm(const bq_sandwich_args *x, void *stream) {
         return bq::aligned_to(p, 16) && (x->rows == 1 || stride % 8 == 0);
     };
     a.gains_s = 0;
+    a.wide_gain = bq::aligned_to(x->post, 16) && bq::aligned_to(x->pre, 16);
     a.wide = x->width % 8 == 0 && row_ok(x->y, x->y_stride) && row_ok(x->gate, x->gate_stride) &&
-             row_ok(x->x, x->x_stride) && row_ok(x->h, x->h_stride) && row_ok(x->h_out, x->h_out_stride) &&
-             bq::aligned_to(x->post, 16) && bq::aligned_to(x->pre, 16);
+             row_ok(x->x, x->x_stride) && row_ok(x->h, x->h_stride) && row_ok(x->h_out, x->h_out_stride) && a.wide_gain;
     cudaError_t e;
     if (x->dtype == BQ_F32)
         e = launch<bq::F32, bq::F32>(a, sms, stream);
