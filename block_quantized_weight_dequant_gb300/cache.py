@@ -56,6 +56,20 @@ def _activation(t, name, shape, dtype, device):
         raise ValueError(f"the last dimension of {name} must be contiguous")
 
 
+def _result(t, name, shape, dtype, device):
+    """An activation that is written: no element of it twice."""
+    _activation(t, name, shape, dtype, device)
+    if not t.is_contiguous() and any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} overlaps itself")
+
+
+def _empty(shape, dtype, like):
+    """A new contiguous tensor on the device of `like` (cheapest in its image)."""
+    if like.shape == shape and like.dtype is dtype and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _first(t, name, device=None):
     """An activation that says dtype, and device if that is None."""
     if not (isinstance(t, _Tensor) and t.dtype in _DTYPES and t.is_cuda and (device is None or t.device == device)):
@@ -89,6 +103,7 @@ def _table(t, n, device):
     return width, (t.stride(0) if n > 1 else width)
 
 
+_KEPT = 256 << 20  # a larger workspace goes back to the allocator after its call
 _workspaces = {}  # (device, stream) -> the largest workspace that its calls have needed
 
 
@@ -96,7 +111,7 @@ def _workspace(nbytes, device):
     """Workspace of a call on the current stream.  Calls on one stream follow one
     another, so they share one that stays with the stream; a captured call gets its
     own, which its graph keeps, since graphs may be replayed side by side."""
-    if torch.cuda.is_current_stream_capturing():
+    if nbytes > _KEPT or torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
     index = device.index
     key = (index, _raw_stream(index))
@@ -141,6 +156,8 @@ class PagedKVCache:
             raise ValueError("the cache must hold at least one page, head, slot and value")
         if k.stride(3) != 1:
             raise ValueError("head_dim must be contiguous")
+        if any(n > 1 and s == 0 for n, s in zip(k.shape, k.stride())):
+            raise ValueError("the cache overlaps itself")
         pages, kv_heads, page_size, head_dim = k.shape
         # a stride over one entry says nothing: leave it out of the checks
         strides = [s if n > 1 else 0 for s, n in zip(k.stride()[:3], k.shape[:3])]
@@ -306,9 +323,9 @@ def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None)
         heads = q.shape[1] if q.dim() == 3 else -1
         _activation(q, "q", (T, heads, D), dtype, dev)
         if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=dtype, device=dev)
+            q_out = _empty((T, heads, D), dtype, q)
         else:
-            _activation(q_out, "q_out", (T, heads, D), dtype, dev)
+            _result(q_out, "q_out", (T, heads, D), dtype, dev)
         qp, op, qs, os = q.data_ptr(), q_out.data_ptr(), _strides(q, T, heads), _strides(q_out, T, heads)
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -365,10 +382,10 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
         _activation(q, "q", shape, dtype, dev)
     width, stride = _table(table, n, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
+        out = _empty(shape, dtype, q)
         os = (heads * D, D)
     else:
-        _activation(out, "out", shape, dtype, dev)
+        _result(out, "out", shape, dtype, dev)
         os = _strides(out, T, heads)
     args = _lib.BqAttentionArgs(_DTYPES[dtype], n, rows, heads, width, cache._scale if scale is None else scale, stride,
                                 *_strides(q, T, heads), *os, q.data_ptr(), out.data_ptr(),
@@ -437,16 +454,16 @@ def sandwich_norm(y, h, pre_gain=None, post_gain=None, gate=None, alpha=1.0, bet
         _dense(post_gain, "post_gain", torch.float32, dev, width)
         post = post_gain.data_ptr()
     if h_out is None:
-        h_out = torch.empty(shape, dtype=h_dtype, device=dev)
+        h_out = _empty(shape, h_dtype, h)
     else:
-        _activation(h_out, "h_out", shape, h_dtype, dev)
+        _result(h_out, "h_out", shape, h_dtype, dev)
     if pre_gain is not None:
         _dense(pre_gain, "pre_gain", torch.float32, dev, width)
         pre = pre_gain.data_ptr()
         if x_out is None:
-            x_out = torch.empty(shape, dtype=dtype, device=dev)
+            x_out = _empty(shape, dtype, y)
         else:
-            _activation(x_out, "x_out", shape, dtype, dev)
+            _result(x_out, "x_out", shape, dtype, dev)
         xp, xs = x_out.data_ptr(), x_out.stride(0)
     elif x_out is not None:
         raise ValueError("x_out without pre_gain")

@@ -423,6 +423,10 @@ def test_attention_refusals():
         bq.PagedKVCache(cache.k, cache.v, torch.zeros(1, device=DEV), None)
     with pytest.raises(TypeError):
         bq.PagedKVCache(cache.k.float(), cache.v.float())
+    with pytest.raises(ValueError, match="overlaps"):
+        bq.PagedKVCache(cache.k[:1].expand(4, -1, -1, -1), cache.v[:1].expand(4, -1, -1, -1))
+    with pytest.raises(ValueError, match="overlaps"):
+        bq.paged_attention(cache, q, table, lens, out=torch.zeros((1, 1, 64), device=DEV).expand(1, 4, 64))
     # no requests: nothing happens
     assert bq.paged_attention(cache, q[:0], table[:0], lens[:0]).shape == (0, 4, 64)
 

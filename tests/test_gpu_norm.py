@@ -124,6 +124,8 @@ def test_refusals():
         bq.sandwich_norm(y, y, g, gate=g.half())
     with pytest.raises(ValueError):
         bq.sandwich_norm(y, y, x_out=y)
+    with pytest.raises(ValueError, match="overlaps"):
+        bq.sandwich_norm(y, y, g, x_out=y[:1].expand(2, 64))
     with pytest.raises(bq.BQError):
         bq.sandwich_norm(y, y, g, eps=-1.0)
     with pytest.raises(bq.BQError):
