@@ -103,11 +103,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     if (gr < groups) *reinterpret_cast<float4 *>(sums + gr * D + 4 * v) = acc;
     __syncthreads();
     const long long at = (long long)token * a.x.out_row_stride + (long long)head * a.x.out_head_stride;
-    const bool empty = len - R + row + 1 <= 0;
     for (int d = tid; d < D; d += JOIN_THREADS) {
         float o = 0.0f;
         for (int k = 0; k < groups; ++k) o += sums[k * D + d];
-        o = empty ? 0.0f : o / sum;
+        o = sum == 0.0f ? 0.0f : o / sum;  // a row that sees nothing
         if constexpr (DT == BQ_F32) ((float *)a.x.out)[at + d] = o;
         else if constexpr (DT == BQ_F16) ((__half *)a.x.out)[at + d] = __float2half_rn(o);
         else ((__nv_bfloat16 *)a.x.out)[at + d] = __float2bfloat16_rn(o);
@@ -143,7 +142,6 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_few_kernel(const __grid_con
     float sum = f * ml.y;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const bool empty = len - R + row + 1 <= 0;
     const long long at = (long long)token * a.x.out_row_stride + (long long)head * a.x.out_head_stride;
     for (int d0 = 0; d0 < D; d0 += 128) {
         const int d = d0 + 4 * lane;
@@ -162,7 +160,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_few_kernel(const __grid_con
             const float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float y = empty ? 0.0f : v[x] / sum;
+                const float y = sum == 0.0f ? 0.0f : v[x] / sum;  // a row that sees nothing
                 if constexpr (DT == BQ_F32) ((float *)a.x.out)[at + d + x] = y;
                 else if constexpr (DT == BQ_F16) ((__half *)a.x.out)[at + d + x] = __float2half_rn(y);
                 else ((__nv_bfloat16 *)a.x.out)[at + d + x] = __float2bfloat16_rn(y);

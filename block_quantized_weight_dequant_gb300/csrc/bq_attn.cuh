@@ -10,7 +10,8 @@
 // chunks' over a thread-block cluster where the table holds few of them (the
 // call is one launch), else in a second kernel.  Which chunks exist depends on the geometry and
 // the length alone, and an empty chunk joins with weight zero, so a row's bits
-// depend on its own inputs and the geometry only.
+// depend on its own inputs and the geometry only.  The largest score's weight is 1
+// (2^SHIFT), so l is 0 for a row that sees nothing and for no other: it gives 0.
 //
 // Bound by HBM: every live byte of the cache is read once (again per 8 NT query
 // rows of a kv head, through L2), about 4 flop per byte and query row.  Measured:
@@ -852,9 +853,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                 __syncwarp();
                 if (lane == 0) m_s[i] = top, l_s[i] = sum;
             } else if (chunks == 1) {  // the result itself
-                const int row = (int)a.group.div((uint32_t)g);
-                const bool empty = len - R + row + 1 <= 0;
-                for (int d = lane; d < D; d += 32) attn_store(a, b, h, g, d, empty ? 0.0f : joined(d) / sum);
+                for (int d = lane; d < D; d += 32) attn_store(a, b, h, g, d, sum == 0.0f ? 0.0f : joined(d) / sum);
             } else {
                 if (lane == 0) a.part_ml[unit * ROWS + i] = make_float2(top, sum);
                 float *dst = a.part_o + (unit * ROWS + i) * D;
@@ -883,8 +882,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                         sum = fmaf(f, peer_float(l_at + 4 * i, k), sum);
                         v = fmaf(f, peer_float(o_at + 4 * (i * S::OROW + d), k), v);
                     }
-                const bool empty = len - R + (int)a.group.div((uint32_t)g) + 1 <= 0;
-                attn_store(a, b, h, g, d, empty ? 0.0f : v / sum);
+                attn_store(a, b, h, g, d, sum == 0.0f ? 0.0f : v / sum);
             }
             cluster_sync();  // shared memory stays until the others have read it
         }
@@ -926,7 +924,8 @@ int attn_occupancy(size_t smem, int *out) {
             [](const bq::AttnArgs &a, int grid, size_t smem, void *stream,                         \
                unsigned int *status) -> cudaError_t {                                              \
                 return bq::launch_pdl(bq::attn_kernel<KV, QP, PP, DP, NT>, dim3((unsigned)grid),   \
-                                      bq::AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, smem, stream, a.cluster ? a.max_chunks : 1, a, status);            \
+                                      bq::ATTN_WARPS * 32, smem, stream,                           \
+                                      a.cluster ? a.max_chunks : 1, a, status);                    \
             }                                                                                      \
     }
 #define BQ_ATTN_INSTS(NAME, KV, QP, PP)                                                            \

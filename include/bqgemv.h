@@ -477,10 +477,11 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
 /* Attention of the last `rows` tokens of each request over its cache:
  *   out[b, r, h] = sum_t softmax_t(scale * q[b, r, h] . k[t, h / group]) v[t, h / group]
  * over positions t < lens[b] - rows + r + 1 (lens counts the new tokens, which
- * have been appended), group = heads / kv_heads.  A row that sees no position
- * gives zeros.  What lies behind a row's positions (stale slots, later draft
- * tokens, NaN) does not reach it; a NaN or infinity within them makes the
- * head's row NaN.  A position whose table entry is outside the pool is
+ * have been appended), group = heads / kv_heads.  A row that sees no position,
+ * or only masked ones or scores of minus infinity, gives zeros.  What lies
+ * behind a row's positions (stale slots, later draft tokens, NaN) does not
+ * reach it; a NaN or infinity within them leaves the head's row NaN or infinite
+ * where it reaches it.  A position whose table entry is outside the pool is
  * treated as masked and sets BQ_DEVERR_PAGE; a length below 0 or beyond
  * table_width * page_size counts as the nearest and sets BQ_DEVERR_LENGTH.
  * Statistics and sums are fp32; with fp32 q the products are exact to fp32

@@ -323,6 +323,38 @@ def test_bad_pages_and_lengths_are_masked_and_reported():
     assert torch.equal(out, full)
 
 
+@pytest.mark.parametrize("kind,dtype,rows", [("f16", F32, 1), ("q8_0", BF16, 3)])
+@pytest.mark.parametrize("lens,width", [([40, 70], 8),       # a chunk each
+                                        ([1000, 300], 64),   # a cluster's chunks
+                                        ([5000, 700], 320),  # many chunks
+                                        ([5000] + [900] * 39, 320)])  # few chunks of many requests
+def test_a_request_of_bad_pages_alone_gives_zeros(kind, dtype, rows, lens, width):
+    """Every position masked: the row sees nothing.  The same with the positions
+    after the first 16 valid: the softmax is over those alone."""
+    g = rng(kind, rows, width, len(lens))
+    page, D, kv, n = 16, 64, 2, len(lens)
+    pages = sum(-(-x // page) for x in lens)
+    cache = filled_cache(g, kind, pages, page, kv, D)
+    table = request_tables(g, lens, page, pages, width)
+    q = normal(g, (n * rows, 2 * kv, D), dtype)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    clean = bq.paged_attention(cache, q, table, at, rows=rows)
+    broken = table.clone()
+    broken[0] = pages
+    out = bq.paged_attention(cache, q, broken, at, rows=rows)
+    assert bq.device_status(clear=True) == _lib.BQ_DEVERR_PAGE
+    assert (out[:rows] == 0).all() and torch.equal(out[rows:], clean[rows:])
+    broken[0] = table[0]
+    broken[0, 0] = -1
+    out = bq.paged_attention(cache, q, broken, at, rows=rows)
+    assert bq.device_status(clear=True) == _lib.BQ_DEVERR_PAGE
+    k, v = plain.values(cache)
+    want, mag, top = plain.attention(k, v, q[:rows].cpu(), table[:1, 1:].cpu(), [lens[0] - page], rows, D ** -0.5)
+    bound = plain.attention_bound(want, mag, top, dtype, kind == "q8_0" and dtype == BF16)
+    assert ((out[:rows].cpu().double() - want).abs() <= bound).all()
+    assert torch.equal(out[rows:], clean[rows:])
+
+
 def test_a_cache_of_more_than_2_to_31_elements():
     """Offsets that pass 32 bits: the pages in use lie at the end of a 10 GB cache."""
     page, D, pages = 256, 128, 80000
