@@ -25,6 +25,7 @@
 // quantizing warps' instructions); 4001 tokens of 16 + 4 + 4, bf16: 13 us; one
 // token: 2.8 us.
 #include <atomic>
+#include <cmath>
 #include <type_traits>
 
 #include "bq_cache.cuh"
@@ -57,13 +58,14 @@ struct Args {
 // so are their quotients below h, which therefore round to less than h.  So the
 // quotient's rounding does not matter: the code is the largest c with |x| >= (c -
 // 1/2) d, a comparison that one FMA decides.  The guess |x| / d + 1/2, rounded
-// down and taken a little small, is that c or one less.
+// down and taken a little small, is that c or one less.  A NaN ends at -127, as in
+// bq_quantize_pack.  d is not 0.
 __device__ __forceinline__ uint32_t q8_code(float x, float d, float inv) {
     const float v = fabsf(x);
     float c = __fadd_rd(__fmaf_rd(v, inv, 0.5f), 8388608.0f) - 8388608.0f;
     if (__fmaf_rn(-(c + 0.5f), d, v) >= 0.0f) c += 1.0f;
-    c = d != 0.0f ? fminf(c, 127.0f) : 0.0f;
-    return __float_as_uint(copysignf(c, x) + 12582912.0f);  // 1.5 2^23: the low bits are the whole number
+    c = fminf(fmaxf(copysignf(c, x), -127.0f), 127.0f);
+    return __float_as_uint(c + 12582912.0f);  // 1.5 2^23: the low bits are the whole number
 }
 
 // 4 elements to shared memory, asynchronously
@@ -286,7 +288,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                         p[0] = g0.x, p[1] = g0.y, p[2] = g0.z, p[3] = g0.w;
                         q[0] = g1.x, q[1] = g1.y, q[2] = g1.z, q[3] = g1.w;
                     }
-                    float m0 = 0.0f, m1 = 0.0f;
+                    // the largest magnitude: a NaN counts only where there is nothing else
+                    float m0 = NAN, m1 = NAN;
                     if (there) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) m0 = fmaxf(m0, fabsf(p[k])), m1 = fmaxf(m1, fabsf(q[k]));
@@ -311,7 +314,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                             for (int k = 0; k < 4; ++k) c[k] = q8_code(z[k], df, inv);
                             const uint32_t word = __byte_perm(__byte_perm(c[0], c[1], 0x0040),
                                                               __byte_perm(c[2], c[3], 0x0040), 0x5410);
-                            *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + f) = word;
+                            // (a scale of 0: the codes are 0)
+                            *reinterpret_cast<uint32_t *>((uint8_t *)plane + at + f) = df != 0.0f ? word : 0u;
                             if (writes_scale) scales[(at + f) >> 5] = d;
                         };
                         quantize(p, m0, f0, (f0 & 31) == 0);

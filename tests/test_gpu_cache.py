@@ -564,6 +564,37 @@ def test_append_odd_alignment_and_no_queries():
     bq.kv_append(cache, k[:0], v[:0], slots[:0])
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("D", [32, 96, 128, 256])
+def test_append_of_any_value_packs_as_the_weights_do(dtype, D):
+    """Q8_0 blocks with NaN (of either sign), infinities, zeros, values too small
+    for an fp16 scale and halfway values: bq_quantize_pack's blocks, bit for bit."""
+    g = rng(24, D, str(dtype))
+    T, kv = 40, 2
+    x = normal(g, (T, kv, D), dtype)
+    x[0] = float("nan")
+    x[1, :, ::5], x[2, :, ::7], x[3, :, 1::9] = float("nan"), float("inf"), float("-inf")
+    x[4, :, ::3] = -x[0, :, ::3]
+    x[5] = 0
+    x[6], x[7, :, 3] = 0, float("nan")
+    x[6, :, 0] = float("nan")
+    x[8] *= 1e-7
+    x[9] = torch.arange(D, device=DEV) % 32 - 15.5
+    x[10, :, ::32] = 127
+    x[10, :, 1::32] = 0.5
+    if dtype is not F16:
+        x[11] *= 1e9  # the scale is infinite
+        x[12] *= 1e-30
+    cache = bq.PagedKVCache.zeros(3, 16, kv, D, "q8_0")
+    bq.kv_append(cache, x, x.flip(0), torch.arange(T, device=DEV))
+    for codes, scales, want in ((cache.k, cache.k_scale, x), (cache.v, cache.v_scale, x.flip(0))):
+        packed = bq.quantize_pack(want.float().reshape(-1, D).contiguous(), "q8_0").cpu().numpy().reshape(T, kv, D // 32, 34)
+        got = codes.transpose(1, 2).reshape(48, kv, D)[:T].cpu().numpy()
+        scale = scales.transpose(1, 2).reshape(48, kv, D // 32)[:T].cpu().numpy()
+        assert np.array_equal(scale.view(np.uint16), packed[..., :2].copy().view(np.uint16)[..., 0])
+        assert np.array_equal(got, packed[..., 2:].view(np.int8).reshape(got.shape))
+
+
 def test_append_slots_beyond_the_pool_are_reported():
     g = rng(23)
     cache = bq.PagedKVCache.zeros(2, 16, 1, 64)
