@@ -364,7 +364,7 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     [requests, width] holds the requests' pages.  heads is a multiple of the
     cache's kv_heads.  A row that sees nothing gives zeros.  scale defaults to
     1 / sqrt(head_dim).  Row r's bits are those of the one-row call at its
-    length.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
+    length.  out may be q.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
     call that may overlap others; None: the stream's own, or in a capture one of
     the call's own."""
     if not isinstance(cache, PagedKVCache):
@@ -430,8 +430,8 @@ def sandwich_norm(y, h, pre_gain=None, post_gain=None, gate=None, alpha=1.0, bet
 
     y: the block's output; h: the residual stream, of y's dtype or fp32; gains
     fp32 [width]; gate of y's dtype, [width] or [rows, width].  Returns (h',
-    x'), x' of y's dtype (None without pre_gain).  h_out may be h, x_out may be
-    y."""
+    x'), x' of y's dtype (None without pre_gain).  y and h may be one tensor, and
+    h_out and x_out may each be y, h or a gate per row of their dtype."""
     _first(y, "y")
     dev, dtype, shape = y.device, y.dtype, y.shape
     if len(shape) != 2:

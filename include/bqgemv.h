@@ -416,7 +416,8 @@ typedef struct {
  * stack entries that are no longer in use are left as they were, and so are
  * the table's rows of requests that do not grow.
  *  - lens_out may be lens, free_count_out may be free_count; apart from that
- *    nothing overlaps (lens_out == new_lens returns BQ_ERR_SHAPE).  refused receives the number of refused requests.
+ *    nothing overlaps (lens_out == new_lens returns BQ_ERR_SHAPE).
+ *  - refused receives the number of refused requests.
  *  - 0 <= requests <= 4096, 1 <= page_size <= 65536, table_width >= 1,
  *    table_stride >= table_width, 0 <= max_tokens < 2^31 - 1, 1 <= pool < 2^31 - 1.
  *  - free_count outside 0 .. pool sets BQ_DEVERR_POOL and counts as the
@@ -491,7 +492,7 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
  * inputs alone: row r of a call with several rows is bit-identical to the
  * one-row call at the length that the row sees.
  *  - q, out: [requests * rows, heads, head_dim] of dtype, row and head strides
- *    in elements.  heads is a multiple of kv_heads, heads <= 4096; 1 <= rows
+ *    in elements.  out may be q, with the same strides.  heads is a multiple of kv_heads, heads <= 4096; 1 <= rows
  *    <= BQ_VERIFY_MAX_ROWS; 0 <= requests <= 4096; scale finite.
  *  - table: int32 [requests, table_width], rows table_stride apart,
  *    table_width * page_size <= 2^23.
@@ -522,7 +523,8 @@ bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *
  *  - dtype: of y, gate and x; h_dtype: of h and h_out; fp32 for h with any
  *    dtype, otherwise the same as dtype.  post, pre: fp32 [width].
  *  - gate: row stride 0 for one gate per channel.  Strides in elements.
- *  - h_out may be h, x may be y; otherwise outputs overlap nothing.
+ *  - y and h may be the same.  An output may be y, h or a gate per row if its
+ *    type and strides are the same; otherwise outputs overlap nothing.
  *  - 0 <= rows < 2^31, 1 <= width <= 16384; pointers aligned to their
  *    elements (16-byte aligned rows take the wide loads); eps finite, >= 0;
  *    alpha and beta finite. */

@@ -422,6 +422,55 @@ def test_attention_on_a_side_stream_and_in_graphs():
             assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("lens,width", [([40, 70], 8), ([1000, 300], 64), ([5000, 700], 320)])
+def test_the_output_may_be_the_queries(lens, width):
+    g = rng(12, width)
+    cache = filled_cache(g, "f16", 400, 16, 2, 64)
+    table = request_tables(g, lens, 16, 400, width)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q = normal(g, (4, 8, 64), F16)
+    want = bq.paged_attention(cache, q, table, at, rows=2)
+    assert bq.paged_attention(cache, q, table, at, rows=2, out=q) is q
+    assert torch.equal(q, want)
+
+
+def test_a_capture_that_forks_and_joins():
+    """Append and norm on a forked stream, attention after the join (two layers'
+    caches), replayed with other inputs: the eager calls' bits."""
+    g = rng(13)
+    page, width = 16, 320
+    caches = [filled_cache(g, "f16", 330, page, 2, 64) for _ in range(2)]
+    table = request_tables(g, [5000], page, 330, width)
+    lens = torch.tensor([5000], dtype=torch.int32, device=DEV)
+    slots = (table[0, 4999 // page].long() * page + 4999 % page).view(1)
+    k, v, q, gain = normal(g, (1, 2, 64)), normal(g, (1, 2, 64)), normal(g, (1, 8, 64)), torch.ones(512, device=DEV)
+
+    def step(side):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            bq.kv_append(caches[0], k, v, slots)
+            h, x = bq.sandwich_norm(q.view(1, 512), q.view(1, 512), gain)
+        bq.kv_append(caches[1], v, k, slots)
+        second = bq.paged_attention(caches[1], q, table, lens)
+        main.wait_stream(side)
+        first = bq.paged_attention(caches[0], x.view(1, 8, 64), table, lens)
+        return h, x, first, second
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        captured = step(side)
+    for _ in range(2):
+        for t in (k, v, q):
+            t.copy_(normal(g, t.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        for a, b in zip(got, step(side)):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+
+
 def test_attention_refusals():
     cache = bq.PagedKVCache.zeros(4, 16, 2, 64)
     table = torch.zeros((1, 2), dtype=torch.int32, device=DEV)

@@ -93,6 +93,23 @@ def test_in_place_strided_and_graph():
     assert torch.equal(again[0], hs) and torch.equal(again[1], xs)
 
 
+@pytest.mark.parametrize("rows,width", [(3, 64), (3, 2047), (2500, 1024), (700, 8192), (700, 5120), (400, 12345)])
+def test_outputs_over_inputs(rows, width):
+    """y, h and h_out one tensor; the outputs over each other's inputs; over a gate."""
+    g = np.random.default_rng([width, 9])
+    y, h, gate = (normal(g, (rows, width)) for _ in range(3))
+    pre, post = 1 + 0.1 * normal(g, (width,)), 1 + 0.1 * normal(g, (width,))
+    want = bq.sandwich_norm(h, h, pre, alpha=1.0, beta=0.0)
+    one = h.clone()
+    got = bq.sandwich_norm(one, one, pre, alpha=1.0, beta=0.0, h_out=one)
+    assert torch.equal(one, want[0]) and torch.equal(got[1], want[1])
+    want = bq.sandwich_norm(y, h, pre, post, gate)
+    for h_out, x_out in ((0, 1), (1, 0), (2, 1), (0, 2)):
+        t = [y.clone(), h.clone(), gate.clone()]
+        bq.sandwich_norm(t[0], t[1], pre, post, t[2], h_out=t[h_out], x_out=t[x_out])
+        assert torch.equal(t[h_out], want[0]) and torch.equal(t[x_out], want[1])
+
+
 def test_zero_rows_and_zero_values():
     width = 64
     z = torch.zeros((3, width), device=DEV)
