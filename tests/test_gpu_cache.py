@@ -355,6 +355,29 @@ def test_a_request_of_bad_pages_alone_gives_zeros(kind, dtype, rows, lens, width
     assert torch.equal(out[rows:], clean[rows:])
 
 
+@pytest.mark.parametrize("kind", ["f16", "q8_0"])
+@pytest.mark.parametrize("lens,page,width,heads,kv,D,rows", [
+    ([0, 1, 40, 17] * 1024, 16, 4, 2, 1, 32, 6),     # the most requests and rows
+    ([5, 700] * 2048, 64, 40, 1, 1, 32, 1),          # more units than wait for a CTA each
+    ([70, 3], 16, 5, 4096, 1024, 32, 1),             # the most heads
+    ([200], 65536, 128, 2, 1, 64, 2),                # the widest table, the largest page
+    ([200, 4], 1, 1 << 20, 2, 1, 64, 1),             # pages of one position in a wide table
+    ([90], 16, 6, 640, 1, 64, 6)])                   # 3840 query rows of one kv head
+def test_attention_at_its_limits(kind, lens, page, width, heads, kv, D, rows):
+    g = rng(kind, page, width, heads)
+    pages = sum(-(-x // page) for x in lens) + 1
+    cache = filled_cache(g, kind, pages, page, kv, D)
+    table = request_tables(g, lens, page, pages, width)
+    check_attention(cache, normal(g, (len(lens) * rows, heads, D)), table, lens, rows=rows)
+
+
+def test_append_at_its_limits():
+    g = rng(25)
+    check_append(g, "f16", F16, 3, 4096, 1024, 8, 0, None, False, 65536, 10)
+    check_append(g, "q8_0", F32, 2, 4096, 1024, 32, 32, None, False, 1, 10)
+    check_append(g, "bf16", F32, 700, 40, 8, 256, 256, [0, 0, 128], True, 16, 10)
+
+
 def test_a_cache_of_more_than_2_to_31_elements():
     """Offsets that pass 32 bits: the pages in use lie at the end of a 10 GB cache."""
     page, D, pages = 256, 128, 80000
