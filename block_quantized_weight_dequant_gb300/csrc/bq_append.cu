@@ -21,7 +21,7 @@
 // put in order through shared memory.
 //
 // Bound by HBM for a prompt, by latency for one token.  Measured: 8192 tokens of
-// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.8 TB/s; into Q8_0 61 us (the
+// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.8 TB/s; into Q8_0 54 us (the
 // quantizing warps' instructions); 4001 tokens of 16 + 4 + 4, bf16: 13 us; one
 // token: 2.8 us.
 #include <atomic>
@@ -46,6 +46,7 @@ struct Args {
     int parts;  // CTAs that share a token's heads
     int warps;  // of a CTA
     int batch;  // tokens at a time
+    int smem;   // of a CTA, beside the static
     int wide, wide_out;  // 4-element accesses of the inputs, of q_out
     // strides (below 2^31) as 32-bit numbers: a product with an index is one instruction
     uint32_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h, page_s, head_s, slot_s;
@@ -87,8 +88,9 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
     constexpr int DMAX = 8 * GL;
     __shared__ __align__(16) float2 cs_s[2][MAX_BATCH][HALF_MAX];
     __shared__ long long row_s[2][MAX_BATCH];
-    extern __shared__ __align__(16) uint8_t ahead_s[];  // [MAX_BATCH][UNROLL][2][threads] vectors
-    __shared__ __align__(16) float order_s[CT == BQ_Q8_0 ? MAX_WARPS * HPW * DMAX : 4];
+    // [MAX_BATCH][UNROLL][2][threads] vectors, then the heads of each warp at a time
+    // where Q8_0 blocks are put in order
+    extern __shared__ __align__(16) uint8_t ahead_s[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int sub = lane / GL, i = lane % GL;
     const int part = blockIdx.x % a.parts;
@@ -109,7 +111,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
     uint32_t src_step[UNROLL];
     T *out[UNROLL];            // of a query of token 0
     uint32_t head_at[UNROLL];  // of a key's or value's head in its page
-    bool any_kept = false;     // a key or value in this warp
+    bool any_kept[UNROLL];     // a key or value among this warp's heads
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
         const int item = ((part * UNROLL + u) * WARPS + warp) * HPW + sub;
@@ -122,14 +124,14 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
         out[u] = type[u] == 0 ? (T *)a.x.q_out + (uint64_t)head * a.o_h : nullptr;
         head_at[u] = head;
         if (!there && CT != BQ_Q8_0) type[u] = 3;
-        any_kept |= type[u] == 1 || type[u] == 2;
+        any_kept[u] = __any_sync(~0u, type[u] == 1 || type[u] == 2);
     }
-    any_kept = __any_sync(~0u, any_kept);
 
     // This lane's values of a token on their way into its own place in shared
     // memory, MAX_BATCH tokens ahead (rows that allow no wide access are read when
     // they are used).
     constexpr int VEC = 4 * (int)sizeof(T);
+    float *order_s = reinterpret_cast<float *>(ahead_s + MAX_BATCH * UNROLL * 2 * (int)blockDim.x * VEC);
     auto place = [&](int b, int u, int v) { return ahead_s + ((b * UNROLL + u) * 2 + v) * (int)blockDim.x * VEC + tid * VEC; };
     auto fetch = [&](long long t, int b) {
         if (a.wide && t < a.x.tokens) {
@@ -271,7 +273,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                 const long long at = row + (long long)((uint64_t)head_at[u] * a.head_s);
                 void *plane = type[u] == 1 ? a.c.k : a.c.v;
                 if constexpr (CT == BQ_Q8_0) {
-                    if (!any_kept) continue;  // only queries in this warp
+                    if (!any_kept[u]) continue;  // only queries
                     int f0 = e0, f1 = e1;     // where the quarters lie
                     bool rows_of_8 = !apart;
                     if (half % 32 && !a.x.interleaved) {  // rotated halves cut blocks: put in order
@@ -331,18 +333,22 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
     }
 }
 
+// shared memory of a warp: its values on their way, and the heads put in order
+constexpr int warp_smem(int element, bool order) {
+    return MAX_BATCH * UNROLL * 2 * 32 * 4 * element + (order ? 32 * 8 * 4 : 0);
+}
+
 template <class E, int CT>
 cudaError_t launch(const Args &a, int grid, void *stream) {
     auto *kern = a.c.head_dim <= 64    ? append_kernel<E, CT, 8>
                  : a.c.head_dim <= 128 ? append_kernel<E, CT, 16>
                                        : append_kernel<E, CT, 32>;
-    const size_t smem = (size_t)MAX_BATCH * UNROLL * 2 * a.warps * 32 * 4 * sizeof(typename E::T);
-    if (smem > 24 * 1024) {  // (up to 24 KB of static shared memory beside it)
+    if (a.smem > 24 * 1024) {  // (up to 9 KB of static shared memory beside it)
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   MAX_BATCH * UNROLL * 2 * MAX_WARPS * 32 * 16);
+                                                   MAX_WARPS * warp_smem(4, true));
         if (e != cudaSuccess) return e;
     }
-    return bq::launch_pdl(kern, dim3((unsigned)grid), a.warps * 32, smem, stream, 1, a);
+    return bq::launch_pdl(kern, dim3((unsigned)grid), a.warps * 32, (size_t)a.smem, stream, 1, a);
 }
 template <class E>
 cudaError_t launch(const Args &a, int grid, void *stream) {
@@ -435,9 +441,13 @@ extern "C" bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_a
     a.warps = (warps + a.parts - 1) / a.parts;
     const int least = 4 * gl / 32 > 4 ? 4 * gl / 32 : 4;
     if (a.warps < least) a.warps = least;
-    // as many CTAs as are resident together (24 warps of 80 registers per SM), at
-    // MAX_BATCH tokens at a time if there are that many
-    const long long fit = (long long)sms * (24 / a.warps);
+    // as many CTAs as are resident together (24 warps of 80 registers per SM, 227 KB
+    // of shared memory with the angles and 1 KB of each CTA's own), at MAX_BATCH
+    // tokens at a time if there are that many
+    const bool order = cache->type == BQ_Q8_0 && x->freq && x->rot / 2 % 32 && !x->interleaved;
+    a.smem = a.warps * warp_smem(es, order);
+    const int by_smem = 228 * 1024 / (a.smem + 2 * MAX_BATCH * 4 * gl * 8 + 1024 + 256);
+    const long long fit = (long long)sms * (24 / a.warps < by_smem ? 24 / a.warps : by_smem);
     const long long each = (x->tokens * a.parts + fit - 1) / fit;
     a.batch = each < 1 ? 1 : each > MAX_BATCH ? MAX_BATCH : (int)each;
     const long long groups = (x->tokens + a.batch - 1) / a.batch;
