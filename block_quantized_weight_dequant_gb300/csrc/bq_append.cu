@@ -21,8 +21,7 @@
 // put in order through shared memory.
 //
 // Bound by HBM for a prompt, by latency for one token.  Measured: 8192 tokens of
-// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.8 TB/s; into Q8_0 54 us (the
-// quantizing warps' instructions); 4001 tokens of 16 + 4 + 4, bf16: 13 us; one
+// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.7 TB/s; into Q8_0 48 us, 5.7 TB/s; 4001 tokens of 16 + 4 + 4, bf16: 13 us; one
 // token: 2.8 us.
 #include <atomic>
 #include <cmath>
@@ -58,15 +57,17 @@ struct Args {
 // fp32 number; the fp32 numbers below it are below it by 2^-24 of it or more, and
 // so are their quotients below h, which therefore round to less than h.  So the
 // quotient's rounding does not matter: the code is the largest c with |x| >= (c -
-// 1/2) d, a comparison that one FMA decides.  The guess |x| / d + 1/2, rounded
-// down and taken a little small, is that c or one less.  A NaN ends at -127, as in
-// bq_quantize_pack.  d is not 0.
-__device__ __forceinline__ uint32_t q8_code(float x, float d, float inv) {
+// 1/2) d.  The guess, |x| / d taken a little small (`inv` is 1 / d less 2^-21 of it or
+// more) and rounded to nearest, is that c or one less.  rest = |x| - guess d is
+// exact: at most d in magnitude and a multiple of |x|'s last place or of d's, so
+// rest >= d / 2 decides.  A NaN ends at -127, as in bq_quantize_pack.  d is not 0.
+__device__ __forceinline__ uint32_t q8_code(float x, float d, float half_d, float inv) {
+    constexpr float WHOLE = 12582912.0f;  // 1.5 2^23: added, the low bits are the whole number
     const float v = fabsf(x);
-    float c = __fadd_rd(__fmaf_rd(v, inv, 0.5f), 8388608.0f) - 8388608.0f;
-    if (__fmaf_rn(-(c + 0.5f), d, v) >= 0.0f) c += 1.0f;
+    float c = __fadd_rn(__fmaf_rn(v, inv, WHOLE), -WHOLE);
+    if (__fmaf_rn(-c, d, v) >= half_d) c += 1.0f;
     c = fminf(fmaxf(copysignf(c, x), -127.0f), 127.0f);
-    return __float_as_uint(c + 12582912.0f);  // 1.5 2^23: the low bits are the whole number
+    return __float_as_uint(c + WHOLE);
 }
 
 // 4 elements to shared memory, asynchronously
@@ -226,7 +227,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
         __syncthreads();  // (the batch after the next rewrites this buffer, two barriers on)
 
         look_up(t0 + stride);
-#pragma unroll
+        // (unrolled, the quantizer's code outgrows the instruction cache: 8192 tokens 54 us against 50)
+#pragma unroll (CT == BQ_Q8_0 ? 1 : MAX_BATCH)
         for (int b = 0; b < MAX_BATCH; ++b) {
             asm volatile("cp.async.wait_group %0;" ::"n"(MAX_BATCH - 1) : "memory");
             float y[UNROLL][2][4];
@@ -309,11 +311,12 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                         auto quantize = [&](const float(&z)[4], float m, int f, bool writes_scale) {
                             const __half d = __float2half_rn(__fdiv_rn(m, 127.0f));
                             const float df = __half2float(d);
-                            // a little below 1 / d, so that the first guess is never too large
-                            const float inv = df != 0.0f ? __fdiv_rn(1.0f - 0x1p-20f, df) : 0.0f;
+                            // a little below 1 / d (the quotient is good to 2 ulp), so that the
+                            // guess is never too large
+                            const float inv = __fdividef(1.0f - 0x1p-20f, df), half_d = 0.5f * df;
                             uint32_t c[4];
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) c[k] = q8_code(z[k], df, inv);
+                            for (int k = 0; k < 4; ++k) c[k] = q8_code(z[k], df, half_d, inv);
                             const uint32_t word = __byte_perm(__byte_perm(c[0], c[1], 0x0040),
                                                               __byte_perm(c[2], c[3], 0x0040), 0x5410);
                             // (a scale of 0: the codes are 0)
