@@ -21,8 +21,8 @@
 // put in order through shared memory.
 //
 // Bound by HBM for a prompt, by latency for one token.  Measured: 8192 tokens of
-// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.7 TB/s; into Q8_0 48 us, 5.7 TB/s; 4001 tokens of 16 + 4 + 4, bf16: 13 us; one
-// token: 2.8 us.
+// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.7 TB/s; into Q8_0 48 us, 5.7
+// TB/s; 4001 tokens of 16 + 4 + 4, bf16: 13 us; one token: 2.8 us.
 #include <atomic>
 #include <cmath>
 #include <type_traits>
@@ -436,13 +436,15 @@ extern "C" bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_a
     a.page_s = (uint32_t)cache->page_stride, a.head_s = (uint32_t)cache->head_stride;
     a.slot_s = (uint32_t)cache->slot_stride;
     // A CTA has a warp for every 2 HPW heads of a token, and enough to turn a
-    // token's pairs; more heads go to more CTAs, each with the angles once more.
+    // token's pairs (a warp left over idles: 16000 tokens of 2 + 2 heads of 64 in
+    // four warps 17 us, in one 10); more heads go to more CTAs, each with the angles
+    // once more.
     const int gl = cache->head_dim <= 64 ? 8 : cache->head_dim <= 128 ? 16 : 32;
     const int of_warp = UNROLL * (32 / gl);
     const int warps = (a.items + of_warp - 1) / of_warp;
     a.parts = (warps + MAX_WARPS - 1) / MAX_WARPS;
     a.warps = (warps + a.parts - 1) / a.parts;
-    const int least = 4 * gl / 32 > 4 ? 4 * gl / 32 : 4;
+    const int least = 4 * gl / 32;
     if (a.warps < least) a.warps = least;
     // as many CTAs as are resident together (24 warps of 80 registers per SM, 227 KB
     // of shared memory with the angles and 1 KB of each CTA's own), at MAX_BATCH
