@@ -17,7 +17,8 @@
 // rows of a kv head, through L2), about 4 flop per byte and query row.  Measured:
 // 48 requests to 12001 positions, bf16, 32 heads over 8, 1.32 GB: 201 us, 6.6 TB/s;
 // one request of 100003, fp16: 40 us, 5.1 TB/s; Q8_0 is bound by instructions
-// (48 requests to 6000: 84 us, 4.2 TB/s; 5 rows of 40 heads over 8 at 24577: 52 us).
+// (48 requests to 6000, bf16 queries: 85 us, 4.2 TB/s; 5 rows of 40 heads over 8 at
+// 24577: 53 us).
 // So the kernel is built around the loads:
 //  - Every warp has a ring of STAGES tiles of K and V rows in shared memory
 //    that it fills itself by 16-byte asynchronous copies (any page size and
