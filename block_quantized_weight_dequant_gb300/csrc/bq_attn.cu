@@ -202,7 +202,10 @@ struct Plan {
 //  - Else the table's capacity is cut into about TARGET units (two CTAs per SM,
 //    one wave), 128 positions at least (two tiles per warp) and 2048 at most (so
 //    that the longest table, 2^23 positions, has 4096 units, whose weights the
-//    join keeps in shared memory).
+//    join keeps in shared memory).  Finer units for ragged requests cost more in
+//    starts and joins than they balance (8 requests to 30000, 2 kv heads: 74 us
+//    against 82, 77 and 82 with two, four and eight times the units; 16 to 4000, 8 kv
+//    heads: 38 against 43, 44, 49).
 constexpr int64_t TARGET = 304, CHUNK_MIN = 128, CHUNK_MAX = 2048, CLUSTER_CHUNK = 256;
 struct Chunking {
     int chunk;
