@@ -4,5 +4,5 @@
 
 #include "bq_attn.cuh"
 
-BQ_ATTN_UNIT(bf16_own, BQ_ATTN_INSTS(bf16_own, bq::KV_BF16, 1, 2),
-             BQ_ATTN_INST(bf16_own, bq::KV_BF16, 1, 2, 64, 4), BQ_ATTN_INST(bf16_own, bq::KV_BF16, 1, 2, 128, 4))
+BQ_ATTN_UNIT(bf16_own, BQ_ATTN_INSTS(bf16_own, bq::KV_BF16, 1, 3),
+             BQ_ATTN_INST(bf16_own, bq::KV_BF16, 1, 3, 64, 4), BQ_ATTN_INST(bf16_own, bq::KV_BF16, 1, 3, 128, 4))

@@ -278,6 +278,48 @@ def test_scores_and_scales_of_any_size(kind):
     check_attention(cache, torch.zeros_like(q), table, lens)
 
 
+WEIGHT_KINDS = [("f16", F16), ("f16", F32), ("f16", BF16), ("bf16", BF16), ("bf16", F32), ("bf16", F16)]
+
+
+def check_weights(kind, dtype, heads, kv):
+    """Weights to fp32 rounding, whatever type the queries have.  Three positions a
+    head: the first of score 0 and value 0; the others, of scores a < 0 and a +
+    2^-17 and values 1 and -1, leave the difference of two weights w next to each
+    other.  Scores are exact sums.  A weight's error: half a step of its argument
+    beside the shift of 15 (2^-21, times ln 2), two ulp of the power of two (2^-22),
+    the scale's and the products' rounding (2^-23 of at most 1) and the parts' 2^-23:
+    below 2^-20 of it.  The difference is off by that of both weights, over their sum
+    and 1, and by the tensor core's sum of three products, 2^-23 each: below 2^-20
+    in all; then the output's own rounding."""
+    D, page = 64, 16
+    shape = (1, kv, page, D)
+    k, v = torch.zeros(shape), torch.zeros(shape)
+    k[..., 1:3, 0], k[..., 2, 1] = 1.0, 1.0
+    v[..., 1, :], v[..., 2, :] = 1.0, -1.0
+    if kind == "q8_0":
+        scale = torch.full((1, kv, page, D // 32), 2.0 ** -6, dtype=F16, device=DEV)
+        cache = bq.PagedKVCache((k * 64).to(torch.int8).to(DEV), (v * 64).to(torch.int8).to(DEV), scale, scale.clone())
+    else:
+        t = {"f16": F16, "bf16": BF16}[kind]
+        cache = bq.PagedKVCache(k.to(t).to(DEV), v.to(t).to(DEV))
+    q = torch.zeros((1, heads, D), dtype=torch.float64)
+    q[0, :, 0] = -(torch.arange(heads) + 40.0) / 128  # 8 bits or fewer: exact in every type
+    q[0, :, 1] = 2.0 ** -17
+    table = torch.zeros((1, 1), dtype=torch.int32, device=DEV)
+    lens = torch.tensor([3], dtype=torch.int32, device=DEV)
+    got = bq.paged_attention(cache, q.to(dtype).to(DEV), table, lens, scale=1.0).cpu().double()
+    w1, w2 = torch.exp(q[0, :, 0]), torch.exp(q[0, :, 0] + q[0, :, 1])
+    want = ((w1 - w2) / (1 + w1 + w2))[None, :, None].expand_as(got)
+    bound = 2.0 ** -20 + plain.EPS[dtype] / 2 * (want.abs() + 2.0 ** -20) + (2.0 ** -25 if dtype is F16 else 0.0)
+    assert ((got - want).abs() <= bound).all(), float((got - want).abs().max())
+
+
+@pytest.mark.parametrize("kind,dtype", WEIGHT_KINDS)
+@pytest.mark.parametrize("heads,kv", [(48, 48), (48, 6), (48, 4), (48, 1)])
+def test_weights_are_good_to_fp32_rounding(kind, dtype, heads, kv):
+    check_weights(kind, dtype, heads, kv)
+
+
 def test_strided_queries_and_outputs():
     g = rng(8)
     lens, page = [130, 20, 5], 16
