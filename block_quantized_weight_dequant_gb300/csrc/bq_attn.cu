@@ -262,8 +262,7 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     const bq::AttnInstance *inst =
         c->type == BQ_F16      ? (same ? bq_internal_attn_f16_own(&n) : bq_internal_attn_f16_split(&n))
         : c->type == BQ_BF16   ? (same ? bq_internal_attn_bf16_own(&n) : bq_internal_attn_bf16_split(&n))
-        : x->dtype == BQ_F16   ? bq_internal_attn_q8_0_own(&n)
-        : x->dtype == BQ_BF16  ? bq_internal_attn_q8_0_bf16(&n)
+        : x->dtype != BQ_F32   ? bq_internal_attn_q8_0_own(&n)
                                : bq_internal_attn_q8_0_split(&n);
     p->inst = nullptr;
     for (int i = 0; i < n; ++i)

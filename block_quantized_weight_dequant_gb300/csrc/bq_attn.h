@@ -51,5 +51,4 @@ const bq::AttnInstance *bq_internal_attn_f16_split(int *n);
 const bq::AttnInstance *bq_internal_attn_bf16_own(int *n);
 const bq::AttnInstance *bq_internal_attn_bf16_split(int *n);
 const bq::AttnInstance *bq_internal_attn_q8_0_own(int *n);
-const bq::AttnInstance *bq_internal_attn_q8_0_bf16(int *n);
 const bq::AttnInstance *bq_internal_attn_q8_0_split(int *n);

@@ -1,4 +1,4 @@
-// bq_attn_q8_0_own.cu -- paged attention over a Q8_0 cache, fp16 queries (bq_attn.cuh).
+// bq_attn_q8_0_own.cu -- paged attention over a Q8_0 cache, 16-bit queries (bq_attn.cuh).
 #include <atomic>
 #include <type_traits>
 

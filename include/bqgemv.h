@@ -485,9 +485,12 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
  * where it reaches it.  A position whose table entry is outside the pool is
  * treated as masked and sets BQ_DEVERR_PAGE; a length below 0 or beyond
  * table_width * page_size counts as the nearest and sets BQ_DEVERR_LENGTH.
- * Statistics and sums are fp32; with fp32 q the products are exact to fp32
- * rounding (queries and probabilities are carried as several 16-bit parts),
- * otherwise probabilities are.  For one geometry (requests, table_width,
+ * Statistics and sums are fp32.  q of the cache's type enters the products as
+ * it is, 16-bit q over a Q8_0 cache to 2^-39 of its row's largest value.  Other
+ * q and all probabilities are carried as 16-bit parts that add up to them:
+ * over a BQ_BF16 cache exactly (24 bits), over BQ_F16 and BQ_Q8_0 caches to
+ * 2^-23 of the number, or 2^-39 of the largest of its row where that is more
+ * (of the probabilities times value scales, for BQ_Q8_0).  For one geometry (requests, table_width,
  * page_size, kv_heads, head_dim, types) each row's bits depend on its own
  * inputs alone: row r of a call with several rows is bit-identical to the
  * one-row call at the length that the row sees.

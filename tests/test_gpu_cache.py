@@ -320,6 +320,12 @@ def test_weights_are_good_to_fp32_rounding(kind, dtype, heads, kv):
     check_weights(kind, dtype, heads, kv)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("heads,kv", [(48, 48), (48, 6), (48, 4), (48, 1)])
+def test_weights_over_a_q8_0_cache_are_good_to_fp32_rounding(dtype, heads, kv):
+    check_weights("q8_0", dtype, heads, kv)
+
+
 def test_strided_queries_and_outputs():
     g = rng(8)
     lens, page = [130, 20, 5], 16
