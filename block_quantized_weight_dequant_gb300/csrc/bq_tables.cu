@@ -292,7 +292,7 @@ extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
     int cluster = 1;
     while (cluster < MAX_CLUSTER && work > 2LL * THREADS * cluster) cluster *= 2;
     const size_t smem = (size_t)(5 * (t->requests + 1)) * sizeof(int);
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {  // (400 bytes of static shared memory count against the 48 KB too)
         const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)(5 * (MAX_REQUESTS + 1) * sizeof(int)));
         if (e != cudaSuccess) return bq::from_cuda_error(e);

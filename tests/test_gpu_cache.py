@@ -810,6 +810,27 @@ def test_block_tables(n, page, in_place):
     check_tables(old, new, page, width, pool, rows + 6000, g, in_place=in_place)
 
 
+def test_block_tables_of_every_shared_memory_size():
+    """Around the request counts whose shared memory passes 48 KB (with the kernel's
+    static part, 2437 and more), in a process that has made no larger call."""
+    code = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import numpy as np
+import test_gpu_cache as t
+g = t.rng(34)
+for n in (2405, 2406, 2407, 2436, 2437, 2440, 2456, 2457, 2458):
+    old = g.integers(0, 40, n)
+    new = np.where(g.random(n) < 0.9, old + 1, 0)
+    t.check_tables(old, new, 16, 4, 4 * n, n, g)
+print("fine")
+"""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", code.format(root=os.path.dirname(tests), tests=tests)], capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
 @pytest.mark.parametrize("seed", range(6))
 def test_block_tables_refuse_what_does_not_fit(seed):
     g = rng(seed, 31)
