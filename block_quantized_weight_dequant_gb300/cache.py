@@ -103,24 +103,6 @@ def _table(t, n, device):
     return width, (t.stride(0) if n > 1 else width)
 
 
-_KEPT = 256 << 20  # a larger workspace goes back to the allocator after its call
-_workspaces = {}  # (device, stream) -> the largest workspace that its calls have needed
-
-
-def _workspace(nbytes, device):
-    """Workspace of a call on the current stream.  Calls on one stream follow one
-    another, so they share one that stays with the stream; a captured call gets its
-    own, which its graph keeps, since graphs may be replayed side by side."""
-    if nbytes > _KEPT or torch.cuda.is_current_stream_capturing():
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    index = device.index
-    key = (index, _raw_stream(index))
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = _workspaces[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return ws
-
-
 def _call(fn, what, device, *args):
     """fn(*args, stream) on `device`'s current stream."""
     index = device.index
@@ -365,8 +347,8 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     cache's kv_heads.  A row that sees nothing gives zeros.  scale defaults to
     1 / sqrt(head_dim).  Row r's bits are those of the one-row call at its
     length.  out may be q.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
-    call that may overlap others; None: the stream's own, or in a capture one of
-    the call's own."""
+    call that may overlap others, also calls of two host threads on one stream;
+    None: one of the call's own from PyTorch's allocator."""
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")
     dev, D = cache.device, cache.head_dim
@@ -400,8 +382,12 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
                 if len(cache._workspace) >= 1024:
                     cache._workspace.clear()
                 cache._workspace[key] = nbytes
+        # One of the call's own, not one that stays with the stream: two threads may
+        # launch on it at once (the call is two kernels), a graph keeps what it captured,
+        # and a handle does not say which stream it was.  The allocator hands it on in
+        # the stream's order.
         if nbytes > 0:
-            workspace = _workspace(nbytes, dev)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:
         _dense(workspace, "workspace", torch.uint8, dev)
         nbytes = workspace.numel()

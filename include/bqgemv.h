@@ -501,7 +501,8 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
  *    table_width * page_size <= 2^23.
  *  - workspace: bq_paged_attention_workspace_bytes bytes, 16-byte aligned;
  *    need not be initialised; not shared by calls that may overlap on the GPU
- *    (two streams, two captured graphs). */
+ *    (two streams, two captured graphs) or that two host threads make at once
+ *    on one stream (a call may be two launches, and others come between). */
 typedef struct {
     int32_t dtype, requests, rows, heads, table_width;
     float scale;

@@ -2,8 +2,11 @@
 without a GPU: every refusal of the C ABI and of the binding, the division by a
 launch constant, and how attention calls are cut."""
 import ctypes
-import re
+import gc
 import os
+import re
+import threading
+import weakref
 
 import pytest
 import torch
@@ -265,3 +268,59 @@ def test_other_objects_are_refused():
         bq.PagedKVCache([[1]], [[1]])
     with pytest.raises(ValueError, match="kind"):
         bq.PagedKVCache.zeros(2, 4, 1, 32, kind="q4_0")
+
+
+# ---- workspaces, with CPU tensors in place of the GPU's and no launch ----
+def host_attention(monkeypatch, call):
+    """A paged_attention call that needs a workspace, `call` in place of the
+    library's (it gets the workspace's address)."""
+    from block_quantized_weight_dequant_gb300 import cache as mod
+    for name in ("_dense", "_first", "_activation", "_result"):
+        monkeypatch.setattr(mod, name, lambda *a, **k: None)
+    monkeypatch.setattr(mod, "_table", lambda t, n, device: (t.shape[1], t.shape[1]))
+    monkeypatch.setattr(mod, "_raw_stream", lambda index: 0)  # one stream for all calls
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)  # (of the current device)
+    monkeypatch.setattr(mod, "_call", lambda fn, what, device, cache, args, ws, nbytes: call(ws))
+    c = object.__new__(bq.PagedKVCache)
+    c.device, c.kv_heads, c.head_dim, c._scale, c._workspace = torch.device("cpu"), 4, 128, 0.1, {}
+    c._c = cache()
+    c._ref = ctypes.byref(c._c)
+    q, table = torch.zeros(1, 16, 128), torch.zeros(1, 4096, dtype=torch.int32)
+    return lambda: bq.paged_attention(c, q, table, torch.ones(1, dtype=torch.int32))
+
+
+def test_calls_of_two_threads_at_once_have_workspaces_of_their_own(monkeypatch):
+    """Both may launch on one stream, their kernels in turn."""
+    both, seen = threading.Barrier(2, timeout=30), []
+
+    def call(ws):
+        if threading.current_thread() is not threading.main_thread():
+            seen.append(ws)
+            both.wait()
+
+    attend = host_attention(monkeypatch, call)
+    attend()
+    threads = [threading.Thread(target=attend) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(seen) == 2 and None not in seen and seen[0] != seen[1]
+
+
+def test_no_workspace_outlives_its_call(monkeypatch):
+    """A kept one would be shared by whatever comes under the same stream handle:
+    a captured call beside eager ones, a stream made after another's end, the
+    threads' default streams."""
+    made, empty = [], torch.empty
+
+    def record(*a, **k):
+        t = empty(*a, **k)
+        if t.dtype == torch.uint8:
+            made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(torch, "empty", record)
+    host_attention(monkeypatch, lambda ws: None)()
+    gc.collect()
+    assert len(made) == 1 and made[0]() is None

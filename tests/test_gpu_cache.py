@@ -4,6 +4,7 @@ where it can go wrong, and a run of them together as a server would use them."""
 import os
 import subprocess
 import sys
+import threading
 import zlib
 
 import numpy as np
@@ -491,6 +492,31 @@ def test_attention_on_a_side_stream_and_in_graphs():
         want = check_attention(cache, q, table, n)
         for _, out in graphs:
             assert torch.equal(out, want)
+
+
+def test_two_threads_on_one_stream():
+    """Calls of two kernels each, launched by two host threads in turn on the
+    default stream: each thread's results are those of its calls alone."""
+    g = rng(14)
+    cache = filled_cache(g, "f16", 400, 16, 2, 64)
+    calls = []
+    for lens in ([5000, 60], [1000, 5100]):
+        table, at = request_tables(g, lens, 16, 400, 320), torch.tensor(lens, dtype=torch.int32, device=DEV)
+        q = normal(g, (2, 8, 64))
+        calls.append((q, table, at, bq.paged_attention(cache, q, table, at)))
+    wrong = [0, 0]
+
+    def work(i):
+        q, table, at, want = calls[i]
+        got = [bq.paged_attention(cache, q, table, at) for _ in range(300)]
+        wrong[i] = sum(not torch.equal(x, want) for x in got)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == [0, 0]
 
 
 @pytest.mark.parametrize("lens,width", [([40, 70], 8), ([1000, 300], 64), ([5000, 700], 320)])
