@@ -2,6 +2,7 @@
 positions and attention, each against a plain 64-bit form at the sizes and masks
 where it can go wrong, and a run of them together as a server would use them."""
 import os
+import re
 import subprocess
 import sys
 import threading
@@ -980,3 +981,19 @@ def test_a_server_step_by_step(kind):
         last = (t.starts[1:].long() - 1).clamp(min=0)
         check_attention(cache, turned[last].contiguous(), t.table, t.lens.tolist())
         assert lens is not None and n == sum(max(0, z - a) for a, z in zip(lens, goal))
+
+
+def test_the_example_of_the_readme():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        code = re.search(r"```python\n(.*?)```", f.read(), flags=re.S).group(1)
+    said = {}
+    exec(code, said)
+    n = said["requests"]
+    assert said["tables"].lens.tolist() == [1] * n and int(said["refused"]) == 0
+    # one position: its value, as the cache holds it
+    v = plain.values(said["cache"])[1]
+    for b in range(n):
+        row = v[int(said["tables"].table[b, 0]), :, 0].repeat_interleave(said["heads"] // said["kv_heads"], 0)
+        assert ((said["out"][b].cpu().double() - row).abs() <= 2.0 ** -20 * row.abs()).all()
+    assert torch.isfinite(said["h"]).all() and torch.isfinite(said["x"]).all()
