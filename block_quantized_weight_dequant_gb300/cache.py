@@ -417,7 +417,8 @@ def sandwich_norm(y, h, pre_gain=None, post_gain=None, gate=None, alpha=1.0, bet
     y: the block's output; h: the residual stream, of y's dtype or fp32; gains
     fp32 [width]; gate of y's dtype, [width] or [rows, width].  Returns (h',
     x'), x' of y's dtype (None without pre_gain).  y and h may be one tensor, and
-    h_out and x_out may each be y, h or a gate per row of their dtype."""
+    h_out and x_out, apart from one another, may each be y, h or a gate per row of
+    their dtype."""
     _first(y, "y")
     dev, dtype, shape = y.device, y.dtype, y.shape
     if len(shape) != 2:

@@ -331,6 +331,7 @@ extern "C" bq_status bq_sandwich_norm(const bq_sandwich_args *x, void *stream) {
     if (!bq::aligned_to(x->h, (uintptr_t)eh) || !bq::aligned_to(x->h_out, (uintptr_t)eh) ||
         !bq::aligned_to(x->post, 4) || !bq::aligned_to(x->pre, 4))
         return BQ_ERR_ALIGN;
+    if (x->x == x->h_out) return BQ_ERR_SHAPE;  // one would be written over the other
     const int sms = bq::device_sms();
     if (!sms) return BQ_ERR_CUDA;
     Args a;

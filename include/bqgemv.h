@@ -528,7 +528,8 @@ bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *
  *    dtype, otherwise the same as dtype.  post, pre: fp32 [width].
  *  - gate: row stride 0 for one gate per channel.  Strides in elements.
  *  - y and h may be the same.  An output may be y, h or a gate per row if its
- *    type and strides are the same; otherwise outputs overlap nothing.
+ *    type and strides are the same; otherwise outputs overlap nothing, nor one
+ *    another (x == h_out returns BQ_ERR_SHAPE).
  *  - 0 <= rows < 2^31, 1 <= width <= 16384; pointers aligned to their
  *    elements (16-byte aligned rows take the wide loads); eps finite, >= 0;
  *    alpha and beta finite. */

@@ -203,6 +203,11 @@ def test_sandwich_arguments(lib, over, status):
     assert lib.bq_sandwich_norm(None, None) == NULL
 
 
+def test_sandwich_outputs_are_apart(lib):
+    """The same address for both outputs, as `h_out=y, x_out=y` gives it."""
+    assert lib.bq_sandwich_norm(sandwich(rows=1, h_out=A + 4096, x=A + 4096), None) == SHAPE
+
+
 def test_structs_match_the_header():
     """Field names and order of the ctypes structs are those of the header."""
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "bqgemv.h")).read()
