@@ -32,6 +32,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _i32(n):
+    """n for a 32-bit field of the C ABI: -1, which is refused, for a number that
+    ctypes would cut short."""
+    n = int(n)
+    return n if -(1 << 31) <= n < 1 << 31 else -1
+
+
 def _need(t, name, dtype=None, like=None):
     """A CUDA tensor of the given dtype on the device of `like`."""
     if not isinstance(t, _Tensor):
@@ -242,7 +249,7 @@ def kv_block_tables(lens, new_lens, table, free_pages, free_count, page_size, sl
     _dense(lens_out, "lens_out", i32, dev, n)
     _dense(free_count_out, "free_count_out", i32, dev, 1)
     _dense(refused, "refused", i32, dev, 1)
-    args = _lib.BqKvTables(n, int(page_size), width, free_pages.numel(), stride, slots.numel(),
+    args = _lib.BqKvTables(n, _i32(page_size), width, _i32(free_pages.numel()), stride, slots.numel(),
                            lens.data_ptr(), new_lens.data_ptr(), table.data_ptr(), free_pages.data_ptr(),
                            free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(), starts.data_ptr(),
                            lens_out.data_ptr(), free_count_out.data_ptr(), refused.data_ptr())
@@ -398,7 +405,7 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
 
 def paged_attention_workspace(cache, requests, rows, heads, width):
     """Bytes of workspace of a paged_attention call of this geometry."""
-    args = _lib.BqAttentionArgs(_lib.BQ_F32, requests, rows, heads, width, 1.0, width)
+    args = _lib.BqAttentionArgs(_lib.BQ_F32, _i32(requests), _i32(rows), _i32(heads), _i32(width), 1.0, int(width))
     nbytes = lib.bq_paged_attention_workspace_bytes(cache._ref, ctypes.byref(args))
     if nbytes < 0:
         raise ValueError(f"no paged_attention of requests={requests} rows={rows} heads={heads} width={width}")

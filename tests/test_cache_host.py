@@ -167,6 +167,18 @@ def test_the_cut_does_not_depend_on_the_query_rows(lib, requests, kv_heads, widt
     assert len(cuts) == 1
 
 
+@pytest.mark.parametrize("over", [dict(requests=(1 << 32) + 1), dict(rows=(1 << 32) + 1), dict(heads=(1 << 32) + 16),
+                                  dict(width=(1 << 32) + 8), dict(rows=1 << 31)])
+def test_sizes_beyond_32_bits_are_not_cut_short(lib, over):
+    class Held:
+        _c = cache()
+        _ref = ctypes.byref(_c)
+
+    assert bq.paged_attention_workspace(Held, 1, 1, 16, 4096) > 0
+    with pytest.raises(ValueError):
+        bq.paged_attention_workspace(Held, **dict(dict(requests=1, rows=1, heads=16, width=8), **over))
+
+
 def test_fast_division(lib):
     f = lib.bq_internal_fast_div
     f.restype, f.argtypes = ctypes.c_uint, [ctypes.c_uint, ctypes.c_uint]

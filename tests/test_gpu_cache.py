@@ -945,6 +945,12 @@ def test_block_table_refusals():
             bq.kv_block_tables(**{**good, name: value})
 
 
+def test_a_page_size_beyond_32_bits_is_refused():
+    t = bq.BlockTables(2, 4, 8, (1 << 32) + 16, 8)
+    with pytest.raises(bq.BQError):
+        t.resize(torch.ones(2, dtype=torch.int32, device=DEV))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
