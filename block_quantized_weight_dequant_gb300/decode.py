@@ -242,6 +242,8 @@ class PagedDecode:
             raise ValueError(f"{self.rows} rows do not share out among {requests} requests")
         each = self.rows // requests
         rope = self.rope
+        if h.shape != self.h.shape and not (self.rows == 1 and h.shape == self.h.shape[1:]):
+            raise ValueError(f"h must be {list(self.h.shape)}, got {list(h.shape)}")
         self.h.copy_(h)
         # x = RMSNorm(h) * attn_gamma
         sandwich_norm(self.h, self.h, pre_gain=self.layers[0]["attn_gamma"], alpha=1.0, beta=0.0, eps=self.eps,

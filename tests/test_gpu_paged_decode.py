@@ -172,3 +172,19 @@ def test_paged_decode_refusals():
     with pytest.raises(ValueError):
         dec.step(torch.zeros((3, HIDDEN), device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV), None,
                  torch.zeros((2, 4), **i32), torch.zeros(2, **i32))
+
+
+def test_a_step_of_fewer_embeddings_than_rows_is_refused():
+    """One embedding is not spread over all rows; of one row it may come flat."""
+    dec, tables = decoder("q8_0", "f16", rows=3), bq.BlockTables(3, 4, 12, 16, 3)
+    tables.resize(tables.lens + 1)
+    more = (tables.slots, tables.positions, tables.table, tables.lens)
+    for shape in ((1, HIDDEN), (HIDDEN,), (3, 1), (4, HIDDEN)):
+        with pytest.raises(ValueError, match="h must be"):
+            dec.step(torch.ones(shape, device=DEV), *more)
+    one, table = decoder("q8_0", "f16"), bq.BlockTables(1, 4, 12, 16, 1)
+    table.resize(table.lens + 1)
+    h = wl.normal_torch(HIDDEN, 1.0, seed=3, stream=12, device=DEV)
+    more = (table.slots, table.positions, table.table, table.lens)
+    a = one.step(h, *more).clone()
+    assert torch.equal(a, one.step(h.view(1, HIDDEN), *more))
