@@ -48,7 +48,9 @@
 // score, a value's scale its weight, both in fp32 before any rounding to parts.
 #pragma once
 
+#include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "bq_attn.h"
 
@@ -920,9 +922,9 @@ int attn_occupancy(size_t smem, int *out) {
 
 // the instances of one cache type and way of carrying queries, for head_dim up to
 // 64, 128 and 256
-#define BQ_ATTN_INST(NAME, KV, QP, PP, DP, NT)                                              \
+#define BQ_ATTN_INST(KV, QP, PP, DP, NT)                                                           \
     {                                                                                              \
-        DP, NT, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,                            \
+        DP, NT, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,                                   \
             bq::attn_occupancy<KV, QP, PP, DP, NT>,                                                \
             [](const bq::AttnArgs &a, int grid, size_t smem, void *stream,                         \
                unsigned int *status) -> cudaError_t {                                              \
@@ -931,10 +933,10 @@ int attn_occupancy(size_t smem, int *out) {
                                       a.cluster ? a.max_chunks : 1, a, status);                    \
             }                                                                                      \
     }
-#define BQ_ATTN_INSTS(NAME, KV, QP, PP)                                                            \
-    BQ_ATTN_INST(NAME, KV, QP, PP, 64, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 64, 2),                  \
-        BQ_ATTN_INST(NAME, KV, QP, PP, 128, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 128, 2),            \
-        BQ_ATTN_INST(NAME, KV, QP, PP, 256, 1), BQ_ATTN_INST(NAME, KV, QP, PP, 256, 2)
+#define BQ_ATTN_INSTS(KV, QP, PP)                                                                  \
+    BQ_ATTN_INST(KV, QP, PP, 64, 1), BQ_ATTN_INST(KV, QP, PP, 64, 2),                              \
+        BQ_ATTN_INST(KV, QP, PP, 128, 1), BQ_ATTN_INST(KV, QP, PP, 128, 2),                        \
+        BQ_ATTN_INST(KV, QP, PP, 256, 1), BQ_ATTN_INST(KV, QP, PP, 256, 2)
 #define BQ_ATTN_UNIT(NAME, ...)                                                                    \
     const bq::AttnInstance *bq_internal_attn_##NAME(int *n) {                                      \
         static const bq::AttnInstance inst[] = {__VA_ARGS__};                                      \
