@@ -261,9 +261,11 @@ class BlockTables:
     """The requests' side of a paged cache, on the GPU: lengths, block table and
     the stack of free pages, shared by all layers' caches.  ``resize`` moves
     every request to its new length and fills ``slots``, ``positions`` and
-    ``starts`` for the tokens that came; it enqueues one kernel, allocates
-    nothing and can be captured in a CUDA graph (new lengths are read from the
-    tensor that it is given)."""
+    ``starts`` for the tokens that came; it enqueues one kernel (two where
+    max_tokens is above 4096), allocates nothing and can be captured in a CUDA
+    graph (new lengths are read from the tensor that it is given).  max_pages is
+    the table's width, which decides how paged_attention cuts its work: one much
+    wider than the requests are long costs time."""
 
     def __init__(self, requests, max_pages, pages, page_size, max_tokens, device="cuda"):
         i32 = dict(dtype=torch.int32, device=device)
@@ -353,7 +355,9 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     [requests, width] holds the requests' pages.  heads is a multiple of the
     cache's kv_heads.  A row that sees nothing gives zeros.  scale defaults to
     1 / sqrt(head_dim).  Row r's bits are those of the one-row call at its
-    length.  out may be q.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
+    length.  The work is cut by the table's width, not by the lengths: a table
+    much wider than its requests leaves a part of the GPU idle (one request of
+    8000 positions: 9 us in a table of that width, 26 in one of 131072).  out may be q.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
     call that may overlap others, also calls of two host threads on one stream;
     None: one of the call's own from PyTorch's allocator."""
     if not isinstance(cache, PagedKVCache):

@@ -206,6 +206,11 @@ struct Plan {
 //    starts and joins than they balance (8 requests to 30000, 2 kv heads: 74 us
 //    against 82, 77 and 82 with two, four and eight times the units; 16 to 4000, 8 kv
 //    heads: 38 against 43, 44, 49).
+// The table's capacity cuts, not the lengths, which the host does not know: a
+// request in a table much wider than itself has few units (one request of 16 heads
+// over 4, fp16: 700 positions 6.9 us in a table of their own, 11.5 in one of 32768,
+// 12.6 in one of 131072; 8000 positions 8.6, 11.7, 26.0; 32768 in one of 131072 28.3
+// against 18.8).
 constexpr int64_t TARGET = 304, CHUNK_MIN = 128, CHUNK_MAX = 2048, CLUSTER_CHUNK = 256;
 struct Chunking {
     int chunk;
@@ -331,8 +336,8 @@ extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_atten
     if (p.inst->occupancy(p.smem, &occ) != 0 || occ < 1) return bq::from_cuda_error(cudaErrorInvalidConfiguration);
     const int64_t slots = (int64_t)sms * occ;
     // Up to DIRECT units per slot the hardware hands them out as CTAs end, whole
-    // chunks before ragged ones (48 requests to 12001: 202 us against 209; Q8_0, 48 to
-    // 6000: 85 against 98).  A unit behind its request's length costs about 4 ns of the
+    // chunks before ragged ones (48 requests to 12001: 202 us against 210; Q8_0, 48 to
+    // 6000, bf16 queries: 92 against 107).  A unit behind its request's length costs about 4 ns of the
     // GPU then, so a table much wider than the requests goes by the scan of the
     // lengths instead.
     constexpr int64_t DIRECT = 8;

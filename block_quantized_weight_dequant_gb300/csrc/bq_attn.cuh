@@ -15,9 +15,9 @@
 //
 // Bound by HBM: every live byte of the cache is read once (again per 8 NT query
 // rows of a kv head, through L2), about 4 flop per byte and query row.  Measured:
-// 48 requests to 12001 positions, bf16, 32 heads over 8, 1.32 GB: 201 us, 6.6 TB/s;
-// one request of 100003, fp16: 40 us, 5.1 TB/s; Q8_0 is bound by instructions
-// (48 requests to 6000, bf16 queries: 93 us, 3.8 TB/s; 5 rows of 40 heads over 8 at
+// 48 requests to 12001 positions, bf16, 32 heads over 8, 1.32 GB: 202 us, 6.5 TB/s;
+// one request of 100003, fp16: 41 us, 5.0 TB/s; Q8_0 is bound by instructions
+// (48 requests to 6000, bf16 queries: 92 us, 3.9 TB/s; 5 rows of 40 heads over 8 at
 // 24577: 53 us).
 // So the kernel is built around the loads:
 //  - Every warp has a ring of STAGES tiles of K and V rows in shared memory
@@ -38,10 +38,12 @@
 // the cache's own type is used as it is; any other is split into QP 16-bit
 // parts (fp16: 2 parts, 22 bits, after scaling the row by a power of two, which
 // lets a bf16 query through in one; bf16: 3 parts, 24 bits), the weights into PP
-// parts: 2 of fp16 (off by 2^-23 of them), 3 of bf16 (24 bits; with two, 17, 0.2% of a
-// bf16 output's values were not the nearest ones, with three 0.02%, where the plain
-// fp32 sum leaves 0.09%: 48 requests to 12001, 201 us against 199; one part of fp16
-// for bf16 queries over Q8_0 left 8.9%: 48 to 6000 93 us against 85).  Each tile's products
+// parts: 2 of fp16 (off by 2^-23 of them), 3 of bf16 (24 bits).  Fewer parts show in a
+// 16-bit output: with two of bf16 (17 bits) 0.2% of its values were not the nearest
+// ones, with three 0.02% are not, plain fp32 sums leave 0.09% (48 requests to 12001:
+// 202 us against 201; 40 to 5000, 32 heads of 64 over one: 28 against 24, the 32-row
+// tile spills); with one of fp16, bf16 queries over Q8_0, 8.9% were not (8 requests to
+// 4000; 48 to 6000: 92 us against 85).  Each tile's products
 // are summed by the tensor core from zero, smallest parts first, and added to
 // the fp32 accumulator by an fp32 FMA, since the tensor core truncates its sums.
 // Q8_0 codes are exact in fp16; a key's scale multiplies its block's partial

@@ -182,8 +182,10 @@ class PagedDecode:
     then logits = lm_head (RMSNorm(h) * final_gamma).
 
     Every product is the package's GEMV (or its verify form, whose rows have the
-    single row's bits), and the calls between them compute each row on its own,
-    so a row of a verify step has the bits of the one-row step.  ``step`` enqueues
+    single row's bits; the gate and up pair, which has no verify form, runs once per
+    row and reads its weights as often), and the calls between them compute each row
+    on its own, so a row of a verify step has the bits of the one-row step.  There is
+    no norm of q and k before their rotation.  ``step`` enqueues
     kernels only and can be captured in a CUDA graph."""
 
     def __init__(self, qtype, layers, lm_head, final_gamma, caches, heads, rope, eps=1e-6, alpha=1.0, beta=1.0,

@@ -498,7 +498,8 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
  *    in elements.  out may be q, with the same strides.  heads is a multiple of kv_heads, heads <= 4096; 1 <= rows
  *    <= BQ_VERIFY_MAX_ROWS; 0 <= requests <= 4096; scale finite.
  *  - table: int32 [requests, table_width], rows table_stride apart,
- *    table_width * page_size <= 2^23.
+ *    table_width * page_size <= 2^23.  The work is cut by table_width, not by
+ *    the lengths: a table much wider than its requests costs time.
  *  - workspace: bq_paged_attention_workspace_bytes bytes, 16-byte aligned;
  *    need not be initialised; not shared by calls that may overlap on the GPU
  *    (two streams, two captured graphs) or that two host threads make at once
