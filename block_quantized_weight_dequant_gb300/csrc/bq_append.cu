@@ -4,8 +4,9 @@
 // Angles: the turn of pair p at position n is n * freq / (2 pi).  freq/(2 pi)
 // is split once per thread into hi + lo (two fp32 words, 48 bits); per token
 // n * hi is formed exactly as product and remainder (one FMUL, one FFMA), each
-// reduced by its nearest whole number, so the fraction of a turn is right to
-// about 2^-24 of a turn plus n * freq * 2^-48, at positions up to 2^31.  fp64
+// reduced by its nearest whole number, and beyond 2^24, where n has a remainder
+// of its own, so are the products with it and with lo.  So the fraction of a turn is
+// right to about 2^-23 of a turn plus n * freq * 2^-50, at positions up to 2^31.  fp64
 // runs once per thread and pair only (its rate is far below fp32's).
 //
 // A CTA takes a few tokens at a time: its threads put the tokens' cosines and
@@ -217,7 +218,12 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2) append_kernel(const __grid_
                 const float p = __fmul_rn(nf, hi);
                 const float e = __fmaf_rn(nf, hi, -p);
                 float f = (p - rintf(p)) + (e - rintf(e));
-                const float rest = __fmaf_rn(nf, lo, nr * hi);
+                float rest = __fmul_rn(nf, lo);
+                if (fabsf(nf) > 0x1p24f) {  // several turns, and nr: by product and remainder too
+                    const float u = __fmul_rn(nr, hi);
+                    const float left = __fmaf_rn(nf, lo, -rest) + __fmaf_rn(nr, hi, -u);
+                    rest = ((rest - rintf(rest)) + (u - rintf(u))) + left;
+                }
                 f += rest - rintf(rest);
                 float s, c;
                 sincospif(2.0f * (f - rintf(f)), &s, &c);

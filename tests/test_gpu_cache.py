@@ -697,6 +697,13 @@ def test_append_far_positions_layouts_and_skipped_tokens(kind, dtype):
     check_append(g, kind, dtype, 5000, 4, 2, 64, 64, None, False, 16, 100, fused=False)
 
 
+@pytest.mark.parametrize("far", [2 ** 24 + 3, 2 ** 26, 2 ** 31 - 1])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_append_many_far_positions(far, interleaved):
+    """Enough positions to meet the ones whose remainder beyond 24 bits is largest."""
+    check_append(rng(far, 26), "f16", F32, 4000, 4, 2, 64, 64, [8, 24], interleaved, 16, far)
+
+
 def test_append_odd_alignment_and_no_queries():
     g = rng(22)
     cache = bq.PagedKVCache.zeros(4, 16, 2, 64)
