@@ -490,7 +490,8 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
  * q and all probabilities are carried as 16-bit parts that add up to them:
  * over a BQ_BF16 cache exactly (24 bits), over BQ_F16 and BQ_Q8_0 caches to
  * 2^-23 of the number, or 2^-39 of the largest of its row where that is more
- * (of the probabilities times value scales, for BQ_Q8_0).  For one geometry (requests, table_width,
+ * (BQ_Q8_0 carries probabilities times value scales: 2^-39 of the largest
+ * probability times the largest value scale).  For one geometry (requests, table_width,
  * page_size, kv_heads, head_dim, types) each row's bits depend on its own
  * inputs alone: row r of a call with several rows is bit-identical to the
  * one-row call at the length that the row sees.

@@ -328,6 +328,31 @@ def test_weights_over_a_q8_0_cache_are_good_to_fp32_rounding(dtype, heads, kv):
     check_weights("q8_0", dtype, heads, kv)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("small", [-2, -8, -14])
+def test_small_value_scales_beside_large_ones(dtype, small):
+    """A value of a small scale that has nearly all the weight, beside one of scale
+    2^10 with a weight of e^-40: off by 2^-23 of itself, and by 2^-39 of the largest
+    scale for each of the two codes; then a few fp32 roundings and the output's."""
+    D, page = 64, 16
+    codes = torch.zeros((1, 1, page, D), dtype=torch.int8, device=DEV)
+    k, v = codes.clone(), torch.from_numpy(rng(51).integers(-127, 128, codes.shape).astype(np.int8)).to(DEV)
+    k[0, 0, 1, 0] = 40
+    scale = torch.ones((1, 1, page, D // 32), dtype=F16, device=DEV)
+    v_scale = scale * 2.0 ** 10
+    v_scale[0, 0, 1] = 2.0 ** small
+    cache = bq.PagedKVCache(k, v, scale, v_scale)
+    q = torch.zeros((1, 4, D), dtype=dtype, device=DEV)
+    q[..., 0] = 1.0
+    out = bq.paged_attention(cache, q, torch.zeros((1, 1), dtype=torch.int32, device=DEV),
+                             torch.tensor([2], dtype=torch.int32, device=DEV), scale=1.0).cpu().double()
+    x = v[0, 0, :2].cpu().double() * torch.tensor([[2.0 ** 10], [2.0 ** small]], dtype=torch.float64)
+    want = (x[0] * np.exp(-40.0) + x[1]) / (1 + np.exp(-40.0))
+    off = 2.0 ** -21 * want.abs() + 2.0 ** -39 * 2.0 ** 10 * 2 * 127
+    bound = off + plain.EPS[dtype] / 2 * (want.abs() + off) + (2.0 ** -25 if dtype is F16 else 0.0)
+    assert ((out - want).abs() <= bound).all(), float((out - want).abs().max())
+
+
 def test_strided_queries_and_outputs():
     g = rng(8)
     lens, page = [130, 20, 5], 16
