@@ -22,7 +22,7 @@
 // put in order through shared memory.
 //
 // Bound by HBM for a prompt, by latency for one token.  Measured: 8192 tokens of
-// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.7 TB/s; into Q8_0 48 us, 5.7
+// 28 + 4 + 4 heads of 128, fp32 into fp16: 50 us, 5.7 TB/s; into Q8_0 48 us, 5.8
 // TB/s; 4001 tokens of 16 + 4 + 4, bf16: 13 us; one token: 2.8 us.
 #include <atomic>
 #include <cmath>
