@@ -24,29 +24,29 @@ def listed():
     """What each case stands for is said beside it."""
     return [
         # one token of a small model whose layers norm queries and keys: latency counts
-        append("normed append, 1 token, f16", "f16", "f32", 1, 16, 8, 128, 128, 1, False, 16, 131000),
+        append("normed append 1 token f16", "f16", "f32", 1, 16, 8, 128, 128, 1, False, 16, 131000),
         # a prompt's chunk
-        append("normed append, 8192 tokens, f16", "f16", "f32", 8192, 28, 4, 128, 128, 1, False, 32, 120000),
+        append("normed append 8192 tokens f16", "f16", "f32", 8192, 28, 4, 128, 128, 1, False, 32, 120000),
         # four answers to one short prompt
-        prefix("prefix attention, 4 requests, 700 shared, f16", "f16", "f32", 4, 1, 1, 16, 8, 128, 16, 700, 90),
+        prefix("prefix attention 4 requests 700 shared f16", "f16", "f32", 4, 1, 1, 16, 8, 128, 16, 700, 90),
         # a server whose requests all begin with the same long document
-        prefix("prefix attention, 96 requests, 32801 shared, bf16", "bf16", "bf16", 96, 1, 1, 32, 8, 128, 64, 32801, 400),
+        prefix("prefix attention 96 requests 32801 shared bf16", "bf16", "bf16", 96, 1, 1, 32, 8, 128, 64, 32801, 400),
         # many requests of a small model under three system prompts
-        prefix("prefix attention, 200 requests, 3 groups of 9001, f16", "f16", "f16", 200, 3, 1, 14, 2, 64, 16, 9001, 300),
+        prefix("prefix attention 200 requests 3 groups of 9001 f16", "f16", "f16", 200, 3, 1, 14, 2, 64, 16, 9001, 300),
         # samples of one long conversation over a quantized cache
-        prefix("prefix attention, 16 requests, 30011 shared, q8_0", "q8_0", "f32", 16, 1, 1, 16, 8, 128, 32, 30011, 500),
+        prefix("prefix attention 16 requests 30011 shared q8_0", "q8_0", "f32", 16, 1, 1, 16, 8, 128, 32, 30011, 500),
         # a prompt forked into fifteen samples beside a few other requests
-        tables("page tables, 24 requests, 15 forks", 24, 16, 15, 1, 3000),
+        tables("page tables 24 requests 15 forks", 24, 16, 15, 1, 3000),
         # a busy server's step: prompts, decode, forks, rollbacks, ended requests
-        tables("page tables, 1000 requests, 120 forks", 1000, 16, 120, 200, 20000),
+        tables("page tables 1000 requests 120 forks", 1000, 16, 120, 200, 20000),
         # the pages that a few forks of one step must have for themselves, in every layer
-        copy("page copy, 6 pages of 28 layers, f16", "f16", 28, 64, 6, 8, 128, 16),
+        copy("page copy 6 pages of 28 layers f16", "f16", 28, 64, 6, 8, 128, 16),
         # what a compaction moves
-        copy("page copy, 200 pages of 28 layers, bf16", "bf16", 28, 450, 200, 8, 128, 16),
+        copy("page copy 200 pages of 28 layers bf16", "bf16", 28, 450, 200, 8, 128, 16),
         # a small server's pool before it gives memory back
-        compact("compaction, 3000 pages", 40, 16, 3000, 0.4),
+        compact("compaction 3000 pages", 40, 16, 3000, 0.4),
         # a large one's
-        compact("compaction, 200000 pages", 600, 16, 200000, 0.5),
+        compact("compaction 200000 pages", 600, 16, 200000, 0.5),
     ]
 
 
