@@ -75,8 +75,8 @@ NCU_TRAFFIC = {
 
 # CUDA sources that no part of the streaming kernel or its planner is built
 # from: changing them leaves the captured traffic valid
-DIGEST_EXCLUDES = ("bq_f16.cu", "bq_cache.cuh", "bq_tables.cu", "bq_append.cu", "bq_norm.cu")
-DIGEST_EXCLUDED_PREFIX = "bq_attn"
+DIGEST_EXCLUDES = ("bq_f16.cu", "bq_cache.cuh", "bq_norm.cu")
+DIGEST_EXCLUDED_PREFIX = ("bq_append", "bq_attn", "bq_pages", "bq_tables")
 
 
 def csrc_digest():

@@ -24,7 +24,7 @@ EXPORTS = ("bq_version", "bq_status_str", "bq_packed_bytes", "bq_quantize_pack",
            "bq_gemv_f16", "bq_gemv_f16_f16out", "bq_device_status",
            "bq_tree_lanes", "bq_stream_workspace_bytes", "bq_stream_plan_create",
            "bq_stream_plan_launch", "bq_stream_plan_tune", "bq_stream_plan_launches",
-           "bq_stream_plan_destroy", "bq_stream_run_noalloc", "bq_kv_block_tables", "bq_kv_append",
+           "bq_stream_plan_destroy", "bq_stream_run_noalloc", "bq_kv_block_tables", "bq_kv_append", "bq_kv_append_norm",
            "bq_paged_attention_workspace_bytes", "bq_paged_attention", "bq_sandwich_norm")
 BQ_NOALLOC_MAX_OPS = 512
 
@@ -64,6 +64,11 @@ class BqKvAppendArgs(ctypes.Structure):
                                        "q_token_stride", "q_head_stride", "q_out_token_stride",
                                        "q_out_head_stride")]
                 + [("slots", _VP), ("positions", _VP), ("position_stride", _I64), ("freq", _VP)])
+
+
+class BqKvNormArgs(ctypes.Structure):
+    """bq_kv_norm_args of include/bqgemv.h"""
+    _fields_ = [("q_gain", _VP), ("k_gain", _VP), ("eps", _F)]
 
 
 class BqAttentionArgs(ctypes.Structure):
@@ -116,6 +121,8 @@ def _declare(lib):
         "bq_stream_run_noalloc": (i32, [i32, ctypes.POINTER(BqOp), i32, vp]),
         "bq_kv_block_tables": (i32, [ctypes.POINTER(BqKvTables), vp]),
         "bq_kv_append": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqKvAppendArgs), vp]),
+        "bq_kv_append_norm": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqKvAppendArgs),
+                                    ctypes.POINTER(BqKvNormArgs), vp]),
         "bq_paged_attention_workspace_bytes": (i64, [ctypes.POINTER(BqKvCache),
                                                      ctypes.POINTER(BqAttentionArgs)]),
         "bq_paged_attention": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqAttentionArgs), vp, i64, vp]),

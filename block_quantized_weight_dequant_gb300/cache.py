@@ -292,7 +292,7 @@ def _strides(t, tokens, heads):
     return (a if tokens > 1 else 0), (b if heads > 1 else 0)
 
 
-def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None):
+def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None, q_norm=None, k_norm=None, eps=1e-6):
     """Store keys and values k, v [tokens, kv_heads, head_dim] at `slots` (int64
     [tokens], < 0: not stored; the others must differ) of `cache`.  With `rope`,
     keys are rotated by `positions` (int32 [axes, tokens], or [tokens] for one
@@ -340,7 +340,17 @@ def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None)
     args = _lib.BqKvAppendArgs(_DTYPES[dtype], heads, rot, axes, inter, sections, T, k.data_ptr(),
                                v.data_ptr(), qp, op, *_strides(k, T, kv), *_strides(v, T, kv), *qs, *os,
                                slots.data_ptr(), pos, ps, freq)
-    _call(lib.bq_kv_append, "kv_append", dev, cache._ref, _byref(args))
+    if q_norm is None and k_norm is None:
+        _call(lib.bq_kv_append, "kv_append", dev, cache._ref, _byref(args))
+        return q_out
+    if q_norm is not None:
+        if q is None:
+            raise ValueError("q_norm without q")
+        _dense(q_norm, "q_norm", torch.float32, dev, D)
+    if k_norm is not None:
+        _dense(k_norm, "k_norm", torch.float32, dev, D)
+    norm = _lib.BqKvNormArgs(*(None if t is None else t.data_ptr() for t in (q_norm, k_norm)), eps)
+    _call(lib.bq_kv_append_norm, "kv_append", dev, cache._ref, _byref(args), _byref(norm))
     return q_out
 
 

@@ -12,18 +12,7 @@ BQ_STATUS_WORD(attn)
 // the status word's device address, looked up once per device
 cudaError_t status_address(unsigned int **out) {
     static std::atomic<unsigned int *> addr[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    unsigned int *p = addr[dev].load();
-    if (!p) {
-        e = cudaGetSymbolAddress(reinterpret_cast<void **>(&p), g_status_attn);
-        if (e != cudaSuccess) return e;
-        addr[dev].store(p);
-    }
-    *out = p;
-    return cudaSuccess;
+    return bq::symbol_address(addr, g_status_attn, out);
 }
 
 constexpr int JOIN_THREADS = 256;

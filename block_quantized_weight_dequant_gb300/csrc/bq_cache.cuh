@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/bqgemv.h"
@@ -195,6 +196,23 @@ inline bq_status check_cache_pointers(const bq_kv_cache *c) {
 
 // SMs of the current device, 0 on failure
 int device_sms();
+
+// the device address of a word, looked up once per device
+inline cudaError_t symbol_address(std::atomic<unsigned int *> (&addr)[64], const unsigned int &symbol,
+                                  unsigned int **out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    unsigned int *p = addr[dev].load();
+    if (!p) {
+        e = cudaGetSymbolAddress(reinterpret_cast<void **>(&p), symbol);
+        if (e != cudaSuccess) return e;
+        addr[dev].store(p);
+    }
+    *out = p;
+    return cudaSuccess;
+}
 
 }  // namespace bq
 

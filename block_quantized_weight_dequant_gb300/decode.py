@@ -175,6 +175,7 @@ class PagedDecode:
 
         x  = RMSNorm(h) * attn_gamma
         q, k, v = Wqkv x (+ bias), q and k turned by their positions
+                                   [normed per head by q_norm, k_norm first if given]
         a  = attention of q over the cache, k and v appended
         h  = alpha h + beta attn_gate (o a)     [(o a) normed by attn_post if given]
         x  = RMSNorm(h) * gamma
@@ -184,16 +185,16 @@ class PagedDecode:
     Every product is the package's GEMV (or its verify form, whose rows have the
     single row's bits; the gate and up pair, which has no verify form, runs once per
     row and reads its weights as often), and the calls between them compute each row
-    on its own, so a row of a verify step has the bits of the one-row step.  There is
-    no norm of q and k before their rotation.  ``step`` enqueues
-    kernels only and can be captured in a CUDA graph."""
+    on its own, so a row of a verify step has the bits of the one-row step.
+    ``step`` enqueues kernels only and can be captured in a CUDA graph."""
 
     def __init__(self, qtype, layers, lm_head, final_gamma, caches, heads, rope, eps=1e-6, alpha=1.0, beta=1.0,
                  rows=1):
         """layers: dicts with packed qkv (the q, k, v rows concatenated, see
         concat_packed), o, gate, up, down, fp32 [hidden] attn_gamma and gamma, and
         optionally qkv_bias (fp32), attn_post, ffn_post (fp32 [hidden] gains of a
-        norm after the block), attn_gate, ffn_gate (fp32 [hidden]); caches: one
+        norm after the block), attn_gate, ffn_gate (fp32 [hidden]), q_norm, k_norm
+        (fp32 [head_dim] gains of the norms of queries and keys); caches: one
         PagedKVCache per layer; heads: query heads; rope: a Rope or None; rows:
         tokens of a step."""
         from . import _packed_shape, _qt
@@ -259,7 +260,8 @@ class PagedDecode:
                 if bias is not None:
                     self._qkv.add_(bias)  # the fused call's one fp32 add
             kv_append(self.caches[l], self._k, self._v, slots, q=self._q, q_out=self._turned, rope=rope,
-                      positions=None if rope is None else positions)
+                      positions=None if rope is None else positions, q_norm=L.get("q_norm"), k_norm=L.get("k_norm"),
+                      eps=self.eps)
             paged_attention(self.caches[l], self._turned, table, lens, rows=each, out=self._a)
             self._product(L["o"], self._a.view(self.rows, -1), self._y)
             self._between(L["gamma"], L.get("attn_post"), L.get("attn_gate"))

@@ -475,6 +475,20 @@ typedef struct {
 } bq_kv_append_args;
 bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, void *stream);
 
+/* The same with norms of queries and keys over each head (RunIT README, kernel
+ * table: the norm of q and k fused with the rotation), before they are turned:
+ *   x = x / sqrt(mean over head_dim of x^2 + eps) * gain
+ * Squares are summed in fp32, in an order that depends on head_dim alone.
+ *  - q_gain, k_gain: fp32 [head_dim], NULL for no norm (both NULL: the call is
+ *    bq_kv_append, bit for bit; q_gain is ignored without q).  Values are not
+ *    normed.  eps finite, >= 0. */
+typedef struct {
+    const float *q_gain, *k_gain;
+    float eps;
+} bq_kv_norm_args;
+bq_status bq_kv_append_norm(const bq_kv_cache *cache, const bq_kv_append_args *args, const bq_kv_norm_args *norm,
+                            void *stream);
+
 /* Attention of the last `rows` tokens of each request over its cache:
  *   out[b, r, h] = sum_t softmax_t(scale * q[b, r, h] . k[t, h / group]) v[t, h / group]
  * over positions t < lens[b] - rows + r + 1 (lens counts the new tokens, which
