@@ -29,7 +29,7 @@ __all__ = ["Q8_0", "Q4_0", "Q4_K", "BLOCK_BYTES", "BQError", "packed_bytes", "qu
            "gemv_qkv_bias", "gemv_f16", "concat_packed",
            "device_status", "tree_lanes", "version", "StreamOp", "StreamPlan",
            "PagedKVCache", "Rope", "BlockTables", "kv_block_tables", "kv_append", "paged_attention",
-           "paged_attention_workspace", "sandwich_norm"]
+           "paged_attention_workspace", "paged_prefix_attention", "paged_prefix_attention_workspace", "sandwich_norm"]
 
 
 def _qt(qtype):
@@ -323,4 +323,5 @@ class StreamPlan:
 
 
 from .cache import (BlockTables, PagedKVCache, Rope, kv_append, kv_block_tables,  # noqa: E402
-                    paged_attention, paged_attention_workspace, sandwich_norm)
+                    paged_attention, paged_attention_workspace, paged_prefix_attention,
+                    paged_prefix_attention_workspace, sandwich_norm)

@@ -14,7 +14,9 @@ BQ_OK, BQ_ERR_NULL, BQ_ERR_SHAPE, BQ_ERR_ALIGN, BQ_ERR_QTYPE, BQ_ERR_CUDA, BQ_ER
 BQ_Q4_0, BQ_Q8_0, BQ_Q4_K = 2, 8, 12
 BQ_F32, BQ_F16, BQ_BF16 = 0, 1, 30
 BQ_VERIFY_MAX_ROWS = 6
+BQ_PREFIX_MAX_GROUPS = 64
 BQ_DEVERR_PAGE, BQ_DEVERR_LENGTH, BQ_DEVERR_SLOT, BQ_DEVERR_POOL = 0x100, 0x200, 0x400, 0x800
+BQ_DEVERR_WAIT = 0x1000
 
 BQ_OP_GEMV, BQ_OP_GATE_UP_SILU = 0, 1
 
@@ -25,7 +27,8 @@ EXPORTS = ("bq_version", "bq_status_str", "bq_packed_bytes", "bq_quantize_pack",
            "bq_tree_lanes", "bq_stream_workspace_bytes", "bq_stream_plan_create",
            "bq_stream_plan_launch", "bq_stream_plan_tune", "bq_stream_plan_launches",
            "bq_stream_plan_destroy", "bq_stream_run_noalloc", "bq_kv_block_tables", "bq_kv_append", "bq_kv_append_norm",
-           "bq_paged_attention_workspace_bytes", "bq_paged_attention", "bq_sandwich_norm")
+           "bq_paged_attention_workspace_bytes", "bq_paged_attention",
+           "bq_paged_prefix_attention_workspace_bytes", "bq_paged_prefix_attention", "bq_sandwich_norm")
 BQ_NOALLOC_MAX_OPS = 512
 
 
@@ -126,6 +129,10 @@ def _declare(lib):
         "bq_paged_attention_workspace_bytes": (i64, [ctypes.POINTER(BqKvCache),
                                                      ctypes.POINTER(BqAttentionArgs)]),
         "bq_paged_attention": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqAttentionArgs), vp, i64, vp]),
+        "bq_paged_prefix_attention_workspace_bytes": (i64, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqAttentionArgs),
+                                                            ctypes.POINTER(i32), ctypes.POINTER(i32), i32]),
+        "bq_paged_prefix_attention": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqAttentionArgs),
+                                            ctypes.POINTER(i32), ctypes.POINTER(i32), i32, vp, i64, vp]),
         "bq_sandwich_norm": (i32, [ctypes.POINTER(BqSandwichArgs), vp]),
     }
     for name, (res, args) in sig.items():

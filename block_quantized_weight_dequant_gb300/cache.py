@@ -18,7 +18,7 @@ from . import _lib
 from ._lib import BQ_VERIFY_MAX_ROWS, lib
 
 __all__ = ["PagedKVCache", "Rope", "BlockTables", "kv_block_tables", "kv_append", "paged_attention",
-           "paged_attention_workspace", "sandwich_norm"]
+           "paged_attention_workspace", "paged_prefix_attention", "paged_prefix_attention_workspace", "sandwich_norm"]
 
 _DTYPES = {torch.float32: _lib.BQ_F32, torch.float16: _lib.BQ_F16, torch.bfloat16: _lib.BQ_BF16}
 _KINDS = {"f16": torch.float16, "bf16": torch.bfloat16, "q8_0": torch.int8}
@@ -423,6 +423,77 @@ def paged_attention_workspace(cache, requests, rows, heads, width):
     nbytes = lib.bq_paged_attention_workspace_bytes(cache._ref, ctypes.byref(args))
     if nbytes < 0:
         raise ValueError(f"no paged_attention of requests={requests} rows={rows} heads={heads} width={width}")
+    return nbytes
+
+
+def _groups(shared, requests):
+    """Host arrays of the groups' counts and shared positions, and how many."""
+    if isinstance(shared, int):
+        shared = [(requests, shared)]
+    counts, positions = zip(*shared) if len(shared) else ((), ())
+    n = len(counts)
+    if not 1 <= n <= _lib.BQ_PREFIX_MAX_GROUPS:
+        raise ValueError(f"shared must have 1 to {_lib.BQ_PREFIX_MAX_GROUPS} groups, got {n}")
+    if sum(counts) != requests:
+        raise ValueError(f"the groups have {sum(counts)} requests, lens has {requests}")
+    array = ctypes.c_int32 * n
+    return array(*map(_i32, counts)), array(*map(_i32, positions)), n
+
+
+def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, out=None, workspace=None):
+    """paged_attention for requests that share the beginning of their histories:
+    the same result, with the shared pages gone through once for all requests of a
+    group.  shared: the number of positions that all requests have in common, or
+    (requests, positions) pairs of groups in the requests' order (host numbers).
+    Whole pages of them count (shared // page_size): those entries of the requests'
+    table rows name the same pages, as kv_shared_tables makes them; what is behind
+    is each request's own.  A request's rows see all its shared positions (lens[b] -
+    rows + 1 of them at least); one that has ended has length 0 and gives zeros.
+    q, table, lens, rows, scale and out as for paged_attention; workspace: uint8,
+    ``paged_prefix_attention_workspace(...)`` bytes, under the same rules."""
+    if not isinstance(cache, PagedKVCache):
+        raise TypeError("cache must be a PagedKVCache")
+    dev, D = cache.device, cache.head_dim
+    if not 1 <= rows <= BQ_VERIFY_MAX_ROWS:
+        raise ValueError(f"rows must be 1 to {BQ_VERIFY_MAX_ROWS}, got {rows}")
+    _dense(lens, "lens", torch.int32, dev)
+    n = lens.numel()
+    _first(q, "q", dev)
+    dtype = q.dtype
+    T, heads = n * rows, (q.shape[1] if q.dim() == 3 else -1)
+    shape = (T, heads, D)
+    _activation(q, "q", shape, dtype, dev)
+    width, stride = _table(table, n, dev)
+    counts, positions, groups = _groups(shared, n)
+    if out is None:
+        out = _empty(shape, dtype, q)
+        os = (heads * D, D)
+    else:
+        _result(out, "out", shape, dtype, dev)
+        os = _strides(out, T, heads)
+    args = _lib.BqAttentionArgs(_DTYPES[dtype], n, rows, heads, width, cache._scale if scale is None else scale, stride,
+                                *_strides(q, T, heads), *os, q.data_ptr(), out.data_ptr(),
+                                table.data_ptr(), lens.data_ptr())
+    ref = _byref(args)
+    if workspace is None:
+        nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ref, counts, positions, groups)
+        if nbytes > 0:  # (one of the call's own, as in paged_attention)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    else:
+        _dense(workspace, "workspace", torch.uint8, dev)
+        nbytes = workspace.numel()
+    _call(lib.bq_paged_prefix_attention, "paged_prefix_attention", dev, cache._ref, ref, counts, positions, groups,
+          None if workspace is None else workspace.data_ptr(), nbytes)
+    return out
+
+
+def paged_prefix_attention_workspace(cache, requests, rows, heads, width, shared, dtype=torch.float32):
+    """Bytes of workspace of a paged_prefix_attention call of this geometry."""
+    args = _lib.BqAttentionArgs(_DTYPES[dtype], _i32(requests), _i32(rows), _i32(heads), _i32(width), 1.0, int(width))
+    nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ctypes.byref(args), *_groups(shared, requests))
+    if nbytes < 0:
+        raise ValueError(f"no paged_prefix_attention of requests={requests} rows={rows} heads={heads} width={width} "
+                         f"shared={shared}")
     return nbytes
 
 

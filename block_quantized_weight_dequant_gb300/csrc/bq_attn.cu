@@ -5,6 +5,8 @@
 
 #include "bq_attn.h"
 
+int bq_internal_status_attn_prefix(unsigned int *flags, int clear);  // bq_attn_prefix.cu
+
 namespace {
 
 BQ_STATUS_WORD(attn)
@@ -219,17 +221,8 @@ Chunking chunking_of(int64_t requests, int64_t kv_heads, int64_t capacity) {
 // validation of shapes and choice of the instance
 bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     if (!c || !x) return BQ_ERR_NULL;
-    const bq_status s = bq::check_cache_shape(c);
+    const bq_status s = bq::check_attention_shape(c, x);
     if (s != BQ_OK) return s;
-    if (!bq::dtype_bytes(x->dtype)) return BQ_ERR_QTYPE;
-    if (x->requests < 0 || x->requests > bq::ATTN_MAX_REQUESTS || x->rows < 1 || x->rows > BQ_VERIFY_MAX_ROWS ||
-        x->heads < 1 || x->heads > 4096 || x->heads % c->kv_heads || x->table_width < 1 ||
-        (int64_t)x->table_width * c->page_size > (1LL << 23) || x->table_stride < x->table_width ||
-        x->table_stride > (1LL << 40) || !std::isfinite(x->scale))
-        return BQ_ERR_SHAPE;
-    const int64_t strides[] = {x->q_row_stride, x->q_head_stride, x->out_row_stride, x->out_head_stride};
-    for (int64_t v : strides)
-        if (v < 0 || v > (1LL << 40)) return BQ_ERR_SHAPE;
     bq::AttnArgs &a = p->a;
     a.c = *c;
     a.x = *x;
@@ -242,25 +235,10 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     a.cluster = how.cluster;
     a.max_chunks = bq::attn_chunks((int)capacity, a.chunk);
     a.scale_log2 = x->scale * 1.44269504088896340736f;
-    const int dim = c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256;
-    // 8 query rows per n-tile, as few row tiles as the registers allow: each
-    // reads the cache again.  A Q8_0 cache takes two n-tiles at most: with four its
-    // code outgrows the instruction cache (5 rows of 40 heads over 8, 24577
-    // positions: 57 us against 63).
-    const int nt = a.group_rows <= 8                                                  ? 1
-                   : a.group_rows <= 16 || dim == 256 || c->type == BQ_Q8_0 ? 2
-                                                                                      : 4;
+    a.mode = bq::ATTN_ALL;
+    const int nt = bq::attn_tiles(c, a.group_rows);
     a.row_tiles = (a.group_rows + 8 * nt - 1) / (8 * nt);
-    int n = 0;
-    const bool same = x->dtype == c->type;
-    const bq::AttnInstance *inst =
-        c->type == BQ_F16      ? (same ? bq_internal_attn_f16_own(&n) : bq_internal_attn_f16_split(&n))
-        : c->type == BQ_BF16   ? (same ? bq_internal_attn_bf16_own(&n) : bq_internal_attn_bf16_split(&n))
-        : x->dtype != BQ_F32   ? bq_internal_attn_q8_0_own(&n)
-                               : bq_internal_attn_q8_0_split(&n);
-    p->inst = nullptr;
-    for (int i = 0; i < n; ++i)
-        if (inst[i].dim == dim && inst[i].nt == nt) p->inst = &inst[i];
+    p->inst = bq::attn_instance(c, x->dtype, nt);
     if (!p->inst) return BQ_ERR_SHAPE;
     p->smem = p->inst->smem + (size_t)(x->requests + 1) * sizeof(int);
     p->units = (int64_t)x->requests * a.max_chunks * c->kv_heads * a.row_tiles;
@@ -275,7 +253,65 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
 
 }  // namespace
 
-int bq_internal_status_attn(unsigned int *flags, int clear) { return read_status_attn(flags, clear); }
+namespace bq {
+
+bq_status check_attention_shape(const bq_kv_cache *c, const bq_attention_args *x) {
+    const bq_status s = check_cache_shape(c);
+    if (s != BQ_OK) return s;
+    if (!dtype_bytes(x->dtype)) return BQ_ERR_QTYPE;
+    if (x->requests < 0 || x->requests > ATTN_MAX_REQUESTS || x->rows < 1 || x->rows > BQ_VERIFY_MAX_ROWS ||
+        x->heads < 1 || x->heads > 4096 || x->heads % c->kv_heads || x->table_width < 1 ||
+        (int64_t)x->table_width * c->page_size > (1LL << 23) || x->table_stride < x->table_width ||
+        x->table_stride > (1LL << 40) || !std::isfinite(x->scale))
+        return BQ_ERR_SHAPE;
+    const int64_t strides[] = {x->q_row_stride, x->q_head_stride, x->out_row_stride, x->out_head_stride};
+    for (int64_t v : strides)
+        if (v < 0 || v > (1LL << 40)) return BQ_ERR_SHAPE;
+    return BQ_OK;
+}
+
+bq_status check_attention_pointers(const bq_kv_cache *c, const bq_attention_args *x) {
+    const bq_status s = check_cache_pointers(c);
+    if (s != BQ_OK) return s;
+    if (!x->q || !x->out || !x->table || !x->lens) return BQ_ERR_NULL;
+    const uintptr_t es = (uintptr_t)dtype_bytes(x->dtype);
+    if (!aligned_to(x->q, es) || !aligned_to(x->out, es) || !aligned_to(x->table, 4) || !aligned_to(x->lens, 4))
+        return BQ_ERR_ALIGN;
+    return BQ_OK;
+}
+
+static int padded_dim(const bq_kv_cache *c) { return c->head_dim <= 64 ? 64 : c->head_dim <= 128 ? 128 : 256; }
+
+// 8 query rows per n-tile, as few row tiles as the registers allow: each
+// reads the cache again.  A Q8_0 cache takes two n-tiles at most: with four its
+// code outgrows the instruction cache (5 rows of 40 heads over 8, 24577
+// positions: 57 us against 63).
+int attn_tiles(const bq_kv_cache *c, int64_t group_rows) {
+    return group_rows <= 8 ? 1 : group_rows <= 16 || padded_dim(c) == 256 || c->type == BQ_Q8_0 ? 2 : 4;
+}
+
+const AttnInstance *attn_instance(const bq_kv_cache *c, int dtype, int nt) {
+    int n = 0;
+    const bool same = dtype == c->type;
+    const AttnInstance *inst =
+        c->type == BQ_F16      ? (same ? bq_internal_attn_f16_own(&n) : bq_internal_attn_f16_split(&n))
+        : c->type == BQ_BF16   ? (same ? bq_internal_attn_bf16_own(&n) : bq_internal_attn_bf16_split(&n))
+        : dtype != BQ_F32      ? bq_internal_attn_q8_0_own(&n)
+                               : bq_internal_attn_q8_0_split(&n);
+    for (int i = 0; i < n; ++i)
+        if (inst[i].dim == padded_dim(c) && inst[i].nt == nt) return &inst[i];
+    return nullptr;
+}
+
+}  // namespace bq
+
+int bq_internal_status_attn(unsigned int *flags, int clear) {
+    unsigned int a = 0, b = 0;
+    int e = read_status_attn(&a, clear);
+    if (e == 0) e = bq_internal_status_attn_prefix(&b, clear);
+    *flags = a | b;
+    return e;
+}
 
 // host hooks for the tests (not in the public header): the launch constant's
 // quotient, and how a call is cut: chunk, chunks, cluster, row tiles
@@ -303,13 +339,8 @@ extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_atten
     bq_status s = plan_of(cache, x, &p);
     if (s != BQ_OK) return s;
     if (x->requests == 0) return BQ_OK;
-    s = bq::check_cache_pointers(cache);
+    s = bq::check_attention_pointers(cache, x);
     if (s != BQ_OK) return s;
-    if (!x->q || !x->out || !x->table || !x->lens) return BQ_ERR_NULL;
-    const uintptr_t es = (uintptr_t)bq::dtype_bytes(x->dtype);
-    if (!bq::aligned_to(x->q, es) || !bq::aligned_to(x->out, es) || !bq::aligned_to(x->table, 4) ||
-        !bq::aligned_to(x->lens, 4))
-        return BQ_ERR_ALIGN;
     bq::AttnArgs &a = p.a;
     const int64_t need = p.ml_bytes + p.o_bytes;
     if (need) {

@@ -255,17 +255,31 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     const int B = a.x.requests, R = a.x.rows, D = a.c.head_dim, KVH = a.c.kv_heads;
     const int most = a.x.table_width * a.c.page_size;
     pdl_wait();
-    if (a.max_chunks > 1 && !a.cluster) pdl_launch_dependents();
+    if ((a.max_chunks > 1 && !a.cluster) || a.mode != ATTN_ALL) pdl_launch_dependents();
 
-    auto length = [&](int b) { return min(max(a.x.lens[b], 0), most); };
+    const bool shared = a.mode == ATTN_PREFIX;
+    // pages before the first position that this launch covers of request b
+    auto skipped = [&](int b) {
+        if (a.mode != ATTN_REST) return 0;
+        int g = 0;
+        while (a.group_end[g] <= b) ++g;  // ends: the groups cover the requests
+        return a.group_pages[g];
+    };
+    auto length = [&](int b) {
+        if (shared) return a.group_pages[b] * a.c.page_size;
+        const int n = min(max(a.x.lens[b], 0), most);
+        return a.mode == ATTN_REST ? attn_rest(n, R, skipped(b) * a.c.page_size) : n;
+    };
     const long long per_chunk = (long long)KVH * a.row_tiles;
     // direct: a CTA per unit that the table can hold, units beyond a request's
     // length are empty.  Else a CTA takes every gridDim.x-th live unit, which
     // exclusive prefix sums of the requests' units tell.
     const bool direct = a.direct;
     auto checked = [&](int b) {
+        if (shared) return;
         const int len = a.x.lens[b];
-        if (len < 0 || len > most) atomicOr(status, BQ_DEVERR_LENGTH);
+        if (len < 0 || len > most || (len && a.mode == ATTN_REST && len - R + 1 < skipped(b) * a.c.page_size))
+            atomicOr(status, BQ_DEVERR_LENGTH);
     };
     if (!direct) {
         const int per = (B + WARPS * 32 - 1) / (WARPS * 32);
@@ -318,12 +332,24 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         }
         const int h = hr / a.row_tiles, rt = hr - h * a.row_tiles;
         const int begin = ck * a.chunk, first_row = rt * ROWS;
+        // ATTN_PREFIX: the group's requests, and the first of them that holds the
+        // shared pages, whose table row tells them
+        int first = b, owner = b, group_rows = a.group_rows;
+        if (shared) {
+            first = b ? a.group_end[b - 1] : 0;
+            group_rows = (a.group_end[b] - first) * R * (int)a.group.d;
+            owner = 0x7fffffff;
+            for (int i = first + lane; i < a.group_end[b] && owner == 0x7fffffff; i += 32)
+                if (min(a.x.lens[i], most) - R + 1 >= length(b)) owner = i;
+            owner = __reduce_min_sync(~0u, owner);
+            if (first_row >= group_rows || owner == 0x7fffffff) continue;  // nobody reads its partial results
+        }
 
         // ---- loads whose addresses do not wait for the length: table entries
         // (there is one for every position of the table), queries ----
-        const int *row_table = a.x.table + b * a.x.table_stride;
+        const int *row_table = a.x.table + owner * a.x.table_stride + skipped(b);
         const int mine = lane & (TILE - 1);  // the position of a tile that this lane looks up
-        const int chunk_end = min(begin + a.chunk, most);
+        const int chunk_end = min(begin + a.chunk, most - skipped(b) * a.c.page_size);
         auto entry_of = [&](int t) { return t < chunk_end ? row_table[a.page.div((uint32_t)t)] : -1; };
         int entry = entry_of(begin + warp * TILE + mine);
         float qx[ROWS / WARPS][DP / 32];
@@ -332,11 +358,11 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
             const int g = first_row + warp + WARPS * k;
             const int row = (int)a.group.div((uint32_t)g);
             const int head = h * (int)a.group.d + g - row * (int)a.group.d;
-            const long long at = ((long long)b * R + row) * a.x.q_row_stride + head * a.x.q_head_stride;
+            const long long at = ((long long)first * R + row) * a.x.q_row_stride + head * a.x.q_head_stride;
 #pragma unroll
             for (int e = 0; e < DP / 32; ++e) {
                 const int d = lane + 32 * e;
-                qx[k][e] = d >= D || g >= a.group_rows ? 0.0f
+                qx[k][e] = d >= D || g >= group_rows ? 0.0f
                            : a.x.dtype == BQ_F32       ? ((const float *)a.x.q)[at + d]
                            : a.x.dtype == BQ_F16       ? __half2float(((const __half *)a.x.q)[at + d])
                                                        : __bfloat162float(((const __nv_bfloat16 *)a.x.q)[at + d]);
@@ -464,7 +490,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int i = 8 * nt + 2 * c + x, g = first_row + i;
-                lim[nt][x] = g < a.group_rows ? len - R + (int)a.group.div((uint32_t)g) + 1 : 0;
+                lim[nt][x] = g >= group_rows ? 0 : shared ? len : len - R + (int)a.group.div((uint32_t)g) + 1;
                 fac[nt][x] = f_s[i];
             }
 
@@ -801,7 +827,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
             // token's NaN is NaN: a tile with positions that some rows do not see is
             // done token by token.  It is the last one of its warp: the new tokens lie
             // within two tiles, which belong to two warps.
-            if (R > 1 && tile + TILE > len - R + 1) {
+            if (R > 1 && !shared && tile + TILE > len - R + 1) {
                 for (int row = R - 1; row >= 0; --row) values(std::true_type{}, row);
             } else {
                 values(std::false_type{}, 0);
@@ -837,7 +863,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         const long long unit = (((long long)b * a.max_chunks + ck) * KVH + h) * a.row_tiles + rt;
         for (int i = warp; i < ROWS; i += WARPS) {
             const int g = first_row + i;
-            if (g >= a.group_rows) break;
+            if (g >= group_rows) break;
             float top = m_s[i];
 #pragma unroll
             for (int w = 1; w < WARPS; ++w) top = fmaxf(top, m_s[w * ROWS + i]);
@@ -859,7 +885,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                 for (int d = lane; d < D; d += 32) reinterpret_cast<float *>(smem)[i * S::OROW + d] = joined(d);
                 __syncwarp();
                 if (lane == 0) m_s[i] = top, l_s[i] = sum;
-            } else if (chunks == 1) {  // the result itself
+            } else if (chunks == 1 && a.mode == ATTN_ALL) {  // the result itself
                 for (int d = lane; d < D; d += 32) attn_store(a, b, h, g, d, sum == 0.0f ? 0.0f : joined(d) / sum);
             } else {
                 if (lane == 0) a.part_ml[unit * ROWS + i] = make_float2(top, sum);

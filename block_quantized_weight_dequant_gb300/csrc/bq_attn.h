@@ -17,6 +17,15 @@ constexpr int ATTN_MAX_REQUESTS = 4096;
 // carries the same factor, so it cancels
 constexpr int ATTN_SHIFT_F16 = 15;
 
+// What a launch of the attention kernel covers.  The two others write partial
+// results alone, which a join of their own puts together (bq_attn_prefix.cu).
+enum {
+    ATTN_ALL = 0,    // all positions of each request
+    ATTN_REST = 1,   // the positions behind the pages that a group of requests shares
+    ATTN_PREFIX = 2  // the shared pages: "requests" are groups, whose rows are all rows of their requests
+};
+constexpr int ATTN_GROUPS = BQ_PREFIX_MAX_GROUPS;
+
 struct AttnArgs {
     bq_kv_cache c;
     bq_attention_args x;
@@ -31,7 +40,16 @@ struct AttnArgs {
     float scale_log2;
     float *part_o;   // [unit][8 NT rows][head_dim] unnormalised, with max_chunks > 1
     float2 *part_ml; // [unit][8 NT rows] running maximum and sum
+    int mode;        // ATTN_ALL, or:
+    int group_end[ATTN_GROUPS];    // requests up to the end of each group
+    int group_pages[ATTN_GROUPS];  // whole pages that its requests share
 };
+
+// positions that request b's rows see behind `shared` ones, from its clamped
+// length: none unless its first row sees all the shared ones
+__host__ __device__ inline int attn_rest(int len, int rows, int shared) {
+    return len - rows + 1 >= shared ? len - shared : 0;
+}
 
 // work units of one request of n positions: at least one, which writes the rows
 __host__ __device__ inline int attn_chunks(int n, int chunk) { return n <= chunk ? 1 : (n + chunk - 1) / chunk; }
@@ -42,6 +60,14 @@ struct AttnInstance {
     int (*occupancy)(size_t smem, int *out);
     cudaError_t (*launch)(const AttnArgs &, int grid, size_t smem, void *stream, unsigned int *status);
 };
+
+// what bqgemv.h says of bq_attention_args: shapes, then pointers (and the cache's)
+bq_status check_attention_shape(const bq_kv_cache *c, const bq_attention_args *x);
+bq_status check_attention_pointers(const bq_kv_cache *c, const bq_attention_args *x);
+// the instance that serves the call's types with nt n-tiles, NULL if there is none
+const AttnInstance *attn_instance(const bq_kv_cache *c, int dtype, int nt);
+// n-tiles for a number of query rows of a kv head
+int attn_tiles(const bq_kv_cache *c, int64_t group_rows);
 
 }  // namespace bq
 

@@ -1,0 +1,310 @@
+// bq_attn_prefix.cu -- attention of requests that share the first pages of their
+// histories (bq_paged_prefix_attention in include/bqgemv.h): planning and join.
+//
+// Mathematics.  A row's positions are the shared ones and those behind them; with
+// the partial maximum m, sum l and unnormalised O of any cut of them
+//   o = sum_i 2^(m_i - max m) O_i / sum_i 2^(m_i - max m) l_i.
+// So the shared pages are gone through once for all query rows of a group of
+// requests (rows of one kv head side by side), the rest once per request by the
+// kernel that serves ordinary calls, and the partial results of both are joined
+// here, in a fixed order: a row's bits depend on its own inputs and the call's
+// geometry alone.
+#include <atomic>
+#include <cmath>
+
+#include "bq_attn.h"
+
+namespace {
+
+BQ_STATUS_WORD(attn_prefix)
+
+cudaError_t status_address(unsigned int **out) {
+    static std::atomic<unsigned int *> addr[64];
+    return bq::symbol_address(addr, g_status_attn_prefix, out);
+}
+
+constexpr int JOIN_THREADS = 256;
+
+// partial results of one of the two passes
+struct Parts {
+    const float *o;
+    const float2 *ml;
+    int chunk, max_chunks, row_tiles, tile_rows;
+};
+struct JoinArgs {
+    bq::AttnArgs a;  // of the rest
+    Parts shared, rest;
+};
+
+// W warps per query row and head: warp w takes the partial results w, w + W, ...
+// in order, then the warps' sums are added in order.
+template <int DT, int W>
+__global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
+    constexpr int ROWS = JOIN_THREADS / 32 / W;
+    __shared__ float4 o_s[W > 1 ? W : 1][W > 1 ? 64 : 1];
+    __shared__ float2 ml_s[W];
+    const bq::AttnArgs &a = j.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = W > 1 ? warp : 0;
+    const int D = a.c.head_dim, R = a.x.rows, KVH = a.c.kv_heads, G = (int)a.group.d;
+    const long long index = (long long)blockIdx.x * ROWS + (W > 1 ? 0 : warp);
+    bq::pdl_wait();
+    const int token = (int)(index / a.x.heads), head = (int)(index - (long long)token * a.x.heads);
+    const int b = token / R, row = token - b * R;
+    if (b >= a.x.requests) return;  // (W > 1: there is no such row)
+    const int h = head / G, in_group = head - h * G;
+    int g = 0;
+    while (a.group_end[g] <= b) ++g;
+    const int first = g ? a.group_end[g - 1] : 0;
+    const int common = a.group_pages[g] * a.c.page_size;
+    const int len = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
+    const bool sees = len - R + 1 >= common;  // else neither pass has anything for it
+    const int ns = sees && common ? bq::attn_chunks(common, j.shared.chunk) : 0;
+    const int n = ns + (sees ? bq::attn_chunks(bq::attn_rest(len, R, common), j.rest.chunk) : 0);
+    const int si = ((b - first) * R + row) * G + in_group, ri = row * G + in_group;
+    // where partial result k lies, in rows
+    auto at = [&](int k) {
+        const Parts &p = k < ns ? j.shared : j.rest;
+        const int c = k < ns ? k : k - ns, of = k < ns ? g : b, i = k < ns ? si : ri;
+        const int t = i / p.tile_rows;
+        const long long unit = (((long long)of * p.max_chunks + c) * KVH + h) * p.row_tiles + t;
+        return unit * p.tile_rows + (i - t * p.tile_rows);
+    };
+    auto stats = [&](int k) { return (k < ns ? j.shared.ml : j.rest.ml)[at(k)]; };
+    float top = -INFINITY;
+    for (int k = w + W * lane; k < n; k += W * 32) top = fmaxf(top, stats(k).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    float4 acc[2] = {};
+    float sum = 0.0f;
+    for (int k0 = w; k0 < n; k0 += W * 32) {
+        const int mine = k0 + W * lane;
+        const float2 ml = mine < n ? stats(mine) : make_float2(-INFINITY, 0.0f);
+        const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
+        float part = f * ml.y;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
+        sum += part;
+        const int many = min(32, (n - k0 + W - 1) / W);
+#pragma unroll 4
+        for (int i = 0; i < many; ++i) {
+            const float x = __shfl_sync(~0u, f, i);
+            const int k = k0 + W * i;
+            const float *src = (k < ns ? j.shared.o : j.rest.o) + at(k) * D;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int d = 128 * e + 4 * lane;
+                if (d >= D) break;
+                const float4 v = *reinterpret_cast<const float4 *>(src + d);
+                acc[e].x = fmaf(x, v.x, acc[e].x);
+                acc[e].y = fmaf(x, v.y, acc[e].y);
+                acc[e].z = fmaf(x, v.z, acc[e].z);
+                acc[e].w = fmaf(x, v.w, acc[e].w);
+            }
+        }
+    }
+    if constexpr (W > 1) {
+        if (lane == 0) ml_s[w] = make_float2(top, sum);
+        o_s[w][lane] = acc[0];
+        o_s[w][lane + 32] = acc[1];
+        __syncthreads();
+        if (w) return;
+        top = -INFINITY;
+        for (int i = 0; i < W; ++i) top = fmaxf(top, ml_s[i].x);
+        sum = 0.0f;
+        acc[0] = acc[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i = 0; i < W; ++i) {
+            const float x = ml_s[i].x == -INFINITY ? 0.0f : exp2f(ml_s[i].x - top);
+            sum = fmaf(x, ml_s[i].y, sum);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float4 v = o_s[i][lane + 32 * e];
+                acc[e].x = fmaf(x, v.x, acc[e].x);
+                acc[e].y = fmaf(x, v.y, acc[e].y);
+                acc[e].z = fmaf(x, v.z, acc[e].z);
+                acc[e].w = fmaf(x, v.w, acc[e].w);
+            }
+        }
+    }
+    const long long to = (long long)token * a.x.out_row_stride + (long long)head * a.x.out_head_stride;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int d = 128 * e + 4 * lane;
+        if (d >= D) break;
+        const float v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const float y = sum == 0.0f ? 0.0f : v[x] / sum;  // a row that sees nothing
+            if constexpr (DT == BQ_F32) ((float *)a.x.out)[to + d + x] = y;
+            else if constexpr (DT == BQ_F16) ((__half *)a.x.out)[to + d + x] = __float2half_rn(y);
+            else ((__nv_bfloat16 *)a.x.out)[to + d + x] = __float2bfloat16_rn(y);
+        }
+    }
+}
+
+template <int DT>
+cudaError_t join(const JoinArgs &j, void *stream) {
+    const int64_t rows = (int64_t)j.a.x.requests * j.a.x.rows * j.a.x.heads;
+    const int chunks = j.shared.max_chunks + j.rest.max_chunks;
+    constexpr int WARPS = JOIN_THREADS / 32;
+    // a warp per row where there are rows enough and few partial results of each
+    if (rows >= 2048 && chunks <= 32)
+        return bq::launch_pdl(prefix_join_kernel<DT, 1>, dim3((unsigned)((rows + WARPS - 1) / WARPS)), JOIN_THREADS, 0,
+                              stream, 1, j);
+    return bq::launch_pdl(prefix_join_kernel<DT, WARPS>, dim3((unsigned)rows), JOIN_THREADS, 0, stream, 1, j);
+}
+
+// one pass of the attention kernel: its arguments, instance and partial results
+struct Pass {
+    bq::AttnArgs a;
+    const bq::AttnInstance *inst;
+    int tile_rows;
+    int64_t units, ml_bytes, o_bytes;
+};
+struct Plan {
+    Pass rest, shared;
+    bool any_shared;
+};
+
+// Positions per unit: about TARGET units (two CTAs on each of 152 SMs), 128 at
+// least, 2048 at most.
+constexpr int64_t TARGET = 304, CHUNK_MIN = 128, CHUNK_MAX = 2048;
+int chunk_of(int64_t pairs, int64_t positions) {
+    const int64_t n = ((pairs * positions + TARGET - 1) / TARGET + 63) / 64 * 64;
+    return (int)(n < CHUNK_MIN ? CHUNK_MIN : n > CHUNK_MAX ? CHUNK_MAX : n);
+}
+
+bool size_parts(Pass *p, int requests) {
+    const bq_kv_cache *c = &p->a.c;
+    p->a.cluster = 0;
+    p->units = (int64_t)requests * p->a.max_chunks * c->kv_heads * p->a.row_tiles;
+    if ((int64_t)requests * p->a.max_chunks > 0x7fffffffLL || p->units > (1LL << 40)) return false;
+    const int64_t part_rows = p->units * p->tile_rows;
+    p->ml_bytes = (part_rows * (int64_t)sizeof(float2) + 15) / 16 * 16;
+    p->o_bytes = part_rows * c->head_dim * (int64_t)sizeof(float);
+    return true;
+}
+
+bool size_pass(Pass *p, int requests, int64_t rows, int64_t positions, int pairs_of) {
+    const bq_kv_cache *c = &p->a.c;
+    const int nt = bq::attn_tiles(c, rows);
+    p->inst = bq::attn_instance(c, p->a.x.dtype, nt);
+    if (!p->inst) return false;
+    p->tile_rows = 8 * nt;
+    p->a.group_rows = (int)rows;
+    p->a.row_tiles = (int)((rows + 8 * nt - 1) / (8 * nt));
+    p->a.chunk = chunk_of((int64_t)pairs_of * c->kv_heads * p->a.row_tiles, positions);
+    p->a.max_chunks = bq::attn_chunks((int)positions, p->a.chunk);
+    return size_parts(p, requests);
+}
+
+bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_t *counts, const int32_t *shared,
+                  int groups, Plan *p) {
+    if (!c || !x) return BQ_ERR_NULL;
+    const bq_status s = bq::check_attention_shape(c, x);
+    if (s != BQ_OK) return s;
+    if (groups < 1 || groups > BQ_PREFIX_MAX_GROUPS) return BQ_ERR_SHAPE;
+    if (!counts || !shared) return BQ_ERR_NULL;
+    const int64_t capacity = (int64_t)x->table_width * c->page_size;
+    bq::AttnArgs &a = p->rest.a;
+    a.c = *c;
+    a.x = *x;
+    a.page.set((uint32_t)c->page_size);
+    a.group.set((uint32_t)(x->heads / c->kv_heads));
+    a.scale_log2 = x->scale * 1.44269504088896340736f;
+    int64_t end = 0, most_rest = 0, most_shared = 0, most_rows = 0;
+    int sharing = 0;
+    const int64_t each = (int64_t)(x->heads / c->kv_heads) * x->rows;
+    for (int g = 0; g < groups; ++g) {
+        if (counts[g] < 0 || shared[g] < 0 || shared[g] > capacity) return BQ_ERR_SHAPE;
+        end += counts[g];
+        if (end > x->requests) return BQ_ERR_SHAPE;
+        const int pages = counts[g] ? shared[g] / c->page_size : 0;
+        a.group_end[g] = (int)end;
+        a.group_pages[g] = pages;
+        const int64_t common = (int64_t)pages * c->page_size;
+        if (counts[g] && capacity - common > most_rest) most_rest = capacity - common;
+        if (common > most_shared) most_shared = common;
+        if (common && counts[g] * each > most_rows) most_rows = counts[g] * each;
+        sharing += common != 0;
+    }
+    if (end != x->requests) return BQ_ERR_SHAPE;
+    p->any_shared = sharing != 0;
+    p->shared.a = a;
+    a.mode = bq::ATTN_REST;
+    if (!size_pass(&p->rest, x->requests, each, most_rest, x->requests)) return BQ_ERR_SHAPE;
+    if (p->any_shared) {
+        bq::AttnArgs &b = p->shared.a;
+        b.mode = bq::ATTN_PREFIX;
+        b.x.requests = groups;
+        if (!size_pass(&p->shared, groups, most_rows, most_shared, sharing))
+            return BQ_ERR_SHAPE;
+    } else {
+        p->shared.ml_bytes = p->shared.o_bytes = 0;
+    }
+    return BQ_OK;
+}
+
+int64_t bytes_of(const Plan &p) {
+    return p.rest.ml_bytes + p.rest.o_bytes + p.shared.ml_bytes + p.shared.o_bytes;
+}
+
+cudaError_t run(Pass *p, int sms, void *stream, unsigned int *status) {
+    const size_t smem = p->inst->smem + (size_t)(p->a.x.requests + 1) * sizeof(int);
+    int occ = 0;
+    if (p->inst->occupancy(smem, &occ) != 0 || occ < 1) return cudaErrorInvalidConfiguration;
+    const int64_t slots = (int64_t)sms * occ;
+    constexpr int64_t DIRECT = 8;  // as in bq_paged_attention
+    p->a.direct = p->units <= DIRECT * slots;
+    const int64_t grid = p->a.direct || p->units < slots ? p->units : slots;
+    return p->inst->launch(p->a, (int)grid, smem, stream, status);
+}
+
+Parts parts_of(const Pass &p) {
+    return {p.a.part_o, p.a.part_ml, p.a.chunk, p.a.max_chunks, p.a.row_tiles, p.tile_rows};
+}
+
+}  // namespace
+
+int bq_internal_status_attn_prefix(unsigned int *flags, int clear) { return read_status_attn_prefix(flags, clear); }
+
+extern "C" int64_t bq_paged_prefix_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args,
+                                                             const int32_t *group_requests, const int32_t *group_shared,
+                                                             int groups) {
+    Plan p;
+    return plan_of(cache, args, group_requests, group_shared, groups, &p) == BQ_OK ? bytes_of(p) : -1;
+}
+
+extern "C" bq_status bq_paged_prefix_attention(const bq_kv_cache *cache, const bq_attention_args *x,
+                                               const int32_t *group_requests, const int32_t *group_shared, int groups,
+                                               void *workspace, int64_t workspace_bytes, void *stream) {
+    Plan p;
+    bq_status s = plan_of(cache, x, group_requests, group_shared, groups, &p);
+    if (s != BQ_OK) return s;
+    if (x->requests == 0) return BQ_OK;
+    s = bq::check_attention_pointers(cache, x);
+    if (s != BQ_OK) return s;
+    if (!workspace) return BQ_ERR_NULL;
+    if (!bq::aligned_to(workspace, 16)) return BQ_ERR_ALIGN;
+    if (workspace_bytes < bytes_of(p)) return BQ_ERR_SHAPE;
+    uint8_t *at = static_cast<uint8_t *>(workspace);
+    for (Pass *pass : {&p.rest, &p.shared}) {
+        pass->a.part_ml = reinterpret_cast<float2 *>(at);
+        pass->a.part_o = reinterpret_cast<float *>(at + pass->ml_bytes);
+        at += pass->ml_bytes + pass->o_bytes;
+    }
+    const int sms = bq::device_sms();
+    if (!sms) return BQ_ERR_CUDA;
+    unsigned int *status = nullptr;
+    cudaError_t e = status_address(&status);
+    if (e == cudaSuccess && p.any_shared) e = run(&p.shared, sms, stream, status);
+    if (e == cudaSuccess) e = run(&p.rest, sms, stream, status);
+    if (e != cudaSuccess) return bq::from_cuda_error(e);
+    JoinArgs j;
+    j.a = p.rest.a;
+    j.rest = parts_of(p.rest);
+    j.shared = p.any_shared ? parts_of(p.shared) : Parts{nullptr, nullptr, 1, 0, 1, 1};
+    e = x->dtype == BQ_F32   ? join<BQ_F32>(j, stream)
+        : x->dtype == BQ_F16 ? join<BQ_F16>(j, stream)
+                             : join<BQ_BF16>(j, stream);
+    return bq::from_cuda_error(e);
+}

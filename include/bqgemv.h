@@ -376,6 +376,7 @@ typedef enum { BQ_F32 = 0, BQ_F16 = 1, BQ_BF16 = 30 } bq_dtype; /* (Q8_0 = 8: bq
 #define BQ_DEVERR_LENGTH 0x200u /* attention: a length below 0 or beyond the table */
 #define BQ_DEVERR_SLOT 0x400u /* append: a slot beyond the pool */
 #define BQ_DEVERR_POOL 0x800u /* tables: the free stack would pass the pool */
+#define BQ_DEVERR_WAIT 0x1000u /* attention over shared pages: a wait inside the kernel ran out (its results are not valid) */
 
 /* One layer's paged cache: `pages` pages of `page_size` positions each, of
  * kv_heads heads of head_dim values.  Value d of head h in slot s of page p
@@ -531,6 +532,30 @@ typedef struct {
 int64_t bq_paged_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args);
 bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *args, void *workspace,
                              int64_t workspace_bytes, void *stream);
+
+/* bq_paged_attention for requests that share the beginning of their histories:
+ * the same result, the shared pages gone through once for all of a group's rows.
+ * The requests come in `groups` groups in order, group g's group_requests[g] of
+ * them sharing their first group_shared[g] positions.  Whole pages count: the
+ * first group_shared[g] / page_size entries of the requests' table rows, which
+ * must name the same pages (they are read from the first request of the group
+ * that sees them).  Positions behind them are each request's own.
+ *  - A request's rows see all its shared positions: lens[b] - rows + 1 >= the
+ *    positions of its shared pages.  One that does not gives zeros, and sets
+ *    BQ_DEVERR_LENGTH unless its length is 0 (an ended request of the batch).
+ *  - group_requests and group_shared are host arrays, read by the call: 1 <=
+ *    groups <= BQ_PREFIX_MAX_GROUPS, counts not negative and summing to
+ *    args->requests, 0 <= group_shared <= table_width * page_size.
+ *  - args, outputs, masks, status bits and workspace as for bq_paged_attention,
+ *    with bq_paged_prefix_attention_workspace_bytes.  A row's bits depend on its
+ *    own inputs and the call's geometry (the groups among it): they are not those
+ *    of bq_paged_attention. */
+#define BQ_PREFIX_MAX_GROUPS 64
+int64_t bq_paged_prefix_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args,
+                                                  const int32_t *group_requests, const int32_t *group_shared, int groups);
+bq_status bq_paged_prefix_attention(const bq_kv_cache *cache, const bq_attention_args *args,
+                                    const int32_t *group_requests, const int32_t *group_shared, int groups,
+                                    void *workspace, int64_t workspace_bytes, void *stream);
 
 /* The norms after one block and before the next, with the block's gate and
  * the residual scales, per row of `width` values:

@@ -1,0 +1,326 @@
+"""Attention of requests that share their first pages (paged_prefix_attention)
+against a plain 64-bit form that knows nothing of sharing."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_dequant_gb300 as bq
+
+import paged_plain as plain
+from test_gpu_cache import BF16, DEV, F16, F32, KINDS, filled_cache, healthy, normal, poison, rng  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def shared_table(g, lens, shared, page, pages, width=None, junk=-1):
+    """A table whose requests have their group's first pages in common: shared is a
+    list of (requests, positions); a request of length 0 has a row of junk."""
+    width = width or max(1, max(-(-n // page) for n in lens))
+    order = g.permutation(pages)
+    table, at, b = np.full((len(lens), width), junk, np.int32), 0, 0
+    for count, positions in shared:
+        common = order[at:at + positions // page]
+        at += common.size
+        for _ in range(count):
+            need = -(-lens[b] // page)
+            if lens[b]:
+                table[b, :common.size] = common
+                table[b, common.size:need] = order[at:at + need - common.size]
+                at += max(0, need - common.size)
+            b += 1
+    assert at <= pages and b == len(lens)
+    return torch.from_numpy(table).to(DEV)
+
+
+def pages_needed(lens, shared, page):
+    b, n = 0, 3
+    for count, positions in shared:
+        n += positions // page + sum(max(0, -(-m // page) - positions // page) for m in lens[b:b + count])
+        b += count
+    return n
+
+
+def bound_of(want, mag, top, dtype, kind):
+    """paged_plain's bound, and what is carried here in fewer bits: over a bf16 cache
+    the weights as two bf16 parts (each leaves half a unit of 2^-8 of the rest:
+    2^-17 of a weight) and the products of a 128-position tile summed by the tensor
+    cores, up to 2 * 32 * 8 additions of the running sum between the fp32 joins,
+    each off by 2^-23 of a sum of magnitudes: 2^-14."""
+    extra = (2.0 ** -17 + 2.0 ** -14) * mag
+    return plain.attention_bound(want, mag, top, dtype, False) + extra * (1 + plain.EPS[dtype])
+
+
+def check(cache, q, table, lens, shared, rows=1, scale=None, out=None, **more):
+    n = len(lens)
+    got = bq.paged_prefix_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV), shared, rows=rows,
+                                    scale=scale, out=out, **more)
+    k, v = plain.values(cache)
+    s = cache.head_dim ** -0.5 if scale is None else scale
+    want, mag, top = plain.attention(k, v, q.cpu(), table.cpu(), lens, rows, s)
+    bound = bound_of(want, mag, top, q.dtype, cache.kind)
+    err = (got.cpu().double() - want).abs()
+    bad = ~(err <= bound)
+    assert not bad.any(), (f"{int(bad.sum())} of {bad.numel()} outside the bound; worst {err[bad].max()} at "
+                           f"{bad.nonzero()[0].tolist()}")
+    assert n == lens.__len__()
+    return got
+
+
+def case(g, kind, dtype, lens, shared, page, heads, kv, D, rows=1, layout="hs", width=None, hurt=True, **more):
+    groups = [(len(lens), shared)] if isinstance(shared, int) else shared
+    pages = pages_needed(lens, groups, page)
+    cache = filled_cache(g, kind, pages, page, kv, D, layout)
+    table = shared_table(g, lens, groups, page, pages, width)
+    if hurt:
+        poison(cache, table, lens)
+    q = normal(g, (len(lens) * rows, heads, D), dtype)
+    return check(cache, q, table, lens, shared, rows=rows, **more), cache, q, table
+
+
+@pytest.mark.parametrize("kind,dtype", KINDS)
+@pytest.mark.parametrize("D,heads,kv", [(128, 16, 4), (64, 14, 2), (96, 6, 3), (256, 4, 1), (32, 5, 5), (160, 2, 2)])
+def test_types_and_heads(kind, dtype, D, heads, kv):
+    """Ragged rests, one of them empty, one request that has ended."""
+    lens = [300, 289, 288, 0, 417, 305]
+    case(rng("p", kind, str(dtype), D), kind, dtype, lens, 288, 16, heads, kv, D)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
+@pytest.mark.parametrize("shared", [0, 1, 15, 16, 17, 127, 128, 129, 255, 257, 640, 1000])
+def test_shared_lengths(kind, dtype, shared):
+    """From nothing to beyond tiles and chunks; what is not a whole page is each request's own."""
+    lens = [shared + 1, shared + 40, shared + 2]
+    case(rng("s", kind, shared), kind, dtype, lens, shared, 16, 8, 2, 128)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("f16", F16), ("bf16", BF16), ("bf16", F32), ("q8_0", BF16)])
+@pytest.mark.parametrize("requests,heads,kv", [(1, 1, 1), (33, 8, 2), (130, 4, 4), (64, 16, 4), (300, 7, 1)])
+def test_many_rows(kind, dtype, requests, heads, kv):
+    """Tiles of query rows, the last one ragged."""
+    g = rng("r", kind, requests)
+    lens = [200 + int(n) for n in g.integers(1, 60, requests)]
+    case(g, kind, dtype, lens, 200, 8, heads, kv, 64)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
+def test_a_long_prefix(kind, dtype):
+    lens = [9003, 9100, 9003, 0, 9777]
+    case(rng("long", kind), kind, dtype, lens, 9003, 24, 8, 2, 128, hurt=False)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
+@pytest.mark.parametrize("rows", [2, 5, 6])
+def test_verify_rows(kind, dtype, rows):
+    """Row r of a request sees rows - 1 - r positions fewer; the first one sees the
+    whole prefix and maybe nothing else."""
+    lens = [256 + rows - 1, 256 + rows, 300, 0, 271]
+    case(rng("v", kind, rows), kind, dtype, lens, 256, 16, 8, 2, 128, rows=rows)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
+def test_groups(kind, dtype):
+    """Groups of several lengths, one that shares nothing, an empty one, one whose
+    first request has ended, one that has ended whole."""
+    shared = [(3, 700), (2, 0), (0, 500), (4, 129), (2, 64), (1, 2000)]
+    lens = [710, 900, 701, 5, 333, 0, 140, 131, 600, 0, 0, 2004]
+    case(rng("g", kind), kind, dtype, lens, shared, 16, 8, 2, 64)
+
+
+def test_groups_of_one():
+    shared = [(1, 10 * i) for i in range(64)]
+    case(rng("g1"), "f16", F16, [10 * i + 7 for i in range(64)], shared, 8, 4, 2, 64)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", BF16)])
+@pytest.mark.parametrize("page,layout", [(1, "hs"), (7, "sh"), (24, "kv"), (128, "sh"), (200, "hs")])
+def test_pages_and_layouts(kind, dtype, page, layout):
+    lens = [500, 433, 470]
+    case(rng("l", kind, page), kind, dtype, lens, 431, page, 6, 2, 64, layout=layout)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.2, 3.0])
+def test_scales(scale):
+    for kind, dtype in (("f16", F32), ("bf16", BF16), ("q8_0", F32)):
+        case(rng("scale", kind), kind, dtype, [400, 390, 385], 384, 16, 8, 2, 128, scale=scale)
+
+
+def test_strided_queries_outputs_in_place_and_a_workspace():
+    g = rng("strides")
+    for kind, dtype in (("f16", F32), ("bf16", BF16), ("q8_0", F32)):
+        lens, page = [400, 390, 385], 16
+        cache = filled_cache(g, kind, 90, page, 2, 64)
+        table = shared_table(g, lens, [(3, 384)], page, 90, width=40)
+        wide = normal(g, (3, 8 + 2, 64 + 1), dtype)
+        q = wide[:, 1:9, 1:]
+        first = check(cache, q, table, lens, 384)
+        again = bq.paged_prefix_attention(cache, q.contiguous(), table, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                          384)
+        assert torch.equal(first, again)
+        room = torch.empty(bq.paged_prefix_attention_workspace(cache, 3, 1, 8, 40, 384, dtype) + 5, dtype=torch.uint8,
+                           device=DEV)
+        room.fill_(255)
+        out = normal(g, (3, 10, 80), dtype)
+        kept = out.clone()
+        view = out[:, 2:, 3:67]
+        bq.paged_prefix_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV), [(3, 384)], out=view,
+                                  workspace=room)
+        assert torch.equal(view, first)
+        kept[:, 2:, 3:67] = view
+        assert torch.equal(out, kept)  # and nothing else
+        same = q.clone()
+        assert torch.equal(bq.paged_prefix_attention(cache, same, table, torch.tensor(lens, dtype=torch.int32, device=DEV),
+                                                     384, out=same), first)
+        assert torch.equal(same, first)
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
+def test_large_scores_and_growing_maxima(kind, dtype):
+    """Scores of hundreds, rising and falling over the positions: the running maximum
+    is replaced again and again, or never after the first tile."""
+    g = rng("grow", kind)
+    page, n = 16, 2048
+    for order in (1, -1):
+        cache = filled_cache(g, kind, n // page + 12, page, 1, 64)
+        table = shared_table(g, [n + 20, n + 9], [(2, n)], page, n // page + 12)
+        ramp = torch.linspace(0.05, 12.0, n, device=DEV)[::order].contiguous() if order == 1 else torch.linspace(
+            12.0, 0.05, n, device=DEV)
+        ids = table[0, :n // page].long()
+        k = ramp.view(-1, 1, page, 1) * (0.5 + 0.5 * torch.rand(n // page, 1, page, 64, device=DEV))
+        if kind == "q8_0":
+            cache.k_scale[ids] = (k.abs().amax(-1, keepdim=True) / 127).to(F16).expand(-1, -1, -1, 2)
+            cache.k[ids] = (k / cache.k_scale[ids].float().repeat_interleave(32, -1)).round().clamp(-127, 127).to(torch.int8)
+        else:
+            cache.k[ids] = k.to(cache.k.dtype)
+        q = (0.5 + normal(g, (2, 4, 64)).abs()).to(dtype)
+        check(cache, q, table, [n + 20, n + 9], n)
+
+
+def test_values_that_are_not_finite_reach_only_their_rows_and_heads():
+    g = rng("inf")
+    for kind, dtype in (("f16", F32), ("bf16", BF16)):
+        lens, page = [300, 290, 289], 16
+        out, cache, q, table = case(g, kind, dtype, lens, 288, page, 4, 2, 64)
+        own = int(table[1, 18])
+        cache.v[own, 1, 0, 3] = float("nan")  # of request 1's own page, head 1
+        hurt = bq.paged_prefix_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV), 288)
+        same = torch.ones_like(out, dtype=torch.bool)
+        same[1, 2:, 3] = False
+        assert torch.equal(out[same], hurt[same]) and hurt[1, 2:, 3].isnan().all()
+        cache.k[int(table[0, 3]), 0, 5, 7] = float("nan")  # of the shared pages, head 0
+        hurt = bq.paged_prefix_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV), 288)
+        assert hurt[:, :2].isnan().all() and torch.equal(hurt[:, 2:][same[:, 2:]], out[:, 2:][same[:, 2:]])
+        qq = q.clone()
+        cache.k[int(table[0, 3]), 0, 5, 7] = 0.0
+        cache.v[own, 1, 0, 3] = 0.0
+        want = bq.paged_prefix_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV), 288)
+        qq[2, 3, 0] = float("inf")  # one row's query
+        hurt = bq.paged_prefix_attention(cache, qq, table, torch.tensor(lens, dtype=torch.int32, device=DEV), 288)
+        keep = torch.ones(3, 4, dtype=torch.bool, device=DEV)
+        keep[2, 3] = False
+        assert torch.equal(hurt[keep], want[keep]) and not hurt[2, 3].isfinite().all()
+
+
+def test_a_row_has_its_bits_whatever_is_beside_it():
+    """Other queries and other requests' own pages do not move a row."""
+    for kind, dtype in (("f16", F32), ("bf16", BF16), ("q8_0", F32)):
+        g = rng("beside", kind)
+        lens = [1100, 1050, 1029, 1033]
+        out, cache, q, table = case(g, kind, dtype, lens, 1024, 16, 8, 2, 128, hurt=False)
+        q2 = q * 3
+        q2[1] = q[1]
+        for b in (0, 2, 3):
+            own = table[b, 64:-(-lens[b] // 16)].long()
+            if cache.k_scale is None:
+                cache.k[own] = -cache.k[own]
+            else:
+                cache.k_scale[own] = cache.k_scale[own] * 2
+        again = bq.paged_prefix_attention(cache, q2, table, torch.tensor(lens, dtype=torch.int32, device=DEV), 1024)
+        assert torch.equal(again[1], out[1])
+
+
+def test_bad_pages_and_short_requests_are_reported():
+    g = rng("bad")
+    for kind, dtype in (("f16", F32), ("bf16", BF16), ("q8_0", F32)):
+        lens, page, pages = [300, 290, 200, 289], 16, 60
+        cache = filled_cache(g, kind, pages, page, 2, 64)
+        table = shared_table(g, [300, 290, 300, 289], [(4, 288)], page, pages)
+        q = normal(g, (4, 4, 64), dtype)
+        at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        out = bq.paged_prefix_attention(cache, q, table, at, 288)
+        assert bq.device_status(clear=True) == 0x200  # request 2 does not see its prefix
+        assert (out[2] == 0).all() and (out[[0, 1, 3]] != 0).any(-1).all()
+        table[:, 3] = pages + 5  # a shared page outside the pool: masked
+        at[2] = 0
+        hurt = bq.paged_prefix_attention(cache, q, table, at, 288)
+        assert bq.device_status(clear=True) == 0x100
+        k, v = plain.values(cache)
+        t = table.cpu().clone()
+        keep = [i for i in range(t.shape[1]) if i != 3]
+        cut = t[:, keep]
+        want, mag, top = plain.attention(k, v, q.cpu(), cut, [n - 16 if n else 0 for n in at.tolist()], 1, 64 ** -0.5)
+        assert ((hurt.cpu().double() - want).abs() <= bound_of(want, mag, top, dtype, kind)).all()
+
+
+def test_captured_and_replayed_with_other_lengths_beside_another_graph():
+    g = rng("graph")
+    page, pages = 16, 200
+    caches = [filled_cache(g, kind, pages, page, 2, 128) for kind in ("f16", "q8_0")]
+    table = shared_table(g, [900, 900, 900], [(3, 640)], page, pages)
+    q = normal(g, (3, 8, 128))
+    lens = torch.tensor([641, 650, 700], dtype=torch.int32, device=DEV)
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for cache in caches:
+        bq.paged_prefix_attention(cache, q, table, lens, 640)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            out = bq.paged_prefix_attention(cache, q, table, lens, 640)
+        graphs.append((graph, out))
+    for step in range(4):
+        lens += 13
+        torch.cuda.synchronize()
+        for (graph, _), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        for cache, (_, out) in zip(caches, graphs):
+            assert torch.equal(out, bq.paged_prefix_attention(cache, q, table, lens, 640))
+
+
+def test_it_agrees_with_ordinary_attention_at_a_servers_size():
+    """Both forms of one call lie within their bounds of one another."""
+    g = rng("both")
+    requests, page = 40, 32
+    lens = [6000 + int(n) for n in g.integers(1, 300, requests)]
+    pages = pages_needed(lens, [(requests, 6000)], page)
+    for kind, dtype in (("f16", F16), ("bf16", BF16), ("q8_0", F32)):
+        cache = filled_cache(g, kind, pages, page, 4, 128)
+        table = shared_table(g, lens, [(requests, 6000)], page, pages)
+        q = normal(g, (requests, 16, 128), dtype)
+        at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        a = bq.paged_attention(cache, q, table, at).double()
+        b = bq.paged_prefix_attention(cache, q, table, at, 6000).double()
+        # outputs are means of thousands of N(0, 1) values (a Q8_0 value's rms is 2.2): below 0.5.
+        # Each is off by half a unit of its type and 2^-13 of the mean magnitude (below 2).
+        assert float((a - b).abs().max()) <= 2 * (plain.EPS[dtype] / 2 * 0.5 + 2.0 ** -13 * 2)
+
+
+def test_nothing_to_do_and_refusals():
+    cache = bq.PagedKVCache.zeros(8, 16, 2, 64)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    q, table, lens = torch.zeros(2, 4, 64, device=DEV), torch.zeros(2, 4, **i32), torch.full((2,), 20, **i32)
+    none = bq.paged_prefix_attention(cache, q[:0], table[:0], lens[:0], 16)
+    assert none.shape == (0, 4, 64)
+    for bad in (-1, 65, [(1, 16)], [(3, 16)], [(3, 16), (-1, 16)], [], [(1, 8)] * 65):
+        with pytest.raises((ValueError, bq.BQError)):
+            bq.paged_prefix_attention(cache, q, table, lens, bad)
+    with pytest.raises(ValueError):
+        bq.paged_prefix_attention(cache, q, table, lens, 16, rows=7)
+    with pytest.raises(TypeError):
+        bq.paged_prefix_attention(cache, q, table, lens.long(), 16)
+    with pytest.raises(ValueError):
+        bq.paged_prefix_attention(cache, q, table[:1], lens, 16)
+    with pytest.raises(bq.BQError):
+        bq.paged_prefix_attention(cache, q, table, lens, 16, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(bq.BQError):
+        bq.paged_prefix_attention(cache, q, table, lens, 16, scale=float("nan"))
