@@ -14,6 +14,10 @@
 
 #include "bq_attn.h"
 
+// bq_attn_tcgen05_<cache>.cu
+cudaError_t bq_internal_prefix_f16(const bq::AttnArgs &, int grid, void *stream, unsigned int *status);
+cudaError_t bq_internal_prefix_bf16(const bq::AttnArgs &, int grid, void *stream, unsigned int *status);
+
 namespace {
 
 BQ_STATUS_WORD(attn_prefix)
@@ -156,7 +160,7 @@ cudaError_t join(const JoinArgs &j, void *stream) {
 // one pass of the attention kernel: its arguments, instance and partial results
 struct Pass {
     bq::AttnArgs a;
-    const bq::AttnInstance *inst;
+    const bq::AttnInstance *inst;  // NULL: the tensor-memory kernel
     int tile_rows;
     int64_t units, ml_bytes, o_bytes;
 };
@@ -195,6 +199,44 @@ bool size_pass(Pass *p, int requests, int64_t rows, int64_t positions, int pairs
     p->a.chunk = chunk_of((int64_t)pairs_of * c->kv_heads * p->a.row_tiles, positions);
     p->a.max_chunks = bq::attn_chunks((int)positions, p->a.chunk);
     return size_parts(p, requests);
+}
+
+// The tensor-memory kernel for 16-bit caches with heads of up to 128 values:
+// tiles of 128 rows, chunks of whole tiles of 128 positions, one CTA per SM.
+bool has_tensor_kernel(const bq_kv_cache *c) { return c->type != BQ_Q8_0 && c->head_dim <= 128; }
+constexpr int TILE = 128;
+
+// Tiles of a chunk: the fewest steps of the whole GPU, a chunk's start, joins and
+// partial results counted as FIXED tiles.  At most MOST tiles, so that the
+// tensor core's sums stay short.
+bool size_tensor_pass(Pass *p, int groups, int64_t rows, int64_t positions, int sms) {
+    constexpr int FIXED = 6, MOST = 64;
+    p->inst = nullptr;
+    p->tile_rows = TILE;
+    p->a.group_rows = (int)rows;
+    p->a.row_tiles = (int)((rows + TILE - 1) / TILE);
+    const int64_t pairs = (int64_t)p->a.c.kv_heads * p->a.row_tiles;
+    const int64_t tiles = (positions + TILE - 1) / TILE;
+    int64_t best = 0, cost = 0;
+    const int64_t least = (tiles + MOST - 1) / MOST;
+    for (int64_t c = least; c < least + 2 * sms && c <= tiles; ++c) {  // chunks of the longest prefix
+        const int64_t n = (tiles + c - 1) / c;
+        if (c > least && n == best) continue;
+        int64_t units = 0;
+        for (int g = 0; g < groups; ++g) {
+            const int64_t of = (int64_t)p->a.group_pages[g] * p->a.c.page_size;
+            const int64_t requests = p->a.group_end[g] - (g ? p->a.group_end[g - 1] : 0);
+            const int64_t row_tiles = (requests * p->a.x.rows * (int)p->a.group.d + TILE - 1) / TILE;
+            units += p->a.c.kv_heads * row_tiles * ((of + n * TILE - 1) / (n * TILE));
+        }
+        const int64_t now = (units + sms - 1) / sms * (n + FIXED);
+        if (!best || now < cost) best = n, cost = now;
+        if (units > 2 * sms && n <= FIXED) break;
+    }
+    p->a.chunk = (int)best * TILE;
+    p->a.max_chunks = bq::attn_chunks((int)positions, p->a.chunk);
+    if ((int64_t)groups * pairs * p->a.max_chunks > 0x7fffffffLL) return false;
+    return size_parts(p, groups);
 }
 
 bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_t *counts, const int32_t *shared,
@@ -236,7 +278,9 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_
         bq::AttnArgs &b = p->shared.a;
         b.mode = bq::ATTN_PREFIX;
         b.x.requests = groups;
-        if (!size_pass(&p->shared, groups, most_rows, most_shared, sharing))
+        // (152 SMs whatever the device: the workspace's size is told without one)
+        if (has_tensor_kernel(c) ? !size_tensor_pass(&p->shared, groups, most_rows, most_shared, 152)
+                                 : !size_pass(&p->shared, groups, most_rows, most_shared, sharing))
             return BQ_ERR_SHAPE;
     } else {
         p->shared.ml_bytes = p->shared.o_bytes = 0;
@@ -249,6 +293,9 @@ int64_t bytes_of(const Plan &p) {
 }
 
 cudaError_t run(Pass *p, int sms, void *stream, unsigned int *status) {
+    if (!p->inst)
+        return p->a.c.type == BQ_F16 ? bq_internal_prefix_f16(p->a, (int)p->units, stream, status)
+                                     : bq_internal_prefix_bf16(p->a, (int)p->units, stream, status);
     const size_t smem = p->inst->smem + (size_t)(p->a.x.requests + 1) * sizeof(int);
     int occ = 0;
     if (p->inst->occupancy(smem, &occ) != 0 || occ < 1) return cudaErrorInvalidConfiguration;
