@@ -28,7 +28,8 @@ __all__ = ["Q8_0", "Q4_0", "Q4_K", "BLOCK_BYTES", "BQError", "packed_bytes", "qu
            "gemv", "gemv_q8_0", "gemv_q4_0", "gemv_q4_k", "gemv_gate_up_silu", "gemv_verify",
            "gemv_qkv_bias", "gemv_f16", "concat_packed",
            "device_status", "tree_lanes", "version", "StreamOp", "StreamPlan",
-           "PagedKVCache", "Rope", "BlockTables", "kv_block_tables", "kv_append", "paged_attention",
+           "PagedKVCache", "Rope", "BlockTables", "SharedBlockTables", "kv_block_tables", "kv_shared_tables",
+           "kv_copy_pages", "kv_compact", "kv_append", "paged_attention",
            "paged_attention_workspace", "paged_prefix_attention", "paged_prefix_attention_workspace", "sandwich_norm"]
 
 
@@ -322,6 +323,6 @@ class StreamPlan:
             self._handle = None
 
 
-from .cache import (BlockTables, PagedKVCache, Rope, kv_append, kv_block_tables,  # noqa: E402
-                    paged_attention, paged_attention_workspace, paged_prefix_attention,
+from .cache import (BlockTables, PagedKVCache, Rope, SharedBlockTables, kv_append,  # noqa: E402
+                    kv_block_tables, kv_compact, kv_copy_pages, kv_shared_tables, paged_attention, paged_attention_workspace, paged_prefix_attention,
                     paged_prefix_attention_workspace, sandwich_norm)

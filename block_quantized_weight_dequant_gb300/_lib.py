@@ -26,7 +26,8 @@ EXPORTS = ("bq_version", "bq_status_str", "bq_packed_bytes", "bq_quantize_pack",
            "bq_gemv_f16", "bq_gemv_f16_f16out", "bq_device_status",
            "bq_tree_lanes", "bq_stream_workspace_bytes", "bq_stream_plan_create",
            "bq_stream_plan_launch", "bq_stream_plan_tune", "bq_stream_plan_launches",
-           "bq_stream_plan_destroy", "bq_stream_run_noalloc", "bq_kv_block_tables", "bq_kv_append", "bq_kv_append_norm",
+           "bq_stream_plan_destroy", "bq_stream_run_noalloc", "bq_kv_block_tables",
+           "bq_kv_shared_tables", "bq_kv_copy_pages", "bq_kv_compact", "bq_kv_append", "bq_kv_append_norm",
            "bq_paged_attention_workspace_bytes", "bq_paged_attention",
            "bq_paged_prefix_attention_workspace_bytes", "bq_paged_prefix_attention", "bq_sandwich_norm")
 BQ_NOALLOC_MAX_OPS = 512
@@ -56,6 +57,19 @@ class BqKvTables(ctypes.Structure):
                 + [(n, _I64) for n in ("table_stride", "max_tokens")]
                 + [(n, _VP) for n in ("lens", "new_lens", "table", "free_pages", "free_count", "slots",
                                       "positions", "starts", "lens_out", "free_count_out", "refused")])
+
+
+class BqKvSharing(ctypes.Structure):
+    """bq_kv_sharing of include/bqgemv.h"""
+    _fields_ = [(n, _VP) for n in ("parents", "refs", "copy_src", "copy_dst", "copy_count")]
+
+
+class BqKvCompactArgs(ctypes.Structure):
+    """bq_kv_compact_args of include/bqgemv.h"""
+    _fields_ = ([(n, _I32) for n in ("requests", "page_size", "table_width", "pool")]
+                + [(n, _I64) for n in ("table_stride", "max_moves")]
+                + [(n, _VP) for n in ("lens", "table", "free_pages", "refs", "copy_src", "copy_dst", "copy_count",
+                                      "moved", "free_count_out")])
 
 
 class BqKvAppendArgs(ctypes.Structure):
@@ -123,6 +137,9 @@ def _declare(lib):
         "bq_stream_plan_destroy": (i32, [vp]),
         "bq_stream_run_noalloc": (i32, [i32, ctypes.POINTER(BqOp), i32, vp]),
         "bq_kv_block_tables": (i32, [ctypes.POINTER(BqKvTables), vp]),
+        "bq_kv_shared_tables": (i32, [ctypes.POINTER(BqKvTables), ctypes.POINTER(BqKvSharing), vp]),
+        "bq_kv_copy_pages": (i32, [ctypes.POINTER(vp), i32, vp, vp, vp, i64, vp]),
+        "bq_kv_compact": (i32, [ctypes.POINTER(BqKvCompactArgs), vp]),
         "bq_kv_append": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqKvAppendArgs), vp]),
         "bq_kv_append_norm": (i32, [ctypes.POINTER(BqKvCache), ctypes.POINTER(BqKvAppendArgs),
                                     ctypes.POINTER(BqKvNormArgs), vp]),

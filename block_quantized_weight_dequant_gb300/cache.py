@@ -17,7 +17,8 @@ import torch
 from . import _lib
 from ._lib import BQ_VERIFY_MAX_ROWS, lib
 
-__all__ = ["PagedKVCache", "Rope", "BlockTables", "kv_block_tables", "kv_append", "paged_attention",
+__all__ = ["PagedKVCache", "Rope", "BlockTables", "SharedBlockTables", "kv_block_tables",
+           "kv_shared_tables", "kv_copy_pages", "kv_compact", "kv_append", "paged_attention",
            "paged_attention_workspace", "paged_prefix_attention", "paged_prefix_attention_workspace", "sandwich_norm"]
 
 _DTYPES = {torch.float32: _lib.BQ_F32, torch.float16: _lib.BQ_F16, torch.bfloat16: _lib.BQ_BF16}
@@ -174,6 +175,7 @@ class PagedKVCache:
         self._c = _lib.BqKvCache(kind, kv_heads, head_dim, page_size, pages, *strides, k.data_ptr(),
                                  v.data_ptr(), ptr(k_scale), ptr(v_scale))
         self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
         self._scale = 1.0 / math.sqrt(head_dim)
         self._workspace = {}  # workspace bytes by call geometry
 
@@ -257,6 +259,106 @@ def kv_block_tables(lens, new_lens, table, free_pages, free_count, page_size, sl
     return refused
 
 
+def kv_shared_tables(lens, new_lens, table, free_pages, free_count, refs, page_size, slots, positions, starts, copy_src,
+                     copy_dst, copy_count, parents=None, lens_out=None, free_count_out=None, refused=None):
+    """kv_block_tables for requests that share pages: `refs` int32 [pool] counts the
+    requests that hold each page (updated in place), and request b with parents[b] >=
+    0 (int32 [requests]; its length must be 0) becomes a fork of that request at
+    min(its length, new_lens[b]) positions before it grows.  A request that grows out
+    of a partly filled page that others hold too gets a page of its own for it; the
+    pages to copy for that are the first `copy_count` [1] of `copy_src` and
+    `copy_dst` [requests] (kv_copy_pages in every layer, before anything is
+    appended).  Pages whose count comes to 0 are free from the next call on.  See
+    bq_kv_shared_tables in include/bqgemv.h for the order.  Returns `refused` [1]."""
+    _need(lens, "lens")
+    dev = lens.device
+    i32 = torch.int32
+    _dense(lens, "lens", i32, dev)
+    n = lens.numel()
+    _dense(new_lens, "new_lens", i32, dev, n)
+    width, stride = _table(table, n, dev)
+    _dense(free_pages, "free_pages", i32, dev)
+    pool = free_pages.numel()
+    _dense(free_count, "free_count", i32, dev, 1)
+    _dense(refs, "refs", i32, dev, pool)
+    _dense(slots, "slots", torch.int64, dev)
+    _dense(positions, "positions", i32, dev, slots.numel())
+    _dense(starts, "starts", i32, dev, n + 1)
+    _dense(copy_src, "copy_src", i32, dev, n)
+    _dense(copy_dst, "copy_dst", i32, dev, n)
+    _dense(copy_count, "copy_count", i32, dev, 1)
+    if parents is not None:
+        _dense(parents, "parents", i32, dev, n)
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    refused = torch.empty(1, dtype=i32, device=dev) if refused is None else refused
+    _dense(lens_out, "lens_out", i32, dev, n)
+    _dense(free_count_out, "free_count_out", i32, dev, 1)
+    _dense(refused, "refused", i32, dev, 1)
+    args = _lib.BqKvTables(n, _i32(page_size), width, _i32(pool), stride, slots.numel(),
+                           lens.data_ptr(), new_lens.data_ptr(), table.data_ptr(), free_pages.data_ptr(),
+                           free_count.data_ptr(), slots.data_ptr(), positions.data_ptr(), starts.data_ptr(),
+                           lens_out.data_ptr(), free_count_out.data_ptr(), refused.data_ptr())
+    sharing = _lib.BqKvSharing(None if parents is None else parents.data_ptr(), refs.data_ptr(), copy_src.data_ptr(),
+                               copy_dst.data_ptr(), copy_count.data_ptr())
+    _call(lib.bq_kv_shared_tables, "kv_shared_tables", dev, _byref(args), _byref(sharing))
+    return refused
+
+
+def kv_copy_pages(caches, src, dst, count=None):
+    """Copy pages src to dst (int32 [pairs]) within each cache of a list (a model's
+    layers: one geometry, strides among it), or of one cache; with `count` (int32
+    [1]) the first `count` pairs only.  Pairs with a negative number are skipped.  No
+    destination may stand twice, or be a source."""
+    if type(caches) is PagedKVCache:
+        caches = (caches,)
+    if not len(caches):
+        return
+    dev = caches[0].device if type(caches[0]) is PagedKVCache else None
+    for c in caches:
+        if type(c) is not PagedKVCache:
+            raise TypeError("caches must be PagedKVCache objects")
+        if c.device != dev:
+            raise ValueError(f"a cache is on {c.device}, expected {dev}")
+    _dense(src, "src", torch.int32, dev)
+    pairs = src.numel()
+    _dense(dst, "dst", torch.int32, dev, pairs)
+    if count is not None:
+        _dense(count, "count", torch.int32, dev, 1)
+    n = len(caches)
+    _call(lib.bq_kv_copy_pages, "kv_copy_pages", dev, (ctypes.c_void_p * n)(*[c._address for c in caches]), n,
+          src.data_ptr(), dst.data_ptr(), None if count is None else count.data_ptr(), pairs)
+
+
+def kv_compact(lens, table, free_pages, free_count, refs, page_size, copy_src, copy_dst, copy_count, moved,
+               free_count_out=None):
+    """Compact the pool of shared pages: the highest pages in use (refs > 0) move to
+    the lowest free ones, as many moves as `copy_src` and `copy_dst` have room for
+    (half the pool is always enough); the rows of `table` and `refs` are renumbered,
+    `free_pages` holds the free pages with the lowest on top and `moved` [pool] each
+    page's new number.  The first `copy_count` [1] of the lists are the pages to copy
+    (kv_copy_pages in every layer) before they are read.  See bq_kv_compact."""
+    _need(lens, "lens")
+    dev, i32 = lens.device, torch.int32
+    _dense(lens, "lens", i32, dev)
+    n = lens.numel()
+    width, stride = _table(table, n, dev)
+    _dense(free_pages, "free_pages", i32, dev)
+    pool = free_pages.numel()
+    _dense(free_count, "free_count", i32, dev, 1)
+    free_count_out = free_count if free_count_out is None else free_count_out
+    _dense(free_count_out, "free_count_out", i32, dev, 1)
+    _dense(refs, "refs", i32, dev, pool)
+    _dense(copy_src, "copy_src", i32, dev)
+    _dense(copy_dst, "copy_dst", i32, dev, copy_src.numel())
+    _dense(copy_count, "copy_count", i32, dev, 1)
+    _dense(moved, "moved", i32, dev, pool)
+    args = _lib.BqKvCompactArgs(n, _i32(page_size), width, _i32(pool), stride, copy_src.numel(), lens.data_ptr(),
+                                table.data_ptr(), free_pages.data_ptr(), refs.data_ptr(), copy_src.data_ptr(),
+                                copy_dst.data_ptr(), copy_count.data_ptr(), moved.data_ptr(), free_count_out.data_ptr())
+    _call(lib.bq_kv_compact, "kv_compact", dev, _byref(args))
+
+
 class BlockTables:
     """The requests' side of a paged cache, on the GPU: lengths, block table and
     the stack of free pages, shared by all layers' caches.  ``resize`` moves
@@ -284,6 +386,52 @@ class BlockTables:
         suffice; returns ``refused``."""
         return kv_block_tables(self.lens, new_lens, self.table, self.free_pages, self.free_count,
                                self.page_size, self.slots, self.positions, self.starts, refused=self.refused)
+
+
+class SharedBlockTables(BlockTables):
+    """BlockTables whose requests may share pages: forks, pages of their own where
+    forks part (copy on write), pages freed when nobody holds them any more, and
+    compaction.  `caches`: the layers' PagedKVCache objects, whose pages are copied
+    as the steps need it; all calls enqueue kernels only and can be captured."""
+
+    def __init__(self, requests, max_pages, pages, page_size, max_tokens, caches=(), device="cuda"):
+        super().__init__(requests, max_pages, pages, page_size, max_tokens, device)
+        i32 = dict(dtype=torch.int32, device=device)
+        self.caches = tuple(caches)
+        for c in self.caches:
+            if (c.pages, c.page_size) != (pages, self.page_size):
+                raise ValueError(f"caches must have {pages} pages of {page_size}, got {c.pages} of {c.page_size}")
+        self.refs = torch.zeros(pages, **i32)
+        self.copy_src, self.copy_dst = torch.full((requests,), -1, **i32), torch.full((requests,), -1, **i32)
+        self.copy_count = torch.zeros(1, **i32)
+        self._moves = None
+
+    def resize(self, new_lens, parents=None):
+        """Lengths become new_lens; request b with parents[b] >= 0 (int32 [requests])
+        starts as a fork of that request.  The pages that this takes are copied in all
+        layers.  Returns ``refused``."""
+        kv_shared_tables(self.lens, new_lens, self.table, self.free_pages, self.free_count, self.refs, self.page_size,
+                         self.slots, self.positions, self.starts, self.copy_src, self.copy_dst, self.copy_count,
+                         parents=parents, refused=self.refused)
+        if self.caches:
+            kv_copy_pages(self.caches, self.copy_src, self.copy_dst, self.copy_count)
+        return self.refused
+
+    def compact(self, max_moves=None):
+        """Move the pages in use to the lowest numbers, max_moves of them at most (half
+        the pool by default, which is all there can be), in the tables and in all
+        layers.  Returns ``moved`` [pages], each page's new number."""
+        room = self.free_pages.numel() // 2 if max_moves is None else int(max_moves)
+        if self._moves is None or self._moves[0].numel() != room:
+            i32 = dict(dtype=torch.int32, device=self.lens.device)
+            self._moves = (torch.empty(room, **i32), torch.empty(room, **i32), torch.empty(1, **i32),
+                           torch.empty(self.free_pages.numel(), **i32))
+        src, dst, count, moved = self._moves
+        kv_compact(self.lens, self.table, self.free_pages, self.free_count, self.refs, self.page_size, src, dst, count,
+                   moved)
+        if self.caches:
+            kv_copy_pages(self.caches, src, dst, count)
+        return moved
 
 
 def _strides(t, tokens, heads):

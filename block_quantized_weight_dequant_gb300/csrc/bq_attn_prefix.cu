@@ -12,11 +12,11 @@
 #include <atomic>
 #include <cmath>
 
-#include "bq_attn.h"
+#include "bq_attn_tcgen05.cuh"
 
 // bq_attn_tcgen05_<cache>.cu
-cudaError_t bq_internal_prefix_f16(const bq::AttnArgs &, int grid, void *stream, unsigned int *status);
-cudaError_t bq_internal_prefix_bf16(const bq::AttnArgs &, int grid, void *stream, unsigned int *status);
+cudaError_t bq_internal_prefix_f16(const bq::TcArgs &, int grid, void *stream, unsigned int *status);
+cudaError_t bq_internal_prefix_bf16(const bq::TcArgs &, int grid, void *stream, unsigned int *status);
 
 namespace {
 
@@ -292,10 +292,63 @@ int64_t bytes_of(const Plan &p) {
     return p.rest.ml_bytes + p.rest.o_bytes + p.shared.ml_bytes + p.shared.o_bytes;
 }
 
+// A map of the pages' 64-value blocks, swizzled as the tensor cores read them;
+// false if the driver has none.
+bool map_of(const bq_kv_cache &c, void *base, int box, bool heads_first, const cuuint64_t *strides, CUtensorMap *out) {
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> known{nullptr};
+    Encode encode = known.load();
+    if (!encode) {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess || !p) {
+            cudaGetLastError();
+            return false;
+        }
+        encode = reinterpret_cast<Encode>(p);
+        known.store(encode);
+    }
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)(heads_first ? c.kv_heads : c.page_size),
+                                (cuuint64_t)(heads_first ? c.page_size : c.kv_heads), (cuuint64_t)c.pages};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)(heads_first ? 1 : box), (cuuint32_t)(heads_first ? box : 1), 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return encode(out, c.type == BQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, base, dims,
+                  strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Boxes and maps of the call's copies; box 0, the copies of 16 bytes, where pages are
+// not whole groups of 8 slots or the strides are none of a tensor map's (each a
+// multiple of the one before, and beyond what that spans).
+void maps_of(const bq_kv_cache &c, bq::TcArgs *t) {
+    t->box = c.page_size & -c.page_size;  // the largest power of two that divides it
+    if (t->box > 128) t->box = 128;
+    const cuuint64_t D = 2 * (cuuint64_t)c.head_dim, S = (cuuint64_t)c.page_size, H = (cuuint64_t)c.kv_heads;
+    const cuuint64_t slot = 2 * (cuuint64_t)c.slot_stride;
+    const cuuint64_t head = H > 1 ? 2 * (cuuint64_t)c.head_stride : slot * S;  // (one entry has no stride)
+    t->heads_first = head < slot;
+    const cuuint64_t n0 = t->heads_first ? H : S, n1 = t->heads_first ? S : H;
+    cuuint64_t strides[3] = {t->heads_first ? head : slot, t->heads_first ? slot : head, 0};
+    strides[2] = c.pages > 1 ? 2 * (cuuint64_t)c.page_stride : strides[1] * n1;
+    const bool fits = t->box >= 8 && strides[0] >= D && strides[1] >= strides[0] * n0 && strides[1] % strides[0] == 0 &&
+                      strides[2] >= strides[1] * n1 && strides[2] % strides[1] == 0;
+    if (!fits || !map_of(c, c.k, t->box, t->heads_first, strides, &t->k) ||
+        !map_of(c, c.v, t->box, t->heads_first, strides, &t->v))
+        t->box = 0;
+}
+
 cudaError_t run(Pass *p, int sms, void *stream, unsigned int *status) {
-    if (!p->inst)
-        return p->a.c.type == BQ_F16 ? bq_internal_prefix_f16(p->a, (int)p->units, stream, status)
-                                     : bq_internal_prefix_bf16(p->a, (int)p->units, stream, status);
+    if (!p->inst) {
+        bq::TcArgs t;
+        t.a = p->a;
+        const bq_kv_cache &c = p->a.c;
+        maps_of(c, &t);
+        return c.type == BQ_F16 ? bq_internal_prefix_f16(t, (int)p->units, stream, status)
+                                : bq_internal_prefix_bf16(t, (int)p->units, stream, status);
+    }
     const size_t smem = p->inst->smem + (size_t)(p->a.x.requests + 1) * sizeof(int);
     int occ = 0;
     if (p->inst->occupancy(smem, &occ) != 0 || occ < 1) return cudaErrorInvalidConfiguration;

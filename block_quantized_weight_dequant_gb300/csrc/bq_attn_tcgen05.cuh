@@ -12,11 +12,11 @@
 // two streams: they take the even and the odd tiles, each with S (128 columns of
 // tensor memory) and O (up to 128) of its own, so that the tensor cores work for
 // one stream while the other one computes its weights; their O are joined at the
-// end.  Warps 8 to 11 bring K and V tiles into a ring in shared memory by 16-byte
+// end.  Warps 8 to 10 bring K and V tiles into a ring in shared memory by 16-byte
 // asynchronous copies (any page size and stride; what is not there is filled with
 // zeros) in the swizzled rows of 128 bytes that the tensor cores read: K with
 // positions as rows and head_dim contiguous, V the same bytes with the summed
-// axis as rows.  One thread of warp 12 issues all products.  The weights go back
+// axis as rows.  One thread of warp 11 issues all products.  The weights go back
 // to tensor memory in the columns of the scores that they come from, and are the
 // first operand of the second product from there.
 //
@@ -28,6 +28,8 @@
 // core's fp32.
 #pragma once
 
+#include <cuda.h>  // CUtensorMap
+
 #include <atomic>
 #include <cmath>
 
@@ -36,7 +38,7 @@
 namespace bq {
 
 constexpr int TC_ROWS = 128, TC_TILE = 128;
-constexpr int TC_SOFTMAX_WARPS = 8, TC_COPY_WARPS = 4, TC_WARPS = 13;
+constexpr int TC_SOFTMAX_WARPS = 8, TC_COPY_WARPS = 3, TC_WARPS = 12;
 constexpr int TC_MASKS = 8;        // tiles whose masks are kept
 constexpr int TC_BLOCK = 128 * 128;  // bytes of 128 rows of 64 values
 constexpr int TC_COLUMNS = 512;      // of tensor memory, all of it
@@ -49,9 +51,11 @@ struct TcShape {
     static constexpr int LIMIT = 227 * 1024, MISC = 3072;
     static constexpr int most = (LIMIT - MISC - Q_BYTES) / SLOT;
     static constexpr int SLOTS = most > 8 ? 8 : most;
-    // loads that are issued before the oldest is waited for.  Above SLOTS - 2 a load
-    // would wait for a slot that is only freed once it has arrived.
-    static constexpr int LAG = SLOTS - 3 > 4 ? 4 : SLOTS - 3;
+    // Loads that are issued before the oldest is waited for.  A tile's keys are told as
+    // arrived once the LAG loads behind them are issued, which takes slots that are free
+    // again: with 3 of 6 the next keys waited for the values two tiles before (DELTA),
+    // above SLOTS - 2 for themselves.
+    static constexpr int LAG = SLOTS >= 8 ? 3 : 1;
     static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + MISC;
     static constexpr int OROW = NB * 64 + 4;  // floats of a row of the join, in the ring's place
     static_assert(SLOTS >= 4 && LAG >= 1 && LAG <= SLOTS - 2);
@@ -61,10 +65,18 @@ struct TcShape {
     static_assert(SLOTS / 2 + 1 < TC_MASKS);
 };
 
+struct TcArgs {
+    AttnArgs a;
+    int box;        // positions of a copy by tensor map: the largest power of two that divides
+                    // a page, 8 to 128; 0: copies of 16 bytes
+    int heads_first;   // of the maps' axes: heads lie closer than slots
+    CUtensorMap k, v;  // [pages][kv heads][slots][head_dim] ([slots][kv heads]), in boxes of 64 values by `box` slots
+};
+
 // shared memory behind the ring
 struct TcMisc {
     uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2], o_full[2], q_full, last;
-    uint32_t mask[TC_MASKS][4];  // positions of a tile that are there
+    uint8_t mask[TC_MASKS][16];  // positions of a tile that are there
     float factor[TC_ROWS];       // of a row's scores
     float2 ml[TC_ROWS];          // of the second stream
     uint32_t tmem;
@@ -146,6 +158,18 @@ __device__ __forceinline__ void tc_store32(uint32_t at, const uint32_t (&v)[32])
         : "memory");
 }
 
+__device__ __forceinline__ void tc_load8(uint32_t at, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(at)
+                 : "memory");
+}
+__device__ __forceinline__ void tc_store8(uint32_t at, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(at)
+                 : "memory");
+}
+
 // A matrix in shared memory in rows of 128 bytes swizzled over 8 rows: its place,
 // the distance of 64-value blocks (where the rows are the summed axis) and of
 // groups of 8 rows
@@ -176,6 +200,20 @@ __device__ __forceinline__ void tc_commit(uint64_t *b) {
 __device__ __forceinline__ void tc_copy16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
 }
+// a box of a tensor map into shared memory, zeros where it is outside; the barrier
+// counts its bytes
+__device__ __forceinline__ void tc_copy_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int page,
+                                            uint64_t *b) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(page), "r"(tc_shared(b))
+        : "memory");
+}
+__device__ __forceinline__ void barrier_arrive_bytes(uint64_t *b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(tc_shared(b)), "r"(bytes)
+                 : "memory");
+}
 template <int N>
 __device__ __forceinline__ void tc_copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -184,6 +222,53 @@ __device__ __forceinline__ float tc_pow2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// pairs of fp32 values, two operations an instruction
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 pair_values(uint64_t p) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t pair_less(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// the pair as two pairs of 16-bit numbers that add up to it
+template <bool HALF>
+__device__ __forceinline__ void pair_parts(uint64_t p, uint32_t &high, uint32_t &low) {
+    const float2 v = pair_values(p);
+    float2 h;
+    if constexpr (HALF) {
+        high = F16::down2(v.x, v.y);
+        h = F16::up2(high);
+    } else {
+        high = BF16::down2(v.x, v.y);
+        h = BF16::up2(high);
+    }
+    const float2 rest = pair_values(pair_less(p, pair_of(h.x, h.y)));
+    low = HALF ? F16::down2(rest.x, rest.y) : BF16::down2(rest.x, rest.y);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 // two values as a pair of 16-bit numbers, and what is left of them
@@ -203,8 +288,9 @@ __device__ __forceinline__ uint32_t tc_part(float &x, float &y) {
 
 template <bool HALF, int QP, int NB>
 __global__ void __launch_bounds__(TC_WARPS * 32, 1)
-    prefix_kernel(const __grid_constant__ AttnArgs a, unsigned int *status) {
+    prefix_kernel(const __grid_constant__ TcArgs args, unsigned int *status) {
     using S = TcShape<QP, NB>;
+    const AttnArgs &a = args.a;
     constexpr int SLOTS = S::SLOTS, LAG = S::LAG;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_s = smem, *ring = smem + S::Q_BYTES;
@@ -240,8 +326,9 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 
     // ---- barriers and tensor memory ----
     if (tid == 0) {
-        for (int i = 0; i < SLOTS; ++i) barrier_init(&misc.full[i], TC_COPY_WARPS), barrier_init(&misc.empty[i], 1);
-        for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], TC_COPY_WARPS);
+        const int copying = args.box ? 1 : TC_COPY_WARPS;
+        for (int i = 0; i < SLOTS; ++i) barrier_init(&misc.full[i], copying), barrier_init(&misc.empty[i], 1);
+        for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], copying);
         for (int i = 0; i < 2; ++i) {
             barrier_init(&misc.s_full[i], 1);
             barrier_init(&misc.p_full[i], TC_SOFTMAX_WARPS / 2);
@@ -263,36 +350,89 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     tc_fence_after();
     const uint32_t tmem = misc.tmem;
 
-    if (warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
-        // ---- copies: K and V of each tile in turn, 32 rows of it by each warp ----
+    if (warp == TC_SOFTMAX_WARPS && args.box) {
+        // ---- copies by tensor maps: K and V of each tile in turn; lane j looks up the
+        // tile's rows 8 j to 8 j + 7 (pages are whole groups of 8) ----
+        const int *row_table = a.x.table + owner * a.x.table_stride;
+        auto entry_of = [&](int t) { return lane < TC_TILE / 8 && t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
+        int entry = entry_of(begin + 8 * lane);
+        const bool starts = lane < TC_TILE / 8 && 8 * lane % args.box == 0;  // a box
+        bool ok = true;
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int p = begin + t * TC_TILE + 8 * lane;
+            const bool in = lane < TC_TILE / 8 && p < end, live = in && entry >= 0 && entry < a.c.pages;
+            if (in && !live) atomicOr(status, BQ_DEVERR_PAGE);
+            const int from = live ? entry : (int)a.c.pages;  // (outside the tensor: zeros)
+            const int slot_of = live ? p - (int)a.page.div((uint32_t)p) * page : 0;
+            entry = entry_of(p + TC_TILE);
+            for (int v = 0; v < 2; ++v) {
+                const int n = 2 * t + v, slot = n % SLOTS;
+                if (!barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) barrier_arrive_bytes(&misc.full[slot], S::SLOT);
+                if (v == 0 && lane < TC_TILE / 8) misc.mask[t % TC_MASKS][lane] = live ? 255 : 0;
+                __syncwarp();
+                if (v == 0 && lane == 0) barrier_arrive(&misc.mask_full[t % TC_MASKS]);
+                if (starts) {
+                    const uint32_t to = tc_shared(ring) + slot * S::SLOT + lane * 1024;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+                        tc_copy_box(to + b * TC_BLOCK, v ? &args.v : &args.k, 64 * b, args.heads_first ? h : slot_of,
+                                    args.heads_first ? slot_of : h, from, &misc.full[slot]);
+                }
+            }
+        }
+    } else if (warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
+        // ---- copies of 16 bytes (none where tensor maps do them): K and V of each tile in turn, every third 8 rows by each warp ----
+        constexpr int GROUPS = TC_TILE / 8, MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;  // of 8 rows
         const int cw = warp - TC_SOFTMAX_WARPS;
         const int *row_table = a.x.table + owner * a.x.table_stride;
         const long long head_off = (long long)h * a.c.head_stride;
-        auto entry_of = [&](int t) { return t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
-        int entry = entry_of(begin + 32 * cw + lane);
-        constexpr int PIECES = 8 * NB, AT_ONCE = 32 / PIECES;  // of a row; rows of a warp at a time
+        // rows that this lane looks up: of this warp's groups 0 to 3, and of 4 and 5
+        auto row_at = [&](int k) { return 8 * (cw + TC_COPY_WARPS * (4 * k + (lane >> 3))) + (lane & 7); };
+        auto entry_of = [&](int row, int t) { return row < TC_TILE && t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
+        int entry[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) entry[k] = entry_of(row_at(k), begin + row_at(k));
+        constexpr int PIECES = 8 * NB, AT_ONCE = 32 / PIECES, TURNS = 8 / AT_ONCE;  // of a row; rows at a time
         const int piece = lane % PIECES, sub = lane / PIECES;
         const bool there = piece < D16 / 8, inside = 8 * piece < D;
-        const uint32_t ring_at = tc_shared(ring) + (piece >> 3) * TC_BLOCK;
+        // a group's rows lie one behind the other where pages are whole groups
+        const bool in_line = page % 8 == 0;
+        const long long hop = 2 * AT_ONCE * a.c.slot_stride;  // bytes from turn to turn
+        const long long lane_at = 2 * sub * a.c.slot_stride + 16 * piece;
+        const uint32_t ring_at = tc_shared(ring) + (piece >> 3) * TC_BLOCK + sub * 128;
+        uint32_t turn_at[TURNS];  // a row's place in its group of 8, swizzled
+#pragma unroll
+        for (int i = 0; i < TURNS; ++i)
+            turn_at[i] = i * AT_ONCE * 128 + (((piece & 7) ^ ((i * AT_ONCE + sub) & 7)) << 4);
         auto arrived = [&](int n) {  // load n is complete: the products may read it
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) barrier_arrive(&misc.full[n % SLOTS]);
         };
         bool ok = true;
-        for (int t = 0; t < tiles && ok; ++t) {
-            const int p = begin + t * TC_TILE + 32 * cw + lane;
-            long long off = -1;
-            if (p < end) {
-                if (entry >= 0 && entry < a.c.pages) {
-                    const uint32_t in_page = (uint32_t)p - a.page.div((uint32_t)p) * a.page.d;
-                    off = entry * a.c.page_stride + in_page * a.c.slot_stride + head_off;
-                } else {
-                    atomicOr(status, BQ_DEVERR_PAGE);
+        for (int t = 0; t < tiles && ok && !args.box; ++t) {
+            long long off[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int p = begin + t * TC_TILE + row_at(k);
+                off[k] = -1;
+                if (row_at(k) < TC_TILE && p < end) {
+                    if (entry[k] >= 0 && entry[k] < a.c.pages) {
+                        const uint32_t in_page = (uint32_t)p - a.page.div((uint32_t)p) * a.page.d;
+                        off[k] = entry[k] * a.c.page_stride + in_page * a.c.slot_stride + head_off;
+                    } else {
+                        atomicOr(status, BQ_DEVERR_PAGE);
+                    }
                 }
+                entry[k] = entry_of(row_at(k), p + TC_TILE);
             }
-            entry = entry_of(p + TC_TILE);
-            const uint32_t live = __ballot_sync(~0u, off >= 0);
+            uint32_t live[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) live[k] = __ballot_sync(~0u, off[k] >= 0);
             for (int v = 0; v < 2; ++v) {
                 const int n = 2 * t + v, slot = n % SLOTS;
                 if (!barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead)) {
@@ -300,20 +440,35 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     break;
                 }
                 // (after the wait: the masks of TC_MASKS tiles before are not in use any more)
-                if (v == 0 && lane == 0) {
-                    misc.mask[t % TC_MASKS][cw] = live;
-                    barrier_arrive(&misc.mask_full[t % TC_MASKS]);
+                if (v == 0) {
+                    const int of = cw + TC_COPY_WARPS * lane;
+                    if (lane < MINE && of < GROUPS)
+                        misc.mask[t % TC_MASKS][of] = (uint8_t)((lane < 4 ? live[0] : live[1]) >> (8 * (lane & 3)));
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(&misc.mask_full[t % TC_MASKS]);
                 }
-                const uint8_t *src = static_cast<const uint8_t *>(v ? a.c.v : a.c.k) + 16 * piece;
-                const uint32_t dst = ring_at + slot * S::SLOT;
-#pragma unroll 8
-                for (int i = 0; i < 32 / AT_ONCE; ++i) {
-                    const int row = i * AT_ONCE + sub;
-                    const long long o = __shfl_sync(~0u, off, row);
-                    const int r = 32 * cw + row;
-                    if (there)
-                        tc_copy16(dst + r * 128 + (((piece & 7) ^ (r & 7)) << 4), src + (o >= 0 && inside ? 2 * o : -16 * piece),
-                                  o >= 0 && inside);
+                const uint8_t *plane = static_cast<const uint8_t *>(v ? a.c.v : a.c.k);
+#pragma unroll
+                for (int q = 0; q < MINE; ++q) {
+                    if (q == MINE - 1 && cw + TC_COPY_WARPS * q >= GROUPS) break;
+                    const uint32_t to = ring_at + slot * S::SLOT + (cw + TC_COPY_WARPS * q) * 1024;
+                    const uint32_t bits = live[q >> 2] >> (8 * (q & 3)) & 255;
+                    if (bits == 255 && in_line) {
+                        const long long o = __shfl_sync(~0u, off[q >> 2], 8 * (q & 3));
+                        const uint8_t *src = plane + 2 * o + lane_at;
+                        if (there) {
+#pragma unroll
+                            for (int i = 0; i < TURNS; ++i)
+                                tc_copy16(to + turn_at[i], inside ? src + i * hop : plane, inside);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < TURNS; ++i) {
+                            const long long o = __shfl_sync(~0u, off[q >> 2], 8 * (q & 3) + i * AT_ONCE + sub);
+                            const bool has = o >= 0 && inside;
+                            if (there) tc_copy16(to + turn_at[i], has ? plane + 2 * o + 16 * piece : plane, has);
+                        }
+                    }
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 if (n >= LAG) {
@@ -323,7 +478,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             }
         }
         tc_copies_wait<0>();
-        if (ok)
+        if (ok && !args.box)
             for (int n = max(0, 2 * tiles - LAG); n < 2 * tiles; ++n) arrived(n);
     } else if (warp == TC_WARPS - 1) {
         // ---- products ----
@@ -394,7 +549,12 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     else if (a.x.dtype == BQ_F16) load_n<F16, 4>((const __half *)a.x.q + at, wide, x);
                     else load_n<BF16, 4>((const __nv_bfloat16 *)a.x.q + at, wide, x);
                 }
-                float factor = a.scale_log2;
+                // the row carries the scale's sign (and zero), so that a larger product is a
+                // larger score
+                const float sign = a.scale_log2 > 0.0f ? 1.0f : a.scale_log2 < 0.0f ? -1.0f : 0.0f;
+                float factor = sign == 0.0f ? 1.0f : fabsf(a.scale_log2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] *= sign;
                 if constexpr (HALF && QP > 1) {
                     // the largest of the row to [2^14, 2^15), as in the ordinary kernel
                     float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
@@ -408,7 +568,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     for (int e = 0; e < 4; ++e) x[e] = x[e] * s1 * s2;
                     factor = factor * ldexpf(1.0f, -(up / 2)) * ldexpf(1.0f, -(up - up / 2));
                 }
-                if (lane == 0) misc.factor[i] = factor;
+                // (above 0: what it multiplies may be minus infinity)
+                if (lane == 0) misc.factor[i] = fmaxf(factor, 1.1754944e-38f);
                 const int piece = (lane & 15) >> 1;
                 uint8_t *to = q_s + (lane >> 4) * TC_BLOCK + i * 128 + ((piece ^ (i & 7)) << 4) + 8 * (lane & 1);
 #pragma unroll
@@ -440,64 +601,81 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             tc_fence_after();
             const uint4 m4 = *reinterpret_cast<const uint4 *>(misc.mask[t % TC_MASKS]);
             const uint32_t mask[4] = {m4.x, m4.y, m4.z, m4.w};
-            uint32_t x[2][32];
-            float top = -INFINITY;
-            tc_load32(s_at, x[0]);
+            if ((m4.x & m4.y & m4.z & m4.w) != ~0u) {  // positions that are not there: minus infinity
+#pragma unroll 1
+                for (int c = 0; c < TC_TILE; c += 8) {
+                    const uint32_t bits = mask[c >> 5] >> (c & 31);
+                    uint32_t o[8];
+                    tc_load8(s_at + c, o);
+                    tc_wait_load();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tc_wait_load();
-                if (c < 3) tc_load32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
-                const uint32_t(&y)[32] = x[c & 1];
-                if (mask[c] == ~0u) {
-                    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) m[k & 3] = fmaxf(m[k & 3], __uint_as_float(y[k]) * factor);
-                    top = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (mask[c] >> k & 1) top = fmaxf(top, __uint_as_float(y[k]) * factor);
+                    for (int k = 0; k < 8; ++k)
+                        if (!(bits >> k & 1)) o[k] = 0xff800000u;
+                    tc_store8(s_at + c, o);
                 }
+                tc_wait_store();
             }
+            uint32_t x[2][32];
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            auto largest = [&](const uint32_t(&y)[32]) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                    m[k / 2 & 3] = max3(m[k / 2 & 3], __uint_as_float(y[k]), __uint_as_float(y[k + 1]));
+            };
             tc_load32(s_at, x[0]);
+            tc_load32(s_at + 32, x[1]);
+            tc_wait_load();
+            largest(x[0]);
+            tc_load32(s_at + 64, x[0]);
+            largest(x[1]);
+            tc_load32(s_at + 96, x[1]);
+            tc_wait_load();
+            largest(x[0]);
+            largest(x[1]);
+            const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * factor;
             const bool grows = top > ref + TC_GROWTH || (ref == -INFINITY && top > ref);
             const float now = grows ? top : ref;
             if (t > s && __any_sync(~0u, grows)) {
                 const float alpha = grows ? tc_pow2(ref - now) : 1.0f;
                 l *= alpha;
-                tc_wait_load();
-                for (int c = 0; c < D16; c += 32) {  // (columns from D16 on are not read)
-                    tc_load32(o_at + c, x[1]);
+#pragma unroll 1
+                for (int c = 0; c < D16; c += 8) {
+                    uint32_t o[8];
+                    tc_load8(o_at + c, o);
                     tc_wait_load();
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) x[1][k] = __float_as_uint(__uint_as_float(x[1][k]) * alpha);
-                    tc_store32(o_at + c, x[1]);
+                    for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                    tc_store8(o_at + c, o);
                 }
             }
             ref = now;
+            tc_load32(s_at, x[0]);
             const float shift = (HALF ? (float)TC_SHIFT_F16 : 0.0f) - (ref == -INFINITY ? 0.0f : ref);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                tc_wait_load();
-                if (c < 3) tc_load32(s_at + 32 * (c + 1), x[(c + 1) & 1]);
-                uint32_t(&y)[32] = x[c & 1];
+            const uint64_t factors = pair_of(factor, factor), shifts = pair_of(shift, shift);
+            uint64_t sum[2] = {0, 0};
+            auto weights = [&](const uint32_t(&y)[32], uint32_t at) {
                 uint32_t w[32];
-                float sum[2] = {0.0f, 0.0f};
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
-                    float u = tc_pow2(fmaf(__uint_as_float(y[k]), factor, shift));
-                    float v = tc_pow2(fmaf(__uint_as_float(y[k + 1]), factor, shift));
-                    if (mask[c] != ~0u) {
-                        if (!(mask[c] >> k & 1)) u = 0.0f;
-                        if (!(mask[c] >> (k + 1) & 1)) v = 0.0f;
-                    }
-                    sum[0] += u, sum[1] += v;
-                    w[k / 2] = tc_part<HALF>(u, v);
-                    w[16 + k / 2] = tc_part<HALF>(u, v);
+                    const float2 e = pair_values(
+                        pair_fma(pair_of(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), factors, shifts));
+                    const uint64_t p = pair_of(tc_pow2(e.x), tc_pow2(e.y));
+                    sum[k / 2 & 1] = pair_add(sum[k / 2 & 1], p);
+                    pair_parts<HALF>(p, w[k / 2], w[16 + k / 2]);
                 }
-                l += sum[0] + sum[1];
-                tc_store32(s_at + 32 * c, w);
+                tc_store32(at, w);
+            };
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 64) {  // (unrolled, the code outgrows the instruction cache)
+                tc_wait_load();
+                tc_load32(s_at + c + 32, x[1]);
+                weights(x[0], s_at + c);
+                tc_wait_load();
+                if (c == 0) tc_load32(s_at + 64, x[0]);
+                weights(x[1], s_at + c + 32);
             }
+            const float2 l2 = pair_values(pair_add(sum[0], sum[1]));
+            l += l2.x + l2.y;
             tc_wait_store();
             tc_fence_before();
             __syncwarp();
@@ -567,7 +745,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 }
 
 template <bool HALF, int QP, int NB>
-cudaError_t prefix_launch_of(const AttnArgs &a, int grid, void *stream, unsigned int *status) {
+cudaError_t prefix_launch_of(const TcArgs &a, int grid, void *stream, unsigned int *status) {
     auto *kern = prefix_kernel<HALF, QP, NB>;
     constexpr int smem = TcShape<QP, NB>::SMEM;
     static std::atomic<bool> ready[64];
@@ -583,8 +761,8 @@ cudaError_t prefix_launch_of(const AttnArgs &a, int grid, void *stream, unsigned
     return launch_pdl(kern, dim3((unsigned)grid), TC_WARPS * 32, smem, stream, 1, a, status);
 }
 template <bool HALF, int QP>
-cudaError_t prefix_launch(const AttnArgs &a, int grid, void *stream, unsigned int *status) {
-    return a.c.head_dim <= 64 ? prefix_launch_of<HALF, QP, 1>(a, grid, stream, status)
+cudaError_t prefix_launch(const TcArgs &a, int grid, void *stream, unsigned int *status) {
+    return a.a.c.head_dim <= 64 ? prefix_launch_of<HALF, QP, 1>(a, grid, stream, status)
                               : prefix_launch_of<HALF, QP, 2>(a, grid, stream, status);
 }
 

@@ -20,22 +20,16 @@
 // of its request follows from the outputs: a request is served if lens_out is
 // new_lens, and grew by its number of rows.  Bound by latency: 256 requests of a
 // decode step 7.0 us, 1000 with prompts (92000 rows) 11.5 us.
-#include "bq_cache.cuh"
+#include "bq_tables.cuh"
 
 namespace {
 
 BQ_STATUS_WORD(tables)
 
 constexpr int THREADS = 512;
-constexpr int ROWS_THREADS = 256, ROWS_EACH = 4;  // of the second kernel: tokens per thread
-constexpr int MAX_REQUESTS = 4096;
 constexpr int MAX_CLUSTER = 8;
-constexpr long long ROWS_ALONE = 4096;
 
-struct Args {
-    bq_kv_tables t;
-    bq::FastDiv page;
-};
+using Args = bq::RowsArgs;
 
 struct Request {
     int lo, hi;          // lengths before and after; equal for a request that is left alone
@@ -57,17 +51,6 @@ __device__ __forceinline__ Request request_of(const Args &a, int lo, int hi) {
     r.held = r.bad ? 0 : pages(lo);
     r.wanted = r.bad ? 0 : pages(hi);
     return r;
-}
-
-// largest i in [0, n) with pre[i] <= x, for a non-decreasing pre with pre[0] <= x
-__device__ __forceinline__ int last_not_above(const int *pre, int n, int x) {
-    int lo = 0, hi = n;  // pre[lo] <= x, pre[hi] > x (or hi == n)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    return lo;
 }
 
 __global__ void __launch_bounds__(THREADS) tables_kernel(const __grid_constant__ Args a, int with_rows) {
@@ -152,7 +135,7 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(const __grid_constant__
     auto page_at = [&](int i) {
         const int at = avail - 1 - i;
         if (at < count) return a.t.free_pages[at];
-        const int b = last_not_above(freed, n, at - count);
+        const int b = bq::last_not_above(freed, n, at - count);
         return a.t.table[b * a.t.table_stride + request(b).wanted + (at - count - freed[b])];
     };
 
@@ -176,11 +159,11 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(const __grid_constant__
     const int step = (int)cluster * THREADS, first = (int)rank * THREADS + tid;
     for (int i = first; i < given; i += step) {
         const int page = page_at(i);
-        const int b = last_not_above(asked, n, i);
+        const int b = bq::last_not_above(asked, n, i);
         a.t.table[b * a.t.table_stride + request(b).held + (i - asked[b])] = page;
     }
     for (int i = first; i < released - given; i += step) {
-        const int b = last_not_above(freed, n, i);
+        const int b = bq::last_not_above(freed, n, i);
         a.t.free_pages[count + i] = a.t.table[b * a.t.table_stride + request(b).wanted + (i - freed[b])];
     }
     if (with_rows) {
@@ -191,7 +174,7 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(const __grid_constant__
             long long slot = -1;
             int position = 0;
             if (t < total) {
-                const int b = last_not_above(rows, n, (int)t);
+                const int b = bq::last_not_above(rows, n, (int)t);
                 const Request r = request(b);
                 if (served(b, r)) {
                     position = r.lo + (int)(t - rows[b]);
@@ -223,12 +206,18 @@ __global__ void __launch_bounds__(THREADS) tables_kernel(const __grid_constant__
     }
 }
 
+}  // namespace
+
+namespace bq {
+
+constexpr int ROWS_THREADS = 256, ROWS_EACH = 4;  // tokens per thread
+
 // the slot map from the finished table: a few tokens per thread
-__global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constant__ RowsArgs a) {
     extern __shared__ int starts[];
     const int n = a.t.requests;
     const long long t0 = ((long long)blockIdx.x * ROWS_THREADS + threadIdx.x) * ROWS_EACH;
-    bq::pdl_wait();
+    pdl_wait();
     for (int b = threadIdx.x; b <= n; b += ROWS_THREADS) starts[b] = a.t.starts[b];
     __syncthreads();
     const long long total = min((long long)starts[n], (long long)a.t.max_tokens);
@@ -259,13 +248,9 @@ __global__ void __launch_bounds__(ROWS_THREADS) rows_kernel(const __grid_constan
         }
 }
 
-}  // namespace
-
-int bq_internal_status_tables(unsigned int *flags, int clear) { return read_status_tables(flags, clear); }
-
-extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
+bq_status check_tables(const bq_kv_tables *t) {
     if (!t) return BQ_ERR_NULL;
-    if (t->requests < 0 || t->requests > MAX_REQUESTS || t->page_size < 1 || t->page_size > 65536 ||
+    if (t->requests < 0 || t->requests > TABLES_MAX_REQUESTS || t->page_size < 1 || t->page_size > 65536 ||
         t->table_width < 1 || t->table_stride < t->table_width || t->table_stride > (1LL << 40) ||
         t->max_tokens < 0 || t->max_tokens > 0x7ffffffeLL || t->pool < 1 || t->pool == 0x7fffffff)
         return BQ_ERR_SHAPE;
@@ -279,14 +264,39 @@ extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
     const void *words[] = {t->lens, t->new_lens, t->table, t->free_pages, t->free_count, t->positions,
                            t->starts, t->lens_out, t->free_count_out, t->refused};
     for (const void *p : words)
-        if (!bq::aligned_to(p, 4)) return BQ_ERR_ALIGN;
-    if (!bq::aligned_to(t->slots, 8)) return BQ_ERR_ALIGN;
+        if (!aligned_to(p, 4)) return BQ_ERR_ALIGN;
+    if (!aligned_to(t->slots, 8)) return BQ_ERR_ALIGN;
+    return BQ_OK;
+}
+
+cudaError_t rows_launch(const bq_kv_tables &t, void *stream) {
+    RowsArgs a;
+    a.t = t;
+    a.page.set((uint32_t)t.page_size);
+    const long long per_cta = (long long)ROWS_THREADS * ROWS_EACH;
+    return launch_pdl(rows_kernel, dim3((unsigned)((t.max_tokens + per_cta - 1) / per_cta)), ROWS_THREADS,
+                      (size_t)(t.requests + 1) * sizeof(int), stream, 1, a);
+}
+
+}  // namespace bq
+
+int bq_internal_status_tables(unsigned int *flags, int clear) {
+    unsigned int a = 0, b = 0;
+    int e = read_status_tables(&a, clear);
+    if (e == 0) e = bq_internal_status_pages(&b, clear);
+    *flags = a | b;
+    return e;
+}
+
+extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
+    const bq_status s = bq::check_tables(t);
+    if (s != BQ_OK) return s;
     Args a;
     a.t = *t;
     a.page.set((uint32_t)t->page_size);
     // One launch for few rows (a decode step), two for many (1000 requests with
     // 92000 rows of prompts: 11.6 us, 41 us in one launch of 8 CTAs).
-    const bool with_rows = t->max_tokens <= ROWS_ALONE;
+    const bool with_rows = t->max_tokens <= bq::TABLES_ROWS_ALONE;
     // CTAs for the pages that may be asked, each of its threads a few
     const long long work = (with_rows ? t->max_tokens : t->max_tokens / t->page_size) + t->requests;
     int cluster = 1;
@@ -294,13 +304,11 @@ extern "C" bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream) {
     const size_t smem = (size_t)(5 * (t->requests + 1)) * sizeof(int);
     if (smem > 47 * 1024) {  // (400 bytes of static shared memory count against the 48 KB too)
         const cudaError_t e = cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)(5 * (MAX_REQUESTS + 1) * sizeof(int)));
+                                                   (int)(5 * (bq::TABLES_MAX_REQUESTS + 1) * sizeof(int)));
         if (e != cudaSuccess) return bq::from_cuda_error(e);
     }
     cudaError_t e = bq::launch_pdl(tables_kernel, dim3((unsigned)cluster), THREADS, smem, stream, cluster, a,
                                    (int)with_rows);
     if (e != cudaSuccess || with_rows) return bq::from_cuda_error(e);
-    const long long per_cta = (long long)ROWS_THREADS * ROWS_EACH;
-    return bq::from_cuda_error(bq::launch_pdl(rows_kernel, dim3((unsigned)((t->max_tokens + per_cta - 1) / per_cta)),
-                                              ROWS_THREADS, (size_t)(t->requests + 1) * sizeof(int), stream, 1, a));
+    return bq::from_cuda_error(bq::rows_launch(a.t, stream));
 }

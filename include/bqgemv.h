@@ -372,7 +372,7 @@ typedef enum { BQ_F32 = 0, BQ_F16 = 1, BQ_BF16 = 30 } bq_dtype; /* (Q8_0 = 8: bq
 /* bits of bq_device_status set by the calls below: the entry concerned is
  * skipped (treated as masked, or not written), nothing is read or written
  * out of range */
-#define BQ_DEVERR_PAGE 0x100u /* attention: a table entry of a live position outside the pool */
+#define BQ_DEVERR_PAGE 0x100u /* a table entry of a live position, or a page to copy, outside the pool */
 #define BQ_DEVERR_LENGTH 0x200u /* attention: a length below 0 or beyond the table */
 #define BQ_DEVERR_SLOT 0x400u /* append: a slot beyond the pool */
 #define BQ_DEVERR_POOL 0x800u /* tables: the free stack would pass the pool */
@@ -437,6 +437,69 @@ typedef struct {
     int32_t *free_count_out, *refused;
 } bq_kv_tables;
 bq_status bq_kv_block_tables(const bq_kv_tables *t, void *stream);
+
+/* The same for requests that share pages: refs[p] says how many requests hold
+ * page p (0: free), and a request may start as a fork of another.
+ *   Request b starts from base = lens[b] positions of its own row; with p =
+ *   parents[b] >= 0 from the first min(lens[p], new_lens[b]) positions of request
+ *   p's row as it was before the call, which it then holds too (counts raised).
+ *   Growing from base to new_lens[b] asks for the pages behind its last, and for
+ *   one more if its last page is partly filled and held by others too (refs > 1
+ *   before the call; always for a fork): that one takes the last page's place in
+ *   its row, and (old, new) is a pair of copy_src, copy_dst, to be copied in
+ *   every layer before anything is appended (bq_kv_copy_pages).  Copies stand in
+ *   the requests' order, the first *copy_count of the lists, -1 behind them.
+ *   Asked pages are popped from the stack in (request, position) order, counts 1.
+ *   Shrinking gives up the pages behind pages(new_lens), a copy the page copied
+ *   from: counts are lowered, and a page whose count comes to 0 is pushed, after
+ *   all pops, in the order of its first release (request, then position).  So a
+ *   page given up in a call is not handed out again by it.
+ * Rows, slots, positions, starts and refusals as above, with base for lens and
+ * the free pages before the call: a refused request keeps its length and pages
+ * (a refused fork stays empty).  A fork is refused too unless lens[b] is 0 and
+ * its parent is another request, no fork itself, of a length within the table.
+ *  - parents: NULL or int32 [requests], < 0: none.  refs: int32 [pool], in place;
+ *    must agree with the rows (for pages 0 .. pool - 1; entries outside are not
+ *    counted and set BQ_DEVERR_PAGE; a wrong count may lose pages, nothing is
+ *    read or written out of range).  copy_src, copy_dst: int32 [requests].
+ *  - t as for bq_kv_block_tables; nothing overlaps but what may there. */
+typedef struct {
+    const int32_t *parents;
+    int32_t *refs, *copy_src, *copy_dst, *copy_count;
+} bq_kv_sharing;
+bq_status bq_kv_shared_tables(const bq_kv_tables *t, const bq_kv_sharing *s, void *stream);
+
+/* Copy pages within each of n caches (a model's layers, all of one geometry):
+ * page src[i] to page dst[i] for i < pairs, or i < *count if that is fewer
+ * (count may be NULL).  Pairs with a negative number are skipped; one beyond the
+ * pool is skipped and sets BQ_DEVERR_PAGE.  Values are copied bit for bit, codes
+ * and scales alike.  No dst is another's dst, nor another's src.
+ *  - caches: host array of n pointers, read by the call.  0 <= pairs < 2^31;
+ *    kv_heads * page_size * head_dim <= 2^30. */
+bq_status bq_kv_copy_pages(const bq_kv_cache *const *caches, int n, const int32_t *src, const int32_t *dst,
+                           const int32_t *count, int64_t pairs, void *stream);
+
+/* Compact the pool: with P pages in use (refs > 0), the highest page in use moves
+ * to the lowest free one, the second highest to the second lowest, and so on
+ * while the one is P or more and the other below, max_moves moves at most.  With
+ * max_moves >= pool / 2 the pages in use are then 0 .. P - 1.
+ *   copy_src, copy_dst [max_moves]: the moves, the first *copy_count of them, -1
+ *   behind; the pages are to be copied (bq_kv_copy_pages) before they are read.
+ *   moved [pool]: each page's new number.  Rows of the table: the entries of
+ *   live positions get their new numbers.  refs move along.
+ *   free_pages: the free pages, the lowest on top (last); *free_count_out = pool -
+ *   P of them; what is behind is left as it was.
+ *  - A live entry outside the pool is left alone and sets BQ_DEVERR_PAGE.
+ *  - 0 <= requests <= 4096, 1 <= page_size <= 65536, table_width >= 1,
+ *    table_stride >= table_width, 1 <= pool < 2^31 - 1, 0 <= max_moves < 2^31 - 1.
+ *    Nothing overlaps. */
+typedef struct {
+    int32_t requests, page_size, table_width, pool;
+    int64_t table_stride, max_moves;
+    const int32_t *lens;
+    int32_t *table, *free_pages, *refs, *copy_src, *copy_dst, *copy_count, *moved, *free_count_out;
+} bq_kv_compact_args;
+bq_status bq_kv_compact(const bq_kv_compact_args *c, void *stream);
 
 /* Append keys and values of `tokens` tokens to the cache, with rotary
  * positions if freq is given: pair p < rot/2 of a head turns by the angle
