@@ -610,9 +610,9 @@ def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, ou
     dtype = q.dtype
     T, heads = n * rows, (q.shape[1] if q.dim() == 3 else -1)
     shape = (T, heads, D)
-    _activation(q, "q", shape, dtype, dev)
+    if q.shape != shape or not q.is_contiguous():
+        _activation(q, "q", shape, dtype, dev)
     width, stride = _table(table, n, dev)
-    counts, positions, groups = _groups(shared, n)
     if out is None:
         out = _empty(shape, dtype, q)
         os = (heads * D, D)
@@ -623,8 +623,18 @@ def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, ou
                                 *_strides(q, T, heads), *os, q.data_ptr(), out.data_ptr(),
                                 table.data_ptr(), lens.data_ptr())
     ref = _byref(args)
+    # the groups' host arrays and the workspace's bytes, by the call's geometry
+    key = (n, rows, heads, width, dtype, shared if type(shared) is int else tuple(map(tuple, shared)))
+    plan = cache._workspace.get(key)
+    if plan is None:
+        groups = _groups(shared, n)
+        plan = (*groups, lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ref, *groups))
+        if plan[3] >= 0:
+            if len(cache._workspace) >= 1024:
+                cache._workspace.clear()
+            cache._workspace[key] = plan
+    counts, positions, groups, nbytes = plan
     if workspace is None:
-        nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ref, counts, positions, groups)
         if nbytes > 0:  # (one of the call's own, as in paged_attention)
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
     else:

@@ -35,8 +35,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const __grid_constan
     const int g = row * (int)a.group.d + head - h * (int)a.group.d;
     const int rt = g / tile_rows, i = g - rt * tile_rows;
     bq::pdl_wait();
-    const int len = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
-    const int chunks = bq::attn_chunks(len, a.chunk);
+    const int chunks = bq::attn_chunks(bq::attn_length(a, b), a.chunk);
     if (chunks == 1) return;
     const long long unit0 = (((long long)b * a.max_chunks) * a.c.kv_heads + h) * a.row_tiles + rt;
     const long long step = (long long)a.c.kv_heads * a.row_tiles;
@@ -118,8 +117,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_few_kernel(const __grid_con
     const int rt = g / tile_rows, i = g - rt * tile_rows;
     bq::pdl_wait();
     if (b >= a.x.requests) return;
-    const int len = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
-    const int chunks = bq::attn_chunks(len, a.chunk);
+    const int chunks = bq::attn_chunks(bq::attn_length(a, b), a.chunk);
     if (chunks == 1) return;
     const long long unit0 = (((long long)b * a.max_chunks) * a.c.kv_heads + h) * a.row_tiles + rt;
     const long long step = (long long)a.c.kv_heads * a.row_tiles;
@@ -333,8 +331,9 @@ extern "C" int64_t bq_paged_attention_workspace_bytes(const bq_kv_cache *cache, 
     return p.ml_bytes + p.o_bytes;
 }
 
-extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, void *workspace,
-                                        int64_t workspace_bytes, void *stream) {
+// the call, over the groups of `shared` if there are any
+bq_status bq_internal_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, const bq::AttnArgs *shared,
+                                      void *workspace, int64_t workspace_bytes, void *stream) {
     Plan p;
     bq_status s = plan_of(cache, x, &p);
     if (s != BQ_OK) return s;
@@ -342,6 +341,11 @@ extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_atten
     s = bq::check_attention_pointers(cache, x);
     if (s != BQ_OK) return s;
     bq::AttnArgs &a = p.a;
+    if (shared) {
+        a.mode = bq::ATTN_WHOLE;
+        for (int g = 0; g < bq::ATTN_GROUPS; ++g)
+            a.group_end[g] = shared->group_end[g], a.group_pages[g] = shared->group_pages[g];
+    }
     const int64_t need = p.ml_bytes + p.o_bytes;
     if (need) {
         if (!workspace) return BQ_ERR_NULL;
@@ -373,4 +377,9 @@ extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_atten
         : x->dtype == BQ_F16 ? join<BQ_F16>(a, tile_rows, stream)
                              : join<BQ_BF16>(a, tile_rows, stream);
     return bq::from_cuda_error(e);
+}
+
+extern "C" bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, void *workspace,
+                                        int64_t workspace_bytes, void *stream) {
+    return bq_internal_paged_attention(cache, x, nullptr, workspace, workspace_bytes, stream);
 }

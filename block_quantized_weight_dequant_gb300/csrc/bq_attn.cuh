@@ -255,20 +255,24 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     const int B = a.x.requests, R = a.x.rows, D = a.c.head_dim, KVH = a.c.kv_heads;
     const int most = a.x.table_width * a.c.page_size;
     pdl_wait();
-    if ((a.max_chunks > 1 && !a.cluster) || a.mode != ATTN_ALL) pdl_launch_dependents();
+    const bool parts = a.mode == ATTN_REST || a.mode == ATTN_PREFIX;  // partial results alone
+    if ((a.max_chunks > 1 && !a.cluster) || parts) pdl_launch_dependents();
 
     const bool shared = a.mode == ATTN_PREFIX;
-    // pages before the first position that this launch covers of request b
-    auto skipped = [&](int b) {
-        if (a.mode != ATTN_REST) return 0;
+    // pages that request b shares
+    auto common = [&](int b) {
         int g = 0;
         while (a.group_end[g] <= b) ++g;  // ends: the groups cover the requests
         return a.group_pages[g];
     };
+    // pages before the first position that this launch covers of request b
+    auto skipped = [&](int b) { return a.mode == ATTN_REST ? common(b) : 0; };
     auto length = [&](int b) {
         if (shared) return a.group_pages[b] * a.c.page_size;
         const int n = min(max(a.x.lens[b], 0), most);
-        return a.mode == ATTN_REST ? attn_rest(n, R, skipped(b) * a.c.page_size) : n;
+        if (a.mode == ATTN_ALL) return n;
+        const int before = common(b) * a.c.page_size, rest = attn_rest(n, R, before);
+        return a.mode == ATTN_REST ? rest : n - R + 1 >= before ? n : 0;
     };
     const long long per_chunk = (long long)KVH * a.row_tiles;
     // direct: a CTA per unit that the table can hold, units beyond a request's
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     auto checked = [&](int b) {
         if (shared) return;
         const int len = a.x.lens[b];
-        if (len < 0 || len > most || (len && a.mode == ATTN_REST && len - R + 1 < skipped(b) * a.c.page_size))
+        if (len < 0 || len > most || (len && a.mode != ATTN_ALL && len - R + 1 < common(b) * a.c.page_size))
             atomicOr(status, BQ_DEVERR_LENGTH);
     };
     if (!direct) {
@@ -885,7 +889,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
                 for (int d = lane; d < D; d += 32) reinterpret_cast<float *>(smem)[i * S::OROW + d] = joined(d);
                 __syncwarp();
                 if (lane == 0) m_s[i] = top, l_s[i] = sum;
-            } else if (chunks == 1 && a.mode == ATTN_ALL) {  // the result itself
+            } else if (chunks == 1 && !parts) {  // the result itself
                 for (int d = lane; d < D; d += 32) attn_store(a, b, h, g, d, sum == 0.0f ? 0.0f : joined(d) / sum);
             } else {
                 if (lane == 0) a.part_ml[unit * ROWS + i] = make_float2(top, sum);

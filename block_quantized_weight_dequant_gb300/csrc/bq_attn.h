@@ -17,12 +17,13 @@ constexpr int ATTN_MAX_REQUESTS = 4096;
 // carries the same factor, so it cancels
 constexpr int ATTN_SHIFT_F16 = 15;
 
-// What a launch of the attention kernel covers.  The two others write partial
-// results alone, which a join of their own puts together (bq_attn_prefix.cu).
+// What a launch of the attention kernel covers.  ATTN_REST and ATTN_PREFIX write
+// partial results alone, which a join of their own puts together (bq_attn_prefix.cu).
 enum {
     ATTN_ALL = 0,    // all positions of each request
     ATTN_REST = 1,   // the positions behind the pages that a group of requests shares
-    ATTN_PREFIX = 2  // the shared pages: "requests" are groups, whose rows are all rows of their requests
+    ATTN_PREFIX = 2, // the shared pages: "requests" are groups, whose rows are all rows of their requests
+    ATTN_WHOLE = 3   // as ATTN_ALL, but nothing for requests that do not see their shared pages
 };
 constexpr int ATTN_GROUPS = BQ_PREFIX_MAX_GROUPS;
 
@@ -54,6 +55,15 @@ __host__ __device__ inline int attn_rest(int len, int rows, int shared) {
 // work units of one request of n positions: at least one, which writes the rows
 __host__ __device__ inline int attn_chunks(int n, int chunk) { return n <= chunk ? 1 : (n + chunk - 1) / chunk; }
 
+// positions that an ATTN_ALL or ATTN_WHOLE launch sees of request b
+__device__ inline int attn_length(const AttnArgs &a, int b) {
+    const int n = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
+    if (a.mode == ATTN_ALL) return n;
+    int g = 0;
+    while (a.group_end[g] <= b) ++g;
+    return n - a.x.rows + 1 >= a.group_pages[g] * a.c.page_size ? n : 0;
+}
+
 struct AttnInstance {
     int dim, nt;  // head_dim up to dim, 8 nt query rows per CTA
     size_t smem;  // without the scan of the requests
@@ -78,3 +88,7 @@ const bq::AttnInstance *bq_internal_attn_bf16_own(int *n);
 const bq::AttnInstance *bq_internal_attn_bf16_split(int *n);
 const bq::AttnInstance *bq_internal_attn_q8_0_own(int *n);
 const bq::AttnInstance *bq_internal_attn_q8_0_split(int *n);
+
+// bq_attn.cu: the call in one pass, with the groups of `shared` (or NULL)
+bq_status bq_internal_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, const bq::AttnArgs *shared,
+                                      void *workspace, int64_t workspace_bytes, void *stream);

@@ -74,36 +74,55 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
         return unit * p.tile_rows + (i - t * p.tile_rows);
     };
     auto stats = [&](int k) { return (k < ns ? j.shared.ml : j.rest.ml)[at(k)]; };
-    float top = -INFINITY;
-    for (int k = w + W * lane; k < n; k += W * 32) top = fmaxf(top, stats(k).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    // AHEAD partial results are on their way while the weights of up to 32 are found;
+    // with more, those come 32 at a time, with a running maximum
+    constexpr int AHEAD = 8;
+    float top = -INFINITY, sum = 0.0f;
     float4 acc[2] = {};
-    float sum = 0.0f;
+    auto fetch = [&](int k, float4(&v)[2]) {
+        const float *src = (k < ns ? j.shared.o : j.rest.o) + at(k) * D;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (128 * e + 4 * lane < D) v[e] = *reinterpret_cast<const float4 *>(src + 128 * e + 4 * lane);
+    };
     for (int k0 = w; k0 < n; k0 += W * 32) {
-        const int mine = k0 + W * lane;
+        const int mine = k0 + W * lane, many = min(32, (n - k0 + W - 1) / W);
         const float2 ml = mine < n ? stats(mine) : make_float2(-INFINITY, 0.0f);
+        float4 o[AHEAD][2];
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            if (i < many) fetch(k0 + W * i, o[i]);
+        float now = ml.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) now = fmaxf(now, __shfl_xor_sync(~0u, now, s));
+        now = fmaxf(now, top);
+        const float back = top == -INFINITY ? 0.0f : exp2f(top - now);
+        top = now;
         const float f = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - top);
         float part = f * ml.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(~0u, part, o);
-        sum += part;
-        const int many = min(32, (n - k0 + W - 1) / W);
-#pragma unroll 4
-        for (int i = 0; i < many; ++i) {
-            const float x = __shfl_sync(~0u, f, i);
-            const int k = k0 + W * i;
-            const float *src = (k < ns ? j.shared.o : j.rest.o) + at(k) * D;
+        for (int s = 16; s > 0; s >>= 1) part += __shfl_xor_sync(~0u, part, s);
+        sum = fmaf(sum, back, part);
+        if (k0 > w) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int d = 128 * e + 4 * lane;
-                if (d >= D) break;
-                const float4 v = *reinterpret_cast<const float4 *>(src + d);
-                acc[e].x = fmaf(x, v.x, acc[e].x);
-                acc[e].y = fmaf(x, v.y, acc[e].y);
-                acc[e].z = fmaf(x, v.z, acc[e].z);
-                acc[e].w = fmaf(x, v.w, acc[e].w);
+            for (int e = 0; e < 2; ++e) acc[e].x *= back, acc[e].y *= back, acc[e].z *= back, acc[e].w *= back;
+        }
+        for (int i0 = 0; i0 < many; i0 += AHEAD) {
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i) {
+                if (i0 + i >= many) break;
+                const float x = __shfl_sync(~0u, f, i0 + i);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    acc[e].x = fmaf(x, o[i][e].x, acc[e].x);
+                    acc[e].y = fmaf(x, o[i][e].y, acc[e].y);
+                    acc[e].z = fmaf(x, o[i][e].z, acc[e].z);
+                    acc[e].w = fmaf(x, o[i][e].w, acc[e].w);
+                }
             }
+#pragma unroll
+            for (int i = 0; i < AHEAD; ++i)
+                if (i0 + AHEAD + i < many) fetch(k0 + W * (i0 + AHEAD + i), o[i]);
         }
     }
     if constexpr (W > 1) {
@@ -167,6 +186,8 @@ struct Pass {
 struct Plan {
     Pass rest, shared;
     bool any_shared;
+    bool whole;     // one pass of the ordinary kernel instead
+    int64_t bytes;  // of workspace
 };
 
 // Positions per unit: about TARGET units (two CTAs on each of 152 SMs), 128 at
@@ -217,11 +238,7 @@ bool size_tensor_pass(Pass *p, int groups, int64_t rows, int64_t positions, int 
     p->a.row_tiles = (int)((rows + TILE - 1) / TILE);
     const int64_t pairs = (int64_t)p->a.c.kv_heads * p->a.row_tiles;
     const int64_t tiles = (positions + TILE - 1) / TILE;
-    int64_t best = 0, cost = 0;
-    const int64_t least = (tiles + MOST - 1) / MOST;
-    for (int64_t c = least; c < least + 2 * sms && c <= tiles; ++c) {  // chunks of the longest prefix
-        const int64_t n = (tiles + c - 1) / c;
-        if (c > least && n == best) continue;
+    auto units_of = [&](int64_t n) {  // with n tiles a chunk
         int64_t units = 0;
         for (int g = 0; g < groups; ++g) {
             const int64_t of = (int64_t)p->a.group_pages[g] * p->a.c.page_size;
@@ -229,15 +246,30 @@ bool size_tensor_pass(Pass *p, int groups, int64_t rows, int64_t positions, int 
             const int64_t row_tiles = (requests * p->a.x.rows * (int)p->a.group.d + TILE - 1) / TILE;
             units += p->a.c.kv_heads * row_tiles * ((of + n * TILE - 1) / (n * TILE));
         }
-        const int64_t now = (units + sms - 1) / sms * (n + FIXED);
-        if (!best || now < cost) best = n, cost = now;
-        if (units > 2 * sms && n <= FIXED) break;
+        return units;
+    };
+    const int64_t most = tiles < MOST ? tiles : MOST;
+    int64_t best = 0, cost = 0;
+    for (int64_t steps = 1; steps <= 4; ++steps) {  // the smallest chunk that gives so many steps
+        int64_t lo = 1, hi = most;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) / 2;
+            if (units_of(mid) <= steps * sms) hi = mid;
+            else lo = mid + 1;
+        }
+        const int64_t now = (units_of(lo) + sms - 1) / sms * (lo + FIXED);
+        if (!best || now < cost) best = lo, cost = now;
     }
     p->a.chunk = (int)best * TILE;
     p->a.max_chunks = bq::attn_chunks((int)positions, p->a.chunk);
     if ((int64_t)groups * pairs * p->a.max_chunks > 0x7fffffffLL) return false;
     return size_parts(p, groups);
 }
+
+// Bytes of shared keys and values, read once for each request, up to which the
+// ordinary kernel serves the call in one pass.
+constexpr int64_t WHOLE = 48LL << 20;
+std::atomic<int64_t> whole_limit{WHOLE};
 
 bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_t *counts, const int32_t *shared,
                   int groups, Plan *p) {
@@ -270,11 +302,23 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_
         sharing += common != 0;
     }
     if (end != x->requests) return BQ_ERR_SHAPE;
+    for (int g = groups; g < bq::ATTN_GROUPS; ++g) a.group_end[g] = (int)end, a.group_pages[g] = 0;
     p->any_shared = sharing != 0;
+    // What the shared pages would be read again for all requests, against the launches
+    // that sharing costs (WHOLE has the figures).
+    int64_t again = 0;
+    for (int g = 0; g < groups; ++g)
+        again += (int64_t)counts[g] * a.group_pages[g] * c->page_size * c->kv_heads * c->head_dim * 2 *
+                 (c->type == BQ_Q8_0 ? 1 : 2);
+    p->whole = !p->any_shared || again <= whole_limit.load(std::memory_order_relaxed);
+    if (p->whole) {
+        p->bytes = bq_paged_attention_workspace_bytes(c, x);
+        return p->bytes < 0 ? BQ_ERR_SHAPE : BQ_OK;
+    }
     p->shared.a = a;
     a.mode = bq::ATTN_REST;
     if (!size_pass(&p->rest, x->requests, each, most_rest, x->requests)) return BQ_ERR_SHAPE;
-    if (p->any_shared) {
+    {
         bq::AttnArgs &b = p->shared.a;
         b.mode = bq::ATTN_PREFIX;
         b.x.requests = groups;
@@ -282,14 +326,9 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_
         if (has_tensor_kernel(c) ? !size_tensor_pass(&p->shared, groups, most_rows, most_shared, 152)
                                  : !size_pass(&p->shared, groups, most_rows, most_shared, sharing))
             return BQ_ERR_SHAPE;
-    } else {
-        p->shared.ml_bytes = p->shared.o_bytes = 0;
     }
+    p->bytes = p->rest.ml_bytes + p->rest.o_bytes + p->shared.ml_bytes + p->shared.o_bytes;
     return BQ_OK;
-}
-
-int64_t bytes_of(const Plan &p) {
-    return p.rest.ml_bytes + p.rest.o_bytes + p.shared.ml_bytes + p.shared.o_bytes;
 }
 
 // A map of the pages' 64-value blocks, swizzled as the tensor cores read them;
@@ -367,11 +406,14 @@ Parts parts_of(const Pass &p) {
 
 int bq_internal_status_attn_prefix(unsigned int *flags, int clear) { return read_status_attn_prefix(flags, clear); }
 
+// host hook for the tests (not in the public header): sets the limit, returns the one before
+extern "C" int64_t bq_internal_prefix_whole_limit(int64_t bytes) { return whole_limit.exchange(bytes < 0 ? WHOLE : bytes); }
+
 extern "C" int64_t bq_paged_prefix_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args,
                                                              const int32_t *group_requests, const int32_t *group_shared,
                                                              int groups) {
     Plan p;
-    return plan_of(cache, args, group_requests, group_shared, groups, &p) == BQ_OK ? bytes_of(p) : -1;
+    return plan_of(cache, args, group_requests, group_shared, groups, &p) == BQ_OK ? p.bytes : -1;
 }
 
 extern "C" bq_status bq_paged_prefix_attention(const bq_kv_cache *cache, const bq_attention_args *x,
@@ -383,9 +425,10 @@ extern "C" bq_status bq_paged_prefix_attention(const bq_kv_cache *cache, const b
     if (x->requests == 0) return BQ_OK;
     s = bq::check_attention_pointers(cache, x);
     if (s != BQ_OK) return s;
+    if (p.whole) return bq_internal_paged_attention(cache, x, &p.rest.a, workspace, workspace_bytes, stream);
     if (!workspace) return BQ_ERR_NULL;
     if (!bq::aligned_to(workspace, 16)) return BQ_ERR_ALIGN;
-    if (workspace_bytes < bytes_of(p)) return BQ_ERR_SHAPE;
+    if (workspace_bytes < p.bytes) return BQ_ERR_SHAPE;
     uint8_t *at = static_cast<uint8_t *>(workspace);
     for (Pass *pass : {&p.rest, &p.shared}) {
         pass->a.part_ml = reinterpret_cast<float2 *>(at);
@@ -396,13 +439,13 @@ extern "C" bq_status bq_paged_prefix_attention(const bq_kv_cache *cache, const b
     if (!sms) return BQ_ERR_CUDA;
     unsigned int *status = nullptr;
     cudaError_t e = status_address(&status);
-    if (e == cudaSuccess && p.any_shared) e = run(&p.shared, sms, stream, status);
+    if (e == cudaSuccess) e = run(&p.shared, sms, stream, status);
     if (e == cudaSuccess) e = run(&p.rest, sms, stream, status);
     if (e != cudaSuccess) return bq::from_cuda_error(e);
     JoinArgs j;
     j.a = p.rest.a;
     j.rest = parts_of(p.rest);
-    j.shared = p.any_shared ? parts_of(p.shared) : Parts{nullptr, nullptr, 1, 0, 1, 1};
+    j.shared = parts_of(p.shared);
     e = x->dtype == BQ_F32   ? join<BQ_F32>(j, stream)
         : x->dtype == BQ_F16 ? join<BQ_F16>(j, stream)
                              : join<BQ_BF16>(j, stream);

@@ -4,13 +4,13 @@
 //
 // The tables are one launch of one thread-block cluster, in phases between cluster
 // barriers: scans of the requests (every CTA does them all, in its shared memory);
-// forked rows copied and counts raised and lowered, by atomics whose sums do not
-// depend on their order; popped pages written; the pages whose count has come to
-// 0 claimed, each by its first release (an atomic minimum over the releases'
-// indices, kept in the count itself as a negative number); then the claims are
-// ranked by a scan over the releases and pushed.  So nothing depends on the order
-// of threads.  Bound by latency: a barrier is a few hundred ns, a phase one or two
-// reads from L2 after one another.
+// then forked rows copied, popped pages written, counts raised and lowered, by
+// atomics whose sums do not depend on their order; then, if pages are given up, the
+// ones whose count has come to 0 claimed, each by its first release (an atomic
+// minimum over the releases' indices, kept in the count itself as a negative
+// number), the claims ranked by a scan over the releases, and pushed.  So nothing
+// depends on the order of threads.  Bound by latency: a barrier is a few hundred ns,
+// a phase one or two reads from L2 after one another.
 //
 // Compaction ranks the pages by ballots and prefix sums over the pool (one cluster),
 // then renumbers the tables over the whole GPU.  Copies are bound by HBM: each
@@ -24,7 +24,7 @@ namespace {
 BQ_STATUS_WORD(pages)
 
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int CLUSTER = 8;
+constexpr int CLUSTER = 8;  // CTAs
 constexpr int CLAIM = -0x7fffffff - 1;  // count of a page that is given back: CLAIM + its first release
 
 struct ShareArgs {
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
     cluster_barrier();
 
     const int step = (int)cluster * THREADS, me = (int)rank * THREADS + tid;
+    const int lane = tid & 31;
     auto row_of = [&](int b) { return a.t.table + (long long)b * a.t.table_stride; };
     auto counted = [&](int page) { return page >= 0 && page < pool; };
     // the i-th released page
@@ -236,23 +237,39 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
         return r.cut ? last_s[b] : row_of(b)[r.wanted + (i - gone[b])];
     };
 
-    // ---- counts ----
-    for (long long i = me; i < all_joined; i += step) {
-        const int b = bq::last_not_above(joined, n, (int)i);
-        const int c = (int)i - joined[b];
-        const int page = row_of((mark_s[b] & PARENT) - 1)[c];
-        row_of(b)[c] = page;
-        if (counted(page)) atomicAdd(&a.s.refs[page], 1);
-        else atomicOr(&g_status_pages, BQ_DEVERR_PAGE);
+    // ---- forked rows, counts, popped pages: nothing that one of them writes is read by
+    // another, but a parent's last page where the parent takes one of its own ----
+    // 32 JOIN entries to a warp at a time, JOIN reads in flight
+    constexpr int JOIN = 4;
+    for (long long i0 = (long long)(me >> 5) * (32 * JOIN); i0 < all_joined; i0 += (long long)(step >> 5) * (32 * JOIN)) {
+        int of[JOIN], col[JOIN], page[JOIN];
+        int b = bq::last_not_above(joined, n, (int)min(i0 + lane, all_joined - 1));
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k) {
+            const long long i = i0 + 32 * k + lane;
+            of[k] = -1;
+            if (i < all_joined) {
+                while (joined[b + 1] <= i) ++b;  // ends: joined[n] > i
+                const int p = (mark_s[b] & PARENT) - 1;
+                of[k] = b, col[k] = (int)i - joined[b];
+                // (the parent may be replacing this entry)
+                const bool last = (mark_s[p] & CUT) && col[k] == pages(base_s[p]) - 1;
+                page[k] = last ? last_s[p] : row_of(p)[col[k]];
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < JOIN; ++k)
+            if (of[k] >= 0) {
+                row_of(of[k])[col[k]] = page[k];
+                if (counted(page[k])) atomicAdd(&a.s.refs[page[k]], 1);
+                else atomicOr(&g_status_pages, BQ_DEVERR_PAGE);
+            }
     }
     for (long long i = me; i < all_gone; i += step) {
         const int page = released((int)i);
         if (counted(page)) atomicSub(&a.s.refs[page], 1);
         else atomicOr(&g_status_pages, BQ_DEVERR_PAGE);
     }
-    cluster_barrier();
-
-    // ---- popped pages; claims ----
     for (int i = me; i < given; i += step) {
         const int b = bq::last_not_above(asked, n, i);
         const Request r = request(b);
@@ -264,40 +281,45 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
             a.s.copy_dst[copied[b]] = page;
         }
     }
-    for (long long i = me; i < all_gone; i += step) {
-        const int page = released((int)i);
-        if (counted(page) && __ldcg(&a.s.refs[page]) <= 0) atomicMin(&a.s.refs[page], CLAIM + (int)i);
-    }
     cluster_barrier();
 
-    // ---- pushes: each thread a run of releases ----
-    const long long run = (all_gone + step - 1) / step;
-    const long long i0 = min(all_gone, me * run), i1 = min(all_gone, i0 + run);
-    auto mine = [&](long long i, int &page) {
-        page = released((int)i);
-        return counted(page) && __ldcg(&a.s.refs[page]) == CLAIM + (int)i;
-    };
-    long long v[1] = {0}, total[1];
-    for (long long i = i0; i < i1; ++i) {
-        int page;
-        v[0] += mine(i, page);
-    }
-    scan_threads<1>(v, total, scratch);
-    if (tid == 0) s_pushed = total[0];
-    cluster_barrier();
-    long long before = 0, pushed = 0;
-    for (uint32_t k = 0; k < cluster; ++k) {
-        const long long p = peer_word(&s_pushed, k);
-        before += k < rank ? p : 0;
-        pushed += p;
-    }
-    long long at = count - given + before + v[0];
-    for (long long i = i0; i < i1; ++i) {
-        int page;
-        if (!mine(i, page)) continue;
-        a.s.refs[page] = 0;
-        if (at < pool) a.t.free_pages[at] = page;
-        ++at;
+    // ---- pages that nobody holds any more ----
+    long long pushed = 0;
+    if (all_gone) {
+        for (long long i = me; i < all_gone; i += step) {
+            const int page = released((int)i);
+            if (counted(page) && __ldcg(&a.s.refs[page]) <= 0) atomicMin(&a.s.refs[page], CLAIM + (int)i);
+        }
+        cluster_barrier();
+        // each thread a run of releases
+        const long long run = (all_gone + step - 1) / step;
+        const long long i0 = min(all_gone, me * run), i1 = min(all_gone, i0 + run);
+        auto mine = [&](long long i, int &page) {
+            page = released((int)i);
+            return counted(page) && __ldcg(&a.s.refs[page]) == CLAIM + (int)i;
+        };
+        long long v[1] = {0}, total[1];
+        for (long long i = i0; i < i1; ++i) {
+            int page;
+            v[0] += mine(i, page);
+        }
+        scan_threads<1>(v, total, scratch);
+        if (tid == 0) s_pushed = total[0];
+        cluster_barrier();
+        long long before = 0;
+        for (uint32_t k = 0; k < cluster; ++k) {
+            const long long p = peer_word(&s_pushed, k);
+            before += k < rank ? p : 0;
+            pushed += p;
+        }
+        long long at = count - given + before + v[0];
+        for (long long i = i0; i < i1; ++i) {
+            int page;
+            if (!mine(i, page)) continue;
+            a.s.refs[page] = 0;
+            if (at < pool) a.t.free_pages[at] = page;
+            ++at;
+        }
     }
 
     // ---- outputs ----
@@ -381,9 +403,19 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
     long long moves = 0;
     for (uint32_t k = 0; k < cluster; ++k) moves = max(moves, peer_word(&s_moves, k));
     const long long room = a.c.max_moves, done = min(moves, room);
+    constexpr int READS = 8;  // in flight
+    int held[READS];
     for (long long q0 = p0; q0 < p1; q0 += 32) {
         const long long p = q0 + lane;
-        const bool in = p < p1, live = in && refs[p] > 0;
+        const int turn = (int)((q0 - p0) / 32 % READS);
+        if (turn == 0) {
+#pragma unroll
+            for (int k = 0; k < READS; ++k) held[k] = p + 32 * k < p1 ? refs[p + 32 * k] : 0;
+        }
+        int now = held[0];
+#pragma unroll
+        for (int k = 1; k < READS; ++k) now = turn == k ? held[k] : now;
+        const bool in = p < p1, live = in && now > 0;
         const uint32_t bits = __ballot_sync(~0u, live);
         const long long below = before + __popc(bits & ((1u << lane) - 1));  // pages in use below p
         before += __popc(bits);
@@ -561,7 +593,7 @@ extern "C" bq_status bq_kv_shared_tables(const bq_kv_tables *t, const bq_kv_shar
     const bool with_rows = t->max_tokens <= bq::TABLES_ROWS_ALONE;
     // one CTA for a step that cannot move much, however it turns out
     const long long work = (with_rows ? t->max_tokens : 0) + (long long)t->requests * t->table_width;
-    const int cluster = work > 4LL * THREADS ? CLUSTER : 1;
+    const int cluster = work > 16LL * THREADS ? CLUSTER : 1;
     const size_t smem = (size_t)(9 * t->requests + 5) * sizeof(int);
     if (smem > 40 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,

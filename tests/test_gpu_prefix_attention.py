@@ -1,15 +1,30 @@
 """Attention of requests that share their first pages (paged_prefix_attention)
 against a plain 64-bit form that knows nothing of sharing."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import block_quantized_weight_dequant_gb300 as bq
+from block_quantized_weight_dequant_gb300 import _lib
 
 import paged_plain as plain
 from test_gpu_cache import BF16, DEV, F16, F32, KINDS, filled_cache, healthy, normal, poison, rng  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, params=["shared", "by size"])
+def limit(request):
+    """Calls that would read little again are served in one pass over whole requests:
+    every test runs with the shared pages gone through once whatever their size, and
+    with the choice as it is."""
+    _lib.lib.bq_internal_prefix_whole_limit.restype = ctypes.c_int64
+    _lib.lib.bq_internal_prefix_whole_limit.argtypes = [ctypes.c_int64]
+    _lib.lib.bq_internal_prefix_whole_limit(0 if request.param == "shared" else -1)
+    yield request.param
+    _lib.lib.bq_internal_prefix_whole_limit(-1)
 
 
 def shared_table(g, lens, shared, page, pages, width=None, junk=-1):
@@ -305,7 +320,7 @@ def test_it_agrees_with_ordinary_attention_at_a_servers_size():
         assert float((a - b).abs().max()) <= 2 * (plain.EPS[dtype] / 2 * 0.5 + 2.0 ** -13 * 2)
 
 
-def test_nothing_to_do_and_refusals():
+def test_nothing_to_do_and_refusals(limit):
     cache = bq.PagedKVCache.zeros(8, 16, 2, 64)
     i32 = dict(dtype=torch.int32, device=DEV)
     q, table, lens = torch.zeros(2, 4, 64, device=DEV), torch.zeros(2, 4, **i32), torch.full((2,), 20, **i32)
@@ -320,7 +335,8 @@ def test_nothing_to_do_and_refusals():
         bq.paged_prefix_attention(cache, q, table, lens.long(), 16)
     with pytest.raises(ValueError):
         bq.paged_prefix_attention(cache, q, table[:1], lens, 16)
-    with pytest.raises(bq.BQError):
-        bq.paged_prefix_attention(cache, q, table, lens, 16, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+    if limit == "shared":  # (the one pass needs no workspace here)
+        with pytest.raises(bq.BQError):
+            bq.paged_prefix_attention(cache, q, table, lens, 16, workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(bq.BQError):
         bq.paged_prefix_attention(cache, q, table, lens, 16, scale=float("nan"))
