@@ -9,16 +9,18 @@
 // memory, is rescaled (by the row's own 2^(m_old - m)) in few tiles.
 //
 // A CTA takes a chunk of the positions for 128 rows.  Warps 0 to 3 and 4 to 7 are
-// two streams: they take the even and the odd tiles, each with S (128 columns of
-// tensor memory) and O (up to 128) of its own, so that the tensor cores work for
-// one stream while the other one computes its weights; their O are joined at the
-// end.  Warps 8 to 10 bring K and V tiles into a ring in shared memory by 16-byte
-// asynchronous copies (any page size and stride; what is not there is filled with
-// zeros) in the swizzled rows of 128 bytes that the tensor cores read: K with
-// positions as rows and head_dim contiguous, V the same bytes with the summed
-// axis as rows.  One thread of warp 11 issues all products.  The weights go back
-// to tensor memory in the columns of the scores that they come from, and are the
-// first operand of the second product from there.
+// two streams: they take the even and the odd tiles, each with scores S (128 columns
+// of tensor memory) of its own, so that the tensor cores work for one stream while
+// the other one computes its weights.  The streams hand the rows' references to one
+// another and add into one O (up to 128 columns); the one that lets a reference grow
+// rescales O.  Warp 8 brings K and V tiles into a ring in shared memory by tensor
+// maps (pages that are whole groups of 8 slots; what is not there is filled with
+// zeros), or warps 8 to 10 by 16-byte asynchronous copies (any page size and
+// stride), in the swizzled rows of 128 bytes that the tensor cores read: K with
+// positions as rows and head_dim contiguous, V the same bytes with the summed axis
+// as rows.  One thread of warp 11 issues all products.  Queries are a first operand
+// in tensor memory; the weights go back there in the columns of the scores that they
+// come from, and are the first operand of the second product.
 //
 // Precision.  A query of the cache's type is used as it is, any other in QP 16-bit
 // parts (fp16 2, after scaling the row by a power of two; bf16 3); weights are two
@@ -32,6 +34,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <cstddef>
 
 #include "bq_attn.h"
 
@@ -41,13 +44,18 @@ constexpr int TC_ROWS = 128, TC_TILE = 128;
 constexpr int TC_SOFTMAX_WARPS = 8, TC_COPY_WARPS = 3, TC_WARPS = 12;
 constexpr int TC_MASKS = 8;        // tiles whose masks are kept
 constexpr int TC_BLOCK = 128 * 128;  // bytes of 128 rows of 64 values
-constexpr int TC_COLUMNS = 512;      // of tensor memory, all of it
+// columns of tensor memory, all of it: scores of two streams, output, queries
+constexpr int TC_COLUMNS = 512, TC_O = 256, TC_Q = 384;
 constexpr float TC_GROWTH = 8.0f;    // log2 of what a weight may be
 constexpr int TC_SHIFT_F16 = 7;      // fp16 weights carry 2^7: up to 2^15, two parts keep 2^-24
 
 template <int QP, int NB>
 struct TcShape {
-    static constexpr int SLOT = NB * TC_BLOCK, Q_BYTES = QP * NB * TC_BLOCK;
+    // queries as a first operand in tensor memory, where their parts fit beside the scores
+    // of both streams and the output: the tensor cores then read K and V alone from
+    // shared memory, whose 128 bytes a cycle bound the kernel otherwise
+    static constexpr bool Q_TENSOR = QP * NB * 32 <= TC_COLUMNS - TC_Q;
+    static constexpr int SLOT = NB * TC_BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_BLOCK;
     static constexpr int LIMIT = 227 * 1024, MISC = 3072;
     static constexpr int most = (LIMIT - MISC - Q_BYTES) / SLOT;
     static constexpr int SLOTS = most > 8 ? 8 : most;
@@ -57,7 +65,7 @@ struct TcShape {
     // above SLOTS - 2 for themselves.
     static constexpr int LAG = SLOTS >= 8 ? 3 : 1;
     static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + MISC;
-    static constexpr int OROW = NB * 64 + 4;  // floats of a row of the join, in the ring's place
+    static constexpr int OROW = NB * 64 + 4;  // floats of a row on its way out, in the ring's place
     static_assert(SLOTS >= 4 && LAG >= 1 && LAG <= SLOTS - 2);
     static_assert(TC_ROWS * OROW * 4 <= SLOTS * SLOT);
     static_assert(SMEM > 114 * 1024, "one CTA per SM: each takes all tensor memory");
@@ -75,14 +83,15 @@ struct TcArgs {
 
 // shared memory behind the ring
 struct TcMisc {
-    uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2], o_full[2], q_full, last;
-    uint8_t mask[TC_MASKS][16];  // positions of a tile that are there
-    float factor[TC_ROWS];       // of a row's scores
-    float2 ml[TC_ROWS];          // of the second stream
+    uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2], q_full, added, o_full;
+    uint64_t ref_full[2][4];     // by stream and warp of it
+    alignas(16) uint8_t mask[TC_MASKS][16];  // positions of a tile that are there
+    float ref[2][TC_ROWS];       // a row's reference after the stream's last tile
+    float sum[2][TC_ROWS];       // of its weights; the largest query values before
     uint32_t tmem;
     uint32_t dead;  // a wait has run out
 };
-static_assert(sizeof(TcMisc) <= 3072);
+static_assert(sizeof(TcMisc) <= 3072 && offsetof(TcMisc, mask) % 16 == 0 && alignof(TcMisc) == 16);
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -311,20 +320,10 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     const int group_rows = (end_request - first) * R * G, first_row = rt * TC_ROWS;
     const int common = a.group_pages[g] * page;
     const int begin = ck * a.chunk, end = min(begin + a.chunk, common);
-    pdl_wait();
-    pdl_launch_dependents();
     if (begin >= end || first_row >= group_rows) return;
-    // the first request that holds the shared pages: its table row tells them
-    int owner = 0x7fffffff;
-    const int most = a.x.table_width * page;
-    for (int i = first + lane; i < end_request && owner == 0x7fffffff; i += 32)
-        if (min(a.x.lens[i], most) - R + 1 >= common) owner = i;
-    owner = __reduce_min_sync(~0u, owner);
-    if (owner == 0x7fffffff) return;  // nobody reads these partial results
-    const int tiles = (end - begin + TC_TILE - 1) / TC_TILE;
     const int D16 = (D + 15) & ~15;
 
-    // ---- barriers and tensor memory ----
+    // ---- barriers and tensor memory, while the kernel before ends ----
     if (tid == 0) {
         const int copying = args.box ? 1 : TC_COPY_WARPS;
         for (int i = 0; i < SLOTS; ++i) barrier_init(&misc.full[i], copying), barrier_init(&misc.empty[i], 1);
@@ -332,10 +331,11 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         for (int i = 0; i < 2; ++i) {
             barrier_init(&misc.s_full[i], 1);
             barrier_init(&misc.p_full[i], TC_SOFTMAX_WARPS / 2);
-            barrier_init(&misc.o_full[i], 1);
+            for (int k = 0; k < 4; ++k) barrier_init(&misc.ref_full[i][k], 1);
         }
         barrier_init(&misc.q_full, TC_SOFTMAX_WARPS);
-        barrier_init(&misc.last, 1);
+        barrier_init(&misc.added, 1);
+        barrier_init(&misc.o_full, 1);
         misc.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -345,12 +345,25 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         tc_fence_before();
+        if (lane < 2 && args.box)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(lane ? &args.v : &args.k) : "memory");
     }
+    pdl_wait();
+    pdl_launch_dependents();
+    // the first request that holds the shared pages: its table row tells them
+    int owner = 0x7fffffff;
+    const int most = a.x.table_width * page;
+    for (int i = first + lane; i < end_request && owner == 0x7fffffff; i += 32)
+        if (min(a.x.lens[i], most) - R + 1 >= common) owner = i;
+    owner = __reduce_min_sync(~0u, owner);
+    // (without one nobody reads these partial results)
+    const int tiles = owner == 0x7fffffff ? 0 : (end - begin + TC_TILE - 1) / TC_TILE;
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem;
 
-    if (warp == TC_SOFTMAX_WARPS && args.box) {
+    if (tiles == 0) {
+    } else if (warp == TC_SOFTMAX_WARPS && args.box) {
         // ---- copies by tensor maps: K and V of each tile in turn; lane j looks up the
         // tile's rows 8 j to 8 j + 7 (pages are whole groups of 8) ----
         const int *row_table = a.x.table + owner * a.x.table_stride;
@@ -500,7 +513,11 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 for (int p = QP - 1; p >= 0; --p)
                     for (int k = 0; k < steps; ++k) {
                         const uint64_t at = (k >> 2) * (TC_BLOCK >> 4) + (k & 3) * 2;
-                        tc_product_shared(d, q_m + p * (NB * TC_BLOCK >> 4) + at, k_m + at, qk_shape, p < QP - 1 || k);
+                        const bool add = p < QP - 1 || k;
+                        if constexpr (S::Q_TENSOR)
+                            tc_product_tensor(d, tmem + TC_Q + p * NB * 32 + 8 * k, k_m + at, qk_shape, add);
+                        else
+                            tc_product_shared(d, q_m + p * (NB * TC_BLOCK >> 4) + at, k_m + at, qk_shape, add);
                     }
                 tc_commit(&misc.empty[slot]);
                 tc_commit(&misc.s_full[t & 1]);
@@ -513,83 +530,128 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 if (!ok) break;
                 tc_fence_after();
                 const uint64_t v_m = ring_m + slot * (S::SLOT >> 4);
-                const uint32_t o = tmem + 256 + s * 128, w = tmem + s * 128;
+                const uint32_t o = tmem + TC_O, w = tmem + s * 128;
                 // 16 positions a step: 8 columns of a weight part; 32 columns hold both
                 // parts of 32 positions
                 for (int k = 0; k < TC_TILE / 16; ++k)
                     for (int p = 1; p >= 0; --p)
                         tc_product_tensor(o, w + 32 * (k >> 1) + 16 * p + 8 * (k & 1), v_m + k * (2048 >> 4), pv_shape,
-                                          t > 1 || k || p == 0);
+                                          t || k || p == 0);
                 tc_commit(&misc.empty[slot]);
-                if (t + 2 >= tiles) tc_commit(&misc.o_full[s]);  // the stream's last tile
-                else scores(t + 2);
+                tc_commit(&misc.added);
+                if (t + 2 < tiles) scores(t + 2);
             }
-            // nothing is in flight when the tensor memory is given back
-            tc_commit(&misc.last);
+            // the end of all products; nothing is in flight when the tensor memory is given back
+            tc_commit(&misc.o_full);
             const uint64_t t0 = tc_nanoseconds();
-            while (!barrier_try(&misc.last, 0) && tc_nanoseconds() - t0 < 100000000ull) {}
+            while (!barrier_try(&misc.o_full, 0) && tc_nanoseconds() - t0 < 100000000ull) {}
         }
         __syncwarp();
     } else {
-        // ---- queries: fp32 -> 16-bit parts in shared memory, 16 rows by each warp ----
-        {
+        const int s = warp >> 2, i = 32 * (warp & 3) + lane;  // stream and row of this thread
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const int es = a.x.dtype == BQ_F32 ? 4 : 2;
+        const bool wide = a.x.q_row_stride % 4 == 0 && a.x.q_head_stride % 4 == 0 &&
+                          (reinterpret_cast<uintptr_t>(a.x.q) & (4 * es - 1)) == 0;
+        // the row carries the scale's sign (and zero), so that a larger product is a
+        // larger score
+        const float sign = a.scale_log2 > 0.0f ? 1.0f : a.scale_log2 < 0.0f ? -1.0f : 0.0f;
+        const float size = sign == 0.0f ? 1.0f : fabsf(a.scale_log2);
+        auto read = [&](int gr, int d, float(&x)[4]) {  // 4 values of a query row of the group
+            x[0] = x[1] = x[2] = x[3] = 0.0f;
+            if (gr >= group_rows || d >= D) return;
+            const int row = (int)a.group.div((uint32_t)gr), head = h * G + gr - row * G;
+            const long long at = ((long long)first * R + row) * a.x.q_row_stride + head * a.x.q_head_stride + d;
+            if (a.x.dtype == BQ_F32) load_n<F32, 4>((const float *)a.x.q + at, wide, x);
+            else if (a.x.dtype == BQ_F16) load_n<F16, 4>((const __half *)a.x.q + at, wide, x);
+            else load_n<BF16, 4>((const __nv_bfloat16 *)a.x.q + at, wide, x);
+        };
+        // powers of two that bring the largest of a row to [2^14, 2^15), as in the ordinary kernel
+        struct Scaling {
+            float a, b, factor;
+        };
+        auto scaling = [&](float top) {
+            int ex = (int)((__float_as_uint(top) >> 23) & 0xff) - 127;
+            if (top < 1.1754944e-38f || ex == 128) ex = 14;  // zero, subnormal or not finite: as it is
+            const int up = 14 - ex;
+            return Scaling{ldexpf(1.0f, up / 2), ldexpf(1.0f, up - up / 2),
+                           size * ldexpf(1.0f, -(up / 2)) * ldexpf(1.0f, -(up - up / 2))};
+        };
+        constexpr bool SCALED = HALF && QP > 1;
+        float factor;
+        if constexpr (S::Q_TENSOR) {
+            // ---- queries into tensor memory, a row to a thread, half of its values to each
+            // stream's threads ----
+            constexpr int EACH = NB * 32;  // values of this thread
+            float x[EACH / 4][4], top = 0.0f;
+#pragma unroll
+            for (int k = 0; k < EACH / 4; ++k) {
+                read(first_row + i, s * EACH + 4 * k, x[k]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[k][e] *= sign;
+                    if constexpr (SCALED) top = fmaxf(top, fabsf(x[k][e]));
+                }
+            }
+            factor = size;
+            Scaling by = {1.0f, 1.0f, size};
+            if constexpr (SCALED) {
+                misc.sum[s][i] = top;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                by = scaling(fmaxf(misc.sum[0][i], misc.sum[1][i]));
+                factor = by.factor;
+            }
+#pragma unroll
+            for (int p = 0; p < QP; ++p)
+#pragma unroll
+                for (int k0 = 0; k0 < EACH / 4; k0 += 4) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float(&y)[4] = x[k0 + k];
+                        if (SCALED && p == 0) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) y[e] = y[e] * by.a * by.b;
+                        }
+                        w[2 * k] = tc_part<HALF>(y[0], y[1]);
+                        w[2 * k + 1] = tc_part<HALF>(y[2], y[3]);
+                    }
+                    tc_store8(tmem + lanes + TC_Q + p * NB * 32 + s * (EACH / 2) + 2 * k0, w);
+                }
+            tc_wait_store();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) barrier_arrive(&misc.q_full);
+        } else {
+            // ---- queries into shared memory, 16 rows to a warp ----
             const int d = 4 * lane;
-            const bool in_tile = d < NB * 64;
-            const int es = a.x.dtype == BQ_F32 ? 4 : 2;
-            const bool wide = a.x.q_row_stride % 4 == 0 && a.x.q_head_stride % 4 == 0 &&
-                              (reinterpret_cast<uintptr_t>(a.x.q) & (4 * es - 1)) == 0;
 #pragma unroll 4
             for (int k = 0; k < TC_ROWS / TC_SOFTMAX_WARPS; ++k) {
-                const int i = warp + TC_SOFTMAX_WARPS * k, gr = first_row + i;
-                float x[4] = {};
-                if (gr < group_rows && d < D) {
-                    const int row = (int)a.group.div((uint32_t)gr), head = h * G + gr - row * G;
-                    const long long at = ((long long)first * R + row) * a.x.q_row_stride + head * a.x.q_head_stride + d;
-                    if (a.x.dtype == BQ_F32) load_n<F32, 4>((const float *)a.x.q + at, wide, x);
-                    else if (a.x.dtype == BQ_F16) load_n<F16, 4>((const __half *)a.x.q + at, wide, x);
-                    else load_n<BF16, 4>((const __nv_bfloat16 *)a.x.q + at, wide, x);
-                }
-                // the row carries the scale's sign (and zero), so that a larger product is a
-                // larger score
-                const float sign = a.scale_log2 > 0.0f ? 1.0f : a.scale_log2 < 0.0f ? -1.0f : 0.0f;
-                float factor = sign == 0.0f ? 1.0f : fabsf(a.scale_log2);
+                const int r = warp + TC_SOFTMAX_WARPS * k;
+                float x[4];
+                read(first_row + r, d, x);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] *= sign;
-                if constexpr (HALF && QP > 1) {
-                    // the largest of the row to [2^14, 2^15), as in the ordinary kernel
-                    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-                    int ex = (int)((__float_as_uint(top) >> 23) & 0xff) - 127;
-                    if (top < 1.1754944e-38f || ex == 128) ex = 14;  // zero, subnormal or not finite: as it is
-                    const int up = 14 - ex;
-                    const float s1 = ldexpf(1.0f, up / 2), s2 = ldexpf(1.0f, up - up / 2);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = x[e] * s1 * s2;
-                    factor = factor * ldexpf(1.0f, -(up / 2)) * ldexpf(1.0f, -(up - up / 2));
-                }
-                // (above 0: what it multiplies may be minus infinity)
-                if (lane == 0) misc.factor[i] = fmaxf(factor, 1.1754944e-38f);
+                static_assert(!SCALED, "fp16 parts fit in tensor memory");
                 const int piece = (lane & 15) >> 1;
-                uint8_t *to = q_s + (lane >> 4) * TC_BLOCK + i * 128 + ((piece ^ (i & 7)) << 4) + 8 * (lane & 1);
+                uint8_t *to = q_s + (lane >> 4) * TC_BLOCK + r * 128 + ((piece ^ (r & 7)) << 4) + 8 * (lane & 1);
 #pragma unroll
                 for (int p = 0; p < QP; ++p) {
                     const uint2 w = make_uint2(tc_part<HALF>(x[0], x[1]), tc_part<HALF>(x[2], x[3]));
-                    if (in_tile) *reinterpret_cast<uint2 *>(to + p * NB * TC_BLOCK) = w;
+                    if (d < NB * 64) *reinterpret_cast<uint2 *>(to + p * NB * TC_BLOCK) = w;
                 }
             }
+            factor = size;
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) barrier_arrive(&misc.q_full);
-            asm volatile("bar.sync 1, 256;" ::: "memory");  // factors of all rows
         }
+        // (above 0: what it multiplies may be minus infinity)
+        factor = fmaxf(factor, 1.1754944e-38f);
 
         // ---- weights of this stream's tiles ----
-        const int s = warp >> 2, i = 32 * (warp & 3) + lane;  // this thread's row
-        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t s_at = tmem + lanes + s * 128, o_at = tmem + lanes + 256 + s * 128;
-        const float factor = misc.factor[i];
-        float ref = -INFINITY, l = 0.0f;
+        const uint32_t s_at = tmem + lanes + s * 128, o_at = tmem + lanes + TC_O;
+        float ref = -INFINITY, l = 0.0f;  // the reference that l belongs to
         bool ok = true;
         for (int t = s; t < tiles; t += 2) {
             ok = barrier_wait(&misc.mask_full[t % TC_MASKS], t / TC_MASKS & 1, dead) &&
@@ -633,11 +695,29 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             largest(x[0]);
             largest(x[1]);
             const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * factor;
-            const bool grows = top > ref + TC_GROWTH || (ref == -INFINITY && top > ref);
-            const float now = grows ? top : ref;
-            if (t > s && __any_sync(~0u, grows)) {
-                const float alpha = grows ? tc_pow2(ref - now) : 1.0f;
-                l *= alpha;
+            // the reference that the tile before left, the other stream's
+            float was = -INFINITY;
+            if (t) {
+                ok = barrier_wait(&misc.ref_full[s ^ 1][warp & 3], (t - 1) >> 1 & 1, dead);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                was = misc.ref[s ^ 1][i];
+            }
+            const bool grows = top > was + TC_GROWTH || (was == -INFINITY && top > was);
+            const float now = grows ? top : was;
+            misc.ref[s][i] = now;
+            __syncwarp();
+            if (lane == 0) barrier_arrive(&misc.ref_full[s][warp & 3]);
+            if (t && __any_sync(~0u, grows)) {  // O of the tiles before, once it is there
+                ok = barrier_wait(&misc.added, (t - 1) & 1, dead);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float alpha = grows ? tc_pow2(was - now) : 1.0f;
 #pragma unroll 1
                 for (int c = 0; c < D16; c += 8) {
                     uint32_t o[8];
@@ -648,6 +728,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     tc_store8(o_at + c, o);
                 }
             }
+            if (ref != now) l *= tc_pow2(ref - now);
             ref = now;
             tc_load32(s_at, x[0]);
             const float shift = (HALF ? (float)TC_SHIFT_F16 : 0.0f) - (ref == -INFINITY ? 0.0f : ref);
@@ -682,52 +763,35 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             if (lane == 0) barrier_arrive(&misc.p_full[s]);
         }
 
-        // ---- join of the streams, in the ring's place: nothing reads or fills it once
-        // the last products of both are complete ----
-        const int last = tiles > 1 ? 2 : 1;
-        for (int k = 0; k < last; ++k) ok = ok && barrier_wait(&misc.o_full[k], 0, dead);
+        // ---- the partial results, through the ring's place: nothing reads or fills it once
+        // the last products are complete ----
+        ok = ok && barrier_wait(&misc.o_full, 0, dead);
         ok = __all_sync(~0u, ok);
         tc_fence_after();
+        misc.ref[s][i] = ref, misc.sum[s][i] = l;
         // partial results of the ordinary kernel carry 2^ATTN_SHIFT_F16 over fp16 caches
         constexpr float LIKE = HALF ? (float)(1 << (ATTN_SHIFT_F16 - TC_SHIFT_F16)) : 1.0f;
         float *row = reinterpret_cast<float *>(ring) + i * S::OROW;
-        if (s == 1 && last == 2) {
-            for (int c = 0; c < D16 && ok; c += 32) {
-                uint32_t x[32];
-                tc_load32(o_at + c, x);
-                tc_wait_load();
+        for (int c = 8 * s; c < D16 && ok; c += 16) {
+            uint32_t x[8];
+            tc_load8(o_at + c, x);
+            tc_wait_load();
 #pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    *reinterpret_cast<float4 *>(row + c + k) =
-                        make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]),
-                                    __uint_as_float(x[k + 3]));
-            }
-            misc.ml[i] = make_float2(ref, l);
+            for (int k = 0; k < 8; k += 4)
+                *reinterpret_cast<float4 *>(row + c + k) =
+                    make_float4(LIKE * __uint_as_float(x[k]), LIKE * __uint_as_float(x[k + 1]),
+                                LIKE * __uint_as_float(x[k + 2]), LIKE * __uint_as_float(x[k + 3]));
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const long long unit = (((long long)g * a.max_chunks + ck) * KVH + h) * a.row_tiles + rt;
-        if (s == 0) {
-            const float2 o = last == 2 ? misc.ml[i] : make_float2(-INFINITY, 0.0f);
-            const float top = fmaxf(ref, o.x);
-            const float f = ref == -INFINITY ? 0.0f : LIKE * tc_pow2(ref - top);
-            const float e = o.x == -INFINITY ? 0.0f : LIKE * tc_pow2(o.x - top);
-            for (int c = 0; c < D16 && ok; c += 32) {
-                uint32_t x[32];
-                tc_load32(o_at + c, x);
-                tc_wait_load();
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    float4 v = last == 2 ? *reinterpret_cast<const float4 *>(row + c + k) : make_float4(0, 0, 0, 0);
-                    v.x = fmaf(f, __uint_as_float(x[k]), e * v.x);
-                    v.y = fmaf(f, __uint_as_float(x[k + 1]), e * v.y);
-                    v.z = fmaf(f, __uint_as_float(x[k + 2]), e * v.z);
-                    v.w = fmaf(f, __uint_as_float(x[k + 3]), e * v.w);
-                    *reinterpret_cast<float4 *>(row + c + k) = v;
-                }
-            }
-            if (first_row + i < group_rows) a.part_ml[unit * TC_ROWS + i] = make_float2(top, fmaf(f, l, e * o.y));
+        if (s == 0 && first_row + i < group_rows) {
+            // O belongs to the last tile's reference, which the other stream's sum may not
+            const int last = (tiles - 1) & 1;
+            const float top = misc.ref[last][i], other = misc.ref[last ^ 1][i];
+            const float f = other == top ? 1.0f : tc_pow2(other - top);
+            a.part_ml[unit * TC_ROWS + i] =
+                make_float2(top, LIKE * (misc.sum[last][i] + (other == -INFINITY ? 0.0f : f * misc.sum[last ^ 1][i])));
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
         if (4 * lane < D) {
             float *dst = a.part_o + unit * TC_ROWS * D + 4 * lane;
             const float *src = reinterpret_cast<const float *>(ring) + 4 * lane;
