@@ -200,6 +200,12 @@ __device__ __forceinline__ void tc_product_tensor(uint32_t d, uint32_t a, uint64
         "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
         : "memory");
 }
+// true for one thread of the warp, the same each time
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
 // the barrier's phase completes with all products issued so far
 __device__ __forceinline__ void tc_commit(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(tc_shared(b))
@@ -494,24 +500,29 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         if (ok && !args.box)
             for (int n = max(0, 2 * tiles - LAG); n < 2 * tiles; ++n) arrived(n);
     } else if (warp == TC_WARPS - 1) {
-        // ---- products ----
-        if (lane == 0) {
-            constexpr uint32_t SHAPE = 1u << 4 | (HALF ? 0u : 1u) << 7 | (HALF ? 0u : 1u) << 10 | (TC_ROWS >> 4) << 24;
-            const uint32_t qk_shape = SHAPE | (TC_TILE >> 3) << 17;
-            const uint32_t pv_shape = SHAPE | 1u << 16 | (uint32_t)(D16 >> 3) << 17;
-            const uint64_t q_m = tc_matrix(tc_shared(q_s)), ring_m = tc_matrix(tc_shared(ring));
-            const int steps = D16 / 16;
-            bool ok = barrier_wait(&misc.q_full, 0, dead);
+        // ---- products: the warp waits, one of its threads issues.  (The addresses are the
+        // warp's, in uniform registers, and the steps unrolled: one thread that worked them
+        // out in a loop took 97 cycles a step, of which the tensor cores need 64.) ----
+        constexpr uint32_t SHAPE = 1u << 4 | (HALF ? 0u : 1u) << 7 | (HALF ? 0u : 1u) << 10 | (TC_ROWS >> 4) << 24;
+        constexpr uint32_t qk_shape = SHAPE | (TC_TILE >> 3) << 17;
+        const uint32_t pv_shape = SHAPE | 1u << 16 | (uint32_t)(D16 >> 3) << 17;
+        const uint64_t q_m = tc_matrix(tc_shared(q_s)), ring_m = tc_matrix(tc_shared(ring));
+        const int steps = D16 / 16;
+        bool ok = barrier_wait(&misc.q_full, 0, dead);
+        auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first
+            const int n = 2 * t, slot = n % SLOTS;
+            ok = ok && barrier_wait(&misc.full[slot], n / SLOTS & 1, dead);
+            ok = __all_sync(~0u, ok);
+            if (!ok) return;
             tc_fence_after();
-            auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first
-                const int n = 2 * t, slot = n % SLOTS;
-                ok = ok && barrier_wait(&misc.full[slot], n / SLOTS & 1, dead);
-                if (!ok) return;
-                tc_fence_after();
-                const uint64_t k_m = ring_m + slot * (S::SLOT >> 4);
-                const uint32_t d = tmem + (t & 1) * 128;
+            const uint64_t k_m = ring_m + slot * (S::SLOT >> 4);
+            const uint32_t d = tmem + (t & 1) * 128;
+            if (elect_one()) {
+#pragma unroll
                 for (int p = QP - 1; p >= 0; --p)
-                    for (int k = 0; k < steps; ++k) {
+#pragma unroll
+                    for (int k = 0; k < 4 * NB; ++k) {
+                        if (k >= steps) break;
                         const uint64_t at = (k >> 2) * (TC_BLOCK >> 4) + (k & 3) * 2;
                         const bool add = p < QP - 1 || k;
                         if constexpr (S::Q_TENSOR)
@@ -521,31 +532,40 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     }
                 tc_commit(&misc.empty[slot]);
                 tc_commit(&misc.s_full[t & 1]);
-            };
-            scores(0);
-            if (tiles > 1) scores(1);
-            for (int t = 0; t < tiles && ok; ++t) {
-                const int n = 2 * t + 1, slot = n % SLOTS, s = t & 1;
-                ok = barrier_wait(&misc.full[slot], n / SLOTS & 1, dead) && barrier_wait(&misc.p_full[s], t >> 1 & 1, dead);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t v_m = ring_m + slot * (S::SLOT >> 4);
-                const uint32_t o = tmem + TC_O, w = tmem + s * 128;
+            }
+            __syncwarp();
+        };
+        scores(0);
+        if (tiles > 1) scores(1);
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int n = 2 * t + 1, slot = n % SLOTS, s = t & 1;
+            ok = barrier_wait(&misc.full[slot], n / SLOTS & 1, dead) && barrier_wait(&misc.p_full[s], t >> 1 & 1, dead);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t v_m = ring_m + slot * (S::SLOT >> 4);
+            const uint32_t o = tmem + TC_O, w = tmem + s * 128;
+            if (elect_one()) {
                 // 16 positions a step: 8 columns of a weight part; 32 columns hold both
                 // parts of 32 positions
-                for (int k = 0; k < TC_TILE / 16; ++k)
+                tc_product_tensor(o, w + 16, v_m, pv_shape, t > 0);
+                tc_product_tensor(o, w, v_m, pv_shape, true);
+#pragma unroll
+                for (int k = 1; k < TC_TILE / 16; ++k)
+#pragma unroll
                     for (int p = 1; p >= 0; --p)
-                        tc_product_tensor(o, w + 32 * (k >> 1) + 16 * p + 8 * (k & 1), v_m + k * (2048 >> 4), pv_shape,
-                                          t || k || p == 0);
+                        tc_product_tensor(o, w + 32 * (k >> 1) + 16 * p + 8 * (k & 1), v_m + k * (2048 >> 4), pv_shape, true);
                 tc_commit(&misc.empty[slot]);
                 tc_commit(&misc.added);
-                if (t + 2 < tiles) scores(t + 2);
             }
-            // the end of all products; nothing is in flight when the tensor memory is given back
-            tc_commit(&misc.o_full);
-            const uint64_t t0 = tc_nanoseconds();
-            while (!barrier_try(&misc.o_full, 0) && tc_nanoseconds() - t0 < 100000000ull) {}
+            __syncwarp();
+            if (t + 2 < tiles) scores(t + 2);
         }
+        // the end of all products; nothing is in flight when the tensor memory is given back
+        if (elect_one()) tc_commit(&misc.o_full);
+        __syncwarp();
+        const uint64_t t0 = tc_nanoseconds();
+        while (!barrier_try(&misc.o_full, 0) && tc_nanoseconds() - t0 < 100000000ull) {}
         __syncwarp();
     } else {
         const int s = warp >> 2, i = 32 * (warp & 3) + lane;  // stream and row of this thread
