@@ -42,10 +42,10 @@ struct JoinArgs {
 
 // W warps per query row and head: warp w takes the partial results w, w + W, ...
 // in order, then the warps' sums are added in order.
-template <int DT, int W>
-__global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
+template <int DT, int W, int DB>
+__global__ void __launch_bounds__(JOIN_THREADS, 4) prefix_join_kernel(const __grid_constant__ JoinArgs j) {
     constexpr int ROWS = JOIN_THREADS / 32 / W;
-    __shared__ float4 o_s[W > 1 ? W : 1][W > 1 ? 64 : 1];
+    __shared__ float4 o_s[W > 1 ? W : 1][W > 1 ? 32 * DB : 1];
     __shared__ float2 ml_s[W];
     const bq::AttnArgs &a = j.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = W > 1 ? warp : 0;
@@ -76,19 +76,19 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
     auto stats = [&](int k) { return (k < ns ? j.shared.ml : j.rest.ml)[at(k)]; };
     // AHEAD partial results are on their way while the weights of up to 32 are found;
     // with more, those come 32 at a time, with a running maximum
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 8 / DB;
     float top = -INFINITY, sum = 0.0f;
-    float4 acc[2] = {};
-    auto fetch = [&](int k, float4(&v)[2]) {
+    float4 acc[DB] = {};
+    auto fetch = [&](int k, float4(&v)[DB]) {
         const float *src = (k < ns ? j.shared.o : j.rest.o) + at(k) * D;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < DB; ++e)
             if (128 * e + 4 * lane < D) v[e] = *reinterpret_cast<const float4 *>(src + 128 * e + 4 * lane);
     };
     for (int k0 = w; k0 < n; k0 += W * 32) {
         const int mine = k0 + W * lane, many = min(32, (n - k0 + W - 1) / W);
         const float2 ml = mine < n ? stats(mine) : make_float2(-INFINITY, 0.0f);
-        float4 o[AHEAD][2];
+        float4 o[AHEAD][DB];
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             if (i < many) fetch(k0 + W * i, o[i]);
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
         sum = fmaf(sum, back, part);
         if (k0 > w) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) acc[e].x *= back, acc[e].y *= back, acc[e].z *= back, acc[e].w *= back;
+            for (int e = 0; e < DB; ++e) acc[e].x *= back, acc[e].y *= back, acc[e].z *= back, acc[e].w *= back;
         }
         for (int i0 = 0; i0 < many; i0 += AHEAD) {
 #pragma unroll
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
                 if (i0 + i >= many) break;
                 const float x = __shfl_sync(~0u, f, i0 + i);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < DB; ++e) {
                     acc[e].x = fmaf(x, o[i][e].x, acc[e].x);
                     acc[e].y = fmaf(x, o[i][e].y, acc[e].y);
                     acc[e].z = fmaf(x, o[i][e].z, acc[e].z);
@@ -127,19 +127,20 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
     }
     if constexpr (W > 1) {
         if (lane == 0) ml_s[w] = make_float2(top, sum);
-        o_s[w][lane] = acc[0];
-        o_s[w][lane + 32] = acc[1];
+#pragma unroll
+        for (int e = 0; e < DB; ++e) o_s[w][lane + 32 * e] = acc[e];
         __syncthreads();
         if (w) return;
         top = -INFINITY;
         for (int i = 0; i < W; ++i) top = fmaxf(top, ml_s[i].x);
         sum = 0.0f;
-        acc[0] = acc[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int e = 0; e < DB; ++e) acc[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int i = 0; i < W; ++i) {
             const float x = ml_s[i].x == -INFINITY ? 0.0f : exp2f(ml_s[i].x - top);
             sum = fmaf(x, ml_s[i].y, sum);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < DB; ++e) {
                 const float4 v = o_s[i][lane + 32 * e];
                 acc[e].x = fmaf(x, v.x, acc[e].x);
                 acc[e].y = fmaf(x, v.y, acc[e].y);
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
     }
     const long long to = (long long)token * a.x.out_row_stride + (long long)head * a.x.out_head_stride;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < DB; ++e) {
         const int d = 128 * e + 4 * lane;
         if (d >= D) break;
         const float v[4] = {acc[e].x, acc[e].y, acc[e].z, acc[e].w};
@@ -164,16 +165,18 @@ __global__ void __launch_bounds__(JOIN_THREADS) prefix_join_kernel(const __grid_
     }
 }
 
+template <int DT, int W>
+cudaError_t join(const JoinArgs &j, int64_t rows, void *stream) {
+    constexpr int PER = JOIN_THREADS / 32 / W;
+    auto *kern = j.a.c.head_dim <= 128 ? prefix_join_kernel<DT, W, 1> : prefix_join_kernel<DT, W, 2>;
+    return bq::launch_pdl(kern, dim3((unsigned)((rows + PER - 1) / PER)), JOIN_THREADS, 0, stream, 1, j);
+}
 template <int DT>
 cudaError_t join(const JoinArgs &j, void *stream) {
     const int64_t rows = (int64_t)j.a.x.requests * j.a.x.rows * j.a.x.heads;
-    const int chunks = j.shared.max_chunks + j.rest.max_chunks;
-    constexpr int WARPS = JOIN_THREADS / 32;
     // a warp per row where there are rows enough and few partial results of each
-    if (rows >= 2048 && chunks <= 32)
-        return bq::launch_pdl(prefix_join_kernel<DT, 1>, dim3((unsigned)((rows + WARPS - 1) / WARPS)), JOIN_THREADS, 0,
-                              stream, 1, j);
-    return bq::launch_pdl(prefix_join_kernel<DT, WARPS>, dim3((unsigned)rows), JOIN_THREADS, 0, stream, 1, j);
+    return rows >= 2048 && j.shared.max_chunks + j.rest.max_chunks <= 32 ? join<DT, 1>(j, rows, stream)
+                                                                         : join<DT, 8>(j, rows, stream);
 }
 
 // one pass of the attention kernel: its arguments, instance and partial results

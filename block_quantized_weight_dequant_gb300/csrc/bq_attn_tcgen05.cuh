@@ -83,7 +83,7 @@ struct TcArgs {
 
 // shared memory behind the ring
 struct TcMisc {
-    uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2], q_full, added, o_full;
+    uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2][2], q_full, added, o_full;
     uint64_t ref_full[2][4];     // by stream and warp of it
     alignas(16) uint8_t mask[TC_MASKS][16];  // positions of a tile that are there
     float ref[2][TC_ROWS];       // a row's reference after the stream's last tile
@@ -112,6 +112,18 @@ __device__ __forceinline__ bool barrier_try(uint64_t *b, uint32_t parity) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(tc_shared(b)), "r"(parity)
+        : "memory");
+    return ok;
+}
+// the same without waiting a while for it
+__device__ __forceinline__ uint32_t barrier_test(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.b32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(tc_shared(b)), "r"(parity)
@@ -336,7 +348,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], copying);
         for (int i = 0; i < 2; ++i) {
             barrier_init(&misc.s_full[i], 1);
-            barrier_init(&misc.p_full[i], TC_SOFTMAX_WARPS / 2);
+            for (int k = 0; k < 2; ++k) barrier_init(&misc.p_full[i][k], TC_SOFTMAX_WARPS / 2);
             for (int k = 0; k < 4; ++k) barrier_init(&misc.ref_full[i][k], 1);
         }
         barrier_init(&misc.q_full, TC_SOFTMAX_WARPS);
@@ -509,57 +521,84 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         const uint64_t q_m = tc_matrix(tc_shared(q_s)), ring_m = tc_matrix(tc_shared(ring));
         const int steps = D16 / 16;
         bool ok = barrier_wait(&misc.q_full, 0, dead);
-        auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first
-            const int n = 2 * t, slot = n % SLOTS;
-            ok = ok && barrier_wait(&misc.full[slot], n / SLOTS & 1, dead);
-            ok = __all_sync(~0u, ok);
-            if (!ok) return;
-            tc_fence_after();
-            const uint64_t k_m = ring_m + slot * (S::SLOT >> 4);
-            const uint32_t d = tmem + (t & 1) * 128;
-            if (elect_one()) {
-#pragma unroll
-                for (int p = QP - 1; p >= 0; --p)
-#pragma unroll
-                    for (int k = 0; k < 4 * NB; ++k) {
-                        if (k >= steps) break;
-                        const uint64_t at = (k >> 2) * (TC_BLOCK >> 4) + (k & 3) * 2;
-                        const bool add = p < QP - 1 || k;
-                        if constexpr (S::Q_TENSOR)
-                            tc_product_tensor(d, tmem + TC_Q + p * NB * 32 + 8 * k, k_m + at, qk_shape, add);
-                        else
-                            tc_product_shared(d, q_m + p * (NB * TC_BLOCK >> 4) + at, k_m + at, qk_shape, add);
-                    }
-                tc_commit(&misc.empty[slot]);
-                tc_commit(&misc.s_full[t & 1]);
-            }
-            __syncwarp();
+        // load n = 2 t of K, 2 t + 1 of V: in slot n % SLOTS, counted along
+        int k_slot = 0, v_slot = 1;
+        uint32_t k_phase = 0, v_phase = 0;
+        auto next = [](int &slot, uint32_t &phase) {
+            slot += 2;
+            if (slot >= SLOTS) slot -= SLOTS, phase ^= 1;
         };
-        scores(0);
-        if (tiles > 1) scores(1);
-        for (int t = 0; t < tiles && ok; ++t) {
-            const int n = 2 * t + 1, slot = n % SLOTS, s = t & 1;
-            ok = barrier_wait(&misc.full[slot], n / SLOTS & 1, dead) && barrier_wait(&misc.p_full[s], t >> 1 & 1, dead);
+        auto waits = [&](uint64_t *b, uint32_t phase) {
+            ok = ok && barrier_wait(b, phase, dead);
             ok = __all_sync(~0u, ok);
+        };
+        auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first; by the elected thread
+            const uint64_t k_m = ring_m + k_slot * (S::SLOT >> 4);
+            const uint32_t d = tmem + (t & 1) * 128;
+#pragma unroll
+            for (int p = QP - 1; p >= 0; --p)
+#pragma unroll
+                for (int k = 0; k < 4 * NB; ++k) {
+                    if (k >= steps) break;
+                    const uint64_t at = (k >> 2) * (TC_BLOCK >> 4) + (k & 3) * 2;
+                    const bool add = p < QP - 1 || k;
+                    if constexpr (S::Q_TENSOR)
+                        tc_product_tensor(d, tmem + TC_Q + p * NB * 32 + 8 * k, k_m + at, qk_shape, add);
+                    else
+                        tc_product_shared(d, q_m + p * (NB * TC_BLOCK >> 4) + at, k_m + at, qk_shape, add);
+                }
+            tc_commit(&misc.empty[k_slot]);
+            tc_commit(&misc.s_full[t & 1]);
+        };
+        for (int t = 0; t < 2 && t < tiles && ok; ++t) {
+            waits(&misc.full[k_slot], k_phase);
             if (!ok) break;
             tc_fence_after();
-            const uint64_t v_m = ring_m + slot * (S::SLOT >> 4);
-            const uint32_t o = tmem + TC_O, w = tmem + s * 128;
+            if (elect_one()) scores(t);
+            __syncwarp();
+            next(k_slot, k_phase);
+        }
+        const uint32_t o = tmem + TC_O;
+        // half of tile t's positions, 16 a step: 8 columns of a weight part; 32 columns
+        // hold both parts of 32 positions
+        auto output = [&](int t, int half) {
+            const uint64_t v_m = ring_m + v_slot * (S::SLOT >> 4);
+            const uint32_t w = tmem + (t & 1) * 128;
+#pragma unroll
+            for (int k = 4 * half; k < 4 * half + 4; ++k)
+#pragma unroll
+                for (int p = 1; p >= 0; --p)
+                    tc_product_tensor(o, w + 32 * (k >> 1) + 16 * p + 8 * (k & 1), v_m + k * (2048 >> 4), pv_shape,
+                                      k || p == 0 || t > 0);
+        };
+        for (int t = 0; t < tiles && ok; ++t) {
+            const int s = t & 1;
+            const bool more = t + 2 < tiles;
+            uint64_t *keys = more ? &misc.full[k_slot] : &misc.full[v_slot];
+            const uint32_t keys_phase = more ? k_phase : v_phase;
+            const uint32_t there = barrier_test(&misc.full[v_slot], v_phase) & barrier_test(keys, keys_phase) &
+                                   barrier_test(&misc.p_full[s][0], t >> 1 & 1);
+            if (!__all_sync(~0u, there)) {
+                waits(&misc.full[v_slot], v_phase);
+                waits(keys, keys_phase);
+                waits(&misc.p_full[s][0], t >> 1 & 1);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) output(t, 0);
+            __syncwarp();
+            if (!__all_sync(~0u, barrier_test(&misc.p_full[s][1], t >> 1 & 1))) waits(&misc.p_full[s][1], t >> 1 & 1);
+            if (!ok) break;
+            tc_fence_after();
             if (elect_one()) {
-                // 16 positions a step: 8 columns of a weight part; 32 columns hold both
-                // parts of 32 positions
-                tc_product_tensor(o, w + 16, v_m, pv_shape, t > 0);
-                tc_product_tensor(o, w, v_m, pv_shape, true);
-#pragma unroll
-                for (int k = 1; k < TC_TILE / 16; ++k)
-#pragma unroll
-                    for (int p = 1; p >= 0; --p)
-                        tc_product_tensor(o, w + 32 * (k >> 1) + 16 * p + 8 * (k & 1), v_m + k * (2048 >> 4), pv_shape, true);
-                tc_commit(&misc.empty[slot]);
+                output(t, 1);
+                tc_commit(&misc.empty[v_slot]);
                 tc_commit(&misc.added);
+                if (more) scores(t + 2);
             }
             __syncwarp();
-            if (t + 2 < tiles) scores(t + 2);
+            next(v_slot, v_phase);
+            next(k_slot, k_phase);
         }
         // the end of all products; nothing is in flight when the tensor memory is given back
         if (elect_one()) tc_commit(&misc.o_full);
@@ -754,7 +793,13 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             const float shift = (HALF ? (float)TC_SHIFT_F16 : 0.0f) - (ref == -INFINITY ? 0.0f : ref);
             const uint64_t factors = pair_of(factor, factor), shifts = pair_of(shift, shift);
             uint64_t sum[2] = {0, 0};
-            auto weights = [&](const uint32_t(&y)[32], uint32_t at) {
+            auto told = [&](int half) {  // half of the weights are in tensor memory
+                tc_wait_store();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(&misc.p_full[s][half]);
+            };
+            auto weights = [&](const uint32_t(&y)[32], int c) {
                 uint32_t w[32];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
@@ -764,23 +809,21 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     sum[k / 2 & 1] = pair_add(sum[k / 2 & 1], p);
                     pair_parts<HALF>(p, w[k / 2], w[16 + k / 2]);
                 }
-                tc_store32(at, w);
+                if (c == 2) told(0);  // (its store has had this chunk's time)
+                tc_store32(s_at + 32 * c, w);
             };
 #pragma unroll 1
-            for (int c = 0; c < 128; c += 64) {  // (unrolled, the code outgrows the instruction cache)
+            for (int c = 0; c < 4; c += 2) {  // (unrolled, the code outgrows the instruction cache)
                 tc_wait_load();
-                tc_load32(s_at + c + 32, x[1]);
-                weights(x[0], s_at + c);
+                tc_load32(s_at + 32 * c + 32, x[1]);
+                weights(x[0], c);
                 tc_wait_load();
                 if (c == 0) tc_load32(s_at + 64, x[0]);
-                weights(x[1], s_at + c + 32);
+                weights(x[1], c + 1);
             }
+            told(1);
             const float2 l2 = pair_values(pair_add(sum[0], sum[1]));
             l += l2.x + l2.y;
-            tc_wait_store();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) barrier_arrive(&misc.p_full[s]);
         }
 
         // ---- the partial results, through the ring's place: nothing reads or fills it once
