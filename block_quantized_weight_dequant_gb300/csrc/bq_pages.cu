@@ -24,7 +24,7 @@ namespace {
 BQ_STATUS_WORD(pages)
 
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
-constexpr int CLUSTER = 8;  // CTAs
+constexpr int CLUSTER = 8, CLUSTER_MOST = 16;  // CTAs
 constexpr int CLAIM = -0x7fffffff - 1;  // count of a page that is given back: CLAIM + its first release
 
 struct ShareArgs {
@@ -367,6 +367,8 @@ struct CompactArgs {
 
 __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant__ CompactArgs a) {
     __shared__ long long scratch[1][WARPS];
+    constexpr int KEPT = 64;
+    __shared__ uint32_t words[WARPS][KEPT];
     __shared__ long long s_live, s_moves;  // pages in use in this CTA's part; moves, in the CTA that meets them
     bq::pdl_wait();
     bq::pdl_launch_dependents();
@@ -378,10 +380,30 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
     const long long warps = (long long)cluster * WARPS;
     const long long run = (pool + warps * 32 - 1) / (warps * 32) * 32;
     const long long p0 = min(pool, (rank * WARPS + warp) * run), p1 = min(pool, p0 + run);
+    // which of its pages are in use, a word for 32 of them, if there is room for all
+    const bool kept = run <= 32 * KEPT;
+    constexpr int READS = 8;  // in flight
+    auto look = [&](long long q0, auto tell) {  // the run's words from page q0 on, READS of them
+        bool live[READS];
+#pragma unroll
+        for (int k = 0; k < READS; ++k) {
+            const long long p = q0 + 32 * k + lane;
+            live[k] = p < p1 && refs[p] > 0;
+        }
+#pragma unroll
+        for (int k = 0; k < READS; ++k) tell(k, __ballot_sync(~0u, live[k]));
+    };
     long long v[1] = {0}, total[1];
-#pragma unroll 8
-    for (long long p = p0 + lane; p < p1; p += 32) v[0] += refs[p] > 0;
-    scan_threads<1>(v, total, scratch);  // pages in use before each thread's, of the warp's in any order:
+    for (long long q0 = p0; q0 < p1; q0 += 32 * READS)
+        look(q0, [&](int k, uint32_t bits) {
+            if (lane == 0) {
+                v[0] += __popc(bits);
+                const long long at = (q0 - p0) / 32 + k;
+                if (kept && at < KEPT) words[warp][at] = bits;
+            }
+        });
+    __syncwarp();
+    scan_threads<1>(v, total, scratch);  // pages in use before each warp's, from its first thread
     long long before = __shfl_sync(~0u, v[0], 0);  // right for lane 0
     if (tid == 0) s_live = total[0], s_moves = -1;
     cluster_barrier();
@@ -403,23 +425,12 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
     long long moves = 0;
     for (uint32_t k = 0; k < cluster; ++k) moves = max(moves, peer_word(&s_moves, k));
     const long long room = a.c.max_moves, done = min(moves, room);
-    constexpr int READS = 8;  // in flight
-    int held[READS];
-    for (long long q0 = p0; q0 < p1; q0 += 32) {
+    auto place = [&](long long q0, uint32_t bits) {  // 32 pages
         const long long p = q0 + lane;
-        const int turn = (int)((q0 - p0) / 32 % READS);
-        if (turn == 0) {
-#pragma unroll
-            for (int k = 0; k < READS; ++k) held[k] = p + 32 * k < p1 ? refs[p + 32 * k] : 0;
-        }
-        int now = held[0];
-#pragma unroll
-        for (int k = 1; k < READS; ++k) now = turn == k ? held[k] : now;
-        const bool in = p < p1, live = in && now > 0;
-        const uint32_t bits = __ballot_sync(~0u, live);
+        const bool in = p < p1, live = bits >> lane & 1;
         const long long below = before + __popc(bits & ((1u << lane) - 1));  // pages in use below p
         before += __popc(bits);
-        if (!in) continue;
+        if (!in) return;
         a.c.moved[p] = (int)p;
         const long long above = many - below - live;  // pages in use above p
         if (p >= many) {
@@ -431,6 +442,12 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
             if (rank_of < done) a.c.copy_dst[rank_of] = (int)p;
             else a.c.free_pages[pool - many - (moves - done) + moves - 1 - rank_of] = (int)p;
         }
+    };
+    if (kept) {
+        for (long long q0 = p0; q0 < p1; q0 += 32) place(q0, words[warp][(q0 - p0) / 32]);
+    } else {
+        for (long long q0 = p0; q0 < p1; q0 += 32 * READS)
+            look(q0, [&](int k, uint32_t bits) { place(q0 + 32 * k, bits); });
     }
     for (long long i = done + rank * THREADS + tid; i < room; i += (long long)cluster * THREADS)
         a.c.copy_src[i] = a.c.copy_dst[i] = -1;
@@ -574,6 +591,35 @@ Plane plane_of(const bq_kv_cache &c, int bytes, int per, int widest) {
     return p;
 }
 
+// CTAs of a cluster for much work: 16 where the device takes such a cluster with
+// this much shared memory (the atomics of a step's forks and the reads of a large
+// pool are shared out among twice the SMs), else 8
+template <class K>
+int largest_cluster(K *kern, size_t smem) {
+    static std::atomic<int> known[64];  // per device: 0 not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CLUSTER;
+    int n = known[dev].load();
+    if (n) return n;
+    n = CLUSTER;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CLUSTER_MOST);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CLUSTER_MOST, attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+        cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) == cudaSuccess && fit > 0)
+        n = CLUSTER_MOST;
+    cudaGetLastError();
+    known[dev].store(n);
+    return n;
+}
+
 }  // namespace
 
 int bq_internal_status_pages(unsigned int *flags, int clear) { return read_status_pages(flags, clear); }
@@ -593,13 +639,16 @@ extern "C" bq_status bq_kv_shared_tables(const bq_kv_tables *t, const bq_kv_shar
     const bool with_rows = t->max_tokens <= bq::TABLES_ROWS_ALONE;
     // one CTA for a step that cannot move much, however it turns out
     const long long work = (with_rows ? t->max_tokens : 0) + (long long)t->requests * t->table_width;
-    const int cluster = work > 16LL * THREADS ? CLUSTER : 1;
     const size_t smem = (size_t)(9 * t->requests + 5) * sizeof(int);
+    constexpr int SMEM_MOST = (int)((9 * bq::TABLES_MAX_REQUESTS + 5) * sizeof(int));
     if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   (int)((9 * bq::TABLES_MAX_REQUESTS + 5) * sizeof(int)));
+        const cudaError_t e = cudaFuncSetAttribute(share_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST);
         if (e != cudaSuccess) return bq::from_cuda_error(e);
     }
+    // (asked with what every call of up to 1000 requests needs; more take 8 CTAs)
+    const int cluster = work <= 16LL * THREADS                ? 1
+                        : work <= 256LL * THREADS || smem > 40 * 1024 ? CLUSTER
+                                                              : largest_cluster(share_kernel, 40 * 1024);
     const cudaError_t e = bq::launch_pdl(share_kernel, dim3((unsigned)cluster), THREADS, smem, stream, cluster, a,
                                          (int)with_rows);
     if (e != cudaSuccess || with_rows) return bq::from_cuda_error(e);
@@ -622,7 +671,7 @@ extern "C" bq_status bq_kv_compact(const bq_kv_compact_args *c, void *stream) {
     CompactArgs a;
     a.c = *c;
     a.page.set((uint32_t)c->page_size);
-    const int cluster = c->pool > 4 * THREADS ? CLUSTER : 1;
+    const int cluster = c->pool <= 4 * THREADS ? 1 : c->pool <= 32 * THREADS ? CLUSTER : largest_cluster(compact_kernel, 0);
     cudaError_t e = bq::launch_pdl(compact_kernel, dim3((unsigned)cluster), THREADS, 0, stream, cluster, a);
     if (e != cudaSuccess || c->requests == 0) return bq::from_cuda_error(e);
     const int across = (c->table_width + RENUMBER_THREADS * 4 - 1) / (RENUMBER_THREADS * 4);
