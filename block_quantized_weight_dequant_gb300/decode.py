@@ -37,7 +37,7 @@ the residual stream.
 import torch
 
 from . import StreamOp, StreamPlan, gemv, gemv_gate_up_silu, gemv_qkv_bias, gemv_verify
-from .cache import kv_append, paged_attention, sandwich_norm
+from .cache import kv_append, paged_attention, paged_prefix_attention, sandwich_norm
 
 
 class DecodeStream:
@@ -234,12 +234,14 @@ class PagedDecode:
         sandwich_norm(self._y, self.h, pre_gain=gain, post_gain=post, gate=gate, alpha=self.alpha, beta=self.beta,
                       eps=self.eps, h_out=self.h, x_out=self._x)
 
-    def step(self, h, slots, positions, table, lens):
+    def step(self, h, slots, positions, table, lens, shared=None):
         """One step: h fp32 [rows, hidden] the tokens' embeddings; slots int64
         [rows] and positions int32 ([rows], or [axes, rows]) of the new tokens, as
         kv_block_tables gives them; table, lens: the requests' tables and lengths,
-        the new tokens counted (rows / requests tokens each).  Returns logits
-        [rows, vocab], a buffer of this object."""
+        the new tokens counted (rows / requests tokens each).  shared: the positions
+        that the requests share, or groups of them, as for paged_prefix_attention
+        (their pages are then read once for all of them).  Returns logits [rows,
+        vocab], a buffer of this object."""
         requests = lens.numel()
         if requests < 1 or self.rows % requests:
             raise ValueError(f"{self.rows} rows do not share out among {requests} requests")
@@ -262,7 +264,10 @@ class PagedDecode:
             kv_append(self.caches[l], self._k, self._v, slots, q=self._q, q_out=self._turned, rope=rope,
                       positions=None if rope is None else positions, q_norm=L.get("q_norm"), k_norm=L.get("k_norm"),
                       eps=self.eps)
-            paged_attention(self.caches[l], self._turned, table, lens, rows=each, out=self._a)
+            if shared is None:
+                paged_attention(self.caches[l], self._turned, table, lens, rows=each, out=self._a)
+            else:
+                paged_prefix_attention(self.caches[l], self._turned, table, lens, shared, rows=each, out=self._a)
             self._product(L["o"], self._a.view(self.rows, -1), self._y)
             self._between(L["gamma"], L.get("attn_post"), L.get("attn_gate"))
             for r in range(self.rows):

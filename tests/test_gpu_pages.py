@@ -1,6 +1,8 @@
 """Pages that requests share: steps with forks against a plain form, copies in all
 layers, compaction, and a server's life of them together, whose requests must read
 back their own tokens."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -336,6 +338,42 @@ def test_a_server_of_forks_reads_back_its_tokens(kind):
     same()
     step([0] * n)
     assert int(t.free_count) == pool and (t.refs == 0).all()
+
+
+@pytest.mark.parametrize("limit", [0, -1])
+def test_a_decode_of_forks_over_their_shared_prefix(limit):
+    """A prompt, three forks of it and steps of all four with the prefix given: the
+    logits of steps that know nothing of it."""
+    from block_quantized_weight_dequant_gb300 import _lib, workloads as wl
+    from test_gpu_paged_decode import HIDDEN, decoder
+
+    hook = _lib.lib.bq_internal_prefix_whole_limit
+    hook.restype, hook.argtypes = ctypes.c_int64, [ctypes.c_int64]
+    h = wl.normal_torch((48, HIDDEN), 1.0, seed=3, stream=14, device=DEV)
+    out = []
+    for shared in (None, 20):
+        one, four = decoder("q8_0", "f16"), decoder("q8_0", "f16", rows=4)
+        four.caches = one.caches
+        t = bq.SharedBlockTables(4, 8, 12, 16, 8, one.caches)
+        for i in range(20):
+            t.resize(cuda([i + 1, 0, 0, 0]))
+            one.step(h[i:i + 1], t.slots[:1], t.positions[:1], t.table[:1], t.lens[:1])
+        hook(limit)
+        try:
+            for i in range(7):
+                parents = cuda([-1, 0, 0, 0]) if i == 0 else None
+                assert int(t.resize(cuda([21 + i] * 4), parents)) == 0
+                rows = h[20 + 4 * i:24 + 4 * i]
+                out.append(four.step(rows, t.slots[:4], t.positions[:4], t.table, t.lens, shared=shared).clone())
+        finally:
+            hook(-1)
+    a, b = torch.stack(out[:7]), torch.stack(out[7:])
+    if limit:  # so little is read again that the ordinary kernel serves the call: the same bits
+        assert torch.equal(a, b)
+    # else the attention outputs differ in the last bits of fp32 (2^-13 of them at most) and
+    # keys or values next to a rounding border of the fp16 cache by 2^-11: as in the decoder's
+    # own test that moves a logit by less than 2^-12 * 16 of their rms
+    assert float((a - b).abs().max()) <= 2.0 ** -12 * 16 * float(a.square().mean().sqrt())
 
 
 def test_captured_steps():
