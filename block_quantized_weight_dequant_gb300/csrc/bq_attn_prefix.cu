@@ -50,9 +50,9 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) prefix_join_kernel(const __gr
     const bq::AttnArgs &a = j.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = W > 1 ? warp : 0;
     const int D = a.c.head_dim, R = a.x.rows, KVH = a.c.kv_heads, G = (int)a.group.d;
-    const long long index = (long long)blockIdx.x * ROWS + (W > 1 ? 0 : warp);
+    const int index = (int)blockIdx.x * ROWS + (W > 1 ? 0 : warp);  // (rows and heads are below 2^27)
     bq::pdl_wait();
-    const int token = (int)(index / a.x.heads), head = (int)(index - (long long)token * a.x.heads);
+    const int token = index / a.x.heads, head = index - token * a.x.heads;
     const int b = token / R, row = token - b * R;
     if (b >= a.x.requests) return;  // (W > 1: there is no such row)
     const int h = head / G, in_group = head - h * G;
@@ -65,25 +65,26 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) prefix_join_kernel(const __gr
     const int ns = sees && common ? bq::attn_chunks(common, j.shared.chunk) : 0;
     const int n = ns + (sees ? bq::attn_chunks(bq::attn_rest(len, R, common), j.rest.chunk) : 0);
     const int si = ((b - first) * R + row) * G + in_group, ri = row * G + in_group;
-    // where partial result k lies, in rows
-    auto at = [&](int k) {
-        const Parts &p = k < ns ? j.shared : j.rest;
-        const int c = k < ns ? k : k - ns, of = k < ns ? g : b, i = k < ns ? si : ri;
+    // where the partial results of each pass lie, in rows: the first and the distance
+    auto first_of = [&](const Parts &p, int of, int i) {
         const int t = i / p.tile_rows;
-        const long long unit = (((long long)of * p.max_chunks + c) * KVH + h) * p.row_tiles + t;
-        return unit * p.tile_rows + (i - t * p.tile_rows);
+        return (((long long)of * p.max_chunks * KVH + h) * p.row_tiles + t) * p.tile_rows + (i - t * p.tile_rows);
     };
-    auto stats = [&](int k) { return (k < ns ? j.shared.ml : j.rest.ml)[at(k)]; };
+    const long long s0 = first_of(j.shared, g, si), sn = (long long)KVH * j.shared.row_tiles * j.shared.tile_rows;
+    const long long r0 = first_of(j.rest, b, ri), rn = (long long)KVH * j.rest.row_tiles * j.rest.tile_rows;
+    const float *s_o = j.shared.o + s0 * D + 4 * lane, *r_o = j.rest.o + r0 * D + 4 * lane;
+    const long long s_hop = sn * D, r_hop = rn * D;
+    auto stats = [&](int k) { return k < ns ? j.shared.ml[s0 + k * sn] : j.rest.ml[r0 + (k - ns) * rn]; };
     // AHEAD partial results are on their way while the weights of up to 32 are found;
     // with more, those come 32 at a time, with a running maximum
-    constexpr int AHEAD = 8 / DB;
+    constexpr int AHEAD = 4;
     float top = -INFINITY, sum = 0.0f;
     float4 acc[DB] = {};
     auto fetch = [&](int k, float4(&v)[DB]) {
-        const float *src = (k < ns ? j.shared.o : j.rest.o) + at(k) * D;
+        const float *src = k < ns ? s_o + k * s_hop : r_o + (k - ns) * r_hop;
 #pragma unroll
         for (int e = 0; e < DB; ++e)
-            if (128 * e + 4 * lane < D) v[e] = *reinterpret_cast<const float4 *>(src + 128 * e + 4 * lane);
+            if (128 * e + 4 * lane < D) v[e] = *reinterpret_cast<const float4 *>(src + 128 * e);
     };
     for (int k0 = w; k0 < n; k0 += W * 32) {
         const int mine = k0 + W * lane, many = min(32, (n - k0 + W - 1) / W);
