@@ -40,31 +40,39 @@
 
 namespace bq {
 
-constexpr int TC_ROWS = 128, TC_TILE = 128;
+constexpr int TC_ROWS = 128;
 constexpr int TC_SOFTMAX_WARPS = 8, TC_COPY_WARPS = 3, TC_WARPS = 12;
 constexpr int TC_MASKS = 8;        // tiles whose masks are kept
-constexpr int TC_BLOCK = 128 * 128;  // bytes of 128 rows of 64 values
+constexpr int TC_QBLOCK = TC_ROWS * 128;  // bytes of all rows' 64 values
 // columns of tensor memory, all of it: scores of two streams, output, queries
 constexpr int TC_COLUMNS = 512, TC_O = 256, TC_Q = 384;
 constexpr float TC_GROWTH = 8.0f;    // log2 of what a weight may be
 constexpr int TC_SHIFT_F16 = 7;      // fp16 weights carry 2^7: up to 2^15, two parts keep 2^-24
 
-template <int QP, int NB>
+template <int QP, int NB, bool Q8>
 struct TcShape {
+    // positions of a tile; bytes of its rows of 64 values; parts of a key or value
+    static constexpr int TILE = Q8 ? 64 : 128, BLOCK = TILE * 128, KP = Q8 ? 2 : 1;
     // queries as a first operand in tensor memory, where their parts fit beside the scores
     // of both streams and the output: the tensor cores then read K and V alone from
     // shared memory, whose 128 bytes a cycle bound the kernel otherwise
     static constexpr bool Q_TENSOR = QP * NB * 32 <= TC_COLUMNS - TC_Q;
-    static constexpr int SLOT = NB * TC_BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_BLOCK;
+    static constexpr int SLOT = KP * NB * BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_QBLOCK;
     static constexpr int LIMIT = 227 * 1024, MISC = 3072;
-    static constexpr int most = (LIMIT - MISC - Q_BYTES) / SLOT;
+    // Q8_0: codes and scales on their way, RAW tiles of them; a lane's 32 codes and a word
+    // with its scale, rows of a copying warp (MINE turns of it) beside one another
+    static constexpr int RAW = 3, LANES = 2 * NB, AT_ONCE = 32 / LANES, GROUPS = TILE / AT_ONCE;
+    static constexpr int MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;
+    static constexpr int RAW_WARP = 32 * (32 + 4), RAW_TILE = 2 * MINE * TC_COPY_WARPS * RAW_WARP;
+    static constexpr int RAW_BYTES = Q8 ? RAW * RAW_TILE : 0;
+    static constexpr int most = (LIMIT - MISC - Q_BYTES - RAW_BYTES) / SLOT;
     static constexpr int SLOTS = most > 8 ? 8 : most;
     // Loads that are issued before the oldest is waited for.  A tile's keys are told as
     // arrived once the LAG loads behind them are issued, which takes slots that are free
     // again: with 3 of 6 the next keys waited for the values two tiles before (DELTA),
     // above SLOTS - 2 for themselves.
     static constexpr int LAG = SLOTS >= 8 ? 3 : 1;
-    static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + MISC;
+    static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + RAW_BYTES + MISC;
     static constexpr int OROW = NB * 64 + 4;  // floats of a row on its way out, in the ring's place
     static_assert(SLOTS >= 4 && LAG >= 1 && LAG <= SLOTS - 2);
     static_assert(TC_ROWS * OROW * 4 <= SLOTS * SLOT);
@@ -85,6 +93,7 @@ struct TcArgs {
 struct TcMisc {
     uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2][2], q_full, added, o_full;
     uint64_t ref_full[2][4];     // by stream and warp of it
+    uint32_t top_scale[2];       // bits of the chunk's largest Q8_0 scales, of keys and values
     alignas(16) uint8_t mask[TC_MASKS][16];  // positions of a tile that are there
     float ref[2][TC_ROWS];       // a row's reference after the stream's last tile
     float sum[2][TC_ROWS];       // of its weights; the largest query values before
@@ -194,8 +203,8 @@ __device__ __forceinline__ void tc_store8(uint32_t at, const uint32_t (&v)[8]) {
 // A matrix in shared memory in rows of 128 bytes swizzled over 8 rows: its place,
 // the distance of 64-value blocks (where the rows are the summed axis) and of
 // groups of 8 rows
-__device__ __forceinline__ uint64_t tc_matrix(uint32_t at) {
-    return (uint64_t)(at >> 4 & 0x3fff) | (uint64_t)(TC_BLOCK >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+__device__ __forceinline__ uint64_t tc_matrix(uint32_t at, int block) {
+    return (uint64_t)(at >> 4 & 0x3fff) | (uint64_t)(block >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
            (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 __device__ __forceinline__ void tc_product_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add) {
@@ -211,6 +220,19 @@ __device__ __forceinline__ void tc_product_tensor(uint32_t d, uint32_t a, uint64
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(b), "r"(shape), "r"((uint32_t)add)
         : "memory");
+}
+__device__ __forceinline__ void tc_store16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Four int8 codes as two pairs of fp16: with b = code + 128 (the sign bit turned)
+// 0x6400 | b is 1024 + b, a whole number that fp16 holds; less 1152 it is the code.
+__device__ __forceinline__ uint2 tc_codes(uint32_t w) {
+    uint2 o;
+    w ^= 0x80808080u;
+    const uint32_t lo = __byte_perm(w, 0x64646464u, 0x4140), hi = __byte_perm(w, 0x64646464u, 0x4342);
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(o.x) : "r"(lo), "r"(0x64806480u));
+    asm("sub.f16x2 %0, %1, %2;" : "=r"(o.y) : "r"(hi), "r"(0x64806480u));
+    return o;
 }
 // true for one thread of the warp, the same each time
 __device__ __forceinline__ bool elect_one() {
@@ -240,6 +262,9 @@ __device__ __forceinline__ void tc_copy_box(uint32_t dst, const CUtensorMap *map
 __device__ __forceinline__ void barrier_arrive_bytes(uint64_t *b, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(tc_shared(b)), "r"(bytes)
                  : "memory");
+}
+__device__ __forceinline__ void tc_copy4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void tc_copies_wait() {
@@ -313,15 +338,16 @@ __device__ __forceinline__ uint32_t tc_part(float &x, float &y) {
     return w;
 }
 
-template <bool HALF, int QP, int NB>
+template <bool HALF, int QP, int NB, bool Q8>
 __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     prefix_kernel(const __grid_constant__ TcArgs args, unsigned int *status) {
-    using S = TcShape<QP, NB>;
+    using S = TcShape<QP, NB, Q8>;
+    constexpr int TILE = S::TILE, BLOCK = S::BLOCK;
     const AttnArgs &a = args.a;
     constexpr int SLOTS = S::SLOTS, LAG = S::LAG;
     extern __shared__ __align__(1024) uint8_t smem[];
     uint8_t *q_s = smem, *ring = smem + S::Q_BYTES;
-    TcMisc &misc = *reinterpret_cast<TcMisc *>(ring + SLOTS * S::SLOT);
+    TcMisc &misc = *reinterpret_cast<TcMisc *>(ring + SLOTS * S::SLOT + S::RAW_BYTES);
     volatile uint32_t *dead = &misc.dead;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.head_dim, R = a.x.rows, KVH = a.c.kv_heads, G = (int)a.group.d;
@@ -343,7 +369,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 
     // ---- barriers and tensor memory, while the kernel before ends ----
     if (tid == 0) {
-        const int copying = args.box ? 1 : TC_COPY_WARPS;
+        const int copying = !Q8 && args.box ? 1 : TC_COPY_WARPS;
         for (int i = 0; i < SLOTS; ++i) barrier_init(&misc.full[i], copying), barrier_init(&misc.empty[i], 1);
         for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], copying);
         for (int i = 0; i < 2; ++i) {
@@ -375,27 +401,195 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         if (min(a.x.lens[i], most) - R + 1 >= common) owner = i;
     owner = __reduce_min_sync(~0u, owner);
     // (without one nobody reads these partial results)
-    const int tiles = owner == 0x7fffffff ? 0 : (end - begin + TC_TILE - 1) / TC_TILE;
+    const int tiles = owner == 0x7fffffff ? 0 : (end - begin + TILE - 1) / TILE;
+    // Q8_0: keys and values go into two fp16 parts.  The chunk's largest scale brings the
+    // largest possible value to [2^14, 2^15): nothing overflows, and what is down to
+    // 2^-29 of it keeps a second part in fp16's range.
+    [[maybe_unused]] const int *row_table = a.x.table + (tiles ? owner : 0) * a.x.table_stride;
+    [[maybe_unused]] float by_keys = 1.0f, by_values = 1.0f;      // what the parts are to be multiplied by
+    [[maybe_unused]] float of_keys = 1.0f, of_values = 1.0f;      // and were
+    // element offset of position p, -1 where there is nothing to read
+    [[maybe_unused]] auto offset_of = [&](int p, int entry) {
+        if (entry < 0 || entry >= a.c.pages) return -1ll;
+        const uint32_t in_page = (uint32_t)p - a.page.div((uint32_t)p) * a.page.d;
+        return (long long)(entry * a.c.page_stride + in_page * a.c.slot_stride + (long long)h * a.c.head_stride);
+    };
+    if constexpr (Q8) {
+        if (tid < 2) misc.top_scale[tid] = 0;
+        __syncthreads();
+        uint32_t top[2] = {0, 0};
+        const int blocks = D >> 5, many = tiles ? (end - begin) * blocks : 0;
+#pragma unroll 4
+        for (int i = tid; i < many; i += TC_WARPS * 32) {
+            const int r = i / blocks, p = begin + r;
+            const long long off = offset_of(p, row_table[a.page.div((uint32_t)p)]);
+            if (off < 0) continue;
+            const long long at = (off >> 5) + (i - r * blocks);
+            const uint32_t k = static_cast<const uint16_t *>(a.c.k_scale)[at] & 0x7fffu;
+            const uint32_t v = static_cast<const uint16_t *>(a.c.v_scale)[at] & 0x7fffu;
+            if (k < 0x7c00u) top[0] = max(top[0], k);  // (the finite ones: ordered as their bits)
+            if (v < 0x7c00u) top[1] = max(top[1], v);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            top[k] = __reduce_max_sync(~0u, top[k]);
+            if (lane == 0) atomicMax(&misc.top_scale[k], top[k]);
+        }
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc.tmem;
+    if constexpr (Q8) {
+        auto power = [](uint32_t bits) {  // 127 scale 2^power is in [2^14, 2^15), or smaller
+            const float top = 127.0f * __half2float(__ushort_as_half((unsigned short)bits));
+            return top == 0.0f ? 0 : 14 - ((int)(__float_as_uint(top) >> 23) - 127);
+        };
+        const int pk = power(misc.top_scale[0]), pv = power(misc.top_scale[1]);
+        by_keys = ldexpf(1.0f, -pk), by_values = ldexpf(1.0f, -pv);
+        of_keys = ldexpf(1.0f, pk), of_values = ldexpf(1.0f, pv);
+    }
 
     if (tiles == 0) {
+    } else if (Q8 && warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
+        // ---- Q8_0: every third 8 (16) rows by each warp, a lane a scale's 32 codes; the next
+        // tile's are on their way while one is put into parts ----
+        if constexpr (Q8) {
+            constexpr int LANES = S::LANES, AT_ONCE = S::AT_ONCE, GROUPS = S::GROUPS, MINE = S::MINE, RAW = S::RAW;
+            const int cw = warp - TC_SOFTMAX_WARPS, part = lane % LANES, sub = lane / LANES;
+            const bool inside = 32 * part < D;
+            // the halves of the 32 codes in an order that keeps a warp's stores apart in the
+            // banks: lanes of another 64-value block take the other half first
+            const int turn = part >> 1 & 1;
+            uint8_t *raw = ring + SLOTS * S::SLOT + cw * S::RAW_WARP;
+            auto place = [&](int t, int v, int q) {
+                return raw + (t % RAW) * S::RAW_TILE + (v * MINE + q) * TC_COPY_WARPS * S::RAW_WARP;
+            };
+            auto row_of = [&](int q) { return (cw + TC_COPY_WARPS * q) * AT_ONCE + sub; };
+            auto entry_of = [&](int q, int t) {
+                const int p = begin + t * TILE + row_of(q);
+                return row_of(q) < TILE && t < tiles && p < end ? row_table[a.page.div((uint32_t)p)] : -1;
+            };
+            int entry[MINE];
+            uint32_t odd = 0;    // likewise: the scale is the second half of its word
+            uint32_t there = 0;  // bits of the rows that this lane looks up, MINE for each of 4 tiles
+            static_assert(4 * MINE <= 32 && RAW < 4);
+            auto ask = [&](int t) {  // tile t's codes and scales; zeros where there is nothing
+                const uint32_t of_tile = ~(((1u << MINE) - 1) << (t % 4 * MINE));
+                there &= of_tile, odd &= of_tile;
+#pragma unroll
+                for (int q = 0; q < MINE; ++q) {
+                    const int p = begin + t * TILE + row_of(q);
+                    const bool in = row_of(q) < TILE && t < tiles && p < end;
+                    const long long off = in ? offset_of(p, entry[q]) : -1;
+                    if (in && off < 0 && part == 0) atomicOr(status, BQ_DEVERR_PAGE);
+                    if (off >= 0) there |= 1u << (t % 4 * MINE + q);
+                    const bool has = off >= 0 && inside;
+                    const long long at = has ? off + 32 * part : 0;
+                    odd |= (uint32_t)(at >> 5 & 1) << (t % 4 * MINE + q);
+#pragma unroll
+                    for (int v = 0; v < 2; ++v) {
+                        const uint8_t *codes = static_cast<const uint8_t *>(v ? a.c.v : a.c.k) + at;
+                        const uint8_t *scale = static_cast<const uint8_t *>(v ? a.c.v_scale : a.c.k_scale) + (at >> 6) * 4;
+                        const uint32_t to = tc_shared(place(t, v, q));
+                        tc_copy16(to + 16 * lane, codes + 16 * turn, has);
+                        tc_copy16(to + 512 + 16 * lane, codes + 16 * (turn ^ 1), has);
+                        // (the word that holds the scale, or where the cache ends with it its half)
+                        tc_copy4(to + 1024 + 4 * lane, scale, !has ? 0 : (at >> 5 & 1) ? 4 : 2);
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+                for (int q = 0; q < MINE; ++q) entry[q] = entry_of(q, t + 1);
+            };
+            bool ok = true;
+#pragma unroll
+            for (int q = 0; q < MINE; ++q) entry[q] = entry_of(q, 0);
+#pragma unroll 1
+            for (int t = 0; t < RAW - 1; ++t) ask(t);
+            for (int t = 0; t < tiles && ok; ++t) {
+                ask(t + RAW - 1);
+                tc_copies_wait<RAW - 1>();  // (a lane reads what it has copied itself)
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    const int n = 2 * t + v, slot = n % SLOTS;
+                    ok = ok && barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    if (v == 0) {
+#pragma unroll
+                        for (int q = 0; q < MINE; ++q) {
+                            const uint32_t live = __ballot_sync(~0u, there >> (t % 4 * MINE + q) & 1);
+                            // a byte for 8 rows, a bit of it for each row's first lane
+                            uint32_t bits = 0;
+#pragma unroll
+                            for (int r = 0; r < AT_ONCE; ++r) bits |= (live >> (r * LANES) & 1) << r;
+                            if (lane < AT_ONCE / 8 && cw + TC_COPY_WARPS * q < GROUPS)
+                                misc.mask[t % TC_MASKS][(cw + TC_COPY_WARPS * q) * (AT_ONCE / 8) + lane] =
+                                    (uint8_t)(bits >> (8 * lane));
+                        }
+                        __syncwarp();
+                        if (lane == 0) barrier_arrive(&misc.mask_full[t % TC_MASKS]);
+                    }
+                    const uint32_t to = tc_shared(ring) + slot * S::SLOT + (part >> 1) * BLOCK;
+#pragma unroll
+                    for (int q = 0; q < MINE; ++q) {
+                        const int row = row_of(q);
+                        if (row >= TILE) continue;
+                        // (a power of two times an fp16 number; exact in fp32, and in fp16 unless so
+                        // small beside the chunk's largest that nothing of it is left)
+                        const uint8_t *from = place(t, v, q);
+                        const uint32_t both = *reinterpret_cast<const uint32_t *>(from + 1024 + 4 * lane);
+                        const float d = __half2float(__ushort_as_half((unsigned short)(both >> (16 * (odd >> (t % 4 * MINE + q) & 1))))) *
+                                        (v ? of_values : of_keys);
+                        const __half2 d2 = __float2half2_rn(d);
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const uint4 c = *reinterpret_cast<const uint4 *>(from + 512 * half + 16 * lane);
+                            const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+                            uint32_t high[8], low[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint2 f = tc_codes(word[i]);
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const uint32_t u = e ? f.y : f.x;
+                                    const __half2 x = *reinterpret_cast<const __half2 *>(&u);
+                                    const __half2 hi = __hmul2(x, d2);
+                                    const __half2 lo = __hfma2(x, d2, __hneg2(hi));
+                                    high[2 * i + e] = *reinterpret_cast<const uint32_t *>(&hi);
+                                    low[2 * i + e] = *reinterpret_cast<const uint32_t *>(&lo);
+                                }
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int piece = 4 * (part & 1) + 2 * (turn ^ half) + i;
+                                const uint32_t at = to + row * 128 + ((piece ^ (row & 7)) << 4);
+                                tc_store16(at, high[4 * i], high[4 * i + 1], high[4 * i + 2], high[4 * i + 3]);
+                                tc_store16(at + NB * BLOCK, low[4 * i], low[4 * i + 1], low[4 * i + 2], low[4 * i + 3]);
+                            }
+                        }
+                    }
+                    fence_async_proxy();
+                    __syncwarp();
+                    if (lane == 0) barrier_arrive(&misc.full[slot]);
+                }
+            }
+            tc_copies_wait<0>();
+        }
     } else if (warp == TC_SOFTMAX_WARPS && args.box) {
         // ---- copies by tensor maps: K and V of each tile in turn; lane j looks up the
         // tile's rows 8 j to 8 j + 7 (pages are whole groups of 8) ----
-        const int *row_table = a.x.table + owner * a.x.table_stride;
-        auto entry_of = [&](int t) { return lane < TC_TILE / 8 && t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
+        auto entry_of = [&](int t) { return lane < TILE / 8 && t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
         int entry = entry_of(begin + 8 * lane);
-        const bool starts = lane < TC_TILE / 8 && 8 * lane % args.box == 0;  // a box
+        const bool starts = lane < TILE / 8 && 8 * lane % args.box == 0;  // a box
         bool ok = true;
         for (int t = 0; t < tiles && ok; ++t) {
-            const int p = begin + t * TC_TILE + 8 * lane;
-            const bool in = lane < TC_TILE / 8 && p < end, live = in && entry >= 0 && entry < a.c.pages;
+            const int p = begin + t * TILE + 8 * lane;
+            const bool in = lane < TILE / 8 && p < end, live = in && entry >= 0 && entry < a.c.pages;
             if (in && !live) atomicOr(status, BQ_DEVERR_PAGE);
             const int from = live ? entry : (int)a.c.pages;  // (outside the tensor: zeros)
             const int slot_of = live ? p - (int)a.page.div((uint32_t)p) * page : 0;
-            entry = entry_of(p + TC_TILE);
+            entry = entry_of(p + TILE);
             for (int v = 0; v < 2; ++v) {
                 const int n = 2 * t + v, slot = n % SLOTS;
                 if (!barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead)) {
@@ -403,27 +597,26 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     break;
                 }
                 if (lane == 0) barrier_arrive_bytes(&misc.full[slot], S::SLOT);
-                if (v == 0 && lane < TC_TILE / 8) misc.mask[t % TC_MASKS][lane] = live ? 255 : 0;
+                if (v == 0 && lane < TILE / 8) misc.mask[t % TC_MASKS][lane] = live ? 255 : 0;
                 __syncwarp();
                 if (v == 0 && lane == 0) barrier_arrive(&misc.mask_full[t % TC_MASKS]);
                 if (starts) {
                     const uint32_t to = tc_shared(ring) + slot * S::SLOT + lane * 1024;
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        tc_copy_box(to + b * TC_BLOCK, v ? &args.v : &args.k, 64 * b, args.heads_first ? h : slot_of,
+                        tc_copy_box(to + b * BLOCK, v ? &args.v : &args.k, 64 * b, args.heads_first ? h : slot_of,
                                     args.heads_first ? slot_of : h, from, &misc.full[slot]);
                 }
             }
         }
     } else if (warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
         // ---- copies of 16 bytes (none where tensor maps do them): K and V of each tile in turn, every third 8 rows by each warp ----
-        constexpr int GROUPS = TC_TILE / 8, MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;  // of 8 rows
+        constexpr int GROUPS = TILE / 8, MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;  // of 8 rows
         const int cw = warp - TC_SOFTMAX_WARPS;
-        const int *row_table = a.x.table + owner * a.x.table_stride;
         const long long head_off = (long long)h * a.c.head_stride;
         // rows that this lane looks up: of this warp's groups 0 to 3, and of 4 and 5
         auto row_at = [&](int k) { return 8 * (cw + TC_COPY_WARPS * (4 * k + (lane >> 3))) + (lane & 7); };
-        auto entry_of = [&](int row, int t) { return row < TC_TILE && t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
+        auto entry_of = [&](int row, int t) { return row < TILE && t < end ? row_table[a.page.div((uint32_t)t)] : -1; };
         int entry[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) entry[k] = entry_of(row_at(k), begin + row_at(k));
@@ -434,7 +627,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         const bool in_line = page % 8 == 0;
         const long long hop = 2 * AT_ONCE * a.c.slot_stride;  // bytes from turn to turn
         const long long lane_at = 2 * sub * a.c.slot_stride + 16 * piece;
-        const uint32_t ring_at = tc_shared(ring) + (piece >> 3) * TC_BLOCK + sub * 128;
+        const uint32_t ring_at = tc_shared(ring) + (piece >> 3) * BLOCK + sub * 128;
         uint32_t turn_at[TURNS];  // a row's place in its group of 8, swizzled
 #pragma unroll
         for (int i = 0; i < TURNS; ++i)
@@ -449,9 +642,9 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             long long off[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const int p = begin + t * TC_TILE + row_at(k);
+                const int p = begin + t * TILE + row_at(k);
                 off[k] = -1;
-                if (row_at(k) < TC_TILE && p < end) {
+                if (row_at(k) < TILE && p < end) {
                     if (entry[k] >= 0 && entry[k] < a.c.pages) {
                         const uint32_t in_page = (uint32_t)p - a.page.div((uint32_t)p) * a.page.d;
                         off[k] = entry[k] * a.c.page_stride + in_page * a.c.slot_stride + head_off;
@@ -459,7 +652,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                         atomicOr(status, BQ_DEVERR_PAGE);
                     }
                 }
-                entry[k] = entry_of(row_at(k), p + TC_TILE);
+                entry[k] = entry_of(row_at(k), p + TILE);
             }
             uint32_t live[2];
 #pragma unroll
@@ -516,9 +709,9 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         // warp's, in uniform registers, and the steps unrolled: one thread that worked them
         // out in a loop took 97 cycles a step, of which the tensor cores need 64.) ----
         constexpr uint32_t SHAPE = 1u << 4 | (HALF ? 0u : 1u) << 7 | (HALF ? 0u : 1u) << 10 | (TC_ROWS >> 4) << 24;
-        constexpr uint32_t qk_shape = SHAPE | (TC_TILE >> 3) << 17;
+        constexpr uint32_t qk_shape = SHAPE | (TILE >> 3) << 17;
         const uint32_t pv_shape = SHAPE | 1u << 16 | (uint32_t)(D16 >> 3) << 17;
-        const uint64_t q_m = tc_matrix(tc_shared(q_s)), ring_m = tc_matrix(tc_shared(ring));
+        const uint64_t q_m = tc_matrix(tc_shared(q_s), TC_QBLOCK), ring_m = tc_matrix(tc_shared(ring), BLOCK);
         const int steps = D16 / 16;
         bool ok = barrier_wait(&misc.q_full, 0, dead);
         // load n = 2 t of K, 2 t + 1 of V: in slot n % SLOTS, counted along
@@ -535,18 +728,22 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first; by the elected thread
             const uint64_t k_m = ring_m + k_slot * (S::SLOT >> 4);
             const uint32_t d = tmem + (t & 1) * 128;
+            // (the product of two second parts is below what either leaves out)
 #pragma unroll
-            for (int p = QP - 1; p >= 0; --p)
+            for (int kp = S::KP - 1; kp >= 0; --kp)
 #pragma unroll
-                for (int k = 0; k < 4 * NB; ++k) {
-                    if (k >= steps) break;
-                    const uint64_t at = (k >> 2) * (TC_BLOCK >> 4) + (k & 3) * 2;
-                    const bool add = p < QP - 1 || k;
-                    if constexpr (S::Q_TENSOR)
-                        tc_product_tensor(d, tmem + TC_Q + p * NB * 32 + 8 * k, k_m + at, qk_shape, add);
-                    else
-                        tc_product_shared(d, q_m + p * (NB * TC_BLOCK >> 4) + at, k_m + at, qk_shape, add);
-                }
+                for (int p = kp ? 0 : QP - 1; p >= 0; --p)
+#pragma unroll
+                    for (int k = 0; k < 4 * NB; ++k) {
+                        if (k >= steps) break;
+                        const uint64_t keys = k_m + (kp * NB + (k >> 2)) * (BLOCK >> 4) + (k & 3) * 2;
+                        const bool add = kp < S::KP - 1 || p < (kp ? 0 : QP - 1) || k;
+                        if constexpr (S::Q_TENSOR)
+                            tc_product_tensor(d, tmem + TC_Q + p * NB * 32 + 8 * k, keys, qk_shape, add);
+                        else
+                            tc_product_shared(d, q_m + (p * NB + (k >> 2)) * (TC_QBLOCK >> 4) + (k & 3) * 2, keys, qk_shape,
+                                              add);
+                    }
             tc_commit(&misc.empty[k_slot]);
             tc_commit(&misc.s_full[t & 1]);
         };
@@ -564,12 +761,15 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         auto output = [&](int t, int half) {
             const uint64_t v_m = ring_m + v_slot * (S::SLOT >> 4);
             const uint32_t w = tmem + (t & 1) * 128;
+            constexpr int STEPS = TILE / 32;
 #pragma unroll
-            for (int k = 4 * half; k < 4 * half + 4; ++k)
-#pragma unroll
-                for (int p = 1; p >= 0; --p)
-                    tc_product_tensor(o, w + 32 * (k >> 1) + 16 * p + 8 * (k & 1), v_m + k * (2048 >> 4), pv_shape,
-                                      k || p == 0 || t > 0);
+            for (int k = STEPS * half; k < STEPS * half + STEPS; ++k) {
+                const uint32_t high = w + 32 * (k >> 1) + 8 * (k & 1);
+                const uint64_t values = v_m + k * (2048 >> 4);
+                tc_product_tensor(o, high + 16, values, pv_shape, k || t > 0);
+                if constexpr (Q8) tc_product_tensor(o, high, values + (NB * BLOCK >> 4), pv_shape, true);
+                tc_product_tensor(o, high, values, pv_shape, true);
+            }
         };
         for (int t = 0; t < tiles && ok; ++t) {
             const int s = t & 1;
@@ -636,7 +836,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             return Scaling{ldexpf(1.0f, up / 2), ldexpf(1.0f, up - up / 2),
                            size * ldexpf(1.0f, -(up / 2)) * ldexpf(1.0f, -(up - up / 2))};
         };
-        constexpr bool SCALED = HALF && QP > 1;
+        constexpr bool SCALED = HALF && (QP > 1 || Q8);
         float factor;
         if constexpr (S::Q_TENSOR) {
             // ---- queries into tensor memory, a row to a thread, half of its values to each
@@ -693,11 +893,11 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 for (int e = 0; e < 4; ++e) x[e] *= sign;
                 static_assert(!SCALED, "fp16 parts fit in tensor memory");
                 const int piece = (lane & 15) >> 1;
-                uint8_t *to = q_s + (lane >> 4) * TC_BLOCK + r * 128 + ((piece ^ (r & 7)) << 4) + 8 * (lane & 1);
+                uint8_t *to = q_s + (lane >> 4) * TC_QBLOCK + r * 128 + ((piece ^ (r & 7)) << 4) + 8 * (lane & 1);
 #pragma unroll
                 for (int p = 0; p < QP; ++p) {
                     const uint2 w = make_uint2(tc_part<HALF>(x[0], x[1]), tc_part<HALF>(x[2], x[3]));
-                    if (d < NB * 64) *reinterpret_cast<uint2 *>(to + p * NB * TC_BLOCK) = w;
+                    if (d < NB * 64) *reinterpret_cast<uint2 *>(to + p * NB * TC_QBLOCK) = w;
                 }
             }
             factor = size;
@@ -705,6 +905,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             __syncwarp();
             if (lane == 0) barrier_arrive(&misc.q_full);
         }
+        if constexpr (Q8) factor *= by_keys;
         // (above 0: what it multiplies may be minus infinity)
         factor = fmaxf(factor, 1.1754944e-38f);
 
@@ -720,12 +921,16 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 break;
             }
             tc_fence_after();
-            const uint4 m4 = *reinterpret_cast<const uint4 *>(misc.mask[t % TC_MASKS]);
-            const uint32_t mask[4] = {m4.x, m4.y, m4.z, m4.w};
-            if ((m4.x & m4.y & m4.z & m4.w) != ~0u) {  // positions that are not there: minus infinity
+            uint32_t mask[TILE / 32], all = ~0u;
+#pragma unroll
+            for (int c = 0; c < TILE / 32; ++c) {
+                mask[c] = reinterpret_cast<const uint32_t *>(misc.mask[t % TC_MASKS])[c];
+                all &= mask[c];
+            }
+            if (all != ~0u) {  // positions that are not there: minus infinity
 #pragma unroll 1
-                for (int c = 0; c < TC_TILE; c += 8) {
-                    const uint32_t bits = mask[c >> 5] >> (c & 31);
+                for (int c = 0; c < TILE; c += 8) {
+                    const uint32_t bits = misc.mask[t % TC_MASKS][c >> 3];
                     uint32_t o[8];
                     tc_load8(s_at + c, o);
                     tc_wait_load();
@@ -747,12 +952,14 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             tc_load32(s_at + 32, x[1]);
             tc_wait_load();
             largest(x[0]);
-            tc_load32(s_at + 64, x[0]);
+            if constexpr (TILE > 64) tc_load32(s_at + 64, x[0]);
             largest(x[1]);
-            tc_load32(s_at + 96, x[1]);
-            tc_wait_load();
-            largest(x[0]);
-            largest(x[1]);
+            if constexpr (TILE > 64) {
+                tc_load32(s_at + 96, x[1]);
+                tc_wait_load();
+                largest(x[0]);
+                largest(x[1]);
+            }
             const float top = fmaxf(max3(m[0], m[1], m[2]), m[3]) * factor;
             // the reference that the tile before left, the other stream's
             float was = -INFINITY;
@@ -809,16 +1016,16 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     sum[k / 2 & 1] = pair_add(sum[k / 2 & 1], p);
                     pair_parts<HALF>(p, w[k / 2], w[16 + k / 2]);
                 }
-                if (c == 2) told(0);  // (its store has had this chunk's time)
+                if (c == TILE / 64) told(0);  // (its store has had this chunk's time)
                 tc_store32(s_at + 32 * c, w);
             };
 #pragma unroll 1
-            for (int c = 0; c < 4; c += 2) {  // (unrolled, the code outgrows the instruction cache)
+            for (int c = 0; c < TILE / 32; c += 2) {  // (unrolled, the code outgrows the instruction cache)
                 tc_wait_load();
                 tc_load32(s_at + 32 * c + 32, x[1]);
                 weights(x[0], c);
                 tc_wait_load();
-                if (c == 0) tc_load32(s_at + 64, x[0]);
+                if (TILE > 64 && c == 0) tc_load32(s_at + 64, x[0]);
                 weights(x[1], c + 1);
             }
             told(1);
@@ -834,6 +1041,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         misc.ref[s][i] = ref, misc.sum[s][i] = l;
         // partial results of the ordinary kernel carry 2^ATTN_SHIFT_F16 over fp16 caches
         constexpr float LIKE = HALF ? (float)(1 << (ATTN_SHIFT_F16 - TC_SHIFT_F16)) : 1.0f;
+        const float out = Q8 ? LIKE * by_values : LIKE;
         float *row = reinterpret_cast<float *>(ring) + i * S::OROW;
         for (int c = 8 * s; c < D16 && ok; c += 16) {
             uint32_t x[8];
@@ -842,8 +1050,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 #pragma unroll
             for (int k = 0; k < 8; k += 4)
                 *reinterpret_cast<float4 *>(row + c + k) =
-                    make_float4(LIKE * __uint_as_float(x[k]), LIKE * __uint_as_float(x[k + 1]),
-                                LIKE * __uint_as_float(x[k + 2]), LIKE * __uint_as_float(x[k + 3]));
+                    make_float4(out * __uint_as_float(x[k]), out * __uint_as_float(x[k + 1]),
+                                out * __uint_as_float(x[k + 2]), out * __uint_as_float(x[k + 3]));
         }
         asm volatile("bar.sync 1, 256;" ::: "memory");
         const long long unit = (((long long)g * a.max_chunks + ck) * KVH + h) * a.row_tiles + rt;
@@ -871,10 +1079,10 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     }
 }
 
-template <bool HALF, int QP, int NB>
+template <bool HALF, int QP, int NB, bool Q8>
 cudaError_t prefix_launch_of(const TcArgs &a, int grid, void *stream, unsigned int *status) {
-    auto *kern = prefix_kernel<HALF, QP, NB>;
-    constexpr int smem = TcShape<QP, NB>::SMEM;
+    auto *kern = prefix_kernel<HALF, QP, NB, Q8>;
+    constexpr int smem = TcShape<QP, NB, Q8>::SMEM;
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -887,10 +1095,10 @@ cudaError_t prefix_launch_of(const TcArgs &a, int grid, void *stream, unsigned i
     }
     return launch_pdl(kern, dim3((unsigned)grid), TC_WARPS * 32, smem, stream, 1, a, status);
 }
-template <bool HALF, int QP>
+template <bool HALF, int QP, bool Q8 = false>
 cudaError_t prefix_launch(const TcArgs &a, int grid, void *stream, unsigned int *status) {
-    return a.a.c.head_dim <= 64 ? prefix_launch_of<HALF, QP, 1>(a, grid, stream, status)
-                              : prefix_launch_of<HALF, QP, 2>(a, grid, stream, status);
+    return a.a.c.head_dim <= 64 ? prefix_launch_of<HALF, QP, 1, Q8>(a, grid, stream, status)
+                              : prefix_launch_of<HALF, QP, 2, Q8>(a, grid, stream, status);
 }
 
 }  // namespace bq

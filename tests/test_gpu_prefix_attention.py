@@ -117,6 +117,58 @@ def test_many_rows(kind, dtype, requests, heads, kv):
     case(g, kind, dtype, lens, 200, 8, heads, kv, 64)
 
 
+@pytest.mark.parametrize("dtype", [F32, F16, BF16])
+@pytest.mark.parametrize("D,page,layout", [(32, 16, "hs"), (96, 24, "sh"), (128, 7, "kv"), (128, 64, "hs"), (64, 16, "sh")])
+def test_many_rows_over_q8_0(dtype, D, page, layout):
+    """Enough rows that codes are put into parts for the tensor cores, ragged tiles of
+    positions, a page outside the pool among them (masked)."""
+    g = rng("q8", str(dtype), D, page)
+    lens = [n + 1 for n in g.integers(700, 760, 29)] + [0]
+    case(g, "q8_0", dtype, lens, 700, page, 6, 3, D, layout=layout)
+    shared = [(20, 700), (10, 333)]
+    lens = [701 + int(n) for n in g.integers(0, 40, 20)] + [334 + int(n) for n in g.integers(0, 40, 10)]
+    out, cache, q, table = case(g, "q8_0", dtype, lens, shared, page, 6, 3, D, layout=layout, hurt=False)
+    bad = 333 // page // 2
+    table[:, bad] = cache.pages + 3
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    hurt = bq.paged_prefix_attention(cache, q, table, at, shared)
+    assert bq.device_status(clear=True) == 0x100
+    keep = [i for i in range(table.shape[1]) if i != bad]
+    want, mag, top = plain.attention(*plain.values(cache), q.cpu(), table.cpu()[:, keep], [n - page for n in lens], 1,
+                                     D ** -0.5)
+    assert ((hurt.cpu().double() - want).abs() <= bound_of(want, mag, top, dtype, "q8_0")).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** -12, 1.0, 3.0e4])
+def test_scales_of_any_size_over_q8_0(dtype, size):
+    """All scales small or large, and a few blocks far above the others.  A value of a
+    block far below the largest of its chunk is off by 2^-39 of what the largest scale's
+    codes reach (127 times it), a score by that much of each of its D products."""
+    g = rng("scales", str(dtype), str(size))
+    D, page, n, requests = 64, 16, 512, 20
+    pages = n // page + requests + 2
+    lens = [n + 3 + b % 9 for b in range(requests)]
+    table = shared_table(g, lens, [(requests, n)], page, pages)
+    for far in (False, True):
+        cache = filled_cache(g, "q8_0", pages, page, 2, D)
+        cache.k_scale.mul_(30 * size).clamp_(max=6.0e4)
+        cache.v_scale.mul_(30 * size).clamp_(max=6.0e4)
+        if far:
+            cache.k_scale[table[0, 5].long(), :, 3, 1] = 6.0e4
+            cache.v_scale[table[0, 7].long(), :, 9, 0] = 6.0e4
+        # scores of a few units whatever the keys' size; with a far block that block decides
+        q = (normal(g, (requests, 4, D)) / max(float(cache.k_scale.max()) * 60, 2.0 ** -30)).to(dtype)
+        out = bq.paged_prefix_attention(cache, q, table, torch.tensor(lens, dtype=torch.int32, device=DEV), n)
+        k, v = plain.values(cache)
+        want, mag, top = plain.attention(k, v, q.cpu(), table.cpu(), lens, 1, D ** -0.5)
+        kt, vt = (127.0 * float(s.max()) for s in (cache.k_scale, cache.v_scale))
+        score = D ** -0.5 * D * float(q.abs().max()) * 2.0 ** -38 * kt
+        extra = 2.0 ** -38 * vt + 2 * score * mag
+        bound = bound_of(want, mag, top, dtype, "q8_0") + extra * (1 + plain.EPS[dtype])
+        assert ((out.cpu().double() - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
 def test_a_long_prefix(kind, dtype):
     lens = [9003, 9100, 9003, 0, 9777]
@@ -208,6 +260,28 @@ def test_large_scores_and_growing_maxima(kind, dtype):
             cache.k[ids] = k.to(cache.k.dtype)
         q = (0.5 + normal(g, (2, 4, 64)).abs()).to(dtype)
         check(cache, q, table, [n + 20, n + 9], n)
+
+
+def test_scales_that_are_not_finite_over_q8_0():
+    """A NaN or infinite scale of a shared value or key reaches the rows of its head and
+    where it lies, and nothing else."""
+    g = rng("nans")
+    lens, page = [300 + b % 5 for b in range(25)], 16
+    out, cache, q, table = case(g, "q8_0", F32, lens, 288, page, 8, 2, 64)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    for bad in (float("nan"), float("inf")):
+        kept = cache.v_scale.clone()
+        cache.v_scale[int(table[0, 4]), 1, 6, 1] = bad  # values 32 to 63 of head 1
+        hurt = bq.paged_prefix_attention(cache, q, table, at, 288)
+        same = torch.ones_like(out, dtype=torch.bool)
+        same[:, 4:, 32:] = False
+        assert torch.equal(hurt[same], out[same]) and not hurt[:, 4:, 32:].isfinite().any()
+        cache.v_scale.copy_(kept)
+        kept = cache.k_scale.clone()
+        cache.k_scale[int(table[0, 4]), 0, 6, 0] = float("nan")
+        hurt = bq.paged_prefix_attention(cache, q, table, at, 288)
+        assert hurt[:, :4].isnan().all() and torch.equal(hurt[:, 4:], out[:, 4:])
+        cache.k_scale.copy_(kept)
 
 
 def test_values_that_are_not_finite_reach_only_their_rows_and_heads():
