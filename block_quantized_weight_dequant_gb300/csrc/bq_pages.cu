@@ -57,48 +57,52 @@ __device__ __forceinline__ long long peer_word(const long long *at, uint32_t ran
     return v;
 }
 
+// Sums that stop at 2^31 - 1, which is more than any pool, max_tokens or number of
+// entries: a stopped sum decides as the true one does.
+__device__ __forceinline__ uint32_t add_up(uint32_t a, uint32_t b) { return min(a + b, 0x7fffffffu); }
+
 // exclusive prefix sums over the CTA's threads of K numbers each, and their totals
 template <int K>
-__device__ __forceinline__ void scan_threads(long long (&v)[K], long long (&total)[K], long long (*scratch)[WARPS]) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long own[K];
+__device__ __forceinline__ void scan_threads(uint32_t (&v)[K], uint32_t (&total)[K], uint32_t (*scratch)[WARPS]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    uint32_t before[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        own[k] = v[k];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(~0u, v[k], o);
-            if (lane >= o) v[k] += u;
+            const uint32_t u = __shfl_up_sync(~0u, v[k], o);
+            if (lane >= o) v[k] = add_up(v[k], u);
         }
         if (lane == 31) scratch[k][warp] = v[k];
+        before[k] = __shfl_up_sync(~0u, v[k], 1);
+        if (lane == 0) before[k] = 0;
     }
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-        long long w = scratch[k][lane];  // WARPS == 32
+        uint32_t w = lane < warps ? scratch[k][lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(~0u, w, o);
-            if (lane >= o) w += u;
+            const uint32_t u = __shfl_up_sync(~0u, w, o);
+            if (lane >= o) w = add_up(w, u);
         }
         total[k] = __shfl_sync(~0u, w, 31);
-        const long long before = __shfl_sync(~0u, w, (warp + 31) & 31);
-        v[k] += (warp ? before : 0) - own[k];
+        const uint32_t others = __shfl_sync(~0u, w, (warp + 31) & 31);
+        v[k] = add_up(before[k], warp ? others : 0);
     }
     __syncthreads();
 }
 
 __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ ShareArgs a, int with_rows) {
     extern __shared__ int sm[];
-    const int n = a.t.requests, tid = threadIdx.x;
+    const int n = a.t.requests, tid = threadIdx.x, threads = blockDim.x;
     // per request: length before its rows, length asked, parent and marks, the page
     // that it copies; exclusive prefix sums
     int *base_s = sm, *want_s = base_s + n, *mark_s = want_s + n, *last_s = mark_s + n;
     int *asked = last_s + n, *rows = asked + n + 1, *gone = rows + n + 1, *joined = gone + n + 1, *copied = joined + n + 1;
-    __shared__ long long scratch[3][WARPS];
+    __shared__ uint32_t scratch[3][WARPS];
     __shared__ long long s_pushed;  // of this CTA
     __shared__ int s_given, s_refused;
-    static_assert(WARPS == 32);
     constexpr int CUT = 1 << 16, BAD = 1 << 17, SERVED = 1 << 18, PARENT = CUT - 1;
     bq::pdl_wait();
     if (!with_rows) bq::pdl_launch_dependents();
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
     };
 
     // ---- what each request starts from ----
-    for (int b = tid; b < n; b += THREADS) {
+    for (int b = tid; b < n; b += threads) {
         const int lo = a.t.lens[b], hi = a.t.new_lens[b];
         int p = a.s.parents ? a.s.parents[b] : -1;
         bool bad = lo < 0 || hi < 0 || lo > most || hi > most;
@@ -163,26 +167,25 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
     };
 
     // ---- asked pages and rows ----
-    const int per = (n + THREADS - 1) / THREADS;
+    const int per = (n + threads - 1) / threads;
     const int b0 = min(n, tid * per), b1 = min(n, b0 + per);
-    const long long TOP = 0x7fffffffLL;  // as in the ordinary tables: a clamped sum decides as the true one
     {
-        long long v[2] = {0, 0}, total[2];
+        uint32_t v[2] = {0, 0}, total[2];
         for (int b = b0; b < b1; ++b) {
             const Request r = request(b);
-            v[0] += r.ask, v[1] += r.new_rows;
+            v[0] = add_up(v[0], r.ask), v[1] = add_up(v[1], r.new_rows);
         }
         scan_threads<2>(v, total, scratch);
         for (int b = b0; b < b1; ++b) {
             const Request r = request(b);
-            asked[b] = (int)min(TOP, v[0]), rows[b] = (int)min(TOP, v[1]);
-            v[0] += r.ask, v[1] += r.new_rows;
+            asked[b] = (int)v[0], rows[b] = (int)v[1];
+            v[0] = add_up(v[0], r.ask), v[1] = add_up(v[1], r.new_rows);
         }
-        if (tid == 0) asked[n] = (int)min(TOP, total[0]), rows[n] = (int)min(TOP, total[1]);
+        if (tid == 0) asked[n] = (int)total[0], rows[n] = (int)total[1];
     }
     __syncthreads();
     int given = 0, refused = 0;
-    for (int b = tid; b < n; b += THREADS) {
+    for (int b = tid; b < n; b += threads) {
         const Request r = request(b);
         const bool ok = !r.bad && (!r.ask || asked[b + 1] <= count) && (!r.new_rows || rows[b + 1] <= a.t.max_tokens);
         if (ok) mark_s[b] |= SERVED;
@@ -203,30 +206,28 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
         return !r.served || r.parent >= 0 ? 0 : r.cut ? 1 : max(0, r.held - r.wanted);
     };
     auto joins = [&](const Request &r) { return r.served && r.parent >= 0 ? r.kept : 0; };
-    long long all_joined, all_gone;
-    int all_copied;
+    int all_joined, all_gone, all_copied;
     {
-        long long v[3] = {0, 0, 0}, total[3];
+        uint32_t v[3] = {0, 0, 0}, total[3];
         for (int b = b0; b < b1; ++b) {
             const Request r = request(b);
-            v[0] += releases(r), v[1] += joins(r), v[2] += r.served && r.cut;
+            v[0] = add_up(v[0], releases(r)), v[1] = add_up(v[1], joins(r)), v[2] += r.served && r.cut;
         }
         scan_threads<3>(v, total, scratch);
         for (int b = b0; b < b1; ++b) {
             const Request r = request(b);
-            gone[b] = (int)min(TOP, v[0]), joined[b] = (int)min(TOP, v[1]), copied[b] = (int)v[2];
-            v[0] += releases(r), v[1] += joins(r), v[2] += r.served && r.cut;
+            gone[b] = (int)v[0], joined[b] = (int)v[1], copied[b] = (int)v[2];
+            v[0] = add_up(v[0], releases(r)), v[1] = add_up(v[1], joins(r)), v[2] += r.served && r.cut;
         }
-        // (indices of entries are 32-bit numbers: a table of 2^31 live entries is larger than
-        // any memory, and what lies beyond is left alone)
-        all_gone = min(TOP, total[0]), all_joined = min(TOP, total[1]), all_copied = (int)total[2];
-        if (tid == 0) gone[n] = (int)all_gone, joined[n] = (int)all_joined, copied[n] = all_copied;
+        // (a table of 2^31 live entries is larger than any memory: what lies beyond is left alone)
+        all_gone = (int)total[0], all_joined = (int)total[1], all_copied = (int)total[2];
+        if (tid == 0) gone[n] = all_gone, joined[n] = all_joined, copied[n] = all_copied;
     }
     __syncthreads();
     // every CTA has read lengths, counts, parents' rows and the free count: they may change
     cluster_barrier();
 
-    const int step = (int)cluster * THREADS, me = (int)rank * THREADS + tid;
+    const int step = (int)cluster * threads, me = (int)rank * threads + tid;
     const int lane = tid & 31;
     auto row_of = [&](int b) { return a.t.table + (long long)b * a.t.table_stride; };
     auto counted = [&](int page) { return page >= 0 && page < pool; };
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
     constexpr int JOIN = 4;
     for (long long i0 = (long long)(me >> 5) * (32 * JOIN); i0 < all_joined; i0 += (long long)(step >> 5) * (32 * JOIN)) {
         int of[JOIN], col[JOIN], page[JOIN];
-        int b = bq::last_not_above(joined, n, (int)min(i0 + lane, all_joined - 1));
+        int b = bq::last_not_above(joined, n, (int)min(i0 + lane, (long long)all_joined - 1));
 #pragma unroll
         for (int k = 0; k < JOIN; ++k) {
             const long long i = i0 + 32 * k + lane;
@@ -292,13 +293,13 @@ __global__ void __launch_bounds__(THREADS) share_kernel(const __grid_constant__ 
         }
         cluster_barrier();
         // each thread a run of releases
-        const long long run = (all_gone + step - 1) / step;
-        const long long i0 = min(all_gone, me * run), i1 = min(all_gone, i0 + run);
+        const long long run = ((long long)all_gone + step - 1) / step;
+        const long long i0 = min((long long)all_gone, me * run), i1 = min((long long)all_gone, i0 + run);
         auto mine = [&](long long i, int &page) {
             page = released((int)i);
             return counted(page) && __ldcg(&a.s.refs[page]) == CLAIM + (int)i;
         };
-        long long v[1] = {0}, total[1];
+        uint32_t v[1] = {0}, total[1];
         for (long long i = i0; i < i1; ++i) {
             int page;
             v[0] += mine(i, page);
@@ -366,7 +367,7 @@ struct CompactArgs {
 };
 
 __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant__ CompactArgs a) {
-    __shared__ long long scratch[1][WARPS];
+    __shared__ uint32_t scratch[1][WARPS];
     constexpr int KEPT = 64;
     __shared__ uint32_t words[WARPS][KEPT];
     __shared__ long long s_live, s_moves;  // pages in use in this CTA's part; moves, in the CTA that meets them
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(THREADS) compact_kernel(const __grid_constant_
 #pragma unroll
         for (int k = 0; k < READS; ++k) tell(k, __ballot_sync(~0u, live[k]));
     };
-    long long v[1] = {0}, total[1];
+    uint32_t v[1] = {0}, total[1];
     for (long long q0 = p0; q0 < p1; q0 += 32 * READS)
         look(q0, [&](int k, uint32_t bits) {
             if (lane == 0) {
@@ -649,7 +650,9 @@ extern "C" bq_status bq_kv_shared_tables(const bq_kv_tables *t, const bq_kv_shar
     const int cluster = work <= 16LL * THREADS                ? 1
                         : work <= 256LL * THREADS || smem > 40 * 1024 ? CLUSTER
                                                               : largest_cluster(share_kernel, 40 * 1024);
-    const cudaError_t e = bq::launch_pdl(share_kernel, dim3((unsigned)cluster), THREADS, smem, stream, cluster, a,
+    // (a barrier of 32 warps costs more than the work of a small step)
+    const int threads = cluster == 1 && t->requests <= 256 ? 256 : THREADS;
+    const cudaError_t e = bq::launch_pdl(share_kernel, dim3((unsigned)cluster), threads, smem, stream, cluster, a,
                                          (int)with_rows);
     if (e != cudaSuccess || with_rows) return bq::from_cuda_error(e);
     return bq::from_cuda_error(bq::rows_launch(a.t, stream));
