@@ -420,7 +420,8 @@ class SharedBlockTables(BlockTables):
     def compact(self, max_moves=None):
         """Move the pages in use to the lowest numbers, max_moves of them at most (half
         the pool by default, which is all there can be), in the tables and in all
-        layers.  Returns ``moved`` [pages], each page's new number."""
+        layers.  Returns ``moved`` [pages], each page's new number (a buffer of this
+        object)."""
         room = self.free_pages.numel() // 2 if max_moves is None else int(max_moves)
         if self._moves is None or self._moves[0].numel() != room:
             i32 = dict(dtype=torch.int32, device=self.lens.device)
@@ -624,7 +625,8 @@ def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, ou
                                 table.data_ptr(), lens.data_ptr())
     ref = _byref(args)
     # the groups' host arrays and the workspace's bytes, by the call's geometry
-    key = (n, rows, heads, width, dtype, shared if type(shared) is int else tuple(map(tuple, shared)))
+    shared = shared if type(shared) is int else tuple(map(tuple, shared))
+    key = (n, rows, heads, width, dtype, shared)
     plan = cache._workspace.get(key)
     if plan is None:
         groups = _groups(shared, n)

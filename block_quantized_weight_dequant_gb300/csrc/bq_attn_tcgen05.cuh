@@ -20,14 +20,16 @@
 // positions as rows and head_dim contiguous, V the same bytes with the summed axis
 // as rows.  One thread of warp 11 issues all products.  Queries are a first operand
 // in tensor memory; the weights go back there in the columns of the scores that they
-// come from, and are the first operand of the second product.
+// come from, and are the first operand of the second product.  Over a Q8_0 cache
+// warps 8 to 10 put codes times scales into parts on the way, tiles of 64 positions.
 //
 // Precision.  A query of the cache's type is used as it is, any other in QP 16-bit
 // parts (fp16 2, after scaling the row by a power of two; bf16 3); weights are two
-// parts: 22 bits over an fp16 cache, 16 over bf16, where a third would not fit
-// beside S in tensor memory (an output's error from it is below 2^-17 of the mean
-// |v|; one part alone would leave 2^-9).  O sums a chunk's tiles in the tensor
-// core's fp32.
+// parts of fp16, 22 bits, three of bf16, 24 bits, or two, 17 bits, where the output is
+// bf16 (an error below 2^-17 of the mean |v|, where the output's rounding is 2^-9 of
+// it; one part alone would leave 2^-9, a third takes a half more of the second
+// product).  Q8_0 codes times scales are two fp16 parts (below).  O sums a chunk's
+// tiles in the tensor core's fp32.
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
@@ -53,10 +55,13 @@ template <int QP, int NB, bool Q8>
 struct TcShape {
     // positions of a tile; bytes of its rows of 64 values; parts of a key or value
     static constexpr int TILE = Q8 ? 64 : 128, BLOCK = TILE * 128, KP = Q8 ? 2 : 1;
-    // queries as a first operand in tensor memory, where their parts fit beside the scores
-    // of both streams and the output: the tensor cores then read K and V alone from
-    // shared memory, whose 128 bytes a cycle bound the kernel otherwise
-    static constexpr bool Q_TENSOR = QP * NB * 32 <= TC_COLUMNS - TC_Q;
+    // Parts of a weight: three of bf16 where the output holds more than a bf16 number.  The
+    // third ones lie where the queries do otherwise.
+    static constexpr int PP = QP == 3 ? 3 : 2;
+    // queries as a first operand in tensor memory beside the scores of both streams and
+    // the output, or in shared memory
+    static constexpr bool Q_TENSOR = PP == 2;
+    static_assert(!Q_TENSOR || QP * NB * 32 <= TC_COLUMNS - TC_Q);
     static constexpr int SLOT = KP * NB * BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_QBLOCK;
     static constexpr int LIMIT = 227 * 1024, MISC = 3072;
     // Q8_0: codes and scales on their way, RAW tiles of them; a lane's 32 codes and a word
@@ -316,6 +321,15 @@ __device__ __forceinline__ void pair_parts(uint64_t p, uint32_t &high, uint32_t 
     }
     const float2 rest = pair_values(pair_less(p, pair_of(h.x, h.y)));
     low = HALF ? F16::down2(rest.x, rest.y) : BF16::down2(rest.x, rest.y);
+}
+// three that do
+template <bool HALF>
+__device__ __forceinline__ void pair_parts(uint64_t p, uint32_t &high, uint32_t &middle, uint32_t &low) {
+    static_assert(!HALF);
+    const float2 v = pair_values(p);
+    high = BF16::down2(v.x, v.y);
+    const float2 h = BF16::up2(high);
+    pair_parts<HALF>(pair_less(p, pair_of(h.x, h.y)), middle, low);
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
@@ -766,7 +780,9 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             for (int k = STEPS * half; k < STEPS * half + STEPS; ++k) {
                 const uint32_t high = w + 32 * (k >> 1) + 8 * (k & 1);
                 const uint64_t values = v_m + k * (2048 >> 4);
-                tc_product_tensor(o, high + 16, values, pv_shape, k || t > 0);
+                if constexpr (S::PP == 3)
+                    tc_product_tensor(o, tmem + TC_Q + (t & 1) * 64 + 8 * k, values, pv_shape, k || t > 0);
+                tc_product_tensor(o, high + 16, values, pv_shape, S::PP == 3 || k || t > 0);
                 if constexpr (Q8) tc_product_tensor(o, high, values + (NB * BLOCK >> 4), pv_shape, true);
                 tc_product_tensor(o, high, values, pv_shape, true);
             }
@@ -1008,16 +1024,22 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             };
             auto weights = [&](const uint32_t(&y)[32], int c) {
                 uint32_t w[32];
+                [[maybe_unused]] uint32_t third[16];
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     const float2 e = pair_values(
                         pair_fma(pair_of(__uint_as_float(y[k]), __uint_as_float(y[k + 1])), factors, shifts));
                     const uint64_t p = pair_of(tc_pow2(e.x), tc_pow2(e.y));
                     sum[k / 2 & 1] = pair_add(sum[k / 2 & 1], p);
-                    pair_parts<HALF>(p, w[k / 2], w[16 + k / 2]);
+                    if constexpr (S::PP == 3) pair_parts<HALF>(p, w[k / 2], w[16 + k / 2], third[k / 2]);
+                    else pair_parts<HALF>(p, w[k / 2], w[16 + k / 2]);
                 }
                 if (c == TILE / 64) told(0);  // (its store has had this chunk's time)
                 tc_store32(s_at + 32 * c, w);
+                if constexpr (S::PP == 3) {
+                    tc_store8(tmem + lanes + TC_Q + s * 64 + 16 * c, reinterpret_cast<uint32_t(&)[8]>(third[0]));
+                    tc_store8(tmem + lanes + TC_Q + s * 64 + 16 * c + 8, reinterpret_cast<uint32_t(&)[8]>(third[8]));
+                }
             };
 #pragma unroll 1
             for (int c = 0; c < TILE / 32; c += 2) {  // (unrolled, the code outgrows the instruction cache)

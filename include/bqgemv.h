@@ -610,9 +610,17 @@ bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *
  *    groups <= BQ_PREFIX_MAX_GROUPS, counts not negative and summing to
  *    args->requests, 0 <= group_shared <= table_width * page_size.
  *  - args, outputs, masks, status bits and workspace as for bq_paged_attention,
- *    with bq_paged_prefix_attention_workspace_bytes.  A row's bits depend on its
- *    own inputs and the call's geometry (the groups among it): they are not those
- *    of bq_paged_attention. */
+ *    with bq_paged_prefix_attention_workspace_bytes.  A wait inside the kernel that
+ *    runs out (a second) sets BQ_DEVERR_WAIT.  A row's bits depend on its own
+ *    inputs, on its chunk's largest scales over a BQ_Q8_0 cache, and on the call's
+ *    geometry (the groups among it): they are not those of bq_paged_attention, but
+ *    where so little is shared that one pass of it serves the call.
+ *  - Over the shared pages heads of up to 128 values go through the tensor cores
+ *    (over BQ_Q8_0 from 33 rows of a kv head on): queries as in bq_paged_attention,
+ *    probabilities to 2^-22 of the number over BQ_F16 and BQ_Q8_0 caches and to
+ *    2^-24 over BQ_BF16 (2^-17 for BQ_BF16 queries, whose outputs hold 2^-9), keys and values of a BQ_Q8_0 cache to 2^-22, or 2^-39 of
+ *    127 times the largest scale of the chunk (at most 8192 positions of a head)
+ *    where that is more, products summed over a chunk in fp32. */
 #define BQ_PREFIX_MAX_GROUPS 64
 int64_t bq_paged_prefix_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args,
                                                   const int32_t *group_requests, const int32_t *group_shared, int groups);
