@@ -28,8 +28,8 @@
 // parts of fp16, 22 bits, three of bf16, 24 bits, or two, 17 bits, where the output is
 // bf16 (an error below 2^-17 of the mean |v|, where the output's rounding is 2^-9 of
 // it; one part alone would leave 2^-9, a third takes a half more of the second
-// product).  Q8_0 codes times scales are two fp16 parts (below).  O sums a chunk's
-// tiles in the tensor core's fp32.
+// product).  Q8_0 codes times scales are two fp16 parts (below).  O is summed by the
+// tensor core over some tiles and by fp32 additions over the chunk (ADDED).
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
@@ -46,22 +46,31 @@ constexpr int TC_ROWS = 128;
 constexpr int TC_SOFTMAX_WARPS = 8, TC_COPY_WARPS = 3, TC_WARPS = 12;
 constexpr int TC_MASKS = 8;        // tiles whose masks are kept
 constexpr int TC_QBLOCK = TC_ROWS * 128;  // bytes of all rows' 64 values
-// columns of tensor memory, all of it: scores of two streams, output, queries
-constexpr int TC_COLUMNS = 512, TC_O = 256, TC_Q = 384;
+constexpr int TC_COLUMNS = 512;      // of tensor memory, all of it
 constexpr float TC_GROWTH = 8.0f;    // log2 of what a weight may be
 constexpr int TC_SHIFT_F16 = 7;      // fp16 weights carry 2^7: up to 2^15, two parts keep 2^-24
 
-template <int QP, int NB, bool Q8>
+template <bool HALF, int QP, int NB, bool Q8>
 struct TcShape {
-    // positions of a tile; bytes of its rows of 64 values; parts of a key or value
-    static constexpr int TILE = Q8 ? 64 : 128, BLOCK = TILE * 128, KP = Q8 ? 2 : 1;
-    // Parts of a weight: three of bf16 where the output holds more than a bf16 number.  The
-    // third ones lie where the queries do otherwise.
+    // Parts of a weight: three of bf16 where the output holds more than a bf16 number.
     static constexpr int PP = QP == 3 ? 3 : 2;
-    // queries as a first operand in tensor memory beside the scores of both streams and
-    // the output, or in shared memory
-    static constexpr bool Q_TENSOR = PP == 2;
-    static_assert(!Q_TENSOR || QP * NB * 32 <= TC_COLUMNS - TC_Q);
+    // positions of a tile; bytes of its rows of 64 values; parts of a key or value
+    static constexpr int TILE = Q8 || PP == 3 ? 64 : 128, BLOCK = TILE * 128, KP = Q8 ? 2 : 1;
+    // The tensor core truncates when it adds to O: after some hundred positions that shows
+    // in an fp32 output (chunks of 1800 positions: off by 4.4e-6 of it, fp32 sums 7e-7;
+    // added up every 512 1.3e-6, every 256 8e-7), after thousands in an fp16 one (1.3% of
+    // the values not the nearest, with 512 0.4%, as fp32 sums leave).  So O is added up
+    // elsewhere in tensor memory, rounded to nearest, every FLUSH tiles, and starts again;
+    // not for bf16 outputs.  Heads of 128 then have their queries in shared memory: 96
+    // requests of 32801 shared, fp16 89 us a call against 77, fp32 queries 117 against 86.
+    static constexpr bool ADDED = HALF || QP == 3;
+    static constexpr int FLUSH = (QP > 1 ? 256 : 512) / TILE;
+    // columns of tensor memory: scores of two streams, O, its sum, and in the rest third
+    // parts of the weights or queries (else these lie in shared memory)
+    static constexpr int O = 2 * TILE, SUM = O + NB * 64, REST = 384;
+    static constexpr bool Q_TENSOR = PP == 2 && (!ADDED || SUM + NB * 64 <= REST);
+    static_assert(!Q_TENSOR || QP * NB * 32 <= TC_COLUMNS - REST);
+    static_assert(PP == 2 || (SUM + NB * 64 <= REST && REST + 2 * TILE / 2 <= TC_COLUMNS));
     static constexpr int SLOT = KP * NB * BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_QBLOCK;
     static constexpr int LIMIT = 227 * 1024, MISC = 3072;
     // Q8_0: codes and scales on their way, RAW tiles of them; a lane's 32 codes and a word
@@ -74,8 +83,8 @@ struct TcShape {
     static constexpr int SLOTS = most > 8 ? 8 : most;
     // Loads that are issued before the oldest is waited for.  A tile's keys are told as
     // arrived once the LAG loads behind them are issued, which takes slots that are free
-    // again: with 3 of 6 the next keys waited for the values two tiles before (DELTA),
-    // above SLOTS - 2 for themselves.
+    // again: with 3 of 6 the next keys waited for the values two tiles before (the pass
+    // 126 us against 104), above SLOTS - 2 for themselves.
     static constexpr int LAG = SLOTS >= 8 ? 3 : 1;
     static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + RAW_BYTES + MISC;
     static constexpr int OROW = NB * 64 + 4;  // floats of a row on its way out, in the ring's place
@@ -96,7 +105,7 @@ struct TcArgs {
 
 // shared memory behind the ring
 struct TcMisc {
-    uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2][2], q_full, added, o_full;
+    uint64_t full[8], empty[8], mask_full[TC_MASKS], s_full[2], p_full[2][2], q_full, added[2], flushed, summed[2], o_full;
     uint64_t ref_full[2][4];     // by stream and warp of it
     uint32_t top_scale[2];       // bits of the chunk's largest Q8_0 scales, of keys and values
     alignas(16) uint8_t mask[TC_MASKS][16];  // positions of a tile that are there
@@ -355,8 +364,8 @@ __device__ __forceinline__ uint32_t tc_part(float &x, float &y) {
 template <bool HALF, int QP, int NB, bool Q8>
 __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     prefix_kernel(const __grid_constant__ TcArgs args, unsigned int *status) {
-    using S = TcShape<QP, NB, Q8>;
-    constexpr int TILE = S::TILE, BLOCK = S::BLOCK;
+    using S = TcShape<HALF, QP, NB, Q8>;
+    constexpr int TILE = S::TILE, BLOCK = S::BLOCK, FLUSH = S::FLUSH;
     const AttnArgs &a = args.a;
     constexpr int SLOTS = S::SLOTS, LAG = S::LAG;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -392,7 +401,11 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             for (int k = 0; k < 4; ++k) barrier_init(&misc.ref_full[i][k], 1);
         }
         barrier_init(&misc.q_full, TC_SOFTMAX_WARPS);
-        barrier_init(&misc.added, 1);
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(&misc.added[i], 1);
+            barrier_init(&misc.summed[i], TC_SOFTMAX_WARPS / 2);
+        }
+        barrier_init(&misc.flushed, TC_SOFTMAX_WARPS / 2);
         barrier_init(&misc.o_full, 1);
         misc.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -741,7 +754,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         };
         auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first; by the elected thread
             const uint64_t k_m = ring_m + k_slot * (S::SLOT >> 4);
-            const uint32_t d = tmem + (t & 1) * 128;
+            const uint32_t d = tmem + (t & 1) * TILE;
             // (the product of two second parts is below what either leaves out)
 #pragma unroll
             for (int kp = S::KP - 1; kp >= 0; --kp)
@@ -753,7 +766,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                         const uint64_t keys = k_m + (kp * NB + (k >> 2)) * (BLOCK >> 4) + (k & 3) * 2;
                         const bool add = kp < S::KP - 1 || p < (kp ? 0 : QP - 1) || k;
                         if constexpr (S::Q_TENSOR)
-                            tc_product_tensor(d, tmem + TC_Q + p * NB * 32 + 8 * k, keys, qk_shape, add);
+                            tc_product_tensor(d, tmem + S::REST + p * NB * 32 + 8 * k, keys, qk_shape, add);
                         else
                             tc_product_shared(d, q_m + (p * NB + (k >> 2)) * (TC_QBLOCK >> 4) + (k & 3) * 2, keys, qk_shape,
                                               add);
@@ -769,20 +782,21 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             __syncwarp();
             next(k_slot, k_phase);
         }
-        const uint32_t o = tmem + TC_O;
+        const uint32_t o = tmem + S::O;
         // half of tile t's positions, 16 a step: 8 columns of a weight part; 32 columns
         // hold both parts of 32 positions
         auto output = [&](int t, int half) {
             const uint64_t v_m = ring_m + v_slot * (S::SLOT >> 4);
-            const uint32_t w = tmem + (t & 1) * 128;
+            const uint32_t w = tmem + (t & 1) * TILE;
+            const bool goes_on = S::ADDED ? t % FLUSH != 0 : t > 0;  // O has something of this sum
             constexpr int STEPS = TILE / 32;
 #pragma unroll
             for (int k = STEPS * half; k < STEPS * half + STEPS; ++k) {
                 const uint32_t high = w + 32 * (k >> 1) + 8 * (k & 1);
                 const uint64_t values = v_m + k * (2048 >> 4);
                 if constexpr (S::PP == 3)
-                    tc_product_tensor(o, tmem + TC_Q + (t & 1) * 64 + 8 * k, values, pv_shape, k || t > 0);
-                tc_product_tensor(o, high + 16, values, pv_shape, S::PP == 3 || k || t > 0);
+                    tc_product_tensor(o, tmem + S::REST + (t & 1) * (TILE / 2) + 8 * k, values, pv_shape, k || goes_on);
+                tc_product_tensor(o, high + 16, values, pv_shape, S::PP == 3 || k || goes_on);
                 if constexpr (Q8) tc_product_tensor(o, high, values + (NB * BLOCK >> 4), pv_shape, true);
                 tc_product_tensor(o, high, values, pv_shape, true);
             }
@@ -799,6 +813,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 waits(keys, keys_phase);
                 waits(&misc.p_full[s][0], t >> 1 & 1);
             }
+            if (S::ADDED && t && t % FLUSH == 0) waits(&misc.flushed, (t / FLUSH - 1) & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) output(t, 0);
@@ -809,7 +824,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             if (elect_one()) {
                 output(t, 1);
                 tc_commit(&misc.empty[v_slot]);
-                tc_commit(&misc.added);
+                tc_commit(&misc.added[s]);
                 if (more) scores(t + 2);
             }
             __syncwarp();
@@ -891,7 +906,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                         w[2 * k] = tc_part<HALF>(y[0], y[1]);
                         w[2 * k + 1] = tc_part<HALF>(y[2], y[3]);
                     }
-                    tc_store8(tmem + lanes + TC_Q + p * NB * 32 + s * (EACH / 2) + 2 * k0, w);
+                    tc_store8(tmem + lanes + S::REST + p * NB * 32 + s * (EACH / 2) + 2 * k0, w);
                 }
             tc_wait_store();
             tc_fence_before();
@@ -900,14 +915,25 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         } else {
             // ---- queries into shared memory, 16 rows to a warp ----
             const int d = 4 * lane;
-#pragma unroll 4
-            for (int k = 0; k < TC_ROWS / TC_SOFTMAX_WARPS; ++k) {
+            constexpr int EACH = TC_ROWS / TC_SOFTMAX_WARPS;
+            float all[EACH][4];  // all rows' values on their way at once
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) read(first_row + warp + TC_SOFTMAX_WARPS * k, d, all[k]);
+#pragma unroll
+            for (int k = 0; k < EACH; ++k) {
                 const int r = warp + TC_SOFTMAX_WARPS * k;
-                float x[4];
-                read(first_row + r, d, x);
+                float(&x)[4] = all[k];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] *= sign;
-                static_assert(!SCALED, "fp16 parts fit in tensor memory");
+                if constexpr (SCALED) {
+                    float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+                    const Scaling by = scaling(top);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = x[e] * by.a * by.b;
+                    if (lane == 0) misc.sum[0][r] = by.factor;
+                }
                 const int piece = (lane & 15) >> 1;
                 uint8_t *to = q_s + (lane >> 4) * TC_QBLOCK + r * 128 + ((piece ^ (r & 7)) << 4) + 8 * (lane & 1);
 #pragma unroll
@@ -916,17 +942,22 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     if (d < NB * 64) *reinterpret_cast<uint2 *>(to + p * NB * TC_QBLOCK) = w;
                 }
             }
-            factor = size;
             fence_async_proxy();
             __syncwarp();
             if (lane == 0) barrier_arrive(&misc.q_full);
+            factor = size;
+            if constexpr (SCALED) {
+                asm volatile("bar.sync 1, 256;" ::: "memory");  // factors of all rows
+                factor = misc.sum[0][i];
+            }
         }
         if constexpr (Q8) factor *= by_keys;
         // (above 0: what it multiplies may be minus infinity)
         factor = fmaxf(factor, 1.1754944e-38f);
 
         // ---- weights of this stream's tiles ----
-        const uint32_t s_at = tmem + lanes + s * 128, o_at = tmem + lanes + TC_O;
+        const uint32_t s_at = tmem + lanes + s * TILE, o_at = tmem + lanes + S::O;
+        [[maybe_unused]] const uint32_t sum_at = tmem + lanes + S::SUM;
         float ref = -INFINITY, l = 0.0f;  // the reference that l belongs to
         bool ok = true;
         for (int t = s; t < tiles; t += 2) {
@@ -993,22 +1024,32 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             __syncwarp();
             if (lane == 0) barrier_arrive(&misc.ref_full[s][warp & 3]);
             if (t && __any_sync(~0u, grows)) {  // O of the tiles before, once it is there
-                ok = barrier_wait(&misc.added, (t - 1) & 1, dead);
+                // (where it starts again with this tile, its sum once it is added there)
+                const bool again = S::ADDED && t % FLUSH == 0;
+                // (A wait by parity must be at most one phase behind: the barriers are one to a
+                // stream, or to every other sum, whose phase before is known to be over.)
+                const int sums = t / FLUSH - 1;
+                ok = again ? barrier_wait(&misc.summed[sums & 1], sums >> 1 & 1, dead)
+                           : barrier_wait(&misc.added[s ^ 1], (t - 1) >> 1 & 1, dead);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const float alpha = grows ? tc_pow2(was - now) : 1.0f;
+                auto rescale = [&](uint32_t at) {
 #pragma unroll 1
-                for (int c = 0; c < D16; c += 8) {
-                    uint32_t o[8];
-                    tc_load8(o_at + c, o);
-                    tc_wait_load();
+                    for (int c = 0; c < D16; c += 8) {
+                        uint32_t o[8];
+                        tc_load8(at + c, o);
+                        tc_wait_load();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-                    tc_store8(o_at + c, o);
-                }
+                        for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                        tc_store8(at + c, o);
+                    }
+                };
+                if (!again) rescale(o_at);
+                if (S::ADDED && t >= FLUSH) rescale(sum_at);
             }
             if (ref != now) l *= tc_pow2(ref - now);
             ref = now;
@@ -1037,8 +1078,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 if (c == TILE / 64) told(0);  // (its store has had this chunk's time)
                 tc_store32(s_at + 32 * c, w);
                 if constexpr (S::PP == 3) {
-                    tc_store8(tmem + lanes + TC_Q + s * 64 + 16 * c, reinterpret_cast<uint32_t(&)[8]>(third[0]));
-                    tc_store8(tmem + lanes + TC_Q + s * 64 + 16 * c + 8, reinterpret_cast<uint32_t(&)[8]>(third[8]));
+                    tc_store8(tmem + lanes + S::REST + s * (TILE / 2) + 16 * c, reinterpret_cast<uint32_t(&)[8]>(third[0]));
+                    tc_store8(tmem + lanes + S::REST + s * (TILE / 2) + 16 * c + 8, reinterpret_cast<uint32_t(&)[8]>(third[8]));
                 }
             };
 #pragma unroll 1
@@ -1053,12 +1094,51 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             told(1);
             const float2 l2 = pair_values(pair_add(sum[0], sum[1]));
             l += l2.x + l2.y;
+            if (S::ADDED && (t + 1) % FLUSH == 0 && t + 1 < tiles) {  // O to its sum, before it starts again
+                ok = barrier_wait(&misc.added[s], t >> 1 & 1, dead);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // O into registers, and it may start again: the sum is not waited for
+                uint32_t o[2 * NB][32];
+#pragma unroll
+                for (int c = 0; c < 2 * NB; ++c) tc_load32(o_at + 32 * c, o[c]);
+                tc_wait_load();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(&misc.flushed);
+                const bool first_time = t + 1 == FLUSH;
+#pragma unroll
+                for (int c = 0; c < 8 * NB; ++c) {
+                    uint32_t u[8];
+                    if (!first_time) {
+                        tc_load8(sum_at + 8 * c, u);
+                        tc_wait_load();
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = __uint_as_float(o[c / 4][8 * (c % 4) + e]);
+                        u[e] = __float_as_uint(first_time ? v : v + __uint_as_float(u[e]));
+                    }
+                    tc_store8(sum_at + 8 * c, u);
+                }
+                tc_wait_store();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) barrier_arrive(&misc.summed[((t + 1) / FLUSH - 1) & 1]);
+            }
         }
 
         // ---- the partial results, through the ring's place: nothing reads or fills it once
         // the last products are complete ----
         ok = ok && barrier_wait(&misc.o_full, 0, dead);
         ok = __all_sync(~0u, ok);
+        if constexpr (S::ADDED) {  // (the one stream may still be at its sum)
+            tc_fence_before();
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+        }
         tc_fence_after();
         misc.ref[s][i] = ref, misc.sum[s][i] = l;
         // partial results of the ordinary kernel carry 2^ATTN_SHIFT_F16 over fp16 caches
@@ -1068,6 +1148,13 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         for (int c = 8 * s; c < D16 && ok; c += 16) {
             uint32_t x[8];
             tc_load8(o_at + c, x);
+            if (S::ADDED && tiles > FLUSH) {
+                uint32_t u[8];
+                tc_load8(sum_at + c, u);
+                tc_wait_load();
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) + __uint_as_float(u[k]));
+            }
             tc_wait_load();
 #pragma unroll
             for (int k = 0; k < 8; k += 4)
@@ -1104,7 +1191,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 template <bool HALF, int QP, int NB, bool Q8>
 cudaError_t prefix_launch_of(const TcArgs &a, int grid, void *stream, unsigned int *status) {
     auto *kern = prefix_kernel<HALF, QP, NB, Q8>;
-    constexpr int smem = TcShape<QP, NB, Q8>::SMEM;
+    constexpr int smem = TcShape<HALF, QP, NB, Q8>::SMEM;
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

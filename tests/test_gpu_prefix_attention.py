@@ -175,6 +175,38 @@ def test_a_long_prefix(kind, dtype):
     case(rng("long", kind), kind, dtype, lens, 9003, 24, 8, 2, 128, hurt=False)
 
 
+@pytest.mark.parametrize("kind,dtype,D", [("f16", F32, 64), ("f16", F16, 128), ("bf16", BF16, 64), ("bf16", F32, 64),
+                                          ("q8_0", F32, 64), ("q8_0", BF16, 128)])
+@pytest.mark.parametrize("shared", [1111, 4100])
+def test_long_chunks(kind, dtype, D, shared):
+    """Row tiles and heads enough for the whole GPU, so that a chunk is many tiles of
+    positions long and O is added up several times; the maximum grows late in some rows.
+    Against the ordinary kernel, whose own error is within its bound."""
+    g = rng("chunks", kind, str(dtype), shared)
+    requests, heads, kv, page = 200, 32, 16, 32
+    lens = [shared + 5 + int(n) for n in g.integers(0, 30, requests)]
+    pages = pages_needed(lens, [(requests, shared)], page)
+    cache = filled_cache(g, kind, pages, page, kv, D)
+    table = shared_table(g, lens, [(requests, shared)], page, pages)
+    late = table[0, shared // page - 2].long()
+    if kind == "q8_0":
+        cache.k_scale[late] *= 3
+    else:
+        cache.k[late] *= 3
+    q = normal(g, (requests * 5, heads, D), dtype)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = bq.paged_attention(cache, q, table, at, rows=5).double()
+    got = bq.paged_prefix_attention(cache, q, table, at, shared, rows=5).double()
+    # values N(0, 1) (Q8_0: rms 2.2, at most 3.81): outputs below 4, mean magnitudes below 4.
+    # Scores below 60 of magnitude 200: both forms are off by at most twice 2^-17 of that in
+    # the weights, 2^-14 in the sums, 2^-17 in bf16 weights, and half a unit of the output.
+    rel = 2 * (2.0 ** -17 * 200 + 2.0 ** -20) + 2.0 ** -14 + 2.0 ** -17
+    assert float((got - want).abs().max()) <= 2 * (rel * 4 + plain.EPS[dtype] / 2 * 4)
+    # and over all of them, where the errors are of both signs: a hundredth of that bound
+    # beside the output's rounding (fp32: sums of thousands of terms, 2^-24 * 64 of them)
+    assert float((got - want).norm() / want.norm()) <= plain.EPS[dtype] + 2.0 ** -16
+
+
 @pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
 @pytest.mark.parametrize("rows", [2, 5, 6])
 def test_verify_rows(kind, dtype, rows):
