@@ -455,3 +455,23 @@ def test_refusals():
         bq.SharedBlockTables(3, 4, 20, 4, 16, caches)
     with pytest.raises(ValueError):
         bq.kv_compact(t.lens, t.table, t.free_pages, t.free_count, t.refs, 4, one, torch.zeros(2, **I32), one.clone(), t.refs)
+
+
+def test_the_readmes_example_of_a_shared_prompt():
+    import os
+    import re
+
+    import paged_plain
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    with open(os.path.join(root, "README.md")) as f:
+        first, second = re.findall(r"```python\n(.*?)```", f.read(), flags=re.S)[:2]
+    said = {}
+    exec(first + second, said)
+    n, lens = said["requests"], [said["prompt"] + 1] * said["requests"]
+    table, cache, q = said["shared"].table.cpu(), said["cache"], said["q"]
+    want, mag, top = paged_plain.attention(*paged_plain.values(cache), q.cpu(), table, lens, 1, cache.head_dim ** -0.5)
+    bound = paged_plain.attention_bound(want, mag, top, F32, False)
+    assert ((said["out"].cpu().double() - want).abs() <= bound).all()
+    # 40 positions in 2 whole pages and a half: the forks share two and have one of their own
+    assert int(said["shared"].refs.max()) == n and int(said["shared"].free_count) == 64 - 2 - n
