@@ -217,7 +217,7 @@ Chunking chunking_of(int64_t requests, int64_t kv_heads, int64_t capacity) {
 }
 
 // validation of shapes and choice of the instance
-bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
+bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p, bool shared = false) {
     if (!c || !x) return BQ_ERR_NULL;
     const bq_status s = bq::check_attention_shape(c, x);
     if (s != BQ_OK) return s;
@@ -236,7 +236,7 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, Plan *p) {
     a.mode = bq::ATTN_ALL;
     const int nt = bq::attn_tiles(c, a.group_rows);
     a.row_tiles = (a.group_rows + 8 * nt - 1) / (8 * nt);
-    p->inst = bq::attn_instance(c, x->dtype, nt);
+    p->inst = bq::attn_instance(c, x->dtype, nt, shared);
     if (!p->inst) return BQ_ERR_SHAPE;
     p->smem = p->inst->smem + (size_t)(x->requests + 1) * sizeof(int);
     p->units = (int64_t)x->requests * a.max_chunks * c->kv_heads * a.row_tiles;
@@ -288,14 +288,19 @@ int attn_tiles(const bq_kv_cache *c, int64_t group_rows) {
     return group_rows <= 8 ? 1 : group_rows <= 16 || padded_dim(c) == 256 || c->type == BQ_Q8_0 ? 2 : 4;
 }
 
-const AttnInstance *attn_instance(const bq_kv_cache *c, int dtype, int nt) {
-    int n = 0;
+const AttnInstance *attn_instance(const bq_kv_cache *c, int dtype, int nt, bool modes) {
+    using Table = const AttnInstance *(*)(int *);
     const bool same = dtype == c->type;
-    const AttnInstance *inst =
-        c->type == BQ_F16      ? (same ? bq_internal_attn_f16_own(&n) : bq_internal_attn_f16_split(&n))
-        : c->type == BQ_BF16   ? (same ? bq_internal_attn_bf16_own(&n) : bq_internal_attn_bf16_split(&n))
-        : dtype != BQ_F32      ? bq_internal_attn_q8_0_own(&n)
-                               : bq_internal_attn_q8_0_split(&n);
+    const Table of[3][2][2] = {
+        {{bq_internal_attn_f16_split, bq_internal_attn_f16_own},
+         {bq_internal_attn_f16_split_shared, bq_internal_attn_f16_own_shared}},
+        {{bq_internal_attn_bf16_split, bq_internal_attn_bf16_own},
+         {bq_internal_attn_bf16_split_shared, bq_internal_attn_bf16_own_shared}},
+        {{bq_internal_attn_q8_0_split, bq_internal_attn_q8_0_own},
+         {bq_internal_attn_q8_0_split_shared, bq_internal_attn_q8_0_own_shared}}};
+    const int kind = c->type == BQ_F16 ? 0 : c->type == BQ_BF16 ? 1 : 2;
+    int n = 0;
+    const AttnInstance *inst = of[kind][modes][kind == 2 ? dtype != BQ_F32 : same](&n);
     for (int i = 0; i < n; ++i)
         if (inst[i].dim == padded_dim(c) && inst[i].nt == nt) return &inst[i];
     return nullptr;
@@ -335,7 +340,7 @@ extern "C" int64_t bq_paged_attention_workspace_bytes(const bq_kv_cache *cache, 
 bq_status bq_internal_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, const bq::AttnArgs *shared,
                                       void *workspace, int64_t workspace_bytes, void *stream) {
     Plan p;
-    bq_status s = plan_of(cache, x, &p);
+    bq_status s = plan_of(cache, x, &p, shared != nullptr);
     if (s != BQ_OK) return s;
     if (x->requests == 0) return BQ_OK;
     s = bq::check_attention_pointers(cache, x);

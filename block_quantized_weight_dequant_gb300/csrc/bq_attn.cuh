@@ -234,13 +234,14 @@ struct AttnShape {
     static_assert(STAGES >= 2 && RING % 16 == 0 && STAGE % 16 == 0 && TILE > BQ_VERIFY_MAX_ROWS);
 };
 
-template <int KV, int QP, int PP, int DP, int NT>
+template <int KV, int QP, int PP, int DP, int NT, bool MODES>
 __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, AttnShape<KV, QP, PP, DP, NT>::OCC)
     attn_kernel(const __grid_constant__ AttnArgs a, unsigned int *status) {
     using S = AttnShape<KV, QP, PP, DP, NT>;
     constexpr bool Q8 = S::Q8, HALF = S::HALF;
     constexpr int TT = S::TT, ROWS = S::ROWS, TILE = S::TILE, STAGES = S::STAGES, ROWB = S::ROWB;
     constexpr int WARPS = S::WARPS;
+    const int mode = MODES ? a.mode : (int)ATTN_ALL;  // (known, it costs the ordinary calls nothing)
     constexpr int MT = DP / 16;  // 16-row tiles of O^T
     constexpr float SHIFT = HALF ? (float)ATTN_SHIFT_F16 : 0.0f;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -255,10 +256,10 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     const int B = a.x.requests, R = a.x.rows, D = a.c.head_dim, KVH = a.c.kv_heads;
     const int most = a.x.table_width * a.c.page_size;
     pdl_wait();
-    const bool parts = a.mode == ATTN_REST || a.mode == ATTN_PREFIX;  // partial results alone
+    const bool parts = mode == ATTN_REST || mode == ATTN_PREFIX;  // partial results alone
     if ((a.max_chunks > 1 && !a.cluster) || parts) pdl_launch_dependents();
 
-    const bool shared = a.mode == ATTN_PREFIX;
+    const bool shared = mode == ATTN_PREFIX;
     // pages that request b shares
     auto common = [&](int b) {
         int g = 0;
@@ -266,13 +267,13 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         return a.group_pages[g];
     };
     // pages before the first position that this launch covers of request b
-    auto skipped = [&](int b) { return a.mode == ATTN_REST ? common(b) : 0; };
+    auto skipped = [&](int b) { return mode == ATTN_REST ? common(b) : 0; };
     auto length = [&](int b) {
         if (shared) return a.group_pages[b] * a.c.page_size;
         const int n = min(max(a.x.lens[b], 0), most);
-        if (a.mode == ATTN_ALL) return n;
+        if (mode == ATTN_ALL) return n;
         const int before = common(b) * a.c.page_size, rest = attn_rest(n, R, before);
-        return a.mode == ATTN_REST ? rest : n - R + 1 >= before ? n : 0;
+        return mode == ATTN_REST ? rest : n - R + 1 >= before ? n : 0;
     };
     const long long per_chunk = (long long)KVH * a.row_tiles;
     // direct: a CTA per unit that the table can hold, units beyond a request's
@@ -282,7 +283,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     auto checked = [&](int b) {
         if (shared) return;
         const int len = a.x.lens[b];
-        if (len < 0 || len > most || (len && a.mode != ATTN_ALL && len - R + 1 < common(b) * a.c.page_size))
+        if (len < 0 || len > most || (len && mode != ATTN_ALL && len - R + 1 < common(b) * a.c.page_size))
             atomicOr(status, BQ_DEVERR_LENGTH);
     };
     if (!direct) {
@@ -927,9 +928,9 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     }
 }
 
-template <int KV, int QP, int PP, int DP, int NT>
+template <int KV, int QP, int PP, int DP, int NT, bool MODES>
 int attn_occupancy(size_t smem, int *out) {
-    auto *kern = attn_kernel<KV, QP, PP, DP, NT>;
+    auto *kern = attn_kernel<KV, QP, PP, DP, NT, MODES>;
     static std::atomic<unsigned long long> known[64];  // per device: smem << 8 | CTAs per SM
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -953,22 +954,22 @@ int attn_occupancy(size_t smem, int *out) {
 }  // namespace bq
 
 // the instances of one cache type and way of carrying queries, for head_dim up to
-// 64, 128 and 256
-#define BQ_ATTN_INST(KV, QP, PP, DP, NT)                                                           \
+// 64, 128 and 256, of the ordinary calls or (MODES) of those over shared pages
+#define BQ_ATTN_INST(KV, QP, PP, DP, NT, MODES)                                                    \
     {                                                                                              \
         DP, NT, (size_t)bq::AttnShape<KV, QP, PP, DP, NT>::SMEM,                                   \
-            bq::attn_occupancy<KV, QP, PP, DP, NT>,                                                \
+            bq::attn_occupancy<KV, QP, PP, DP, NT, MODES>,                                         \
             [](const bq::AttnArgs &a, int grid, size_t smem, void *stream,                         \
                unsigned int *status) -> cudaError_t {                                              \
-                return bq::launch_pdl(bq::attn_kernel<KV, QP, PP, DP, NT>, dim3((unsigned)grid),   \
-                                      bq::ATTN_WARPS * 32, smem, stream,                           \
+                return bq::launch_pdl(bq::attn_kernel<KV, QP, PP, DP, NT, MODES>,                  \
+                                      dim3((unsigned)grid), bq::ATTN_WARPS * 32, smem, stream,     \
                                       a.cluster ? a.max_chunks : 1, a, status);                    \
             }                                                                                      \
     }
-#define BQ_ATTN_INSTS(KV, QP, PP)                                                                  \
-    BQ_ATTN_INST(KV, QP, PP, 64, 1), BQ_ATTN_INST(KV, QP, PP, 64, 2),                              \
-        BQ_ATTN_INST(KV, QP, PP, 128, 1), BQ_ATTN_INST(KV, QP, PP, 128, 2),                        \
-        BQ_ATTN_INST(KV, QP, PP, 256, 1), BQ_ATTN_INST(KV, QP, PP, 256, 2)
+#define BQ_ATTN_INSTS(KV, QP, PP, MODES)                                                           \
+    BQ_ATTN_INST(KV, QP, PP, 64, 1, MODES), BQ_ATTN_INST(KV, QP, PP, 64, 2, MODES),                \
+        BQ_ATTN_INST(KV, QP, PP, 128, 1, MODES), BQ_ATTN_INST(KV, QP, PP, 128, 2, MODES),          \
+        BQ_ATTN_INST(KV, QP, PP, 256, 1, MODES), BQ_ATTN_INST(KV, QP, PP, 256, 2, MODES)
 #define BQ_ATTN_UNIT(NAME, ...)                                                                    \
     const bq::AttnInstance *bq_internal_attn_##NAME(int *n) {                                      \
         static const bq::AttnInstance inst[] = {__VA_ARGS__};                                      \

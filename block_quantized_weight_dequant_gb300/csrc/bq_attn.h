@@ -74,8 +74,9 @@ struct AttnInstance {
 // what bqgemv.h says of bq_attention_args: shapes, then pointers (and the cache's)
 bq_status check_attention_shape(const bq_kv_cache *c, const bq_attention_args *x);
 bq_status check_attention_pointers(const bq_kv_cache *c, const bq_attention_args *x);
-// the instance that serves the call's types with nt n-tiles, NULL if there is none
-const AttnInstance *attn_instance(const bq_kv_cache *c, int dtype, int nt);
+// the instance that serves the call's types with nt n-tiles, in ATTN_ALL or another
+// mode, NULL if there is none
+const AttnInstance *attn_instance(const bq_kv_cache *c, int dtype, int nt, bool modes);
 // n-tiles for a number of query rows of a kv head
 int attn_tiles(const bq_kv_cache *c, int64_t group_rows);
 
@@ -83,11 +84,17 @@ int attn_tiles(const bq_kv_cache *c, int64_t group_rows);
 
 // instance tables by cache type and split; n receives the number
 const bq::AttnInstance *bq_internal_attn_f16_own(int *n);
+const bq::AttnInstance *bq_internal_attn_f16_own_shared(int *n);
 const bq::AttnInstance *bq_internal_attn_f16_split(int *n);
+const bq::AttnInstance *bq_internal_attn_f16_split_shared(int *n);
 const bq::AttnInstance *bq_internal_attn_bf16_own(int *n);
+const bq::AttnInstance *bq_internal_attn_bf16_own_shared(int *n);
 const bq::AttnInstance *bq_internal_attn_bf16_split(int *n);
+const bq::AttnInstance *bq_internal_attn_bf16_split_shared(int *n);
 const bq::AttnInstance *bq_internal_attn_q8_0_own(int *n);
+const bq::AttnInstance *bq_internal_attn_q8_0_own_shared(int *n);
 const bq::AttnInstance *bq_internal_attn_q8_0_split(int *n);
+const bq::AttnInstance *bq_internal_attn_q8_0_split_shared(int *n);
 
 // bq_attn.cu: the call in one pass, with the groups of `shared` (or NULL)
 bq_status bq_internal_paged_attention(const bq_kv_cache *cache, const bq_attention_args *x, const bq::AttnArgs *shared,

@@ -1,0 +1,5 @@
+// bq_attn_bf16_own_shared.cu -- attention passes around shared pages of a bf16 cache, bf16 queries (bq_attn.cuh).
+#include "bq_attn.cuh"
+
+BQ_ATTN_UNIT(bf16_own_shared, BQ_ATTN_INSTS(bq::KV_BF16, 1, 3, true),
+             BQ_ATTN_INST(bq::KV_BF16, 1, 3, 64, 4, true), BQ_ATTN_INST(bq::KV_BF16, 1, 3, 128, 4, true))

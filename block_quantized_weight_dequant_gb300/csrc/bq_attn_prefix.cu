@@ -217,7 +217,7 @@ bool size_parts(Pass *p, int requests) {
 bool size_pass(Pass *p, int requests, int64_t rows, int64_t positions, int pairs_of) {
     const bq_kv_cache *c = &p->a.c;
     const int nt = bq::attn_tiles(c, rows);
-    p->inst = bq::attn_instance(c, p->a.x.dtype, nt);
+    p->inst = bq::attn_instance(c, p->a.x.dtype, nt, true);
     if (!p->inst) return false;
     p->tile_rows = 8 * nt;
     p->a.group_rows = (int)rows;
