@@ -100,6 +100,40 @@ def test_types_and_heads(kind, dtype, D, heads, kv):
     case(rng("p", kind, str(dtype), D), kind, dtype, lens, 288, 16, heads, kv, D)
 
 
+@pytest.mark.parametrize("kind,dtype", [("f16", F16), ("f16", F32), ("bf16", BF16), ("bf16", F32)])
+@pytest.mark.parametrize("D,page", [(8, 8), (24, 16), (40, 40), (72, 5), (120, 24)])
+def test_odd_heads(kind, dtype, D, page):
+    """Heads that are no whole steps or blocks of the tensor cores, one kv head and three."""
+    for kv in (1, 3):
+        g = rng("odd", kind, str(dtype), D, kv)
+        case(g, kind, dtype, [650, 641, 699, 0, 640], 640, page, 4 * kv, kv, D, layout=("hs", "sh")[kv == 3])
+
+
+@pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
+def test_pages_beyond_32_bits(kind, dtype):
+    """Pages whose offset is above 2^31 elements (2^32 bytes in 16 bits), copied there
+    from the front first."""
+    g = rng("far", kind)
+    D, kv, page, pool, requests, shared = 128, 8, 16, 140000, 12, 700
+    small = filled_cache(g, kind, 160, page, kv, D)
+    lens = [shared + 1 + int(n) for n in g.integers(0, 20, requests)]
+    near = shared_table(g, lens, [(requests, shared)], page, 160)
+    planes = [torch.empty((pool,) + t.shape[1:], dtype=t.dtype, device=DEV) for t in
+              (small.k, small.v) + (() if small.k_scale is None else (small.k_scale, small.v_scale))]
+    for big, t in zip(planes, (small.k, small.v, small.k_scale, small.v_scale)):
+        big[:160] = t
+    cache = bq.PagedKVCache(*planes)
+    assert cache.k.stride(0) * (pool - 200) > 2 ** 31
+    src = torch.arange(160, dtype=torch.int32, device=DEV)
+    bq.kv_copy_pages(cache, src, pool - 1 - src)
+    q = normal(g, (requests, 16, D), dtype)
+    at = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    want = bq.paged_prefix_attention(small, q, near, at, shared)
+    far = torch.where(near >= 0, pool - 1 - near, near)
+    assert torch.equal(bq.paged_prefix_attention(cache, q, far, at, shared), want)
+    assert torch.equal(bq.paged_attention(cache, q, far, at), bq.paged_attention(small, q, near, at))
+
+
 @pytest.mark.parametrize("kind,dtype", [("f16", F32), ("bf16", BF16), ("q8_0", F32)])
 @pytest.mark.parametrize("shared", [0, 1, 15, 16, 17, 127, 128, 129, 255, 257, 640, 1000])
 def test_shared_lengths(kind, dtype, shared):
