@@ -442,6 +442,50 @@ def test_captured_and_replayed_with_other_lengths_beside_another_graph():
             assert torch.equal(out, bq.paged_prefix_attention(cache, q, table, lens, 640))
 
 
+@pytest.mark.parametrize("kind", ["f16", "bf16", "q8_0"])
+@pytest.mark.parametrize("requests,shared,heads,kv,D", [(40, 2049, 16, 4, 128), (9, 1030, 14, 2, 64)])
+def test_steps_back_to_back(kind, requests, shared, heads, kv, D):
+    """A token appended and attended, step after step with nothing between the launches,
+    eager and replayed, has the bits of the steps that are waited for."""
+    g, page, own, steps = rng("steps", kind, requests), 16, 4, 12
+    whole = shared // page
+    at = whole * page + 3
+    first = filled_cache(g, kind, whole + requests * own, page, kv, D)
+    planes = [t for t in (first.k, first.v, first.k_scale, first.v_scale) if t is not None]
+    table = torch.arange(whole, dtype=torch.int32).expand(requests, -1)
+    table = torch.cat([table, whole + torch.arange(requests * own, dtype=torch.int32).view(requests, own)], 1).to(DEV)
+    k, v = (normal(g, (steps, requests, kv, D), F16) for _ in range(2))
+    q = normal(g, (steps, requests, heads, D), F16)
+    slots = [table[:, (at + i) // page].long() * page + (at + i) % page for i in range(steps)]
+    lens = [torch.full((requests,), at + i + 1, dtype=torch.int32, device=DEV) for i in range(steps)]
+
+    def run(cache, wait):
+        out = []
+        for i in range(steps):
+            bq.kv_append(cache, k[i], v[i], slots[i])
+            wait()
+            out.append(bq.paged_prefix_attention(cache, q[i], table, lens[i], shared))
+            wait()
+        return out
+
+    def fresh():
+        return bq.PagedKVCache(*[t.clone() for t in planes])
+
+    want = run(fresh(), torch.cuda.synchronize)
+    for _ in range(4):
+        got = run(fresh(), lambda: None)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    cache = fresh()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(cache, lambda: None)
+    for _ in range(4):
+        for x, y in zip((cache.k, cache.v, cache.k_scale, cache.v_scale), planes):
+            x.copy_(y)
+        graph.replay()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 def test_it_agrees_with_ordinary_attention_at_a_servers_size():
     """Both forms of one call lie within their bounds of one another."""
     g = rng("both")
