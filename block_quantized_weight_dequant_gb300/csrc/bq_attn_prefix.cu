@@ -230,8 +230,8 @@ bool size_pass(Pass *p, int requests, int64_t rows, int64_t positions, int pairs
 // The tensor-memory kernel for heads of up to 128 values: tiles of 128 rows, chunks
 // of whole tiles of positions, one CTA per SM.  Over a Q8_0 cache, whose codes it has
 // to put into two 16-bit parts, for more rows of a kv head than two passes of the
-// ordinary kernel's 16: 30011 shared, 8 kv heads of 128, fp32 queries, 32 rows 79 us
-// against 56, 48 rows 80 against 92, 128 rows 90 against 192.
+// ordinary kernel's 16: 30011 shared, 8 kv heads of 128, fp32 queries, 32 rows 59 us
+// against 53, 48 rows 68 against 90, 128 rows 89 against 185.
 constexpr int64_t Q8_ROWS = 32;
 bool has_tensor_kernel(const bq_kv_cache *c, int64_t rows) {
     return c->head_dim <= 128 && (c->type != BQ_Q8_0 || rows > Q8_ROWS);

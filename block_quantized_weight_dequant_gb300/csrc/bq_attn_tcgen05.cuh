@@ -21,7 +21,14 @@
 // as rows.  One thread of warp 11 issues all products.  Queries are a first operand
 // in tensor memory; the weights go back there in the columns of the scores that they
 // come from, and are the first operand of the second product.  Over a Q8_0 cache
-// warps 8 to 10 put codes times scales into parts on the way, tiles of 64 positions.
+// warps 8 to 10, and those of warps 0 to 7 whose 32 rows are none of the group's, put
+// codes times scales into parts on the way, tiles of 64 positions: 48 rows of a kv head
+// 80 -> 68 us a call, 96 86 -> 74 (30011 shared, 8 kv heads of 128).
+//
+// Bounds.  96 requests of 32801 shared, bf16, 32 over 8 heads of 128: 57 us, 901 TFLOP/s
+// of scores and values counted once; products keep the tensor pipe busy for 55% (second
+// parts of the weights half of PV), the issue of their instructions 35%, and 144 of 152
+// SMs have a chunk.  Over Q8_0 the putting into parts: 128 rows 4400 cycles a tile.
 //
 // Precision.  A query of the cache's type is used as it is, any other in QP 16-bit
 // parts (fp16 2, after scaling the row by a power of two; bf16 3); weights are two
@@ -73,11 +80,11 @@ struct TcShape {
     static_assert(PP == 2 || (SUM + NB * 64 <= REST && REST + 2 * TILE / 2 <= TC_COLUMNS));
     static constexpr int SLOT = KP * NB * BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_QBLOCK;
     static constexpr int LIMIT = 227 * 1024, MISC = 3072;
-    // Q8_0: codes and scales on their way, RAW tiles of them; a lane's 32 codes and a word
-    // with its scale, rows of a copying warp (MINE turns of it) beside one another
+    // Q8_0: codes and scales on their way, RAW tiles of them, by groups of AT_ONCE rows; a
+    // lane's 32 codes and a word with its scale
     static constexpr int RAW = 3, LANES = 2 * NB, AT_ONCE = 32 / LANES, GROUPS = TILE / AT_ONCE;
     static constexpr int MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;
-    static constexpr int RAW_WARP = 32 * (32 + 4), RAW_TILE = 2 * MINE * TC_COPY_WARPS * RAW_WARP;
+    static constexpr int RAW_WARP = 32 * (32 + 4), RAW_TILE = 2 * GROUPS * RAW_WARP;
     static constexpr int RAW_BYTES = Q8 ? RAW * RAW_TILE : 0;
     static constexpr int most = (LIMIT - MISC - Q_BYTES - RAW_BYTES) / SLOT;
     static constexpr int SLOTS = most > 8 ? 8 : most;
@@ -389,23 +396,31 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     const int begin = ck * a.chunk, end = min(begin + a.chunk, common);
     if (begin >= end || first_row >= group_rows) return;
     const int D16 = (D + 15) & ~15;
+    // Q8_0: softmax warps whose 32 rows are none of the group's put codes into parts instead
+    const int quads = Q8 ? min(4, (group_rows - first_row + 31) / 32) : 4;  // warps of a stream with rows
+    const int copiers = TC_COPY_WARPS + 2 * (4 - quads);
+    const bool softmax = warp < TC_SOFTMAX_WARPS && (!Q8 || (warp & 3) < quads);
+    auto softmax_sync = [&] {
+        if constexpr (Q8) asm volatile("bar.sync 1, %0;" ::"r"(64 * quads) : "memory");
+        else asm volatile("bar.sync 1, 256;" ::: "memory");
+    };
 
     // ---- barriers and tensor memory, while the kernel before ends ----
     if (tid == 0) {
-        const int copying = !Q8 && args.box ? 1 : TC_COPY_WARPS;
+        const int copying = Q8 ? copiers : args.box ? 1 : TC_COPY_WARPS;
         for (int i = 0; i < SLOTS; ++i) barrier_init(&misc.full[i], copying), barrier_init(&misc.empty[i], 1);
         for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], copying);
         for (int i = 0; i < 2; ++i) {
             barrier_init(&misc.s_full[i], 1);
-            for (int k = 0; k < 2; ++k) barrier_init(&misc.p_full[i][k], TC_SOFTMAX_WARPS / 2);
+            for (int k = 0; k < 2; ++k) barrier_init(&misc.p_full[i][k], quads);
             for (int k = 0; k < 4; ++k) barrier_init(&misc.ref_full[i][k], 1);
         }
-        barrier_init(&misc.q_full, TC_SOFTMAX_WARPS);
+        barrier_init(&misc.q_full, 2 * quads);
         for (int i = 0; i < 2; ++i) {
             barrier_init(&misc.added[i], 1);
-            barrier_init(&misc.summed[i], TC_SOFTMAX_WARPS / 2);
+            barrier_init(&misc.summed[i], quads);
         }
-        barrier_init(&misc.flushed, TC_SOFTMAX_WARPS / 2);
+        barrier_init(&misc.flushed, quads);
         barrier_init(&misc.o_full, 1);
         misc.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -445,17 +460,26 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         if (tid < 2) misc.top_scale[tid] = 0;
         __syncthreads();
         uint32_t top[2] = {0, 0};
-        const int blocks = D >> 5, many = tiles ? (end - begin) * blocks : 0;
-#pragma unroll 4
-        for (int i = tid; i < many; i += TC_WARPS * 32) {
-            const int r = i / blocks, p = begin + r;
-            const long long off = offset_of(p, row_table[a.page.div((uint32_t)p)]);
-            if (off < 0) continue;
-            const long long at = (off >> 5) + (i - r * blocks);
-            const uint32_t k = static_cast<const uint16_t *>(a.c.k_scale)[at] & 0x7fffu;
-            const uint32_t v = static_cast<const uint16_t *>(a.c.v_scale)[at] & 0x7fffu;
-            if (k < 0x7c00u) top[0] = max(top[0], k);  // (the finite ones: ordered as their bits)
-            if (v < 0x7c00u) top[1] = max(top[1], v);
+        // (positions to threads, so that few loads wait for one another: with scales to
+        // threads this took a third of the pass)
+        const int blocks = D >> 5, last = tiles ? end : begin;
+        for (int p0 = begin + tid; p0 < last; p0 += 4 * TC_WARPS * 32) {
+            long long at[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int p = p0 + u * TC_WARPS * 32;
+                at[u] = p < last ? offset_of(p, row_table[a.page.div((uint32_t)p)]) : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int j = 0; j < 2 * NB; ++j) {
+                    if (at[u] < 0 || j >= blocks) continue;
+                    const uint32_t k = static_cast<const uint16_t *>(a.c.k_scale)[(at[u] >> 5) + j] & 0x7fffu;
+                    const uint32_t v = static_cast<const uint16_t *>(a.c.v_scale)[(at[u] >> 5) + j] & 0x7fffu;
+                    if (k < 0x7c00u) top[0] = max(top[0], k);  // (the finite ones: ordered as their bits)
+                    if (v < 0x7c00u) top[1] = max(top[1], v);
+                }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -477,24 +501,27 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     }
 
     if (tiles == 0) {
-    } else if (Q8 && warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
-        // ---- Q8_0: every third 8 (16) rows by each warp, a lane a scale's 32 codes; the next
+    } else if (Q8 && !softmax && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
+        // ---- Q8_0: 8 (16) rows to each warp in turn, a lane a scale's 32 codes; the next
         // tile's are on their way while one is put into parts ----
         if constexpr (Q8) {
             constexpr int LANES = S::LANES, AT_ONCE = S::AT_ONCE, GROUPS = S::GROUPS, MINE = S::MINE, RAW = S::RAW;
-            const int cw = warp - TC_SOFTMAX_WARPS, part = lane % LANES, sub = lane / LANES;
+            const int cw = warp >= TC_SOFTMAX_WARPS ? warp - TC_SOFTMAX_WARPS
+                                                    : TC_COPY_WARPS + (warp >> 2) * (4 - quads) + (warp & 3) - quads;
+            const int mine = cw < GROUPS ? (GROUPS - cw + copiers - 1) / copiers : 0;  // groups of this warp
+            const int part = lane % LANES, sub = lane / LANES;
             const bool inside = 32 * part < D;
             // the halves of the 32 codes in an order that keeps a warp's stores apart in the
             // banks: lanes of another 64-value block take the other half first
             const int turn = part >> 1 & 1;
-            uint8_t *raw = ring + SLOTS * S::SLOT + cw * S::RAW_WARP;
+            uint8_t *raw = ring + SLOTS * S::SLOT;
             auto place = [&](int t, int v, int q) {
-                return raw + (t % RAW) * S::RAW_TILE + (v * MINE + q) * TC_COPY_WARPS * S::RAW_WARP;
+                return raw + (t % RAW) * S::RAW_TILE + (v * GROUPS + cw + copiers * q) * S::RAW_WARP;
             };
-            auto row_of = [&](int q) { return (cw + TC_COPY_WARPS * q) * AT_ONCE + sub; };
+            auto row_of = [&](int q) { return (cw + copiers * q) * AT_ONCE + sub; };
             auto entry_of = [&](int q, int t) {
                 const int p = begin + t * TILE + row_of(q);
-                return row_of(q) < TILE && t < tiles && p < end ? row_table[a.page.div((uint32_t)p)] : -1;
+                return q < mine && t < tiles && p < end ? row_table[a.page.div((uint32_t)p)] : -1;
             };
             int entry[MINE];
             uint32_t odd = 0;    // likewise: the scale is the second half of its word
@@ -505,8 +532,9 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 there &= of_tile, odd &= of_tile;
 #pragma unroll
                 for (int q = 0; q < MINE; ++q) {
+                    if (q >= mine) break;
                     const int p = begin + t * TILE + row_of(q);
-                    const bool in = row_of(q) < TILE && t < tiles && p < end;
+                    const bool in = t < tiles && p < end;
                     const long long off = in ? offset_of(p, entry[q]) : -1;
                     if (in && off < 0 && part == 0) atomicOr(status, BQ_DEVERR_PAGE);
                     if (off >= 0) there |= 1u << (t % 4 * MINE + q);
@@ -550,8 +578,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                             uint32_t bits = 0;
 #pragma unroll
                             for (int r = 0; r < AT_ONCE; ++r) bits |= (live >> (r * LANES) & 1) << r;
-                            if (lane < AT_ONCE / 8 && cw + TC_COPY_WARPS * q < GROUPS)
-                                misc.mask[t % TC_MASKS][(cw + TC_COPY_WARPS * q) * (AT_ONCE / 8) + lane] =
+                            if (lane < AT_ONCE / 8 && q < mine)
+                                misc.mask[t % TC_MASKS][(cw + copiers * q) * (AT_ONCE / 8) + lane] =
                                     (uint8_t)(bits >> (8 * lane));
                         }
                         __syncwarp();
@@ -560,8 +588,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     const uint32_t to = tc_shared(ring) + slot * S::SLOT + (part >> 1) * BLOCK;
 #pragma unroll
                     for (int q = 0; q < MINE; ++q) {
+                        if (q >= mine) break;
                         const int row = row_of(q);
-                        if (row >= TILE) continue;
                         // (a power of two times an fp16 number; exact in fp32, and in fp16 unless so
                         // small beside the chunk's largest that nothing of it is left)
                         const uint8_t *from = place(t, v, q);
@@ -806,11 +834,11 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             const bool more = t + 2 < tiles;
             uint64_t *keys = more ? &misc.full[k_slot] : &misc.full[v_slot];
             const uint32_t keys_phase = more ? k_phase : v_phase;
-            const uint32_t there = barrier_test(&misc.full[v_slot], v_phase) & barrier_test(keys, keys_phase) &
+            const uint32_t there = barrier_test(&misc.full[v_slot], v_phase) & (Q8 || barrier_test(keys, keys_phase)) &
                                    barrier_test(&misc.p_full[s][0], t >> 1 & 1);
             if (!__all_sync(~0u, there)) {
                 waits(&misc.full[v_slot], v_phase);
-                waits(keys, keys_phase);
+                if (!Q8) waits(keys, keys_phase);
                 waits(&misc.p_full[s][0], t >> 1 & 1);
             }
             if (S::ADDED && t && t % FLUSH == 0) waits(&misc.flushed, (t / FLUSH - 1) & 1);
@@ -825,9 +853,18 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 output(t, 1);
                 tc_commit(&misc.empty[v_slot]);
                 tc_commit(&misc.added[s]);
-                if (more) scores(t + 2);
+                if (!Q8 && more) scores(t + 2);
             }
             __syncwarp();
+            // Q8_0: with 5 slots those keys take the place of the values before, and are put
+            // into parts while the products above run
+            if (Q8 && more) {
+                waits(keys, keys_phase);
+                if (!ok) break;
+                tc_fence_after();
+                if (elect_one()) scores(t + 2);
+                __syncwarp();
+            }
             next(v_slot, v_phase);
             next(k_slot, k_phase);
         }
@@ -887,7 +924,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             Scaling by = {1.0f, 1.0f, size};
             if constexpr (SCALED) {
                 misc.sum[s][i] = top;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                softmax_sync();
                 by = scaling(fmaxf(misc.sum[0][i], misc.sum[1][i]));
                 factor = by.factor;
             }
@@ -947,7 +984,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             if (lane == 0) barrier_arrive(&misc.q_full);
             factor = size;
             if constexpr (SCALED) {
-                asm volatile("bar.sync 1, 256;" ::: "memory");  // factors of all rows
+                softmax_sync();  // factors of all rows
                 factor = misc.sum[0][i];
             }
         }
@@ -1137,7 +1174,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         ok = __all_sync(~0u, ok);
         if constexpr (S::ADDED) {  // (the one stream may still be at its sum)
             tc_fence_before();
-            asm volatile("bar.sync 1, 256;" ::: "memory");
+            softmax_sync();
         }
         tc_fence_after();
         misc.ref[s][i] = ref, misc.sum[s][i] = l;
@@ -1162,7 +1199,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     make_float4(out * __uint_as_float(x[k]), out * __uint_as_float(x[k + 1]),
                                 out * __uint_as_float(x[k + 2]), out * __uint_as_float(x[k + 3]));
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        softmax_sync();
         const long long unit = (((long long)g * a.max_chunks + ck) * KVH + h) * a.row_tiles + rt;
         if (s == 0 && first_row + i < group_rows) {
             // O belongs to the last tile's reference, which the other stream's sum may not
@@ -1175,7 +1212,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         if (4 * lane < D) {
             float *dst = a.part_o + unit * TC_ROWS * D + 4 * lane;
             const float *src = reinterpret_cast<const float *>(ring) + 4 * lane;
-            for (int r = warp; r < TC_ROWS && first_row + r < group_rows; r += TC_SOFTMAX_WARPS)
+            for (int r = s * quads + (warp & 3); r < TC_ROWS && first_row + r < group_rows; r += 2 * quads)
                 *reinterpret_cast<float4 *>(dst + r * D) = *reinterpret_cast<const float4 *>(src + r * S::OROW);
         }
         tc_fence_before();

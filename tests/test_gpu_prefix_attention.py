@@ -173,6 +173,15 @@ def test_many_rows_over_q8_0(dtype, D, page, layout):
     assert ((hurt.cpu().double() - want).abs() <= bound_of(want, mag, top, dtype, "q8_0")).all()
 
 
+@pytest.mark.parametrize("D,dtype,layout", [(64, F16, "hs"), (128, F32, "kv")])
+@pytest.mark.parametrize("rows", [33, 64, 65, 97, 161])
+def test_tiles_partly_filled_over_q8_0(D, dtype, layout, rows):
+    """Rows that fill one to four of a tile's quarters, and a second tile's first: the
+    warps of the others put codes into parts."""
+    g = rng("quarters", str(dtype), D, rows)
+    case(g, "q8_0", dtype, [400 + int(n) for n in g.integers(0, 20, rows)], 400, 16, 1, 1, D, layout=layout)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("size", [2.0 ** -20, 2.0 ** -12, 1.0, 3.0e4])
 def test_scales_of_any_size_over_q8_0(dtype, size):
