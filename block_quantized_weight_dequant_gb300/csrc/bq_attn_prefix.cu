@@ -9,6 +9,11 @@
 // kernel that serves ordinary calls, and the partial results of both are joined
 // here, in a fixed order: a row's bits depend on its own inputs and the call's
 // geometry alone.
+//
+// Bounds: by size, the products of the shared pass (96 requests of 32801 shared, bf16,
+// 32 over 8 heads of 128: 82 us, 57 of them that pass, the rests beside its end and
+// behind it), the ordinary kernel's instructions (16 requests of 30011 over Q8_0: 55 us)
+// or the chain of three launches (200 requests in 3 groups of 9001: 30 us).
 #include <atomic>
 #include <cmath>
 

@@ -10,11 +10,13 @@
 // minimum over the releases' indices, kept in the count itself as a negative
 // number), the claims ranked by a scan over the releases, and pushed.  So nothing
 // depends on the order of threads.  Bound by latency: a barrier is a few hundred ns,
-// a phase one or two reads from L2 after one another.
+// a phase one or two reads from L2 after one another.  24 requests with 15 forks 11 us,
+// 1000 with 120 forks 33 us, the token rows' launch with it.
 //
 // Compaction ranks the pages by ballots and prefix sums over the pool (one cluster),
-// then renumbers the tables over the whole GPU.  Copies are bound by HBM: each
-// thread has 64 bytes in flight, 16 KB per CTA and turn.
+// then renumbers the tables over the whole GPU: 3000 pages 7 us, 200000 pages 20.
+// Copies are bound by HBM: each thread has 64 bytes in flight, 16 KB per CTA and turn;
+// 200 pages of 28 layers, 367 MB there and back, 113 us, 6.5 TB/s.
 #include <atomic>
 
 #include "bq_tables.cuh"
