@@ -79,7 +79,7 @@ struct TcShape {
     static_assert(!Q_TENSOR || QP * NB * 32 <= TC_COLUMNS - REST);
     static_assert(PP == 2 || (SUM + NB * 64 <= REST && REST + 2 * TILE / 2 <= TC_COLUMNS));
     static constexpr int SLOT = KP * NB * BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_QBLOCK;
-    static constexpr int LIMIT = 227 * 1024, MISC = 3072;
+    static constexpr int LIMIT = 227 * 1024, MISC = 3 * 1024;
     // Q8_0: codes and scales on their way, RAW tiles of them, by groups of AT_ONCE rows; a
     // lane's 32 codes and a word with its scale
     static constexpr int RAW = 3, LANES = 2 * NB, AT_ONCE = 32 / LANES, GROUPS = TILE / AT_ONCE;
@@ -121,7 +121,7 @@ struct TcMisc {
     uint32_t tmem;
     uint32_t dead;  // a wait has run out
 };
-static_assert(sizeof(TcMisc) <= 3072 && offsetof(TcMisc, mask) % 16 == 0 && alignof(TcMisc) == 16);
+static_assert(sizeof(TcMisc) <= 3 * 1024 && offsetof(TcMisc, mask) % 16 == 0 && alignof(TcMisc) == 16);
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
