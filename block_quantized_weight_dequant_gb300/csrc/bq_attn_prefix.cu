@@ -243,16 +243,14 @@ bool has_tensor_kernel(const bq_kv_cache *c, int64_t rows) {
 }
 constexpr int TILE_ROWS = 128;
 // positions of its tiles, as TcShape has them
-int tile_positions(const bq_kv_cache *c, int dtype) {
-    return c->type == BQ_Q8_0 || (c->type == BQ_BF16 && dtype != BQ_BF16) ? 64 : 128;
-}
+int tile_positions(const bq_kv_cache *c) { return c->type == BQ_F16 ? 128 : 64; }
 
 // Tiles of a chunk: the fewest steps of the whole GPU, a chunk's start, joins and
 // partial results counted as FIXED tiles.  At most MOST tiles, so that the
 // tensor core's sums stay short.
 bool size_tensor_pass(Pass *p, int groups, int64_t rows, int64_t positions, int sms) {
     constexpr int FIXED = 6, MOST = 64;
-    const int TILE = tile_positions(&p->a.c, p->a.x.dtype);
+    const int TILE = tile_positions(&p->a.c);
     p->inst = nullptr;
     p->tile_rows = TILE_ROWS;
     p->a.group_rows = (int)rows;
@@ -386,7 +384,7 @@ bool map_of(const bq_kv_cache &c, void *base, int box, bool heads_first, const c
 // not whole groups of 8 slots or the strides are none of a tensor map's (each a
 // multiple of the one before, and beyond what that spans).
 void maps_of(const bq_kv_cache &c, bq::TcArgs *t) {
-    const int most = tile_positions(&c, t->a.x.dtype);
+    const int most = tile_positions(&c);
     t->box = c.page_size & -c.page_size;  // the largest power of two that divides it
     if (t->box > most) t->box = most;
     const cuuint64_t D = 2 * (cuuint64_t)c.head_dim, S = (cuuint64_t)c.page_size, H = (cuuint64_t)c.kv_heads;

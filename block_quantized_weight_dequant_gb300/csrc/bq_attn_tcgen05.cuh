@@ -1,16 +1,16 @@
 // bq_attn_tcgen05.cuh -- the shared pages of a group of requests gone through once
 // for all its query rows (the first pass of bq_paged_prefix_attention in
-// include/bqgemv.h) over 16-bit caches with heads of up to 128 values.
+// include/bqgemv.h), for heads of up to 128 values.
 //
-// Mathematics.  For 128 query rows of one kv head at a time and tiles of 128
-// positions: S = Q K^T, P = 2^(factor S - m), O = O + P V with a running reference
+// Mathematics.  For 128 query rows of one kv head at a time and tiles of 128 positions
+// (64 over bf16 and Q8_0 caches): S = Q K^T, P = 2^(factor S - m), O = O + P V with a running reference
 // m and sum l per row.  m follows the running maximum only when that has grown
 // by more than 2^8: weights are at most 2^8 then and O, which stays in tensor
 // memory, is rescaled (by the row's own 2^(m_old - m)) in few tiles.
 //
 // A CTA takes a chunk of the positions for 128 rows.  Warps 0 to 3 and 4 to 7 are
-// two streams: they take the even and the odd tiles, each with scores S (128 columns
-// of tensor memory) of its own, so that the tensor cores work for one stream while
+// two streams: they take the even and the odd tiles, each with scores S (a column
+// of tensor memory for each position) of its own, so that the tensor cores work for one stream while
 // the other one computes its weights.  The streams hand the rows' references to one
 // another and add into one O (up to 128 columns); the one that lets a reference grow
 // rescales O.  Warp 8 brings K and V tiles into a ring in shared memory by tensor
@@ -32,11 +32,12 @@
 //
 // Precision.  A query of the cache's type is used as it is, any other in QP 16-bit
 // parts (fp16 2, after scaling the row by a power of two; bf16 3); weights are two
-// parts of fp16, 22 bits, three of bf16, 24 bits, or two, 17 bits, where the output is
-// bf16 (an error below 2^-17 of the mean |v|, where the output's rounding is 2^-9 of
-// it; one part alone would leave 2^-9, a third takes a half more of the second
-// product).  Q8_0 codes times scales are two fp16 parts (below).  O is summed by the
-// tensor core over some tiles and by fp32 additions over the chunk (ADDED).
+// parts of fp16, off by 2^-23, or three of bf16, 24 bits, as in the ordinary kernel
+// (two of bf16, 17 bits, and O summed by the tensor core alone would do with bf16
+// outputs but where terms cancel or a sum lies next to a rounding border: 0.7% of the
+// outputs of 96 requests of 32801 shared were then not the nearest, 0.09% of an fp32
+// form's).  Q8_0 codes times scales are two fp16 parts (below).  O is summed by the
+// tensor core over some tiles and by fp32 additions over the chunk (FLUSH).
 #pragma once
 
 #include <cuda.h>  // CUtensorMap
@@ -59,25 +60,23 @@ constexpr int TC_SHIFT_F16 = 7;      // fp16 weights carry 2^7: up to 2^15, two 
 
 template <bool HALF, int QP, int NB, bool Q8>
 struct TcShape {
-    // Parts of a weight: three of bf16 where the output holds more than a bf16 number.
-    static constexpr int PP = QP == 3 ? 3 : 2;
+    static constexpr int PP = HALF ? 2 : 3;  // parts of a weight
     // positions of a tile; bytes of its rows of 64 values; parts of a key or value
     static constexpr int TILE = Q8 || PP == 3 ? 64 : 128, BLOCK = TILE * 128, KP = Q8 ? 2 : 1;
     // The tensor core truncates when it adds to O: after some hundred positions that shows
     // in an fp32 output (chunks of 1800 positions: off by 4.4e-6 of it, fp32 sums 7e-7;
-    // added up every 512 1.3e-6, every 256 8e-7), after thousands in an fp16 one (1.3% of
-    // the values not the nearest, with 512 0.4%, as fp32 sums leave).  So O is added up
-    // elsewhere in tensor memory, rounded to nearest, every FLUSH tiles, and starts again;
-    // not for bf16 outputs.  Heads of 128 then have their queries in shared memory: 96
+    // added up every 512 1.3e-6, every 256 8e-7), after thousands in a 16-bit one (fp16 1.3%
+    // of the values not the nearest, with 512 0.4%, as fp32 sums leave; bf16, 32801 shared,
+    // weights of three parts, with 512 0.12%, with 256 0.07%, fp32 sums 0.09%).  So O is
+    // added up elsewhere in tensor memory, rounded to nearest, every FLUSH tiles, and
+    // starts again.  fp16 heads of 128 then have their queries in shared memory: 96
     // requests of 32801 shared, fp16 89 us a call against 77, fp32 queries 117 against 86.
-    static constexpr bool ADDED = HALF || QP == 3;
-    static constexpr int FLUSH = (QP > 1 ? 256 : 512) / TILE;
+    static constexpr int FLUSH = (HALF && QP == 1 ? 512 : 256) / TILE;
     // columns of tensor memory: scores of two streams, O, its sum, and in the rest third
-    // parts of the weights or queries (else these lie in shared memory)
-    static constexpr int O = 2 * TILE, SUM = O + NB * 64, REST = 384;
-    static constexpr bool Q_TENSOR = PP == 2 && (!ADDED || SUM + NB * 64 <= REST);
-    static_assert(!Q_TENSOR || QP * NB * 32 <= TC_COLUMNS - REST);
-    static_assert(PP == 2 || (SUM + NB * 64 <= REST && REST + 2 * TILE / 2 <= TC_COLUMNS));
+    // parts of the weights and, where there is room, queries (else these lie in shared memory)
+    static constexpr int O = 2 * TILE, SUM = O + NB * 64, THIRD = 384, QUERIES = THIRD + (PP == 3 ? TILE : 0);
+    static constexpr bool Q_TENSOR = SUM + NB * 64 <= THIRD && QUERIES + QP * NB * 32 <= TC_COLUMNS;
+    static_assert(SUM + NB * 64 <= (PP == 3 ? THIRD : TC_COLUMNS));
     static constexpr int SLOT = KP * NB * BLOCK, Q_BYTES = Q_TENSOR ? 0 : QP * NB * TC_QBLOCK;
     static constexpr int LIMIT = 227 * 1024, MISC = 3 * 1024;
     // Q8_0: codes and scales on their way, RAW tiles of them, by groups of AT_ONCE rows; a
@@ -93,11 +92,13 @@ struct TcShape {
     // again: with 3 of 6 the next keys waited for the values two tiles before (the pass
     // 126 us against 104), above SLOTS - 2 for themselves.
     static constexpr int LAG = SLOTS >= 8 ? 3 : 1;
-    static constexpr int SMEM = Q_BYTES + SLOTS * SLOT + RAW_BYTES + MISC;
+    // (one CTA per SM: each takes all tensor memory)
+    static constexpr int NEED = Q_BYTES + SLOTS * SLOT + RAW_BYTES + MISC, ALONE = 115 * 1024;
+    static constexpr int SMEM = NEED > ALONE ? NEED : ALONE;
     static constexpr int OROW = NB * 64 + 4;  // floats of a row on its way out, in the ring's place
     static_assert(SLOTS >= 4 && LAG >= 1 && LAG <= SLOTS - 2);
     static_assert(TC_ROWS * OROW * 4 <= SLOTS * SLOT);
-    static_assert(SMEM > 114 * 1024, "one CTA per SM: each takes all tensor memory");
+    static_assert(2 * (SMEM + 1024) > 228 * 1024 && SMEM <= LIMIT);
     // a copying warp is at most SLOTS / 2 tiles past one whose values are in use
     static_assert(SLOTS / 2 + 1 < TC_MASKS);
 };
@@ -794,7 +795,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                         const uint64_t keys = k_m + (kp * NB + (k >> 2)) * (BLOCK >> 4) + (k & 3) * 2;
                         const bool add = kp < S::KP - 1 || p < (kp ? 0 : QP - 1) || k;
                         if constexpr (S::Q_TENSOR)
-                            tc_product_tensor(d, tmem + S::REST + p * NB * 32 + 8 * k, keys, qk_shape, add);
+                            tc_product_tensor(d, tmem + S::QUERIES + p * NB * 32 + 8 * k, keys, qk_shape, add);
                         else
                             tc_product_shared(d, q_m + (p * NB + (k >> 2)) * (TC_QBLOCK >> 4) + (k & 3) * 2, keys, qk_shape,
                                               add);
@@ -816,14 +817,14 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         auto output = [&](int t, int half) {
             const uint64_t v_m = ring_m + v_slot * (S::SLOT >> 4);
             const uint32_t w = tmem + (t & 1) * TILE;
-            const bool goes_on = S::ADDED ? t % FLUSH != 0 : t > 0;  // O has something of this sum
+            const bool goes_on = t % FLUSH != 0;  // O has something of this sum
             constexpr int STEPS = TILE / 32;
 #pragma unroll
             for (int k = STEPS * half; k < STEPS * half + STEPS; ++k) {
                 const uint32_t high = w + 32 * (k >> 1) + 8 * (k & 1);
                 const uint64_t values = v_m + k * (2048 >> 4);
                 if constexpr (S::PP == 3)
-                    tc_product_tensor(o, tmem + S::REST + (t & 1) * (TILE / 2) + 8 * k, values, pv_shape, k || goes_on);
+                    tc_product_tensor(o, tmem + S::THIRD + (t & 1) * (TILE / 2) + 8 * k, values, pv_shape, k || goes_on);
                 tc_product_tensor(o, high + 16, values, pv_shape, S::PP == 3 || k || goes_on);
                 if constexpr (Q8) tc_product_tensor(o, high, values + (NB * BLOCK >> 4), pv_shape, true);
                 tc_product_tensor(o, high, values, pv_shape, true);
@@ -841,7 +842,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 if (!Q8) waits(keys, keys_phase);
                 waits(&misc.p_full[s][0], t >> 1 & 1);
             }
-            if (S::ADDED && t && t % FLUSH == 0) waits(&misc.flushed, (t / FLUSH - 1) & 1);
+            if (t && t % FLUSH == 0) waits(&misc.flushed, (t / FLUSH - 1) & 1);
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) output(t, 0);
@@ -943,7 +944,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                         w[2 * k] = tc_part<HALF>(y[0], y[1]);
                         w[2 * k + 1] = tc_part<HALF>(y[2], y[3]);
                     }
-                    tc_store8(tmem + lanes + S::REST + p * NB * 32 + s * (EACH / 2) + 2 * k0, w);
+                    tc_store8(tmem + lanes + S::QUERIES + p * NB * 32 + s * (EACH / 2) + 2 * k0, w);
                 }
             tc_wait_store();
             tc_fence_before();
@@ -994,7 +995,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 
         // ---- weights of this stream's tiles ----
         const uint32_t s_at = tmem + lanes + s * TILE, o_at = tmem + lanes + S::O;
-        [[maybe_unused]] const uint32_t sum_at = tmem + lanes + S::SUM;
+        const uint32_t sum_at = tmem + lanes + S::SUM;
         float ref = -INFINITY, l = 0.0f;  // the reference that l belongs to
         bool ok = true;
         for (int t = s; t < tiles; t += 2) {
@@ -1062,7 +1063,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             if (lane == 0) barrier_arrive(&misc.ref_full[s][warp & 3]);
             if (t && __any_sync(~0u, grows)) {  // O of the tiles before, once it is there
                 // (where it starts again with this tile, its sum once it is added there)
-                const bool again = S::ADDED && t % FLUSH == 0;
+                const bool again = t % FLUSH == 0;
                 // (A wait by parity must be at most one phase behind: the barriers are one to a
                 // stream, or to every other sum, whose phase before is known to be over.)
                 const int sums = t / FLUSH - 1;
@@ -1086,7 +1087,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                     }
                 };
                 if (!again) rescale(o_at);
-                if (S::ADDED && t >= FLUSH) rescale(sum_at);
+                if (t >= FLUSH) rescale(sum_at);
             }
             if (ref != now) l *= tc_pow2(ref - now);
             ref = now;
@@ -1115,8 +1116,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 if (c == TILE / 64) told(0);  // (its store has had this chunk's time)
                 tc_store32(s_at + 32 * c, w);
                 if constexpr (S::PP == 3) {
-                    tc_store8(tmem + lanes + S::REST + s * (TILE / 2) + 16 * c, reinterpret_cast<uint32_t(&)[8]>(third[0]));
-                    tc_store8(tmem + lanes + S::REST + s * (TILE / 2) + 16 * c + 8, reinterpret_cast<uint32_t(&)[8]>(third[8]));
+                    tc_store8(tmem + lanes + S::THIRD + s * (TILE / 2) + 16 * c, reinterpret_cast<uint32_t(&)[8]>(third[0]));
+                    tc_store8(tmem + lanes + S::THIRD + s * (TILE / 2) + 16 * c + 8, reinterpret_cast<uint32_t(&)[8]>(third[8]));
                 }
             };
 #pragma unroll 1
@@ -1131,7 +1132,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             told(1);
             const float2 l2 = pair_values(pair_add(sum[0], sum[1]));
             l += l2.x + l2.y;
-            if (S::ADDED && (t + 1) % FLUSH == 0 && t + 1 < tiles) {  // O to its sum, before it starts again
+            if ((t + 1) % FLUSH == 0 && t + 1 < tiles) {  // O to its sum, before it starts again
                 ok = barrier_wait(&misc.added[s], t >> 1 & 1, dead);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
@@ -1172,10 +1173,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         // the last products are complete ----
         ok = ok && barrier_wait(&misc.o_full, 0, dead);
         ok = __all_sync(~0u, ok);
-        if constexpr (S::ADDED) {  // (the one stream may still be at its sum)
-            tc_fence_before();
-            softmax_sync();
-        }
+        tc_fence_before();
+        softmax_sync();  // (the one stream may still be at its sum)
         tc_fence_after();
         misc.ref[s][i] = ref, misc.sum[s][i] = l;
         // partial results of the ordinary kernel carry 2^ATTN_SHIFT_F16 over fp16 caches
@@ -1185,7 +1184,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         for (int c = 8 * s; c < D16 && ok; c += 16) {
             uint32_t x[8];
             tc_load8(o_at + c, x);
-            if (S::ADDED && tiles > FLUSH) {
+            if (tiles > FLUSH) {
                 uint32_t u[8];
                 tc_load8(sum_at + c, u);
                 tc_wait_load();

@@ -617,10 +617,12 @@ bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *
  *    where so little is shared that one pass of it serves the call.
  *  - Over the shared pages heads of up to 128 values go through the tensor cores
  *    (over BQ_Q8_0 from 33 rows of a kv head on): queries as in bq_paged_attention,
- *    probabilities to 2^-22 of the number over BQ_F16 and BQ_Q8_0 caches and to
- *    2^-24 over BQ_BF16 (2^-17 for BQ_BF16 queries, whose outputs hold 2^-9), keys and values of a BQ_Q8_0 cache to 2^-22, or 2^-39 of
- *    127 times the largest scale of the chunk (at most 8192 positions of a head)
- *    where that is more, products summed over a chunk in fp32. */
+ *    probabilities exactly (24 bits) over a BQ_BF16 cache, to 2^-23 of the number or
+ *    2^-32 of the largest of its row, where that is more, over BQ_F16 and BQ_Q8_0
+ *    ones, keys and values of a BQ_Q8_0 cache to 2^-22, or 2^-39 of 127 times the
+ *    largest scale of the chunk (at most 4096 positions of a head) where that is
+ *    more.  The tensor cores sum products of 256 positions (512 where both queries
+ *    and cache are BQ_F16, or BQ_Q8_0 with 16-bit queries), fp32 the rest. */
 #define BQ_PREFIX_MAX_GROUPS 64
 int64_t bq_paged_prefix_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args,
                                                   const int32_t *group_requests, const int32_t *group_shared, int groups);
