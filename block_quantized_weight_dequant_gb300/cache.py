@@ -404,7 +404,9 @@ class SharedBlockTables(BlockTables):
         self.refs = torch.zeros(pages, **i32)
         self.copy_src, self.copy_dst = torch.full((requests,), -1, **i32), torch.full((requests,), -1, **i32)
         self.copy_count = torch.zeros(1, **i32)
-        self._moves = None
+        # (kept as long as this object, whatever compact is asked: a graph holds their addresses)
+        self._moves = (torch.empty(pages // 2, **i32), torch.empty(pages // 2, **i32), torch.empty(1, **i32),
+                       torch.empty(pages, **i32))
 
     def resize(self, new_lens, parents=None):
         """Lengths become new_lens; request b with parents[b] >= 0 (int32 [requests])
@@ -422,12 +424,11 @@ class SharedBlockTables(BlockTables):
         the pool by default, which is all there can be), in the tables and in all
         layers.  Returns ``moved`` [pages], each page's new number (a buffer of this
         object)."""
-        room = self.free_pages.numel() // 2 if max_moves is None else int(max_moves)
-        if self._moves is None or self._moves[0].numel() != room:
-            i32 = dict(dtype=torch.int32, device=self.lens.device)
-            self._moves = (torch.empty(room, **i32), torch.empty(room, **i32), torch.empty(1, **i32),
-                           torch.empty(self.free_pages.numel(), **i32))
         src, dst, count, moved = self._moves
+        if max_moves is not None:
+            if max_moves < 0:
+                raise ValueError(f"max_moves must not be negative, got {max_moves}")
+            src, dst = src[:int(max_moves)], dst[:int(max_moves)]
         kv_compact(self.lens, self.table, self.free_pages, self.free_count, self.refs, self.page_size, src, dst, count,
                    moved)
         if self.caches:

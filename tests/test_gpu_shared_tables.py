@@ -1,0 +1,46 @@
+"""SharedBlockTables and the calls on shared pages at their ends: captured calls beside
+others, caches that do not fit, pools beyond what one pass keeps in mind."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_dequant_gb300 as bq
+
+import pages_plain
+from test_gpu_cache import DEV, healthy, rng  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+I32 = dict(dtype=torch.int32, device=DEV)
+
+
+def cuda(x, dtype=torch.int32):
+    return torch.as_tensor(np.asarray(x), dtype=dtype, device=DEV)
+
+
+def test_a_captured_compaction_after_eager_ones_of_fewer_moves():
+    """A graph of a compaction goes on after calls with other max_moves: it finds its
+    lists, and writes nothing that was allocated since."""
+    def made():
+        caches = [bq.PagedKVCache.zeros(64, 4, 1, 32) for _ in range(2)]
+        for c in caches:
+            c.k.copy_(torch.arange(64, device=DEV).view(64, 1, 1, 1).expand_as(c.k))
+        return bq.SharedBlockTables(5, 12, 64, 4, 64, caches)
+
+    t, twin = made(), made()
+    t.compact()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moved = t.compact()
+    for most in (3, 0, 32):
+        t.compact(most)
+    others = [torch.full((n,), 7, **I32) for n in (32, 32, 1, 64) * 8]
+    for lens in ([40, 9, 20, 0, 31], [0, 9, 20, 14, 0], [3, 0, 24, 14, 9], [0, 0, 0, 0, 40]):
+        t.resize(cuda(lens))
+        twin.resize(cuda(lens))
+        graph.replay()
+        assert torch.equal(twin.compact(), moved)
+        for a in ("lens", "table", "free_pages", "free_count", "refs"):
+            assert torch.equal(getattr(t, a), getattr(twin, a)), a
+        assert all(torch.equal(a.k, b.k) for a, b in zip(t.caches, twin.caches))
+    assert all((x == 7).all() for x in others)
