@@ -399,11 +399,15 @@ class SharedBlockTables(BlockTables):
         i32 = dict(dtype=torch.int32, device=device)
         self.caches = tuple(caches)
         for c in self.caches:
+            if type(c) is not PagedKVCache:
+                raise TypeError("caches must be PagedKVCache objects")
             if (c.pages, c.page_size) != (pages, self.page_size):
                 raise ValueError(f"caches must have {pages} pages of {page_size}, got {c.pages} of {c.page_size}")
         self.refs = torch.zeros(pages, **i32)
         self.copy_src, self.copy_dst = torch.full((requests,), -1, **i32), torch.full((requests,), -1, **i32)
         self.copy_count = torch.zeros(1, **i32)
+        # (of no pairs: caches that a step could not copy in are refused here, not with its tables changed)
+        kv_copy_pages(self.caches, self.copy_src[:0], self.copy_dst[:0])
         # (kept as long as this object, whatever compact is asked: a graph holds their addresses)
         self._moves = (torch.empty(pages // 2, **i32), torch.empty(pages // 2, **i32), torch.empty(1, **i32),
                        torch.empty(pages, **i32))

@@ -44,3 +44,17 @@ def test_a_captured_compaction_after_eager_ones_of_fewer_moves():
             assert torch.equal(getattr(t, a), getattr(twin, a)), a
         assert all(torch.equal(a.k, b.k) for a, b in zip(t.caches, twin.caches))
     assert all((x == 7).all() for x in others)
+
+
+def test_caches_that_a_step_could_not_copy_in_are_refused_when_the_tables_are_made():
+    good = bq.PagedKVCache.zeros(20, 4, 2, 64)
+    other = [bq.PagedKVCache.zeros(20, 4, 1, 64), bq.PagedKVCache.zeros(20, 4, 2, 32),
+             bq.PagedKVCache.zeros(20, 4, 2, 64, "bf16"),
+             bq.PagedKVCache(*[torch.zeros(20, 4, 2, 64, dtype=torch.float16, device=DEV).transpose(1, 2) for _ in "kv"])]
+    for bad in other:
+        with pytest.raises(bq.BQError):
+            bq.SharedBlockTables(3, 4, 20, 4, 16, [good, bad])
+    with pytest.raises(TypeError):
+        bq.SharedBlockTables(3, 4, 20, 4, 16, [good, None])
+    t = bq.SharedBlockTables(3, 4, 20, 4, 16, [good, bq.PagedKVCache.zeros(20, 4, 2, 64)])
+    assert int(t.resize(cuda([5, 0, 1]))) == 0
