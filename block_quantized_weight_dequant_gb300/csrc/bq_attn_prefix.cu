@@ -401,12 +401,19 @@ void maps_of(const bq_kv_cache &c, bq::TcArgs *t) {
         t->box = 0;
 }
 
+// waits of the tensor-memory kernel: their limit, and a barrier to hold (for the tests)
+constexpr uint64_t WAIT_NS = 1000000000;
+std::atomic<uint64_t> wait_ns{WAIT_NS};
+std::atomic<int> hold{bq::TC_HOLD_NONE};
+
 cudaError_t run(Pass *p, int sms, void *stream, unsigned int *status) {
     if (!p->inst) {
         bq::TcArgs t;
         t.a = p->a;
         const bq_kv_cache &c = p->a.c;
         t.box = t.heads_first = 0;
+        t.wait_ns = wait_ns.load(std::memory_order_relaxed);
+        t.hold = hold.load(std::memory_order_relaxed);
         if (c.type == BQ_Q8_0) return bq_internal_prefix_q8_0(t, (int)p->units, stream, status);
         maps_of(c, &t);
         return c.type == BQ_F16 ? bq_internal_prefix_f16(t, (int)p->units, stream, status)
@@ -432,6 +439,15 @@ int bq_internal_status_attn_prefix(unsigned int *flags, int clear) { return read
 
 // host hook for the tests (not in the public header): sets the limit, returns the one before
 extern "C" int64_t bq_internal_prefix_whole_limit(int64_t bytes) { return whole_limit.exchange(bytes < 0 ? WHOLE : bytes); }
+
+// likewise: calls from now on hold a barrier (a TcHold, 0: none) and wait for wait_ns at
+// most (0: the ordinary limit); nonzero for a barrier that there is not
+extern "C" int bq_internal_prefix_hold(int barrier, unsigned long long limit_ns) {
+    if (barrier < 0 || barrier >= bq::TC_HOLD_KINDS) return -1;
+    hold.store(barrier);
+    wait_ns.store(limit_ns ? limit_ns : WAIT_NS);
+    return 0;
+}
 
 extern "C" int64_t bq_paged_prefix_attention_workspace_bytes(const bq_kv_cache *cache, const bq_attention_args *args,
                                                              const int32_t *group_requests, const int32_t *group_shared,

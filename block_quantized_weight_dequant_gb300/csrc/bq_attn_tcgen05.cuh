@@ -108,7 +108,16 @@ struct TcArgs {
     int box;        // positions of a copy by tensor map: the largest power of two that divides
                     // a page, 8 to 128; 0: copies of 16 bytes
     int heads_first;   // of the maps' axes: heads lie closer than slots
+    int hold;          // TcHold
+    uint64_t wait_ns;  // how long a wait lasts at most
     CUtensorMap k, v;  // [pages][kv heads][slots][head_dim] ([slots][kv heads]), in boxes of 64 values by `box` slots
+};
+
+// Barriers that a launch can be told to hold (more arrivals than ever come), so that a test
+// sees the waits run out: the kernel gives up, says so and returns.
+enum TcHold {
+    TC_HOLD_NONE, TC_HOLD_QUERIES, TC_HOLD_FULL, TC_HOLD_EMPTY, TC_HOLD_MASK, TC_HOLD_SCORES, TC_HOLD_WEIGHTS,
+    TC_HOLD_REFERENCE, TC_HOLD_FLUSHED, TC_HOLD_END, TC_HOLD_KINDS
 };
 
 // shared memory behind the ring
@@ -166,22 +175,29 @@ __device__ __forceinline__ uint64_t tc_nanoseconds() {
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-// Waits for a phase of the barrier, for a second at most; false if that has run
-// out here or in another thread of the CTA, which then leaves its loop.
-static __device__ __noinline__ bool barrier_wait_long(uint64_t *b, uint32_t parity, volatile uint32_t *dead) {
+// Waits for a phase of the barrier, for `ns` at most; false if that has run out here or
+// in another thread of the CTA.  Lanes of a warp may be told differently: it votes
+// before it goes by the answer.
+static __device__ __noinline__ bool barrier_wait_long(uint64_t *b, uint32_t parity, volatile uint32_t *dead, uint64_t ns) {
     const uint64_t t0 = tc_nanoseconds();
     while (!barrier_try(b, parity)) {
         if (*dead) return false;
-        if (tc_nanoseconds() - t0 > 1000000000ull) {
+        if (tc_nanoseconds() - t0 > ns) {
             *dead = 1;
             return false;
         }
     }
     return true;
 }
-__device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity, volatile uint32_t *dead) {
+__device__ __forceinline__ bool barrier_wait(uint64_t *b, uint32_t parity, volatile uint32_t *dead, uint64_t ns) {
     if (barrier_try(b, parity)) return true;
-    return barrier_wait_long(b, parity, dead);
+    return barrier_wait_long(b, parity, dead, ns);
+}
+// The end of what a CTA has under way, before its memory is another's: a tenth of a
+// second at most, whoever has given up.
+static __device__ __noinline__ void barrier_wait_end(uint64_t *b, uint32_t parity) {
+    const uint64_t t0 = tc_nanoseconds();
+    while (!barrier_try(b, parity) && tc_nanoseconds() - t0 < 100000000ull) {}
 }
 
 // 32 columns of the warp's 32 lanes of tensor memory
@@ -380,6 +396,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     uint8_t *q_s = smem, *ring = smem + S::Q_BYTES;
     TcMisc &misc = *reinterpret_cast<TcMisc *>(ring + SLOTS * S::SLOT + S::RAW_BYTES);
     volatile uint32_t *dead = &misc.dead;
+    const uint64_t limit = args.wait_ns;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int D = a.c.head_dim, R = a.x.rows, KVH = a.c.kv_heads, G = (int)a.group.d;
     const int page = a.c.page_size;
@@ -409,20 +426,24 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     // ---- barriers and tensor memory, while the kernel before ends ----
     if (tid == 0) {
         const int copying = Q8 ? copiers : args.box ? 1 : TC_COPY_WARPS;
-        for (int i = 0; i < SLOTS; ++i) barrier_init(&misc.full[i], copying), barrier_init(&misc.empty[i], 1);
-        for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], copying);
-        for (int i = 0; i < 2; ++i) {
-            barrier_init(&misc.s_full[i], 1);
-            for (int k = 0; k < 2; ++k) barrier_init(&misc.p_full[i][k], quads);
-            for (int k = 0; k < 4; ++k) barrier_init(&misc.ref_full[i][k], 1);
+        auto held = [&](TcHold which) { return args.hold == which ? 1 << 16 : 0; };
+        for (int i = 0; i < SLOTS; ++i) {
+            barrier_init(&misc.full[i], copying + (i ? 0 : held(TC_HOLD_FULL)));
+            barrier_init(&misc.empty[i], 1 + (i ? 0 : held(TC_HOLD_EMPTY)));
         }
-        barrier_init(&misc.q_full, 2 * quads);
+        for (int i = 0; i < TC_MASKS; ++i) barrier_init(&misc.mask_full[i], copying + (i ? 0 : held(TC_HOLD_MASK)));
+        for (int i = 0; i < 2; ++i) {
+            barrier_init(&misc.s_full[i], 1 + held(TC_HOLD_SCORES));
+            for (int k = 0; k < 2; ++k) barrier_init(&misc.p_full[i][k], quads + (k ? held(TC_HOLD_WEIGHTS) : 0));
+            for (int k = 0; k < 4; ++k) barrier_init(&misc.ref_full[i][k], 1 + (k ? 0 : held(TC_HOLD_REFERENCE)));
+        }
+        barrier_init(&misc.q_full, 2 * quads + held(TC_HOLD_QUERIES));
         for (int i = 0; i < 2; ++i) {
             barrier_init(&misc.added[i], 1);
             barrier_init(&misc.summed[i], quads);
         }
-        barrier_init(&misc.flushed, quads);
-        barrier_init(&misc.o_full, 1);
+        barrier_init(&misc.flushed, quads + held(TC_HOLD_FLUSHED));
+        barrier_init(&misc.o_full, 1 + held(TC_HOLD_END));
         misc.dead = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -568,7 +589,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
                     const int n = 2 * t + v, slot = n % SLOTS;
-                    ok = ok && barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead);
+                    ok = ok && barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead, limit);
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     if (v == 0) {
@@ -639,6 +660,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         int entry = entry_of(begin + 8 * lane);
         const bool starts = lane < TILE / 8 && 8 * lane % args.box == 0;  // a box
         bool ok = true;
+        int issued = 0;  // loads
         for (int t = 0; t < tiles && ok; ++t) {
             const int p = begin + t * TILE + 8 * lane;
             const bool in = lane < TILE / 8 && p < end, live = in && entry >= 0 && entry < a.c.pages;
@@ -648,10 +670,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             entry = entry_of(p + TILE);
             for (int v = 0; v < 2; ++v) {
                 const int n = 2 * t + v, slot = n % SLOTS;
-                if (!barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(~0u, barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead, limit));
+                if (!ok) break;
                 if (lane == 0) barrier_arrive_bytes(&misc.full[slot], S::SLOT);
                 if (v == 0 && lane < TILE / 8) misc.mask[t % TC_MASKS][lane] = live ? 255 : 0;
                 __syncwarp();
@@ -663,8 +683,13 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                         tc_copy_box(to + b * BLOCK, v ? &args.v : &args.k, 64 * b, args.heads_first ? h : slot_of,
                                     args.heads_first ? slot_of : h, from, &misc.full[slot]);
                 }
+                ++issued;
             }
         }
+        if (!ok)  // (else the products have read them all)
+            for (int n = max(0, issued - SLOTS); n < issued; ++n)
+                barrier_wait_end(&misc.full[n % SLOTS], n / SLOTS & 1);
+        __syncwarp();
     } else if (warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
         // ---- copies of 16 bytes (none where tensor maps do them): K and V of each tile in turn, every third 8 rows by each warp ----
         constexpr int GROUPS = TILE / 8, MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;  // of 8 rows
@@ -715,10 +740,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             for (int k = 0; k < 2; ++k) live[k] = __ballot_sync(~0u, off[k] >= 0);
             for (int v = 0; v < 2; ++v) {
                 const int n = 2 * t + v, slot = n % SLOTS;
-                if (!barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(~0u, barrier_wait(&misc.empty[slot], (n / SLOTS & 1) ^ 1, dead, limit));
+                if (!ok) break;
                 // (after the wait: the masks of TC_MASKS tiles before are not in use any more)
                 if (v == 0) {
                     const int of = cw + TC_COPY_WARPS * lane;
@@ -769,7 +792,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         const uint32_t pv_shape = SHAPE | 1u << 16 | (uint32_t)(D16 >> 3) << 17;
         const uint64_t q_m = tc_matrix(tc_shared(q_s), TC_QBLOCK), ring_m = tc_matrix(tc_shared(ring), BLOCK);
         const int steps = D16 / 16;
-        bool ok = barrier_wait(&misc.q_full, 0, dead);
+        bool ok = __all_sync(~0u, barrier_wait(&misc.q_full, 0, dead, limit));
         // load n = 2 t of K, 2 t + 1 of V: in slot n % SLOTS, counted along
         int k_slot = 0, v_slot = 1;
         uint32_t k_phase = 0, v_phase = 0;
@@ -778,7 +801,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             if (slot >= SLOTS) slot -= SLOTS, phase ^= 1;
         };
         auto waits = [&](uint64_t *b, uint32_t phase) {
-            ok = ok && barrier_wait(b, phase, dead);
+            ok = ok && barrier_wait(b, phase, dead, limit);
             ok = __all_sync(~0u, ok);
         };
         auto scores = [&](int t) {  // S = Q K^T of tile t, smallest parts first; by the elected thread
@@ -872,8 +895,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         // the end of all products; nothing is in flight when the tensor memory is given back
         if (elect_one()) tc_commit(&misc.o_full);
         __syncwarp();
-        const uint64_t t0 = tc_nanoseconds();
-        while (!barrier_try(&misc.o_full, 0) && tc_nanoseconds() - t0 < 100000000ull) {}
+        barrier_wait_end(&misc.o_full, 0);
         __syncwarp();
     } else {
         const int s = warp >> 2, i = 32 * (warp & 3) + lane;  // stream and row of this thread
@@ -999,8 +1021,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         float ref = -INFINITY, l = 0.0f;  // the reference that l belongs to
         bool ok = true;
         for (int t = s; t < tiles; t += 2) {
-            ok = barrier_wait(&misc.mask_full[t % TC_MASKS], t / TC_MASKS & 1, dead) &&
-                 barrier_wait(&misc.s_full[s], t >> 1 & 1, dead);
+            ok = barrier_wait(&misc.mask_full[t % TC_MASKS], t / TC_MASKS & 1, dead, limit) &&
+                 barrier_wait(&misc.s_full[s], t >> 1 & 1, dead, limit);
             if (!__all_sync(~0u, ok)) {
                 ok = false;
                 break;
@@ -1049,7 +1071,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             // the reference that the tile before left, the other stream's
             float was = -INFINITY;
             if (t) {
-                ok = barrier_wait(&misc.ref_full[s ^ 1][warp & 3], (t - 1) >> 1 & 1, dead);
+                ok = barrier_wait(&misc.ref_full[s ^ 1][warp & 3], (t - 1) >> 1 & 1, dead, limit);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
@@ -1067,8 +1089,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 // (A wait by parity must be at most one phase behind: the barriers are one to a
                 // stream, or to every other sum, whose phase before is known to be over.)
                 const int sums = t / FLUSH - 1;
-                ok = again ? barrier_wait(&misc.summed[sums & 1], sums >> 1 & 1, dead)
-                           : barrier_wait(&misc.added[s ^ 1], (t - 1) >> 1 & 1, dead);
+                ok = again ? barrier_wait(&misc.summed[sums & 1], sums >> 1 & 1, dead, limit)
+                           : barrier_wait(&misc.added[s ^ 1], (t - 1) >> 1 & 1, dead, limit);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
@@ -1133,7 +1155,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             const float2 l2 = pair_values(pair_add(sum[0], sum[1]));
             l += l2.x + l2.y;
             if ((t + 1) % FLUSH == 0 && t + 1 < tiles) {  // O to its sum, before it starts again
-                ok = barrier_wait(&misc.added[s], t >> 1 & 1, dead);
+                ok = barrier_wait(&misc.added[s], t >> 1 & 1, dead, limit);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
@@ -1171,7 +1193,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
 
         // ---- the partial results, through the ring's place: nothing reads or fills it once
         // the last products are complete ----
-        ok = ok && barrier_wait(&misc.o_full, 0, dead);
+        ok = ok && barrier_wait(&misc.o_full, 0, dead, limit);
         ok = __all_sync(~0u, ok);
         tc_fence_before();
         softmax_sync();  // (the one stream may still be at its sum)

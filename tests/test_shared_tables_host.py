@@ -27,3 +27,15 @@ def test_compact_keeps_its_buffers(monkeypatch, pages):
             assert a.storage_offset() == b.storage_offset() == 0
     with pytest.raises(ValueError, match="max_moves"):
         t.compact(-1)
+
+
+def test_the_hook_of_held_barriers_takes_those_that_there_are():
+    """What a GPU test of the bounded waits is made with (not in the public header)."""
+    import ctypes
+
+    from block_quantized_weight_dequant_gb300 import _lib
+
+    hook = _lib.lib.bq_internal_prefix_hold
+    hook.restype, hook.argtypes = ctypes.c_int, [ctypes.c_int, ctypes.c_ulonglong]
+    assert hook(-1, 0) == -1 and hook(10, 0) == -1
+    assert hook(9, 1000) == 0 and hook(0, 0) == 0
