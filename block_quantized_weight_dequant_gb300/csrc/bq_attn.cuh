@@ -277,10 +277,10 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     auto skipped = [&](int b) { return mode == ATTN_REST ? common(b) : 0; };
     auto length = [&](int b) {
         if (shared) return a.group_pages[b] * a.c.page_size;
-        const int n = min(max(a.x.lens[b], 0), most);
+        const int n = attn_clamped(a.x.lens[b], most);
         if (mode == ATTN_ALL) return n;
         const int before = common(b) * a.c.page_size, rest = attn_rest(n, R, before);
-        return mode == ATTN_REST ? rest : n - R + 1 >= before ? n : 0;
+        return mode == ATTN_REST ? rest : attn_sees(n, R, before) ? n : 0;
     };
     const long long per_chunk = (long long)KVH * a.row_tiles;
     // direct: a CTA per unit that the table can hold, units beyond a request's
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     auto checked = [&](int b) {
         if (shared) return;
         const int len = a.x.lens[b];
-        if (len < 0 || len > most || (len && mode != ATTN_ALL && len - R + 1 < common(b) * a.c.page_size))
+        if (len < 0 || len > most || (len && mode != ATTN_ALL && !attn_sees(len, R, common(b) * a.c.page_size)))
             atomicOr(status, BQ_DEVERR_LENGTH);
     };
     if (!direct) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
             group_rows = (a.group_end[b] - first) * R * (int)a.group.d;
             owner = 0x7fffffff;
             for (int i = first + lane; i < a.group_end[b] && owner == 0x7fffffff; i += 32)
-                if (min(a.x.lens[i], most) - R + 1 >= length(b)) owner = i;
+                if (attn_sees(attn_clamped(a.x.lens[i], most), R, length(b))) owner = i;
             owner = __reduce_min_sync(~0u, owner);
             if (first_row >= group_rows || owner == 0x7fffffff) continue;  // nobody reads its partial results
         }

@@ -46,10 +46,14 @@ struct AttnArgs {
     int group_pages[ATTN_GROUPS];  // whole pages that its requests share
 };
 
-// positions that request b's rows see behind `shared` ones, from its clamped
-// length: none unless its first row sees all the shared ones
+// a request's length, of which the table holds `most` (a difference of one as it was
+// given may pass 2^31)
+__host__ __device__ inline int attn_clamped(int len, int most) { return len < 0 ? 0 : len < most ? len : most; }
+// whether a request's rows see all of `shared` positions, from its clamped length
+__host__ __device__ inline bool attn_sees(int len, int rows, int shared) { return len - rows + 1 >= shared; }
+// positions that its rows see behind them: none unless they see the shared ones
 __host__ __device__ inline int attn_rest(int len, int rows, int shared) {
-    return len - rows + 1 >= shared ? len - shared : 0;
+    return attn_sees(len, rows, shared) ? len - shared : 0;
 }
 
 // work units of one request of n positions: at least one, which writes the rows
@@ -57,11 +61,11 @@ __host__ __device__ inline int attn_chunks(int n, int chunk) { return n <= chunk
 
 // positions that an ATTN_ALL or ATTN_WHOLE launch sees of request b
 __device__ inline int attn_length(const AttnArgs &a, int b) {
-    const int n = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
+    const int n = attn_clamped(a.x.lens[b], a.x.table_width * a.c.page_size);
     if (a.mode == ATTN_ALL) return n;
     int g = 0;
     while (a.group_end[g] <= b) ++g;
-    return n - a.x.rows + 1 >= a.group_pages[g] * a.c.page_size ? n : 0;
+    return attn_sees(n, a.x.rows, a.group_pages[g] * a.c.page_size) ? n : 0;
 }
 
 struct AttnInstance {

@@ -66,8 +66,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, 4) prefix_join_kernel(const __gr
     while (a.group_end[g] <= b) ++g;
     const int first = g ? a.group_end[g - 1] : 0;
     const int common = a.group_pages[g] * a.c.page_size;
-    const int len = min(max(a.x.lens[b], 0), a.x.table_width * a.c.page_size);
-    const bool sees = len - R + 1 >= common;  // else neither pass has anything for it
+    const int len = bq::attn_clamped(a.x.lens[b], a.x.table_width * a.c.page_size);
+    const bool sees = bq::attn_sees(len, R, common);  // else neither pass has anything for it
     const int ns = sees && common ? bq::attn_chunks(common, j.shared.chunk) : 0;
     const int n = ns + (sees ? bq::attn_chunks(bq::attn_rest(len, R, common), j.rest.chunk) : 0);
     const int si = ((b - first) * R + row) * G + in_group, ri = row * G + in_group;

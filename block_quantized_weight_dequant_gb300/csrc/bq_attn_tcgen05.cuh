@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
     int owner = 0x7fffffff;
     const int most = a.x.table_width * page;
     for (int i = first + lane; i < end_request && owner == 0x7fffffff; i += 32)
-        if (min(a.x.lens[i], most) - R + 1 >= common) owner = i;
+        if (attn_sees(attn_clamped(a.x.lens[i], most), R, common)) owner = i;
     owner = __reduce_min_sync(~0u, owner);
     // (without one nobody reads these partial results)
     const int tiles = owner == 0x7fffffff ? 0 : (end - begin + TILE - 1) / TILE;
