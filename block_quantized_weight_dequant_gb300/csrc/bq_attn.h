@@ -49,8 +49,11 @@ struct AttnArgs {
 // a request's length, of which the table holds `most` (a difference of one as it was
 // given may pass 2^31)
 __host__ __device__ inline int attn_clamped(int len, int most) { return len < 0 ? 0 : len < most ? len : most; }
-// whether a request's rows see all of `shared` positions, from its clamped length
-__host__ __device__ inline bool attn_sees(int len, int rows, int shared) { return len - rows + 1 >= shared; }
+// whether a request's rows see all of `shared` positions, from its clamped length (none
+// are seen by a request shorter than its rows, too)
+__host__ __device__ inline bool attn_sees(int len, int rows, int shared) {
+    return shared == 0 || len - rows + 1 >= shared;
+}
 // positions that its rows see behind them: none unless they see the shared ones
 __host__ __device__ inline int attn_rest(int len, int rows, int shared) {
     return attn_sees(len, rows, shared) ? len - shared : 0;

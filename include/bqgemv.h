@@ -604,8 +604,9 @@ bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *
  * must name the same pages (they are read from the first request of the group
  * that sees them).  Positions behind them are each request's own.
  *  - A request's rows see all its shared positions: lens[b] - rows + 1 >= the
- *    positions of its shared pages.  One that does not gives zeros, and sets
- *    BQ_DEVERR_LENGTH unless its length is 0 (an ended request of the batch).
+ *    positions of its shared pages, if there are any.  One that does not gives
+ *    zeros, and sets BQ_DEVERR_LENGTH unless its length is 0 (an ended request of
+ *    the batch).
  *  - group_requests and group_shared are host arrays, read by the call: 1 <=
  *    groups <= BQ_PREFIX_MAX_GROUPS, counts not negative and summing to
  *    args->requests, 0 <= group_shared <= table_width * page_size.

@@ -1,11 +1,12 @@
-"""Lengths at their ends in attention over shared pages."""
+"""Lengths at their ends in attention over shared pages: out of range, and shorter than
+the call's rows."""
 import pytest
 import torch
 
 import block_quantized_weight_dequant_gb300 as bq
 
 from test_gpu_cache import BF16, DEV, F16, F32, filled_cache, healthy, normal, rng  # noqa: F401
-from test_gpu_prefix_attention import limit, pages_needed, shared_table  # noqa: F401
+from test_gpu_prefix_attention import case, limit, pages_needed, shared_table  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 KINDS = [("f16", F32, 4), ("bf16", BF16, 4), ("q8_0", F32, 4), ("q8_0", BF16, 40), ("f16", F16, 40)]
@@ -31,3 +32,17 @@ def test_a_length_below_zero_is_none_whatever_its_size(kind, dtype, heads, rows,
     got = bq.paged_prefix_attention(cache, q, table, at, shared, rows=rows)
     assert bq.device_status(clear=True) == 0x200
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kind,dtype,heads", KINDS)
+@pytest.mark.parametrize("rows", [2, 4, 6])
+def test_requests_shorter_than_the_rows_where_no_page_is_shared(kind, dtype, heads, rows):
+    """With nothing shared there is nothing to see: the last rows have their positions, as
+    in the ordinary call, and nothing is reported."""
+    for shared in (0, 15, [(2, 0), (0, 64), (3, 15), (2, 0)], [(2, 0), (3, 320), (2, 9)]):
+        lens = [1, rows, 0, rows - 1, 3, 2, 1]
+        if shared == [(2, 0), (3, 320), (2, 9)]:
+            lens[2:5] = [0, 320 + rows, 340]
+        g = rng("short", kind, heads, rows)
+        case(g, kind, dtype, lens, shared, 16, heads, 1, 64, rows=rows, width=23)  # (groups share no more than it holds)
+        assert bq.device_status(clear=True) == 0
