@@ -255,14 +255,7 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
     uint8_t *ring = smem + warp * S::RING;
     const int B = a.x.requests, R = a.x.rows, D = a.c.head_dim, KVH = a.c.kv_heads;
     const int most = a.x.table_width * a.c.page_size;
-    // The launch over own pages comes behind the one over the shared pages, of which it
-    // needs nothing: it starts once all CTAs of that have their own wait behind them, so
-    // what was before both is complete (the fence drops what this SM's L1 may still hold
-    // of it), and one CTA waits at its end, for the join.  It fills the SMs that the other
-    // leaves: 96 requests of 32801 shared 86.0 -> 82.0 us, 200 of 9001 30.9 -> 29.9, 16 of
-    // 30011 over Q8_0 58.1 -> 54.6.
-    if (mode == ATTN_REST) __threadfence();
-    else pdl_wait();
+    pdl_wait();
     const bool parts = mode == ATTN_REST || mode == ATTN_PREFIX;  // partial results alone
     if ((a.max_chunks > 1 && !a.cluster) || parts) pdl_launch_dependents();
 
@@ -933,7 +926,6 @@ __global__ void __launch_bounds__(AttnShape<KV, QP, PP, DP, NT>::WARPS * 32, Att
         }
         __syncthreads();  // the next unit fills the rings and rewrites q_s and m_s
     }
-    if (mode == ATTN_REST && blockIdx.x == 0) pdl_wait();
 }
 
 template <int KV, int QP, int PP, int DP, int NT, bool MODES>

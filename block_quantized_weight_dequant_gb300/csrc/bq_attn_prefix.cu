@@ -10,10 +10,12 @@
 // here, in a fixed order: a row's bits depend on its own inputs and the call's
 // geometry alone.
 //
-// Bounds: by size, the products of the shared pass (96 requests of 32801 shared, bf16,
-// 32 over 8 heads of 128: 82 us, 57 of them that pass, the rests beside its end and
-// behind it), the ordinary kernel's instructions (16 requests of 30011 over Q8_0: 55 us)
-// or the chain of three launches (200 requests in 3 groups of 9001: 30 us).
+// Bounds: by size, the shared pass (96 requests of 32801 shared, bf16, 32 over 8 heads
+// of 128: 136 us a call), the ordinary kernel's instructions (16 requests of 30011 over
+// Q8_0: 62 us) or the chain of three launches (200 requests in 3 groups of 9001: 32 us).
+// The launches follow one another, each waiting for the one before to end: own pages that
+// started while the shared ones were gone through, without that wait, took 8, 5 and 1 us
+// less, but nothing that is documented orders their reads behind the writes before the call.
 #include <atomic>
 #include <cmath>
 

@@ -38,8 +38,7 @@ __device__ __forceinline__ void pdl_launch_dependents() {
 }
 
 // Launch with programmatic dependent launch allowed: every kernel launched
-// here executes pdl_wait before its first access to global memory (attn_kernel's
-// launch over requests' own pages alone knows the kernel before it, and need not).
+// here executes pdl_wait before its first access to global memory.
 // `cluster` > 1: CTAs per thread-block cluster.
 template <typename... P, typename... A>
 inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, int threads, size_t smem, void *stream,
