@@ -287,12 +287,16 @@ bool size_tensor_pass(Pass *p, int groups, int64_t rows, int64_t positions, int 
     return size_parts(p, groups);
 }
 
-// Shared keys and values, counted once for each request, up to which the ordinary
-// kernel serves the call in one pass.  Measured, the calls captured in a graph, 16
-// heads over 8 of 128, both ways: fp16 cache, 32 M values (8 requests of 2048 shared)
-// 15.5 us in one pass, 18.7 shared; 64 M (32 of 1024) 25.1 and 20.0; 128 M (8 of 8192)
-// 34.7 and 22.5; Q8_0, 32 M (8 of 2048) 16.3 and 20.9; 64 M (32 of 1024) 25.7 and 23.0.
-constexpr int64_t WHOLE = 48LL << 20;
+// Shared keys and values, counted once for each request of a group but one (a group of
+// one reads nothing again), up to which the ordinary kernel serves the call in one pass.
+// Measured, the calls captured in a graph, 16 heads over 8 of 128, one pass and shared:
+//                                        fp16       bf16       fp32 / fp16  fp32 / Q8_0
+//    16 M values (2 requests of 8192)     13.4 18.8  13.9 22.0  14.4 26.5    15.1 16.6 us
+//    30 M (16 of 1024)                    15.2 18.1  15.7 17.4  16.4 23.5    18.0 20.9
+//    43 M (8 of 3136)                     19.9 17.2  20.6 17.8  21.3 22.8    21.7 20.6
+//    64 M (17 of 2048)                    23.8 18.8  24.9 18.6  25.9 24.2    26.5 26.6
+//   128 M (9 of 8192)                     38.2 19.8  41.0 23.1  41.8 27.4    41.6 29.6
+constexpr int64_t WHOLE = 40LL << 20;
 std::atomic<int64_t> whole_limit{WHOLE};
 
 bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_t *counts, const int32_t *shared,
@@ -332,7 +336,8 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_
     // that sharing costs (WHOLE has the figures).
     int64_t again = 0;
     for (int g = 0; g < groups; ++g)
-        again += 2LL * counts[g] * a.group_pages[g] * c->page_size * c->kv_heads * c->head_dim;
+        if (counts[g])
+            again += 2LL * (counts[g] - 1) * a.group_pages[g] * c->page_size * c->kv_heads * c->head_dim;
     p->whole = !p->any_shared || again <= whole_limit.load(std::memory_order_relaxed);
     if (p->whole) {
         p->bytes = bq_paged_attention_workspace_bytes(c, x);

@@ -1,0 +1,32 @@
+"""How calls over shared pages are cut, on the host without a GPU."""
+import pytest
+
+from block_quantized_weight_dequant_gb300 import _lib
+
+from test_cache_host import attention, cache, lib  # noqa: F401
+from test_shared_host import groups
+
+
+def needs(lib, x, c, *pairs):  # noqa: F811
+    """Workspace bytes over the groups, and of the ordinary call, which is one pass."""
+    return (lib.bq_paged_prefix_attention_workspace_bytes(c, x, *groups(*pairs)),
+            lib.bq_paged_attention_workspace_bytes(c, x))
+
+
+@pytest.mark.parametrize("kind", [_lib.BQ_F16, _lib.BQ_BF16, _lib.BQ_Q8_0])
+def test_groups_of_one_request_read_nothing_again(lib, kind):  # noqa: F811
+    """However long, they are one pass of the ordinary kernel, alone or beside each other;
+    two requests that share as much are not, and then they alone count."""
+    c = cache(kind, kv_heads=8, head_dim=128, slot_stride=128, head_stride=2048, page_stride=16384)
+    width = 8192
+    one = attention(requests=1, heads=16, table_width=width, table_stride=width)
+    shared, whole = needs(lib, one, c, (1, width * 16))
+    assert shared == whole
+    many = attention(requests=64, heads=16, table_width=width, table_stride=width)
+    shared, whole = needs(lib, many, c, *[(1, 100000 + 16 * i) for i in range(64)])
+    assert shared == whole
+    shared, whole = needs(lib, many, c, *[(1, 100000)] * 62, (2, 100000))
+    assert shared != whole
+    # 2 * 8 * 128 values a position, read once more: 16 M of them
+    shared, whole = needs(lib, many, c, *[(1, 100000)] * 62, (2, 8192))
+    assert shared == whole
