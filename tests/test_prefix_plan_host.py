@@ -1,4 +1,6 @@
 """How calls over shared pages are cut, on the host without a GPU."""
+import ctypes
+
 import pytest
 
 from block_quantized_weight_dequant_gb300 import _lib
@@ -30,3 +32,19 @@ def test_groups_of_one_request_read_nothing_again(lib, kind):  # noqa: F811
     # 2 * 8 * 128 values a position, read once more: 16 M of them
     shared, whole = needs(lib, many, c, *[(1, 100000)] * 62, (2, 8192))
     assert shared == whole
+
+
+def test_the_type_of_the_queries_does_not_move_the_workspace(lib):  # noqa: F811
+    """paged_prefix_attention_workspace may be asked without it."""
+    limit = lib.bq_internal_prefix_whole_limit
+    limit.restype, limit.argtypes = ctypes.c_int64, [ctypes.c_int64]
+    limit(0)
+    try:
+        for kind in (_lib.BQ_F16, _lib.BQ_BF16, _lib.BQ_Q8_0):
+            c = cache(kind, kv_heads=8, head_dim=128, slot_stride=128, head_stride=2048, page_stride=16384)
+            need = {lib.bq_paged_prefix_attention_workspace_bytes(
+                c, attention(requests=96, heads=32, dtype=dtype, table_width=4000, table_stride=4000), *groups((96, 32801)))
+                for dtype in (_lib.BQ_F32, _lib.BQ_F16, _lib.BQ_BF16)}
+            assert len(need) == 1 and need.pop() > 0
+    finally:
+        limit(-1)
