@@ -338,7 +338,7 @@ bq_status plan_of(const bq_kv_cache *c, const bq_attention_args *x, const int32_
     for (int g = 0; g < groups; ++g)
         if (counts[g])
             again += 2LL * (counts[g] - 1) * a.group_pages[g] * c->page_size * c->kv_heads * c->head_dim;
-    p->whole = !p->any_shared || again <= whole_limit.load(std::memory_order_relaxed);
+    p->whole = !p->any_shared || again < whole_limit.load(std::memory_order_relaxed);
     if (p->whole) {
         p->bytes = bq_paged_attention_workspace_bytes(c, x);
         return p->bytes < 0 ? BQ_ERR_SHAPE : BQ_OK;
