@@ -58,3 +58,37 @@ def test_caches_that_a_step_could_not_copy_in_are_refused_when_the_tables_are_ma
         bq.SharedBlockTables(3, 4, 20, 4, 16, [good, None])
     t = bq.SharedBlockTables(3, 4, 20, 4, 16, [good, bq.PagedKVCache.zeros(20, 4, 2, 64)])
     assert int(t.resize(cuda([5, 0, 1]))) == 0
+
+
+@pytest.mark.parametrize("pool", [2048 * 32 * 16, 2048 * 32 * 16 + 1, 1300003])
+@pytest.mark.parametrize("used", [0.3, 0.97])
+def test_compaction_of_pools_beyond_the_bits_it_keeps(pool, used):
+    """Beyond 2048 pages for each warp of 16 CTAs the counts are read again in place of bits
+    kept of them: all moves, few of them, and no page left in its place."""
+    g = rng("large", pool, int(used * 100))
+    count, page = int(used * pool), 2
+    order = g.permutation(pool)
+    cut = [0, count // 2, count - 5, count]
+    table = np.full((3, count // 2 + 9), -1, np.int32)
+    lens, refs = np.zeros(3, np.int32), np.zeros(pool, np.int32)
+    for b in range(3):
+        row = order[cut[b]:cut[b + 1]]
+        table[b, :row.size], lens[b] = row, 2 * row.size - 1
+        refs[row] += 1
+    refs[order[:7]] += 1  # some are held twice
+    free = np.full(pool, -1, np.int32)
+    free[:pool - count] = order[count:]
+    for room in (pool // 9, pool // 2, 3):
+        want = pages_plain.compact(lens, table, free, refs, page, room)
+        t, f, r = cuda(table), cuda(free), cuda(refs)
+        src, dst, moved = (torch.empty(k, **I32) for k in (room, room, pool))
+        copies, left = torch.empty(1, **I32), torch.empty(1, **I32)
+        bq.kv_compact(cuda(lens), t, f, cuda([pool - count]), r, page, src, dst, copies, moved, free_count_out=left)
+        assert bq.device_status(clear=True) == 0
+        n = len(want[4])
+        assert int(copies) == n and int(left) == want[3]
+        assert torch.equal(torch.stack([src, dst]), cuda(np.array(want[4] + [(-1, -1)] * (room - n)).T))
+        for got, told in ((t, want[0]), (f, want[1]), (r, want[2]), (moved, want[5])):
+            assert torch.equal(got, cuda(told))
+        table, free, refs = want[0], want[1], want[2]
+    assert (refs[:count] > 0).all() and (refs[count:] == 0).all()
