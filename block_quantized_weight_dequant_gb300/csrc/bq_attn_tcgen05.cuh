@@ -4,9 +4,9 @@
 //
 // Mathematics.  For 128 query rows of one kv head at a time and tiles of 128 positions
 // (64 over bf16 and Q8_0 caches): S = Q K^T, P = 2^(factor S - m), O = O + P V with a running reference
-// m and sum l per row.  m follows the running maximum only when that has grown
-// by more than 2^8: weights are at most 2^8 then and O, which stays in tensor
-// memory, is rescaled (by the row's own 2^(m_old - m)) in few tiles.
+// m and sum l per row.  m follows the running maximum only when that has grown by
+// more than 2^GROWTH, 2^8 or 2^4: weights are at most that then and O, which stays in
+// tensor memory, is rescaled (by the row's own 2^(m_old - m)) in few tiles.
 //
 // A CTA takes a chunk of the positions for 128 rows.  Warps 0 to 3 and 4 to 7 are
 // two streams: they take the even and the odd tiles, each with scores S (a column
@@ -55,12 +55,17 @@ constexpr int TC_SOFTMAX_WARPS = 8, TC_COPY_WARPS = 3, TC_WARPS = 12;
 constexpr int TC_MASKS = 8;        // tiles whose masks are kept
 constexpr int TC_QBLOCK = TC_ROWS * 128;  // bytes of all rows' 64 values
 constexpr int TC_COLUMNS = 512;      // of tensor memory, all of it
-constexpr float TC_GROWTH = 8.0f;    // log2 of what a weight may be
-constexpr int TC_SHIFT_F16 = 7;      // fp16 weights carry 2^7: up to 2^15, two parts keep 2^-24
 
 template <bool HALF, int QP, int NB, bool Q8>
 struct TcShape {
     static constexpr int PP = HALF ? 2 : 3;  // parts of a weight
+    // log2 of what a weight may be.  fp16 ones carry 2^SHIFT, so that they are up to 2^15, and
+    // their parts keep 2^-25: 2^-32 of the reference's weight, or 2^-36 for fp32 queries, whose
+    // outputs would show it where a position far above all others has little value (with
+    // 2^-32 errors of up to 4e-5 of them, e^12 beside 1).  O is rescaled more often then, if
+    // scores spread: 96 requests of 32801 shared, fp32 queries over fp16, scores of N(0, 1)
+    // 122 us a call either way, of N(0, 9) 155 against 131.
+    static constexpr int GROWTH = HALF && QP > 1 ? 4 : 8, SHIFT = HALF ? 15 - GROWTH : 0;
     // positions of a tile; bytes of its rows of 64 values; parts of a key or value
     static constexpr int TILE = Q8 || PP == 3 ? 64 : 128, BLOCK = TILE * 128, KP = Q8 ? 2 : 1;
     // The tensor core truncates when it adds to O: after some hundred positions that shows
@@ -1078,7 +1083,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 }
                 was = misc.ref[s ^ 1][i];
             }
-            const bool grows = top > was + TC_GROWTH || (was == -INFINITY && top > was);
+            const bool grows = top > was + (float)S::GROWTH || (was == -INFINITY && top > was);
             const float now = grows ? top : was;
             misc.ref[s][i] = now;
             __syncwarp();
@@ -1114,7 +1119,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
             if (ref != now) l *= tc_pow2(ref - now);
             ref = now;
             tc_load32(s_at, x[0]);
-            const float shift = (HALF ? (float)TC_SHIFT_F16 : 0.0f) - (ref == -INFINITY ? 0.0f : ref);
+            const float shift = (float)S::SHIFT - (ref == -INFINITY ? 0.0f : ref);
             const uint64_t factors = pair_of(factor, factor), shifts = pair_of(shift, shift);
             uint64_t sum[2] = {0, 0};
             auto told = [&](int half) {  // half of the weights are in tensor memory
@@ -1200,7 +1205,7 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
         tc_fence_after();
         misc.ref[s][i] = ref, misc.sum[s][i] = l;
         // partial results of the ordinary kernel carry 2^ATTN_SHIFT_F16 over fp16 caches
-        constexpr float LIKE = HALF ? (float)(1 << (ATTN_SHIFT_F16 - TC_SHIFT_F16)) : 1.0f;
+        constexpr float LIKE = HALF ? (float)(1 << (ATTN_SHIFT_F16 - S::SHIFT)) : 1.0f;
         const float out = Q8 ? LIKE * by_values : LIKE;
         float *row = reinterpret_cast<float *>(ring) + i * S::OROW;
         for (int c = 8 * s; c < D16 && ok; c += 16) {

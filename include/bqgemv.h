@@ -618,9 +618,9 @@ bq_status bq_paged_attention(const bq_kv_cache *cache, const bq_attention_args *
  *    where so little is shared that one pass of it serves the call.
  *  - Over the shared pages heads of up to 128 values go through the tensor cores
  *    (over BQ_Q8_0 from 33 rows of a kv head on): queries as in bq_paged_attention,
- *    probabilities exactly (24 bits) over a BQ_BF16 cache, to 2^-23 of the number or
- *    2^-32 of the largest of its row, where that is more, over BQ_F16 and BQ_Q8_0
- *    ones, keys and values of a BQ_Q8_0 cache to 2^-22, or 2^-39 of 127 times the
+ *    probabilities exactly (24 bits) over a BQ_BF16 cache, to 2^-23 of the number or,
+ *    where that is more, 2^-32 of the largest of its row (2^-36 for BQ_F32 queries)
+ *    over BQ_F16 and BQ_Q8_0 ones, keys and values of a BQ_Q8_0 cache to 2^-22, or 2^-39 of 127 times the
  *    largest scale of the chunk (at most 4096 positions of a head) where that is
  *    more.  The tensor cores sum products of 256 positions (512 where both queries
  *    and cache are BQ_F16, or BQ_Q8_0 with 16-bit queries), fp32 the rest. */

@@ -116,3 +116,32 @@ def test_long_sums_next_to_a_border_of_the_output(kind, dtype):
     # and the joins: under 32 roundings of 2^-24.
     adds = (256 if dtype == F32 or kind == "bf16" else 512) // 16 * (2 if kind == "f16" else 3)
     held(out, want, dtype, (adds * 2.0 ** -23 + 2.0 ** -19) * mag)
+
+
+@pytest.mark.parametrize("kind,dtype", PATHS)
+def test_weights_far_below_the_largest(kind, dtype):
+    """One position of each request's row takes e^9 to e^12 times the weight of any other
+    and has value 0, so that the outputs are what the small weights make of it. As many kv
+    heads as the GPU has places: all positions are one chunk."""
+    g = rng("sink", kind, str(dtype))
+    D, page, n, kv, requests = 64, 16, 2048, 152, 40
+    whole = n // page
+    k, v = np.zeros((whole + requests, kv, page, D)), np.ones((whole + requests, kv, page, D))
+    k[1, :, 5, 0], v[1, :, 5] = 1.0, 0.0
+    cache = cache_of(kind, k, v)
+    table = torch.arange(whole, dtype=torch.int32).expand(requests, -1)
+    table = torch.cat([table, whole + torch.arange(requests, dtype=torch.int32)[:, None]], 1).to(DEV)
+    q = torch.zeros(requests, kv, D, dtype=dtype, device=DEV)
+    q[:, :, 0] = torch.from_numpy(9.0 + 3.0 * g.random((requests, kv))).to(dtype).to(DEV)
+    out = bq.paged_prefix_attention(cache, q, table, torch.full((requests,), n + 1, dtype=torch.int32, device=DEV), n,
+                                    scale=1.0)
+    want = ((n - 1 + 1) / (q[:, :, :1].double().exp() + n)).expand(-1, -1, D)
+    # A small weight beside the large one: an exponent of at most 18 of a factor right to
+    # 2^-23 and rounded twice at 2^-21, times ln 2; two powers of 2^-22; parts of 2^-23, and
+    # for fp32 queries at most 2^-36 of the largest weight, of which it is 2^-17.4 or more
+    # (2^-32 for others). Sums: under 32 roundings of 2^-24, and 2^-18 for what the tensor
+    # cores lose of them (the reckoning of the test above, of 48 additions).
+    rel = np.log(2.0) * (18 * 2.0 ** -23 + 2.0 ** -20) + 2.0 ** -21 + 2.0 ** -23 + 2.0 ** -19
+    rel += (48 if dtype == F32 or kind == "bf16" else 96) * 2.0 ** -23
+    rel += 0.0 if kind == "bf16" else 2.0 ** (17.4 - (36 if dtype == F32 else 32))
+    held(out, want, dtype, rel * want)
