@@ -248,11 +248,11 @@ constexpr int TILE_ROWS = 128;
 int tile_positions(const bq_kv_cache *c) { return c->type == BQ_F16 ? 128 : 64; }
 
 // Tiles of a chunk: the fewest steps of the whole GPU, a chunk's start, joins and
-// partial results counted as FIXED tiles.  At most MOST tiles, so that the
-// tensor core's sums stay short.
+// partial results counted as FIXED tiles.  At most 8192 positions, or 4096 of a Q8_0
+// cache, whose parts go by the chunk's largest scale.
 bool size_tensor_pass(Pass *p, int groups, int64_t rows, int64_t positions, int sms) {
-    constexpr int FIXED = 6, MOST = 64;
-    const int TILE = tile_positions(&p->a.c);
+    constexpr int FIXED = 6;
+    const int TILE = tile_positions(&p->a.c), MOST = (p->a.c.type == BQ_Q8_0 ? 4096 : 8192) / TILE;
     p->inst = nullptr;
     p->tile_rows = TILE_ROWS;
     p->a.group_rows = (int)rows;
