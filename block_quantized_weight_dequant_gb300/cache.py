@@ -391,8 +391,9 @@ class BlockTables:
 class SharedBlockTables(BlockTables):
     """BlockTables whose requests may share pages: forks, pages of their own where
     forks part (copy on write), pages freed when nobody holds them any more, and
-    compaction.  `caches`: the layers' PagedKVCache objects, whose pages are copied
-    as the steps need it; all calls enqueue kernels only and can be captured."""
+    compaction.  `caches`: the layers' PagedKVCache objects, of one geometry and
+    device, whose pages are copied as the steps need it; all calls enqueue kernels only
+    and can be captured."""
 
     def __init__(self, requests, max_pages, pages, page_size, max_tokens, caches=(), device="cuda"):
         super().__init__(requests, max_pages, pages, page_size, max_tokens, device)
@@ -452,7 +453,8 @@ def kv_append(cache, k, v, slots, q=None, q_out=None, rope=None, positions=None,
     keys are rotated by `positions` (int32 [axes, tokens], or [tokens] for one
     axis), and so are queries q [tokens, heads, head_dim] into q_out (a new
     tensor, or q itself).  Inputs may be slices of one projection's rows.
-    Returns q_out, or None without q."""
+    With q_norm, k_norm (fp32 [head_dim] gains) queries and keys are normed per
+    head first, x / sqrt(mean x^2 + eps) * gain.  Returns q_out, or None without q."""
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")
     dev, kv, D = cache.device, cache.kv_heads, cache.head_dim
@@ -596,13 +598,19 @@ def _groups(shared, requests):
 
 def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, out=None, workspace=None):
     """paged_attention for requests that share the beginning of their histories:
-    the same result, with the shared pages gone through once for all requests of a
-    group.  shared: the number of positions that all requests have in common, or
+    the same result to the last bits, with the shared pages gone through once for all
+    requests of a group.  Those bits are paged_attention's own only where one pass of it
+    serves the call, little being shared: else a row's depend on the call's geometry
+    (requests, rows and groups too, so that a verify row's are not the one-row
+    call's), sums are in another order, and over fp16 and Q8_0 caches weights keep
+    2^-32 of the largest of their row (2^-36 for fp32 queries), where paged_attention
+    keeps 2^-39; over bf16 they are exact in both.  shared: the number of positions that all requests have in common, or
     (requests, positions) pairs of groups in the requests' order (host numbers).
     Whole pages of them count (shared // page_size): those entries of the requests'
     table rows name the same pages, as kv_shared_tables makes them; what is behind
-    is each request's own.  A request's rows see all its shared positions (lens[b] -
-    rows + 1 of them at least); one that has ended has length 0 and gives zeros.
+    is each request's own.  A request's rows see all its shared positions, if there
+    are any (lens[b] - rows + 1 is at least as many); one that has ended has length 0
+    and gives zeros.
     q, table, lens, rows, scale and out as for paged_attention; workspace: uint8,
     ``paged_prefix_attention_workspace(...)`` bytes, under the same rules."""
     if not isinstance(cache, PagedKVCache):
@@ -653,7 +661,8 @@ def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, ou
 
 
 def paged_prefix_attention_workspace(cache, requests, rows, heads, width, shared, dtype=torch.float32):
-    """Bytes of workspace of a paged_prefix_attention call of this geometry."""
+    """Bytes of workspace of a paged_prefix_attention call of this geometry, whatever
+    the queries' dtype."""
     args = _lib.BqAttentionArgs(_DTYPES[dtype], _i32(requests), _i32(rows), _i32(heads), _i32(width), 1.0, int(width))
     nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ctypes.byref(args), *_groups(shared, requests))
     if nbytes < 0:

@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 2)
             }
             if constexpr (NORM) {
                 // a head's values lie on GL neighbouring lanes: a butterfly sums their
-                // squares in an order that depends on head_dim alone
+                // squares in an order that depends on head_dim, and on rot and interleaved,
+                // which say what values a lane has
 #pragma unroll
                 for (int u = 0; u < UNROLL; ++u) {
                     if (!any_normed[u]) continue;

@@ -10,9 +10,10 @@
 // here, in a fixed order: a row's bits depend on its own inputs and the call's
 // geometry alone.
 //
-// Bounds: by size, the shared pass (96 requests of 32801 shared, bf16, 32 over 8 heads
-// of 128: 136 us a call), the ordinary kernel's instructions (16 requests of 30011 over
-// Q8_0: 62 us) or the chain of three launches (200 requests in 3 groups of 9001: 32 us).
+// Bounds: by size, the shared pass (96 requests of 32801 shared, bf16, 32 over 8 heads of
+// 128: 125 us a call, 96 of them that pass), the ordinary kernel's instructions (16
+// requests of 30011 over Q8_0: 58 us) or the chain of three launches (200 requests in 3
+// groups of 9001: 31 us).
 // The launches follow one another, each waiting for the one before to end: own pages that
 // started while the shared ones were gone through, without that wait, took 8, 5 and 1 us
 // less, but nothing that is documented orders their reads behind the writes before the call.
@@ -237,8 +238,8 @@ bool size_pass(Pass *p, int requests, int64_t rows, int64_t positions, int pairs
 // The tensor-memory kernel for heads of up to 128 values: tiles of 128 rows, chunks
 // of whole tiles of positions, one CTA per SM.  Over a Q8_0 cache, whose codes it has
 // to put into two 16-bit parts, for more rows of a kv head than two passes of the
-// ordinary kernel's 16: 30011 shared, 8 kv heads of 128, fp32 queries, 32 rows 59 us
-// against 53, 48 rows 68 against 90, 128 rows 89 against 185.
+// ordinary kernel's 16: 30011 shared, 8 kv heads of 128, fp32 queries, 32 rows 65 us
+// against 57, 48 rows 74 against 92, 128 rows 92 against 189.
 constexpr int64_t Q8_ROWS = 32;
 bool has_tensor_kernel(const bq_kv_cache *c, int64_t rows) {
     return c->head_dim <= 128 && (c->type != BQ_Q8_0 || rows > Q8_ROWS);

@@ -22,13 +22,14 @@
 // in tensor memory; the weights go back there in the columns of the scores that they
 // come from, and are the first operand of the second product.  Over a Q8_0 cache
 // warps 8 to 10, and those of warps 0 to 7 whose 32 rows are none of the group's, put
-// codes times scales into parts on the way, tiles of 64 positions: 48 rows of a kv head
-// 80 -> 68 us a call, 96 86 -> 74 (30011 shared, 8 kv heads of 128).
+// codes times scales into parts on the way: the latter take 12 us off a call of 48 or 96
+// rows of a kv head (30011 shared, 8 kv heads of 128).
 //
-// Bounds.  96 requests of 32801 shared, bf16, 32 over 8 heads of 128: 57 us, 901 TFLOP/s
-// of scores and values counted once; products keep the tensor pipe busy for 55% (second
-// parts of the weights half of PV), the issue of their instructions 35%, and 144 of 152
-// SMs have a chunk.  Over Q8_0 the putting into parts: 128 rows 4400 cycles a tile.
+// Bounds.  96 requests of 32801 shared, bf16, 32 over 8 heads of 128: 96 us, 535 TFLOP/s
+// of scores and values counted once; products keep the tensor pipe busy for 44% (second
+// and third parts of the weights two thirds of PV), the handing over of tiles of 64
+// positions takes the rest, and 144 of 152 SMs have a chunk.  Over Q8_0 the putting into
+// parts: 128 rows 4400 cycles a tile.
 //
 // Precision.  A query of the cache's type is used as it is, any other in QP 16-bit
 // parts (fp16 2, after scaling the row by a power of two; bf16 3); weights are two
@@ -75,7 +76,7 @@ struct TcShape {
     // weights of three parts, with 512 0.12%, with 256 0.07%, fp32 sums 0.09%).  So O is
     // added up elsewhere in tensor memory, rounded to nearest, every FLUSH tiles, and
     // starts again.  fp16 heads of 128 then have their queries in shared memory: 96
-    // requests of 32801 shared, fp16 89 us a call against 77, fp32 queries 117 against 86.
+    // requests of 32801 shared take 12 us more a call, with fp32 queries 31 more.
     static constexpr int FLUSH = (HALF && QP == 1 ? 512 : 256) / TILE;
     // columns of tensor memory: scores of two streams, O, its sum, and in the rest third
     // parts of the weights and, where there is room, queries (else these lie in shared memory)
@@ -696,7 +697,8 @@ __global__ void __launch_bounds__(TC_WARPS * 32, 1)
                 barrier_wait_end(&misc.full[n % SLOTS], n / SLOTS & 1);
         __syncwarp();
     } else if (warp >= TC_SOFTMAX_WARPS && warp < TC_SOFTMAX_WARPS + TC_COPY_WARPS) {
-        // ---- copies of 16 bytes (none where tensor maps do them): K and V of each tile in turn, every third 8 rows by each warp ----
+        // ---- copies of 16 bytes (none where tensor maps do them): K and V of each tile in
+        // turn, every third 8 rows by each warp ----
         constexpr int GROUPS = TILE / 8, MINE = (GROUPS + TC_COPY_WARPS - 1) / TC_COPY_WARPS;  // of 8 rows
         const int cw = warp - TC_SOFTMAX_WARPS;
         const long long head_off = (long long)h * a.c.head_stride;

@@ -185,7 +185,8 @@ class PagedDecode:
     Every product is the package's GEMV (or its verify form, whose rows have the
     single row's bits; the gate and up pair, which has no verify form, runs once per
     row and reads its weights as often), and the calls between them compute each row
-    on its own, so a row of a verify step has the bits of the one-row step.
+    on its own, so a row of a verify step has the bits of the one-row step (but with
+    ``shared`` pages, whose attention cuts its sums by the whole step).
     ``step`` enqueues kernels only and can be captured in a CUDA graph."""
 
     def __init__(self, qtype, layers, lm_head, final_gamma, caches, heads, rope, eps=1e-6, alpha=1.0, beta=1.0,
@@ -240,8 +241,9 @@ class PagedDecode:
         kv_block_tables gives them; table, lens: the requests' tables and lengths,
         the new tokens counted (rows / requests tokens each).  shared: the positions
         that the requests share, or groups of them, as for paged_prefix_attention
-        (their pages are then read once for all of them).  Returns logits [rows,
-        vocab], a buffer of this object."""
+        (their pages are then read once for all of them, and the logits are those of a
+        step without it but for the last bits).  Returns logits [rows, vocab], a buffer
+        of this object."""
         requests = lens.numel()
         if requests < 1 or self.rows % requests:
             raise ValueError(f"{self.rows} rows do not share out among {requests} requests")

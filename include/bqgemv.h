@@ -542,7 +542,8 @@ bq_status bq_kv_append(const bq_kv_cache *cache, const bq_kv_append_args *args, 
 /* The same with norms of queries and keys over each head (RunIT README, kernel
  * table: the norm of q and k fused with the rotation), before they are turned:
  *   x = x / sqrt(mean over head_dim of x^2 + eps) * gain
- * Squares are summed in fp32, in an order that depends on head_dim alone.
+ * Squares are summed in fp32, in an order that depends on head_dim, rot and
+ * interleaved alone.
  *  - q_gain, k_gain: fp32 [head_dim], NULL for no norm (both NULL: the call is
  *    bq_kv_append, bit for bit; q_gain is ignored without q).  Values are not
  *    normed.  eps finite, >= 0. */
