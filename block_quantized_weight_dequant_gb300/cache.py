@@ -11,6 +11,8 @@ GPU-resident paged cache.)
 """
 import ctypes
 import math
+import operator
+from numbers import Integral
 
 import torch
 
@@ -582,11 +584,19 @@ def paged_attention_workspace(cache, requests, rows, heads, width):
     return nbytes
 
 
+def _shared(shared):
+    """A call's `shared` as an int or a tuple of pairs, which tell its plan apart."""
+    if type(shared) is int:
+        return shared
+    return int(shared) if isinstance(shared, Integral) else tuple(map(tuple, shared))
+
+
 def _groups(shared, requests):
     """Host arrays of the groups' counts and shared positions, and how many."""
-    if isinstance(shared, int):
+    if type(shared) is int:
         shared = [(requests, shared)]
-    counts, positions = zip(*shared) if len(shared) else ((), ())
+    pairs = [(operator.index(n), operator.index(positions)) for n, positions in shared]
+    counts, positions = zip(*pairs) if pairs else ((), ())
     n = len(counts)
     if not 1 <= n <= _lib.BQ_PREFIX_MAX_GROUPS:
         raise ValueError(f"shared must have 1 to {_lib.BQ_PREFIX_MAX_GROUPS} groups, got {n}")
@@ -638,7 +648,7 @@ def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, ou
                                 table.data_ptr(), lens.data_ptr())
     ref = _byref(args)
     # the groups' host arrays and the workspace's bytes, by the call's geometry
-    shared = shared if type(shared) is int else tuple(map(tuple, shared))
+    shared = _shared(shared)
     key = (n, rows, heads, width, dtype, shared)
     plan = cache._workspace.get(key)
     if plan is None:
@@ -664,7 +674,7 @@ def paged_prefix_attention_workspace(cache, requests, rows, heads, width, shared
     """Bytes of workspace of a paged_prefix_attention call of this geometry, whatever
     the queries' dtype."""
     args = _lib.BqAttentionArgs(_DTYPES[dtype], _i32(requests), _i32(rows), _i32(heads), _i32(width), 1.0, int(width))
-    nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ctypes.byref(args), *_groups(shared, requests))
+    nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ctypes.byref(args), *_groups(_shared(shared), requests))
     if nbytes < 0:
         raise ValueError(f"no paged_prefix_attention of requests={requests} rows={rows} heads={heads} width={width} "
                          f"shared={shared}")

@@ -48,3 +48,23 @@ def test_the_type_of_the_queries_does_not_move_the_workspace(lib):  # noqa: F811
             assert len(need) == 1 and need.pop() > 0
     finally:
         limit(-1)
+
+
+def test_whole_numbers_of_any_kind_say_what_is_shared():
+    """numpy's among them; others are refused, not cut to whole ones."""
+    import numpy as np
+
+    from block_quantized_weight_dequant_gb300.cache import _groups, _shared
+
+    def told(shared, requests):
+        counts, positions, n = _groups(_shared(shared), requests)
+        return list(zip(counts, positions))
+
+    for one in (40, np.int64(40), np.int32(40), np.array([40])[0]):
+        assert told(one, 3) == [(3, 40)]
+    pairs = np.array([[2, 40], [1, 0]])
+    for several in (pairs, pairs.tolist(), [(np.int32(2), 40), (1, np.int64(0))], (p for p in pairs)):
+        assert told(several, 3) == [(2, 40), (1, 0)]
+    for bad in (40.0, 40.5, [(2, 40.5), (1, 0)], [(2.0, 40), (1, 0)], "40", [40, 1], None):
+        with pytest.raises((TypeError, ValueError)):
+            told(bad, 3)
