@@ -525,9 +525,10 @@ def paged_attention(cache, q, table, lens, rows=1, scale=None, out=None, workspa
     1 / sqrt(head_dim).  Row r's bits are those of the one-row call at its
     length.  The work is cut by the table's width, not by the lengths: a table
     much wider than its requests leaves a part of the GPU idle (one request of
-    8000 positions: 9 us in a table of that width, 26 in one of 131072).  out may be q.  workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per
-    call that may overlap others, also calls of two host threads on one stream;
-    None: one of the call's own from PyTorch's allocator."""
+    8000 positions: 9 us in a table of that width, 26 in one of 131072).  out may be q.
+    workspace: uint8, ``paged_attention_workspace(...)`` bytes, one per call that may
+    overlap others, also calls of two host threads on one stream; None: one of the
+    call's own from PyTorch's allocator."""
     if not isinstance(cache, PagedKVCache):
         raise TypeError("cache must be a PagedKVCache")
     dev, D = cache.device, cache.head_dim
@@ -614,7 +615,8 @@ def paged_prefix_attention(cache, q, table, lens, shared, rows=1, scale=None, ou
     (requests, rows and groups too, so that a verify row's are not the one-row
     call's), sums are in another order, and over fp16 and Q8_0 caches weights keep
     2^-32 of the largest of their row (2^-36 for fp32 queries), where paged_attention
-    keeps 2^-39; over bf16 they are exact in both.  shared: the number of positions that all requests have in common, or
+    keeps 2^-39; over bf16 they are exact in both.
+    shared: the number of positions that all requests have in common, or
     (requests, positions) pairs of groups in the requests' order (host numbers).
     Whole pages of them count (shared // page_size): those entries of the requests'
     table rows name the same pages, as kv_shared_tables makes them; what is behind
@@ -674,7 +676,8 @@ def paged_prefix_attention_workspace(cache, requests, rows, heads, width, shared
     """Bytes of workspace of a paged_prefix_attention call of this geometry, whatever
     the queries' dtype."""
     args = _lib.BqAttentionArgs(_DTYPES[dtype], _i32(requests), _i32(rows), _i32(heads), _i32(width), 1.0, int(width))
-    nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ctypes.byref(args), *_groups(_shared(shared), requests))
+    nbytes = lib.bq_paged_prefix_attention_workspace_bytes(cache._ref, ctypes.byref(args),
+                                                           *_groups(_shared(shared), requests))
     if nbytes < 0:
         raise ValueError(f"no paged_prefix_attention of requests={requests} rows={rows} heads={heads} width={width} "
                          f"shared={shared}")
